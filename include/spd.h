@@ -421,6 +421,139 @@ spd_status spd_prefill_block_sparse_attention(const spd_prefill_config *cfg, int
  * SPD_ERR_DEVICE_CHECK if a kernel's own check tripped, else SPD_OK. */
 spd_status spd_prefill_check(const void *workspace, spd_stream stream);
 
+/* ---- dense attention with score rules ------------------------------------ */
+/*
+ * How a query's score of a key is made, in this order:
+ *   s = scale q . k                 scale 0: 1 / sqrt(head_dim)
+ *   s = softcap tanh(s / softcap)   softcap 0: no cap
+ *   s = s - slopes[h] |pos_q - pos_k|   slopes device fp32 [Hq]; NULL: no bias
+ * Scores, softmax statistics and sums are fp32.  A zero-initialised rule is the
+ * plain softmax(q . k / sqrt(head_dim)).
+ */
+typedef struct {
+  float scale;         /* finite, >= 0 */
+  float softcap;       /* finite, >= 0 */
+  const float *slopes; /* device [num_q_heads], 4-byte aligned, or NULL */
+} spd_score_rule;
+
+/* Type of the output: fp32 (softmax weights enter the products with v with
+ * about 16 bits for bf16 inputs, 22 for fp16), or the type of the inputs
+ * (weights rounded to it once, the fp32 sums rounded to it at the end). */
+typedef enum { SPD_OUT_F32 = 0, SPD_OUT_DTYPE = 1 } spd_out;
+
+typedef struct {
+  int num_q_heads, num_kv_heads, head_dim; /* Hq % Hkv == 0 (any quotient), Hkv 1..128,
+                                              Hq <= 1024, d in {64, 128} */
+  spd_dtype dtype;                         /* of q, k and v */
+  spd_out out;
+  spd_score_rule rule;
+} spd_dense_config;
+
+/*
+ * Attention of q_len queries over kv_len keys of one packed row: a whole
+ * prompt, the next chunk of one (its queries against every key so far), or a
+ * single token (q_len 1).  Query i stands at position kv_len - q_len + i, key
+ * t at position t.
+ *   out[i][h] = sum_t softmax_t(s(i, t)) v_t over key_begin[i] <= t < key_end[i]
+ * A query whose interval holds no key gets 0.
+ *   q    device [q_len][Hq][d], rows q_stride elements apart
+ *   k, v device [kv_len][Hkv][d], rows k_stride / v_stride elements apart
+ *        (strides multiples of 8, at least a row; pointers 16-byte aligned)
+ *   key_begin, key_end  device int32 [q_len], clamped to [0, kv_len]; both NULL:
+ *        causal, [0, position + 1).  spd_document_key_ranges makes them for
+ *        packed documents.
+ *   out  device [q_len][Hq][d], fp32 or dtype (cfg->out), 16-byte aligned.
+ *   workspace  device, 256-byte aligned, at least spd_prefill_attention_sizes
+ *        bytes (which may be 0, then NULL); one call at a time per workspace.
+ *        The size is computed for the current device.
+ * A key or value that a query does not attend never reaches it, finite or not;
+ * an attended value that is not finite makes the query's output not finite.
+ * All pointers are of one device; the call runs on it whichever is current.
+ * SPD_ERR_INVALID_ARG / SPD_ERR_CAPACITY on bad arguments (nothing enqueued);
+ * SPD_ERR_CUDA if a launch fails.
+ */
+spd_status spd_prefill_attention_sizes(const spd_dense_config *cfg, int q_len, int kv_len,
+                                       size_t *workspace_bytes);
+spd_status spd_prefill_attention(const spd_dense_config *cfg, int q_len, int kv_len, const void *q,
+                                 long long q_stride, const void *k, long long k_stride,
+                                 const void *v, long long v_stride, const int *key_begin,
+                                 const int *key_end, void *out, void *workspace,
+                                 size_t workspace_bytes, spd_stream stream);
+
+/* Waits for `stream` and reads (and clears) the error word that
+ * spd_prefill_attention's kernels share on the device of `out`:
+ * SPD_ERR_DEVICE_CHECK if a kernel's own check tripped since it was last read,
+ * else SPD_OK. */
+spd_status spd_prefill_attention_check(const void *out, spd_stream stream);
+
+/*
+ * Key intervals of n_tokens tokens packed from documents: document i holds the
+ * tokens offsets[i] <= t < offsets[i + 1] and its first prefix[i] tokens are
+ * seen by all of its tokens; the others are seen causally.
+ *   key_begin[t] = offsets[i], key_end[t] = max(t + 1, offsets[i] + min(prefix[i], length_i))
+ * Tokens outside every document (padding) get an empty interval.
+ *   offsets  device int32 [n_docs + 1], ascending;  prefix  device int32
+ *   [n_docs] or NULL (causal);  key_begin, key_end  device int32 [n_tokens].
+ */
+spd_status spd_document_key_ranges(const int *offsets, const int *prefix, int n_docs, int n_tokens,
+                                   int *key_begin, int *key_end, spd_stream stream);
+
+/*
+ * Decode attention of a batch whose sequences all continue one prefix, over
+ * every token of both (no page selection; step counters and selections stay as
+ * they are).  The prefix is a sequence of the context like any other, filled
+ * once by spd_kv_append; each listed sequence holds only its own tokens.  The
+ * prefix's keys and values are read once for the batch.
+ *   out[i][h] = sum_t softmax_t(s) v_t over the prefix's Lp tokens (positions
+ *               0 .. Lp - 1) and the sequence's own L_i (Lp .. Lp + L_i - 1);
+ *               the query stands at the newest, Lp + L_i - 1
+ *   prefix_id  live sequence with tokens, not in seq_ids; -1: no prefix (then
+ *              every listed sequence needs a token)
+ *   q    device [n_seqs][Hq][d];  out device [n_seqs][Hq][d], fp32 or dtype
+ *   rule NULL: plain
+ *   weights_in, weights_out  device fp32 [n_seqs][Hkv][weights_stride] or NULL:
+ *        weights_out[i][g][t] = weights_in[i][g][t] + the softmax weights of the
+ *        group's query heads on the sequence's own token t, summed, for t < L_i
+ *        (what lies behind is left as it was; NULL weights_in: 0).  The same
+ *        array may be both.  weights_stride >= every L_i.
+ *   workspace  device, 256-byte aligned, at least spd_shared_prefix_sizes bytes
+ *        for the same sequences (host lengths); one call at a time per workspace.
+ * SPD_ERR_INVALID_ARG for a context with streaming heads or fp8 storage;
+ * SPD_ERR_STATE for a prefix without tokens, or a sequence without tokens when
+ * there is no prefix.  Device checks are reported by spd_check_status.
+ */
+spd_status spd_shared_prefix_sizes(spd_ctx *ctx, int prefix_id, const int *seq_ids, int n_seqs,
+                                   int weights, size_t *workspace_bytes);
+spd_status spd_shared_prefix_attention(spd_ctx *ctx, const void *q, int prefix_id,
+                                       const int *seq_ids, int n_seqs, const spd_score_rule *rule,
+                                       spd_out out_type, void *out, const float *weights_in,
+                                       float *weights_out, long long weights_stride,
+                                       void *workspace, size_t workspace_bytes,
+                                       spd_stream stream);
+
+/*
+ * Eviction by accumulated attention weight: for every listed pair, kv head g of
+ * the source (L tokens) keeps m = min(keep, L) tokens -- its min(recent, m)
+ * newest and, of the others, those of the greatest weights[i][g][t] (ties to
+ * the lower position; NaN counts as the greatest) -- and they become tokens
+ * 0 .. m - 1 of the destination, in their order, with exact page metadata.
+ * Every kv head keeps its own tokens.  The source stays as it was (free it, or
+ * keep it as a prefix); the destination must be empty and takes pages as in
+ * spd_kv_append (all or nothing: SPD_ERR_NO_PAGES / SPD_ERR_CAPACITY change
+ * nothing).
+ *   weights  device fp32 [n_seqs][Hkv][weights_stride], weights_stride >= every L
+ *   kept     device int32 [n_seqs][Hkv][keep]: the kept positions, ascending, -1
+ *            behind the m-th
+ *   kept_weights  device fp32 [n_seqs][Hkv][keep] or NULL: their weights, 0
+ *            behind (the weights to go on accumulating from)
+ * Positions are renumbered: a later distance bias counts the kept tokens only.
+ * SPD_ERR_INVALID_ARG for a context with streaming heads; fp8 storage is
+ * supported.
+ */
+spd_status spd_kv_evict(spd_ctx *ctx, const int *src_ids, const int *dst_ids, int n_seqs, int keep,
+                        int recent, const float *weights, long long weights_stride, int *kept,
+                        float *kept_weights, spd_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

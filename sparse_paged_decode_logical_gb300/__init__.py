@@ -13,7 +13,8 @@ the device buffers with torch and takes torch tensors.
 import ctypes
 import os
 
-__all__ = ["SpdError", "SparsePagedKVCache", "lib", "LIB_PATH", "make_config"]
+__all__ = ["SpdError", "SparsePagedKVCache", "lib", "LIB_PATH", "make_config",
+           "prefill_block_sparse_attention", "prefill_attention", "document_key_ranges"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libspd.so")
 
@@ -55,6 +56,17 @@ class spd_prefill_config(ctypes.Structure):
                 ("dense_below", ctypes.c_int)]
 
 
+class spd_score_rule(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("slopes", ctypes.c_void_p)]
+
+
+class spd_dense_config(ctypes.Structure):
+    _fields_ = [("num_q_heads", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("out", ctypes.c_int),
+                ("rule", spd_score_rule)]
+
+
 class spd_sizes(ctypes.Structure):
     _fields_ = [(f, ctypes.c_size_t) for f in BUFFER_FIELDS]
 
@@ -76,7 +88,7 @@ def lib():
                           "or python sparse_paged_decode_logical_gb300/build.py)")
     L = ctypes.CDLL(LIB_PATH)
     vp, ip, i, st = ctypes.c_void_p, ctypes.POINTER(ctypes.c_int), ctypes.c_int, ctypes.c_int
-    ll = ctypes.POINTER(ctypes.c_longlong)
+    ll, i64 = ctypes.POINTER(ctypes.c_longlong), ctypes.c_longlong
     sig = {
         "spd_query_sizes": [ctypes.POINTER(spd_config), ctypes.POINTER(spd_sizes)],
         "spd_create": [ctypes.POINTER(spd_config), ctypes.POINTER(spd_buffers),
@@ -103,6 +115,16 @@ def lib():
         "spd_prefill_block_sparse_attention": [ctypes.POINTER(spd_prefill_config), i, vp, vp, vp,
                                                vp, vp, vp, vp, vp, ctypes.c_size_t, vp],
         "spd_prefill_check": [vp, vp],
+        "spd_prefill_attention_sizes": [ctypes.POINTER(spd_dense_config), i, i,
+                                        ctypes.POINTER(ctypes.c_size_t)],
+        "spd_prefill_attention": [ctypes.POINTER(spd_dense_config), i, i, vp, i64, vp, i64, vp,
+                                  i64, vp, vp, vp, vp, ctypes.c_size_t, vp],
+        "spd_prefill_attention_check": [vp, vp],
+        "spd_document_key_ranges": [vp, vp, i, i, vp, vp, vp],
+        "spd_shared_prefix_sizes": [vp, i, ip, i, i, ctypes.POINTER(ctypes.c_size_t)],
+        "spd_shared_prefix_attention": [vp, vp, i, ip, i, ctypes.POINTER(spd_score_rule), i, vp,
+                                        vp, vp, i64, vp, ctypes.c_size_t, vp],
+        "spd_kv_evict": [vp, ip, ip, i, i, i, vp, i64, vp, vp, vp],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -459,6 +481,78 @@ class SparsePagedKVCache:
             _check(st, "spd_decode_step", self.ctx)
         return out
 
+    def shared_prefix_attention(self, q, prefix_id, seq_ids, scale=0.0, softcap=0.0, slopes=None,
+                                weights_in=None, weights_out=None, out_dtype=None, out=None,
+                                stream=None):
+        """Decode attention of sequences that all continue the sequence
+        ``prefix_id`` (None: no prefix) over every token of both: returns out
+        [n][Hq][d], fp32 or (out_dtype) the cache's type.  scale 0 is
+        1/sqrt(d); softcap caps the scores by a tanh; slopes fp32 [Hq] bias
+        them by distance.  weights_out fp32 [n][Hkv][>= longest own length]
+        receives weights_in (None: 0) plus the softmax weight of every own
+        token, summed over the query heads of its kv head."""
+        t = self.torch
+        ids, n = _ids(seq_ids)
+        prefix_id = -1 if prefix_id is None else int(prefix_id)
+        qp = self._ptr(q, (n, self.Hq, self.d), self.dtype)
+        if out_dtype is None:
+            out_dtype = t.float32 if out is None else out.dtype
+        if out_dtype not in (t.float32, self.dtype):
+            raise ValueError("out_dtype must be torch.float32 or %s" % self.dtype)
+        if out is None:
+            out = t.empty((n, self.Hq, self.d), dtype=out_dtype, device=self.device)
+        op = self._ptr(out, (n, self.Hq, self.d), out_dtype)
+        rule = _rule(scale, softcap, slopes, self.Hq, self.device)
+        w_in = w_out = None
+        stride = 0
+        if weights_out is not None:
+            if weights_out.dim() != 3:
+                raise ValueError("weights_out must be [n][Hkv][stride]")
+            stride = weights_out.shape[2]
+            w_out = self._ptr(weights_out, (n, self.Hkv, stride), t.float32)
+            if weights_in is not None:
+                w_in = self._ptr(weights_in, (n, self.Hkv, stride), t.float32)
+        elif weights_in is not None:
+            raise ValueError("weights_in needs weights_out")
+        ws = ctypes.c_size_t()
+        st = lib().spd_shared_prefix_sizes(self.ctx, prefix_id, ids, n, w_out is not None,
+                                           ctypes.byref(ws))
+        if st != SPD_OK:
+            _check(st, "spd_shared_prefix_sizes", self.ctx)
+        raw = self._stream(stream)
+        work = _workspace(t, ws.value, self.device, raw, stream)
+        st = lib().spd_shared_prefix_attention(
+            self.ctx, qp, prefix_id, ids, n, ctypes.byref(rule),
+            0 if out_dtype == t.float32 else 1, op, w_in, w_out, stride, work.data_ptr(),
+            ws.value, raw or None)
+        if st != SPD_OK:
+            _check(st, "spd_shared_prefix_attention", self.ctx)
+        return out
+
+    def kv_evict(self, src_ids, dst_ids, keep, recent, weights, stream=None):
+        """Compact each source sequence into an empty destination sequence:
+        every kv head keeps its `recent` newest tokens and the best of the
+        others by weights fp32 [n][Hkv][>= longest source], `keep` in all.
+        Returns (kept int32 [n][Hkv][keep], -1 padded, and their weights)."""
+        t = self.torch
+        src, n = _ids(src_ids)
+        dst, nd = _ids(dst_ids)
+        if n != nd:
+            raise ValueError("as many destinations as sources are needed")
+        if weights.dim() != 3:
+            raise ValueError("weights must be [n][Hkv][stride]")
+        keep = int(keep)
+        if keep < 1:
+            raise ValueError("keep must be >= 1")
+        wp = self._ptr(weights, (n, self.Hkv, weights.shape[2]), t.float32)
+        kept = t.empty((n, self.Hkv, keep), dtype=t.int32, device=self.device)
+        kw = t.empty((n, self.Hkv, keep), dtype=t.float32, device=self.device)
+        raw = self._stream(stream)
+        _check(lib().spd_kv_evict(self.ctx, src, dst, n, keep, int(recent), wp, weights.shape[2],
+                                  kept.data_ptr(), kw.data_ptr(), raw or None), "spd_kv_evict",
+               self.ctx)
+        return kept, kw
+
     def selection(self, seq_id, kv_head, stream=None):
         return spd_get_selection(self.ctx, seq_id, kv_head, self._stream(stream))
 
@@ -512,3 +606,121 @@ def prefill_block_sparse_attention(q, k, v, w_q, w_k, block=64, token_budget=409
     if check:
         _check(lib().spd_prefill_check(work.data_ptr(), st or None), "spd_prefill_check")
     return out, blocks
+
+
+# ---- dense attention with score rules ------------------------------------------
+
+def _rule(scale, softcap, slopes, num_q_heads, device):
+    import torch
+    if slopes is not None:
+        if slopes.dtype != torch.float32 or tuple(slopes.shape) != (num_q_heads,) \
+                or not slopes.is_contiguous() or slopes.device != device:
+            raise ValueError("slopes must be a contiguous fp32 [%d] tensor on %s"
+                             % (num_q_heads, device))
+        slopes = slopes.data_ptr()
+    return spd_score_rule(float(scale or 0.0), float(softcap or 0.0), slopes)
+
+
+def _workspace(torch, nbytes, device, raw, stream):
+    """A call's workspace, not reused by the allocator before the stream that
+    the call runs on has done with it."""
+    work = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    if stream is not None:
+        work.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                           else torch.cuda.ExternalStream(raw, device=device))
+    return work
+
+
+def _token_stride(t, name):
+    """Elements between the rows of a [tokens][heads][d] tensor."""
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    if t.shape[0] == 1:
+        return t.shape[1] * t.shape[2]
+    return t.stride(0)
+
+
+def prefill_attention(q, k, v, key_begin=None, key_end=None, scale=0.0, softcap=0.0, slopes=None,
+                      out_dtype=None, out=None, stream=None, check=False):
+    """Attention of a prompt, a chunk of one or a single token (spd_prefill_attention).
+
+    q [Lq][Hq][d], k, v [Lk][Hkv][d] (fp16 or bf16, one CUDA device; rows may
+    be strided, as in a fused projection's output).  key_begin, key_end int32
+    [Lq]: query i attends the keys key_begin[i] <= t < key_end[i] (an empty
+    interval gives 0); None: causal, the queries standing at the end of the
+    keys.  scale 0 is 1/sqrt(d); softcap caps the scores by a tanh; slopes fp32
+    [Hq] bias them by distance.  Returns out [Lq][Hq][d], fp32 or (out_dtype)
+    the type of q.  check=True waits and raises if a kernel's own check
+    tripped."""
+    import torch
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k, v must be [tokens][heads][head_dim]")
+    Lq, Hq, d = q.shape
+    Lk, Hkv, _ = k.shape
+    dt, dev = q.dtype, q.device
+    if dt not in (torch.float16, torch.bfloat16) or k.dtype != dt or v.dtype != dt:
+        raise ValueError("q, k, v must share one dtype, fp16 or bf16")
+    if dev.type != "cuda" or k.device != dev or v.device != dev:
+        raise ValueError("q, k, v must be on one CUDA device")
+    if tuple(k.shape) != (Lk, Hkv, d) or tuple(v.shape) != (Lk, Hkv, d):
+        raise ValueError("k and v must be [Lk][Hkv][%d]" % d)
+    if (key_begin is None) != (key_end is None):
+        raise ValueError("key_begin and key_end come together")
+    for t in (key_begin, key_end):
+        if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != (Lq,)
+                              or not t.is_contiguous() or t.device != dev):
+            raise ValueError("key_begin and key_end must be contiguous int32 [%d] on %s" % (Lq, dev))
+    if out_dtype is None:
+        out_dtype = torch.float32 if out is None else out.dtype
+    if out_dtype not in (torch.float32, dt):
+        raise ValueError("out_dtype must be torch.float32 or %s" % dt)
+    if out is None:
+        out = torch.empty((Lq, Hq, d), dtype=out_dtype, device=dev)
+    elif out.dtype != out_dtype or tuple(out.shape) != (Lq, Hq, d) or not out.is_contiguous() \
+            or out.device != dev:
+        raise ValueError("out must be a contiguous %s tensor (%d, %d, %d) on %s"
+                         % (out_dtype, Lq, Hq, d, dev))
+    cfg = spd_dense_config(Hq, Hkv, d, 1 if dt == torch.bfloat16 else 0,
+                           0 if out_dtype == torch.float32 else 1,
+                           _rule(scale, softcap, slopes, Hq, dev))
+    ws = ctypes.c_size_t()
+    st = lib().spd_prefill_attention_sizes(ctypes.byref(cfg), Lq, Lk, ctypes.byref(ws))
+    if st != SPD_OK:
+        _check(st, "spd_prefill_attention_sizes")
+    raw = torch.cuda.current_stream(dev).cuda_stream if stream is None else (
+        stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    work = _workspace(torch, ws.value, dev, raw, stream) if ws.value else None
+    st = lib().spd_prefill_attention(
+        ctypes.byref(cfg), Lq, Lk, q.data_ptr(), _token_stride(q, "q"), k.data_ptr(),
+        _token_stride(k, "k"), v.data_ptr(), _token_stride(v, "v"),
+        key_begin.data_ptr() if key_begin is not None else None,
+        key_end.data_ptr() if key_end is not None else None, out.data_ptr(),
+        work.data_ptr() if work is not None else None, ws.value, raw or None)
+    if st != SPD_OK:
+        _check(st, "spd_prefill_attention")
+    if check:
+        _check(lib().spd_prefill_attention_check(out.data_ptr(), raw or None),
+               "spd_prefill_attention_check")
+    return out
+
+
+def document_key_ranges(offsets, n_tokens, prefix=None, stream=None):
+    """Key intervals of packed documents (spd_document_key_ranges): offsets
+    int32 [documents + 1], prefix int32 [documents] or None (causal).  Returns
+    (key_begin, key_end) int32 [n_tokens] for :func:`prefill_attention`."""
+    import torch
+    dev = offsets.device
+    n = offsets.shape[0] - 1 if offsets.dim() == 1 else 0
+    for t, shape in ((offsets, (n + 1,)), (prefix, (n,))):
+        if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != shape or n < 1
+                              or not t.is_contiguous() or t.device != dev or dev.type != "cuda"):
+            raise ValueError("offsets int32 [documents + 1] and prefix int32 [documents], "
+                             "contiguous, on one CUDA device")
+    kb = torch.empty(int(n_tokens), dtype=torch.int32, device=dev)
+    ke = torch.empty(int(n_tokens), dtype=torch.int32, device=dev)
+    raw = torch.cuda.current_stream(dev).cuda_stream if stream is None else (
+        stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    _check(lib().spd_document_key_ranges(
+        offsets.data_ptr(), prefix.data_ptr() if prefix is not None else None, n, int(n_tokens),
+        kb.data_ptr(), ke.data_ptr(), raw or None), "spd_document_key_ranges")
+    return kb, ke

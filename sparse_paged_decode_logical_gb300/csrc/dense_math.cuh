@@ -1,0 +1,40 @@
+// The score rule's arithmetic, shared by the dense attention kernels.
+#pragma once
+#include "dense.h"
+#include "ptx.cuh"
+
+namespace spd {
+
+// tanh(z) = z T(z^2).  T as polynomials fitted for least relative error:
+// |z| <= 0.6, 5 terms (7e-8; 3 x 2^-24 with fp32 arithmetic), and |z| <= 1, 7
+// terms (5e-8; 3 x 2^-24).  Beyond 1, 1 - 2 / (1 + e^2z) has no cancellation
+// left (2 / (1 + e^2) = 0.24).
+__device__ __forceinline__ float2 f2_dup(float x) { return make_float2(x, x); }
+
+// cap tanh(s / cap) in base-2 units, for |s / cap| <= 0.6: two scores at once.
+__device__ __forceinline__ float2 cap_small(const ScoreRule &r, float2 s) {
+  constexpr float c[5] = {0.9999999403953552f, -0.33332309126853943f, 0.13310173153877258f,
+                          -0.05210147798061371f, 0.01547542680054903f};
+  const float2 z = f2_mul(s, f2_dup(r.z_in)), y = f2_mul(s, f2_dup(r.scale_log2)), u = f2_mul(z, z);
+  float2 p = f2_dup(c[4]);
+#pragma unroll
+  for (int i = 3; i >= 0; --i) p = f2_fma(p, u, f2_dup(c[i]));
+  return f2_mul(y, p);
+}
+
+// The same for any score.
+__device__ __forceinline__ float cap_any(const ScoreRule &r, float s) {
+  constexpr float c[7] = {0.9999999403953552f,  -0.33332839608192444f, 0.13325203955173492f,
+                          -0.05345702916383743f, 0.020289979875087738f, -0.006203378085047007f,
+                          0.001041022245772183f};
+  const float z = s * r.z_in, u = z * z;
+  float p = c[6];
+#pragma unroll
+  for (int i = 5; i >= 0; --i) p = fmaf(p, u, c[i]);
+  const float e = ex2_approx(fabsf(z) * 2.8853900817779268f);  // e^(2 |z|)
+  const float far = copysignf(r.cap_out - __fdividef(2.f * r.cap_out, 1.f + e), s);
+  // (a NaN score fails the comparison's negation and stays NaN through p)
+  return fabsf(z) > 1.f ? far : s * r.scale_log2 * p;
+}
+
+}  // namespace spd

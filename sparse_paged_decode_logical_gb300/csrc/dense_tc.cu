@@ -1,0 +1,786 @@
+// Dense attention with score rules on the 5th-generation tensor cores: prompts
+// whose queries each attend an interval of keys, and the shared prefix of a
+// decode batch.
+//
+//   x(r, t) = rule(q_r . k_t)  (ScoreRule, base 2), keys begin_r <= t < end_r
+//   o_r = sum_t 2^(x - m_r) v_t / sum_t 2^(x - m_r)
+//
+// One CTA per (head group, kv head, tile, key split): two matrices of 128 query
+// rows, a row being one (token, query head of the group) pair, so that the
+// heads that share K and V share their tiles too.  Keys come in blocks of 64,
+// two blocks (a pair) per stage of a two-stage TMA ring:
+//   S_m = Q_m . K^T     tcgen05.mma M 128 x N 128 (64 for a lone last block),
+//                       fp32 in tensor memory;
+//   softmax             one row per thread: score rule, mask, online max and
+//                       sum in fp32, weights written back over S as 16 bits;
+//   O_m += P_m . V      A = P from tensor memory, fp32 accumulation.
+// Outputs of 32 bits (kSplitP) keep P as a 16-bit high part and the 16-bit
+// rounding of the rest, two products per block: P . V then holds about 16 bits
+// (bf16) or 22 (fp16) of each weight.  Outputs of 16 bits round P once, which
+// is an error of the same size as the rounding of the output.
+//
+// A matrix skips the pairs that none of its rows attends.  With `dup` (at most
+// 128 rows) both matrices hold the same rows and take turns at the pairs, so
+// that one's softmax still runs beside the other's products; each then counts
+// as a split of its own.  Splits leave unnormalised sums to a combining kernel.
+//
+// Blocks that some row attends only in part ("edge" blocks) are masked, and
+// their V tile is scanned: a value that is not finite is replaced by zero in
+// shared memory (0 x NaN would reach rows that do not attend the key) and added
+// back, in the epilogue, to the rows that do.  Rows of a page behind the
+// sequence's end are zeroed the same way.
+//
+// Warps: 0 .. 7 softmax (matrix warp / 4), 8 and 9 issue matrix 0's and 1's
+// MMAs, 10 loads, 11 scans V.  Every wait is bounded.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <limits.h>
+#include <math_constants.h>
+
+#include "dense.h"
+#include "dense_math.cuh"
+#include "ptx.cuh"
+#include "spd_internal.h"
+
+namespace spd {
+namespace {
+
+constexpr uint32_t kDtWait = 1u << 22;  // bounded mbarrier polls
+constexpr float kDtRescaleAbove = 8.f;  // log2 growth of a row max that moves it
+
+template <int D>
+struct DtSmem {
+  static constexpr int KB = D / 64;               // 64-column sub-tiles of a row
+  static constexpr int kStages = 2;               // K / V ring, a pair of blocks per stage
+  static constexpr int kStageBytes = KB * 16384;  // K (or V) of two 64-row blocks
+  static constexpr int kQ = 0;                    // [2][KB][128 x 128 B]
+  static constexpr int kK = 2 * KB * 16384;       // [stage][KB][block u][64 x 128 B]
+  static constexpr int kV = kK + kStages * kStageBytes;  // [stage][block u][KB][64 x 128 B]
+  static constexpr int kBars = kV + kStages * kStageBytes;
+  // mbarriers: Q; per stage K full, V full, V scanned, empty; per matrix S
+  // full (per pair), P full (per block of a pair), O done (per block), pair
+  // done, O final, drain; the start of matrix 1.  Every waiter is at most one
+  // completion behind the barrier that it polls by parity.
+  static constexpr int kBarQ = 0;
+  static constexpr int kBarKF = 1;
+  static constexpr int kBarVF = kBarKF + kStages;
+  static constexpr int kBarVC = kBarVF + kStages;
+  static constexpr int kBarKE = kBarVC + kStages;
+  static constexpr int kBarSF = kBarKE + kStages;
+  static constexpr int kBarPF = kBarSF + 2;
+  static constexpr int kBarOD = kBarPF + 4;
+  static constexpr int kBarOP = kBarOD + 2;
+  static constexpr int kBarOF = kBarOP + 2;
+  static constexpr int kBarDR = kBarOF + 2;
+  static constexpr int kNumBars = kBarDR + 2;
+  static constexpr int kMisc = kBars + 8 * kNumBars;  // ints, see below
+  static constexpr int kBytes = kMisc + 64 + 1024;    // + alignment slack
+  // tensor-memory columns: S / P of matrix m, block u at 128 m + 64 u; O_m at
+  // 256 + D m
+  static constexpr int kAlloc = 512;
+  static constexpr int kMmaWarp = 8, kLoadWarp = 10, kScanWarp = 11;
+  static constexpr int kThreads = 12 * 32;
+  static_assert(kBytes <= 232448, "shared memory");
+};
+// kMisc: [0] tensor-memory base, [1] fail flag, [2] a V value was not finite,
+// [3 + 4 m ..] of matrix m: least begin, greatest end, greatest begin, least end
+constexpr int kMiscFail = 1, kMiscBad = 2, kMiscRange = 3;
+
+__device__ __forceinline__ void dt_set_err(int *err, int code, int a, int b, int c) {
+  if (atomicCAS(err, 0, code) == 0) {
+    err[1] = a;
+    err[2] = b;
+    err[3] = c;
+  }
+}
+
+// Bounded wait; gives up early once another role has raised the fail flag.
+__device__ __forceinline__ bool dt_wait(uint64_t *bar, uint32_t parity, volatile int *fail) {
+  for (uint32_t i = 0; i < kDtWait; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 255u && *fail) return false;
+  }
+  *fail = 1;
+  return false;
+}
+// Bounded wait that the fail flag does not cut short (work in flight).
+__device__ __forceinline__ void dt_drain(uint64_t *bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kDtWait; ++i)
+    if (mbar_try_wait(bar, parity)) return;
+}
+
+// Two weights rounded to 16 bits (element 0 in the low half); with the split,
+// also the 16-bit rounding of what that left.
+template <typename T> struct Weights;
+template <> struct Weights<__nv_bfloat16> {
+  static constexpr bool bf16 = true;
+  static __device__ __forceinline__ uint32_t round(float2 p) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(p.x, p.y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+  static __device__ __forceinline__ void split(float2 p, uint32_t &hi, uint32_t &lo) {
+    hi = round(p);
+    lo = round(f2_sub(p, make_float2(__uint_as_float(hi << 16),
+                                     __uint_as_float(hi & 0xffff0000u))));
+  }
+  static __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+};
+template <> struct Weights<__half> {
+  static constexpr bool bf16 = false;
+  static __device__ __forceinline__ uint32_t round(float2 p) {
+    const __half2 h = __floats2half2_rn(p.x, p.y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+  static __device__ __forceinline__ void split(float2 p, uint32_t &hi, uint32_t &lo) {
+    hi = round(p);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    lo = round(f2_sub(p, f));
+  }
+  static __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+};
+
+// Which 16-bit halves of a word are not finite: (x & exponent) == exponent.
+__device__ __forceinline__ uint32_t nonfinite_halves(uint32_t x, uint32_t exponent) {
+  uint32_t m = 0;
+  if ((x & exponent & 0xffffu) == (exponent & 0xffffu)) m |= 0xffffu;
+  if ((x & exponent & 0xffff0000u) == (exponent & 0xffff0000u)) m |= 0xffff0000u;
+  return m;
+}
+
+// Where a prompt call's kernels record a failed check: one word (and details)
+// per device that loads the library, zero until then, read and cleared by
+// dense_error_word.
+__device__ int g_dense_err[4];
+
+template <typename T, int D, bool kSplitP>
+__global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
+    dense_tc_kernel(const __grid_constant__ DenseTcParams p) {
+  using Sm = DtSmem<D>;
+  constexpr int KB = Sm::KB, S = Sm::kStages;
+  extern __shared__ uint8_t dt_smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(dt_smem_raw) + 1023) & ~uintptr_t(1023));
+  int *const err = p.err ? p.err : g_dense_err;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Sm::kBars);
+  int *misc = reinterpret_cast<int *>(smem + Sm::kMisc);
+  volatile int *fail = misc + kMiscFail;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the last tiles (most keys when causal) first; heads fastest, so that the
+  // CTAs that run together read the same K and V
+  const int units_h = p.Hkv * p.HG;
+  const int hg_hk = blockIdx.x % units_h, rest = blockIdx.x / units_h;
+  const int hk = hg_hk / p.HG, hg = hg_hk % p.HG;
+  const int split = rest % p.nsplit, tile = p.tiles - 1 - rest / p.nsplit;
+  const int unit = tile * units_h + hg_hk;
+  const int tpm = 128 / p.HP;                        // tokens per matrix
+  const int tok0 = tile * (p.dup ? tpm : 2 * tpm);   // the unit's first token
+  const int h0 = hk * p.G + hg * p.HP;               // the group's first query head
+
+  if (warp == Sm::kMmaWarp) tmem_alloc(reinterpret_cast<uint32_t *>(misc), Sm::kAlloc);
+  if (tid == Sm::kLoadWarp * 32) {
+    for (int x = 0; x < Sm::kNumBars; ++x)
+      mbar_init(&bars[x], (x >= Sm::kBarPF && x < Sm::kBarOD)   ? 4  // P: one per softmax warp
+                          : (x >= Sm::kBarKE && x < Sm::kBarSF) ? 2  // empty: one per MMA warp
+                                                                : 1);
+    *fail = 0;
+    misc[kMiscBad] = 0;
+    for (int m = 0; m < 2; ++m) {
+      misc[kMiscRange + 4 * m] = INT_MAX;
+      misc[kMiscRange + 4 * m + 1] = 0;
+      misc[kMiscRange + 4 * m + 2] = 0;
+      misc[kMiscRange + 4 * m + 3] = INT_MAX;
+    }
+    fence_mbar_init();
+    prefetch_tmap(&p.tm_q);
+    prefetch_tmap(&p.tm_k);
+    prefetch_tmap(&p.tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, (uint32_t)misc[0], 0);  // warp-uniform
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- the interval of keys of every row, and of each matrix ----
+  int rbeg = 0, rend = 0;  // of softmax thread tid's row (an empty one: 0, 0)
+  const int m_row = (warp >> 2) & 1, row = tid & 127;
+  const int tok = tok0 + (p.dup ? 0 : m_row * tpm) + row / p.HP;
+  const int h_row = h0 + row % p.HP;
+  if (warp < 8) {
+    if (tok < p.Lq) {
+      if (p.paged) {
+        rend = p.Lk;
+      } else if (p.key_begin) {
+        rbeg = max(p.key_begin[tok], 0);
+        rend = min(p.key_end[tok], p.Lk);
+      } else {
+        rend = min(p.pos0 + tok + 1, p.Lk);
+      }
+      if (rbeg >= rend) rbeg = rend = 0;
+    }
+    const bool some = rend > 0;
+    const int b0 = __reduce_min_sync(0xffffffffu, some ? rbeg : INT_MAX);
+    const int e1 = __reduce_max_sync(0xffffffffu, some ? rend : 0);
+    const int b1 = __reduce_max_sync(0xffffffffu, some ? rbeg : 0);
+    const int e0 = __reduce_min_sync(0xffffffffu, some ? rend : INT_MAX);
+    if (lane == 0) {
+      int *rg = misc + kMiscRange + 4 * m_row;
+      atomicMin(rg, b0);
+      atomicMax(rg + 1, e1);
+      atomicMax(rg + 2, b1);
+      atomicMin(rg + 3, e0);
+    }
+  }
+  __syncthreads();
+  const int *rg = misc + kMiscRange;
+  // the split's blocks [kb0, kb0 + n) of the CTA's range, in pairs [0, np)
+  const int all_beg = min(rg[0], rg[4]), all_end = max(rg[1], rg[5]);
+  const int full_beg = max(rg[2], rg[6]), full_end = min(rg[3], rg[7]);
+  int kb0 = 0, n = 0;
+  if (all_beg < all_end) {
+    const int first = all_beg / kDenseBlock, last = (all_end + kDenseBlock - 1) / kDenseBlock;
+    const int per = ((last - first + p.nsplit - 1) / p.nsplit + 1) & ~1;  // whole pairs
+    kb0 = first + split * per;
+    n = max(0, min(last - kb0, per));
+  }
+  const int np = (n + 1) / 2;
+  // the pairs that matrix m computes: [lo_m, hi_m), or with dup every second one
+  auto pair_lo = [&](int m) {
+    return p.dup ? 0 : rg[4 * m] >= rg[4 * m + 1]
+                           ? 0
+                           : min(np, max(0, rg[4 * m] / kDenseBlock - kb0) / 2);
+  };
+  auto pair_hi = [&](int m) {
+    if (p.dup) return np;
+    if (rg[4 * m] >= rg[4 * m + 1]) return 0;
+    const int last = (rg[4 * m + 1] + kDenseBlock - 1) / kDenseBlock - kb0;  // blocks
+    return min(np, max(0, last + 1) / 2);
+  };
+  auto is_edge = [&](int j) {  // block j of the split: some row attends only a part of it
+    const int key0 = (kb0 + j) * kDenseBlock;
+    return key0 < full_beg || key0 + kDenseBlock > full_end;
+  };
+
+  if (warp == Sm::kLoadWarp) {
+    // ---- TMA: Q once, then K and V of every pair through the ring ----
+    if (lane == 0 && np > 0) {
+      int issued = 0;
+      bool ok = true;
+      mbar_arrive_expect_tx(&bars[Sm::kBarQ], 2 * KB * 16384);
+      for (int mm = 0; mm < 2; ++mm)
+        for (int kb = 0; kb < KB; ++kb)
+          tma_load_4d(smem + Sm::kQ + (mm * KB + kb) * 16384, &p.tm_q, 0, kb, h0,
+                      tok0 + (p.dup ? 0 : mm * tpm), &bars[Sm::kBarQ]);
+      for (int pp = 0; pp < np && ok; ++pp) {
+        const int s = pp % S, nbk = min(2, n - 2 * pp);
+        if (pp >= S && !(ok = dt_wait(&bars[Sm::kBarKE + s], ((pp / S) - 1) & 1, fail))) break;
+        const int key0 = (kb0 + 2 * pp) * kDenseBlock;
+        uint8_t *kt = smem + Sm::kK + s * Sm::kStageBytes, *vt = smem + Sm::kV + s * Sm::kStageBytes;
+        if (!p.paged) {
+          mbar_arrive_expect_tx(&bars[Sm::kBarKF + s], nbk * KB * 8192);
+          for (int u = 0; u < nbk; ++u)
+            for (int kb = 0; kb < KB; ++kb)
+              tma_load_4d(kt + kb * 16384 + u * 8192, &p.tm_k, 0, kb, hk, key0 + 64 * u,
+                          &bars[Sm::kBarKF + s]);
+          mbar_arrive_expect_tx(&bars[Sm::kBarVF + s], nbk * KB * 8192);
+          for (int u = 0; u < nbk; ++u)
+            for (int kb = 0; kb < KB; ++kb)
+              tma_load_4d(vt + (u * KB + kb) * 8192, &p.tm_v, 0, kb, hk, key0 + 64 * u,
+                          &bars[Sm::kBarVF + s]);
+        } else {
+          // boxes of box_rows rows, none of which crosses a page; only those
+          // that hold a token of the sequence
+          const int br = p.box_rows;
+          const int nbox = (min(64 * nbk, p.Lk - key0) + br - 1) / br;
+          int planes[128 / 16];
+          for (int b = 0; b < nbox; ++b) {
+            const int blk = (key0 + b * br) / p.P;
+            const int phys = blk < p.max_pp ? p.page_row[blk] : -1;
+            if (phys < 0 || phys >= p.num_phys) {
+              dt_set_err(err, blk < p.max_pp ? kDevBadPhys : kDevBadPage, hk, blk, phys);
+              *fail = 1;
+              ok = false;
+              break;
+            }
+            planes[b & 7] = phys * p.Hkv + hk;
+          }
+          if (!ok) break;
+          mbar_arrive_expect_tx(&bars[Sm::kBarKF + s], nbox * KB * br * 128);
+          for (int b = 0; b < nbox; ++b)
+            for (int kb = 0; kb < KB; ++kb)
+              tma_load_4d(kt + kb * 16384 + b * br * 128, &p.tm_k, 0, (key0 + b * br) % p.P, kb,
+                          planes[b & 7], &bars[Sm::kBarKF + s]);
+          mbar_arrive_expect_tx(&bars[Sm::kBarVF + s], nbox * KB * br * 128);
+          for (int b = 0; b < nbox; ++b) {
+            const int u = b * br / 64, r0 = b * br % 64;
+            for (int kb = 0; kb < KB; ++kb)
+              tma_load_4d(vt + (u * KB + kb) * 8192 + r0 * 128, &p.tm_v, 0, (key0 + b * br) % p.P,
+                          kb, planes[b & 7], &bars[Sm::kBarVF + s]);
+          }
+        }
+        ++issued;
+      }
+      // every copy lands before the CTA leaves (other roles may have given up)
+      dt_drain(&bars[Sm::kBarQ], 0);
+      for (int pp = max(0, issued - S); pp < issued; ++pp) {
+        dt_drain(&bars[Sm::kBarKF + pp % S], (pp / S) & 1);
+        dt_drain(&bars[Sm::kBarVF + pp % S], (pp / S) & 1);
+      }
+    }
+  } else if (warp == Sm::kScanWarp) {
+    // ---- V of edge blocks: values that are not finite (and rows behind the
+    // sequence's end, whatever they hold) become zero before the products ----
+    constexpr uint32_t kExp = Weights<T>::bf16 ? 0x7f807f80u : 0x7c007c00u;
+    bool ok = true;
+    for (int pp = 0; pp < np && ok; ++pp) {
+      const int s = pp % S, nbk = min(2, n - 2 * pp);
+      ok = __all_sync(0xffffffffu, dt_wait(&bars[Sm::kBarVF + s], (pp / S) & 1, fail));
+      if (!ok) break;
+      bool touched = false, bad = false;
+      for (int u = 0; u < nbk; ++u) {
+        if (!is_edge(2 * pp + u)) continue;
+        uint8_t *vt = smem + Sm::kV + s * Sm::kStageBytes + u * KB * 8192;
+        const int keep = p.Lk - (kb0 + 2 * pp + u) * kDenseBlock;  // rows of the sequence
+        for (int c = lane; c < KB * 512; c += 32) {
+          uint4 *w = reinterpret_cast<uint4 *>(vt + c * 16);
+          uint4 x = *w;
+          if (((c & 511) >> 3) >= keep) {
+            *w = make_uint4(0, 0, 0, 0);
+            touched = true;
+            continue;
+          }
+          if (p.paged) continue;
+          const uint32_t m0 = nonfinite_halves(x.x, kExp), m1 = nonfinite_halves(x.y, kExp),
+                         m2 = nonfinite_halves(x.z, kExp), m3 = nonfinite_halves(x.w, kExp);
+          if (m0 | m1 | m2 | m3) {
+            *w = make_uint4(x.x & ~m0, x.y & ~m1, x.z & ~m2, x.w & ~m3);
+            touched = bad = true;
+          }
+        }
+      }
+      if (bad) misc[kMiscBad] = 1;
+      if (touched) fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[Sm::kBarVC + s]);
+    }
+  } else if (warp >= Sm::kMmaWarp) {
+    // ---- MMA issue for matrix m (the whole warp, one elected lane issuing) ----
+    const int m = warp - Sm::kMmaWarp;
+    const bool bf = Weights<T>::bf16;
+    const uint32_t idesc_s2 = umma_idesc_f16(bf, 128, 128, 0, 0);  // Q . K^T, a pair
+    const uint32_t idesc_s1 = umma_idesc_f16(bf, 128, 64, 0, 0);   // Q . K^T, a lone block
+    const uint32_t idesc_o = umma_idesc_f16(bf, 128, 64, 0, 1);    // P . V: V MN-major
+    const uint64_t dq = umma_desc_sw128(smem_u32(smem + Sm::kQ + m * KB * 16384), 16, 1024);
+    const uint64_t dk = umma_desc_sw128(smem_u32(smem + Sm::kK), 16, 1024);
+    const uint64_t dv = umma_desc_sw128(smem_u32(smem + Sm::kV), 16, 1024);
+    const uint32_t t_o = tmem + 256 + D * m;
+    const int lo = pair_lo(m), hi = pair_hi(m), dup = p.dup;
+    auto mine = [&](int pp) { return pp >= lo && pp < hi && (!dup || (pp & 1) == m); };
+    auto wwait = [&](uint64_t *bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, dt_wait(bar, parity, fail));
+    };
+    auto issue_s = [&](int pp) {
+      const uint64_t kt = dk + (uint64_t)(((pp % S) * Sm::kStageBytes) >> 4);
+      const uint32_t idesc = n - 2 * pp >= 2 ? idesc_s2 : idesc_s1;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t off = (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+        umma_f16_warp(tmem + 128 * m, dq + off, kt + off, idesc, kk > 0);
+      }
+      umma_commit_warp(&bars[Sm::kBarSF + m]);
+    };
+    bool ok = np > 0 && wwait(&bars[Sm::kBarQ], 0);
+    bool any = false;
+    int i = 0, last = -1;  // pairs of this matrix so far; its last pair
+    for (int pp = lo; pp < hi; ++pp)
+      if (mine(pp)) last = pp;
+    int ready = -1;  // the pair whose S has been issued
+    for (int pp = 0; pp < np && ok; ++pp) {
+      const int s = pp % S, nbk = min(2, n - 2 * pp);
+      if (!mine(pp)) {
+        // not this matrix's: the stage is free as far as it is concerned, once
+        // it has been filled
+        if (!(ok = wwait(&bars[Sm::kBarKF + s], (pp / S) & 1))) break;
+        if (!(ok = wwait(&bars[Sm::kBarVC + s], (pp / S) & 1))) break;
+        if (lane == 0) mbar_arrive(&bars[Sm::kBarKE + s]);
+        continue;
+      }
+      if (ready < pp) {
+        if (!(ok = wwait(&bars[Sm::kBarKF + s], (pp / S) & 1))) break;
+        if (i > 0 && !(ok = wwait(&bars[Sm::kBarOP + m], (i - 1) & 1))) break;
+        tc_fence_after();
+        issue_s(pp);
+        any = true;
+      }
+      if (!(ok = wwait(&bars[Sm::kBarVC + s], (pp / S) & 1))) break;
+      for (int u = 0; u < nbk; ++u) {
+        if (!(ok = wwait(&bars[Sm::kBarPF + 2 * m + u], i & 1))) break;
+        tc_fence_after();
+        const uint64_t vt = dv + (uint64_t)((s * Sm::kStageBytes + u * KB * 8192) >> 4);
+        const uint32_t pa = tmem + 128 * m + 64 * u;
+#pragma unroll
+        for (int half = 0; half < KB; ++half)
+#pragma unroll
+          for (int part = 0; part < (kSplitP ? 2 : 1); ++part)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_f16_ts_warp(t_o + 64 * half, pa + 32 * part + 8 * kk,
+                               vt + (uint64_t)((half * 8192 + kk * 2048) >> 4), idesc_o,
+                               i > 0 || u > 0 || part > 0 || kk > 0);
+        umma_commit_warp(&bars[Sm::kBarOD + m]);
+      }
+      if (!ok) break;
+      umma_commit_warp(&bars[Sm::kBarOP + m]);
+      if (pp == last) umma_commit_warp(&bars[Sm::kBarOF + m]);
+      umma_commit_warp(&bars[Sm::kBarKE + s]);
+      ++i;
+    }
+    if (any) {  // every MMA of this warp done before the CTA frees its memory
+      umma_commit_warp(&bars[Sm::kBarDR + m]);
+      if (lane == 0) dt_drain(&bars[Sm::kBarDR + m], 0);
+    }
+  } else {
+    // ---- softmax: one query row per thread ----
+    const int m = warp >> 2;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t t_o = lanes + 256 + D * m;
+    const int lo = pair_lo(m), hi = pair_hi(m), step = p.dup ? 2 : 1;
+    const float slope = p.rule.slopes && tok < p.Lq ? p.rule.slopes[h_row] * 1.4426950408889634f : 0.f;
+    // a prompt's distances count from the row's nearest key, so that the bias of
+    // the keys that matter keeps its bits however far they are (the nearest key
+    // of a decode row is its own newest token, at distance 0)
+    const int pos = p.paged ? p.Lk + (tok < p.Lq ? p.lens[tok] : 0) - 1 : p.pos0 + tok;
+    const float near = p.paged ? 0.f : (float)max(0, max(pos - rend + 1, rbeg - pos));
+    const bool rule = p.rule.cap_out > 0.f || p.rule.slopes != nullptr;
+    const float sc = rule ? 1.f : p.rule.scale_log2;
+    float m_run = -CUDART_INF_F, l_run = 0.f;
+    bool ok = true;
+    int i = 0, blocks = 0;
+    for (int pp = p.dup ? m : lo; pp < hi && ok; pp += step, ++i) {
+      const int nbk = min(2, n - 2 * pp);
+      ok = dt_wait(&bars[Sm::kBarSF + m], i & 1, fail);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;  // the tensor-memory accesses are warp-wide
+      tc_fence_after();
+#pragma unroll 1
+      for (int u = 0; u < nbk; ++u, ++blocks) {
+        const uint32_t t_s = lanes + 128 * m + 64 * u;
+        const int key0 = (kb0 + 2 * pp + u) * kDenseBlock;
+        uint32_t s[64];
+        tmem_ld64_sync(t_s, s);
+        if (rule) {
+          if (p.rule.cap_out > 0.f) {
+            // the short polynomial when it holds for the warp's 64 x 32 scores
+            float big = 0.f;
+#pragma unroll
+            for (int c = 0; c < 64; c += 2)
+              big = fmax3f(big, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
+            if (__all_sync(0xffffffffu, big <= p.rule.small)) {
+#pragma unroll
+              for (int c = 0; c < 64; c += 2) {
+                const float2 x = cap_small(
+                    p.rule, make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])));
+                s[c] = __float_as_uint(x.x);
+                s[c + 1] = __float_as_uint(x.y);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                s[c] = __float_as_uint(cap_any(p.rule, __uint_as_float(s[c])));
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              s[c] = __float_as_uint(__uint_as_float(s[c]) * p.rule.scale_log2);
+          }
+          if (p.rule.slopes) {
+            const float d0 = (float)(pos - key0);
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              s[c] = __float_as_uint(
+                  fmaf(-slope, fabsf(d0 - (float)c) - near, __uint_as_float(s[c])));
+          }
+        }
+        if (is_edge(2 * pp + u)) {
+          const int c0 = rbeg - key0, c1 = rend - key0;
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (c < c0 || c >= c1) s[c] = 0xff800000u;  // -inf
+        }
+        float mq[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mq[k] = __uint_as_float(s[k]);
+#pragma unroll
+        for (int c = 4; c < 60; c += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mq[k] = fmax3f(mq[k], __uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1]));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mq[k] = fmaxf(mq[k], __uint_as_float(s[60 + k]));
+        const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * sc;
+        const bool need = mx > m_run + kDtRescaleAbove;
+        if (__any_sync(0xffffffffu, need)) {
+          const float m_new = need ? mx : m_run;
+          const float alpha = need ? (m_run == -CUDART_INF_F ? 0.f : exp2f(m_run - m_new)) : 1.f;
+          if (blocks > 0) {  // O_m follows the new max once the block before has landed
+            ok = dt_wait(&bars[Sm::kBarOD + m], (blocks - 1) & 1, fail);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32_sync(t_o + 32 * c, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(t_o + 32 * c, o);
+            }
+            tmem_wait_st();
+          }
+          l_run *= alpha;
+          m_run = m_new;
+        }
+        // weights 2^(x - m); a row that has met no key yet keeps 2^(-inf - 0) = 0
+        const float base = m_run == -CUDART_INF_F ? 0.f : m_run;
+        uint32_t hi_w[32];
+        uint32_t lo_w[kSplitP ? 32 : 1];
+        const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-base, -base);
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float2 x = f2_fma(
+              make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sc2, nm2);
+          const float2 w = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+          ls[c & 1] = f2_add(ls[c & 1], w);
+          if constexpr (kSplitP) Weights<T>::split(w, hi_w[c], lo_w[c]);
+          else hi_w[c] = Weights<T>::round(w);
+        }
+        l_run += (ls[0].x + ls[1].x) + (ls[0].y + ls[1].y);
+        tmem_st32(t_s, hi_w);
+        if constexpr (kSplitP) tmem_st32(t_s + 32, lo_w);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[Sm::kBarPF + 2 * m + u]);
+      }
+    }
+    if (ok && blocks > 0) {
+      ok = dt_wait(&bars[Sm::kBarOF + m], 0, fail);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    if (ok) {
+      const bool live = tok < p.Lq, empty = rend == 0;
+      const bool fix = *reinterpret_cast<volatile int *>(misc + kMiscBad) && live && !empty;
+      const size_t pr = ((size_t)unit * p.nsplit + split) * kDenseRows + m * 128 + row;
+      if (!p.out && live) p.part_ml[pr] = make_float2(m_run, empty ? 0.f : l_run);
+      const float inv = empty ? 0.f : p.out ? 1.f / l_run : 1.f;
+      const size_t orow = ((size_t)tok * p.Hq + h_row) * D;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t r[32];
+        __syncwarp();
+        if (blocks > 0) {
+          tmem_ld32_sync(t_o + 32 * c, r);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = 0u;
+        }
+        if (!live) continue;
+        float f[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) f[e] = empty ? 0.f : __uint_as_float(r[e]) * inv;
+        if (fix) {
+          // the values that the scan took out, back into the rows that attend them
+          const T *vg = static_cast<const T *>(p.v) + (size_t)hk * D + 32 * c;
+          const int k1 = min(rend, (kb0 + n) * kDenseBlock);
+          for (int t = max(rbeg, kb0 * kDenseBlock); t < k1; ++t) {
+            if (!is_edge(t / kDenseBlock - kb0)) {
+              t = (t / kDenseBlock + 1) * kDenseBlock - 1;
+              continue;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float x = Weights<T>::to_f(vg[(size_t)t * p.v_stride + e]);
+              if (!isfinite(x)) f[e] += x;
+            }
+          }
+        }
+        if (!p.out) {
+          float *o = p.part_o + pr * D + 32 * c;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4 *>(o + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        } else if (p.out_f32) {
+          float *o = static_cast<float *>(p.out) + orow + 32 * c;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4 *>(o + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        } else {
+          T *o = static_cast<T *>(p.out) + orow + 32 * c;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            *reinterpret_cast<uint4 *>(o + e) =
+                make_uint4(Weights<T>::round(make_float2(f[e], f[e + 1])),
+                           Weights<T>::round(make_float2(f[e + 2], f[e + 3])),
+                           Weights<T>::round(make_float2(f[e + 4], f[e + 5])),
+                           Weights<T>::round(make_float2(f[e + 6], f[e + 7])));
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0 && *fail) dt_set_err(err, kDevTimeout, hk, tile, split);  // (an earlier error stays)
+  if (warp == Sm::kMmaWarp) tmem_dealloc(tmem, Sm::kAlloc);
+}
+
+// ---- joining the splits of a prompt's rows --------------------------------------
+// One warp per query row (token, head): M = max m_s, out = sum 2^(m_s - M) o_s
+// / sum 2^(m_s - M) l_s.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) dense_prompt_combine_kernel(
+    const __grid_constant__ DenseTcParams p, void *out) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (w >= (long long)p.Lq * p.Hq) return;
+  const int tok = (int)(w / p.Hq), h = (int)(w % p.Hq);
+  const int hk = h / p.G, hg = (h % p.G) / p.HP;
+  const int rt = p.dup ? 128 : kDenseRows, ns = p.nsplit * kDenseRows / rt;
+  const int tpt = rt / p.HP, tile = tok / tpt;
+  const int r = (tok % tpt) * p.HP + h % p.HP;
+  const size_t unit = (size_t)tile * p.Hkv * p.HG + hk * p.HG + hg;
+  const float2 *ml = p.part_ml + unit * ns * rt + r;
+  const float *po = p.part_o + (unit * ns * rt + r) * D;
+  float M = -CUDART_INF_F;
+  float2 mine[kDenseMaxSplits / 32];
+#pragma unroll
+  for (int k = 0; k < kDenseMaxSplits / 32; ++k) {
+    const int s = lane + 32 * k;
+    mine[k] = s < ns ? ml[(size_t)s * rt] : make_float2(-CUDART_INF_F, 0.f);
+    M = fmaxf(M, mine[k].x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float base = M == -CUDART_INF_F ? 0.f : M;
+  float L = 0.f, f[kDenseMaxSplits / 32];
+#pragma unroll
+  for (int k = 0; k < kDenseMaxSplits / 32; ++k) {
+    f[k] = lane + 32 * k < ns ? exp2f(mine[k].x - base) : 0.f;
+    L += mine[k].y * f[k];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  constexpr int E = D / 32;
+  float acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int s = 0; s < ns; ++s) {
+    // a split that holds none of the row's keys left zeros (or nothing to weigh)
+    const float fs = __shfl_sync(0xffffffffu, s < 32 ? f[0] : f[kDenseMaxSplits / 32 - 1], s & 31);
+    const float *o = po + (size_t)s * rt * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(o[e], fs, acc[e]);
+  }
+  bool empty;  // (a row whose interval holds no key is zero, one whose weights vanish is not)
+  if (p.key_begin) {
+    empty = max(p.key_begin[tok], 0) >= min(p.key_end[tok], p.Lk);
+  } else {
+    empty = min(p.pos0 + tok + 1, p.Lk) <= 0;
+  }
+  const float inv = empty ? 0.f : 1.f / L;
+  const size_t at = ((size_t)tok * p.Hq + h) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] *= inv;
+  if (p.out_f32) {
+    float *o = static_cast<float *>(out) + at;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = acc[e];
+  } else {
+    uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<T *>(out) + at);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) o[e / 2] = Weights<T>::round(make_float2(acc[e], acc[e + 1]));
+  }
+}
+
+// ---- intervals of packed documents ------------------------------------------------
+// Token t of document i (offsets[i] <= t < offsets[i + 1]) attends from the
+// document's start to the later of itself and the document's prefix; tokens
+// outside every document attend nothing.
+__global__ void __launch_bounds__(256) document_ranges_kernel(const int *offsets,
+                                                              const int *prefix, int n_docs,
+                                                              int total, int *kb, int *ke) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int t = blockIdx.x * 256 + threadIdx.x;
+  if (t >= total) return;
+  int lo = 0, hi = n_docs;  // the last document that starts at or before t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (offsets[mid] <= t) lo = mid + 1;
+    else hi = mid;
+  }
+  const int i = lo - 1;
+  int b = 0, e = 0;
+  if (i >= 0 && t < offsets[i + 1]) {
+    b = max(offsets[i], 0);
+    const int seen = prefix ? max(prefix[i], 0) : 0;
+    const int end = min(offsets[i + 1], total);
+    e = max(t + 1, b + min(seen, end - b));
+  }
+  kb[t] = b;
+  ke[t] = e;
+}
+
+template <typename T, int D, bool kSplitP>
+cudaError_t launch_dt(const DenseTcParams &p, cudaStream_t st) {
+  auto k = dense_tc_kernel<T, D, kSplitP>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       DtSmem<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k, p.tiles * p.nsplit * p.Hkv * p.HG, DtSmem<D>::kThreads,
+                    (size_t)DtSmem<D>::kBytes, st, p);
+}
+
+template <typename T>
+cudaError_t launch_dt_d(const DenseTcParams &p, int d, bool split_p, cudaStream_t st) {
+  if (d == 64) return split_p ? launch_dt<T, 64, true>(p, st) : launch_dt<T, 64, false>(p, st);
+  return split_p ? launch_dt<T, 128, true>(p, st) : launch_dt<T, 128, false>(p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_dense_tc(const DenseTcParams &p, int dtype, int d, bool split_p,
+                            cudaStream_t st) {
+  return dtype == 0 ? launch_dt_d<__half>(p, d, split_p, st)
+                    : launch_dt_d<__nv_bfloat16>(p, d, split_p, st);
+}
+
+cudaError_t launch_dense_prompt_combine(const DenseTcParams &p, int dtype, int d, void *out,
+                                        cudaStream_t st) {
+  const int grid = (int)(((long long)p.Lq * p.Hq + 7) / 8);
+  if (dtype == 0)
+    return d == 64 ? launch_pdl(dense_prompt_combine_kernel<__half, 64>, grid, 256, 0, st, p, out)
+                   : launch_pdl(dense_prompt_combine_kernel<__half, 128>, grid, 256, 0, st, p, out);
+  return d == 64
+             ? launch_pdl(dense_prompt_combine_kernel<__nv_bfloat16, 64>, grid, 256, 0, st, p, out)
+             : launch_pdl(dense_prompt_combine_kernel<__nv_bfloat16, 128>, grid, 256, 0, st, p, out);
+}
+
+// The current device's error word, cleared.
+cudaError_t dense_error_word(int (&w)[4]) {
+  cudaError_t e = cudaMemcpyFromSymbol(w, g_dense_err, sizeof w);
+  if (e != cudaSuccess || w[0] == 0) return e;
+  const int zero[4] = {0, 0, 0, 0};
+  return cudaMemcpyToSymbol(g_dense_err, zero, sizeof zero);
+}
+
+cudaError_t launch_document_ranges(const int *offsets, const int *prefix, int n_docs, int total,
+                                   int *key_begin, int *key_end, cudaStream_t st) {
+  return launch_pdl(document_ranges_kernel, (total + 255) / 256, 256, 0, st, offsets, prefix,
+                    n_docs, total, key_begin, key_end);
+}
+
+}  // namespace spd

@@ -213,6 +213,29 @@ spd_status attention_with_scratch(spd_ctx *c, const void *q, const int *ids, int
                                   cudaStream_t st, const DecodeScratch &scratch);
 spd_status fail_message(spd_ctx *c, spd_status s, const char *msg);
 
+// What the dense-attention and eviction entry points read of a context.
+struct CtxView {
+  const spd_config *cfg;
+  const spd_buffers *buf;
+  const CUtensorMap *tm_k, *tm_v;
+  int G, Hd, Hs, R, max_pp, kv_fp8;
+  int device, num_sms;
+  int *err;
+};
+// Host facts only (no device call); ctx_device fills device, num_sms and the
+// tensor maps in, setting the context up on its device the first time.
+void ctx_view(spd_ctx *c, CtxView *v);
+spd_status ctx_device(spd_ctx *c, cudaStream_t st, CtxView *v);
+spd_status check_live(spd_ctx *c, const int *ids, int n);
+long long seq_length(const spd_ctx *c, int id);
+// Takes physical pages for tokens[i] tokens of each listed empty sequence, all
+// or nothing (SPD_ERR_NO_PAGES / SPD_ERR_CAPACITY change nothing).
+spd_status check_fill(spd_ctx *c, const int *ids, const int *tokens, int n);
+spd_status fill_pages(spd_ctx *c, const int *ids, const int *tokens, int n, cudaStream_t st);
+void set_filled(spd_ctx *c, const int *ids, const int *tokens, int n);
+// The context enqueued n kernels on the stream.
+void note_launches(spd_ctx *c, cudaStream_t st, int n);
+
 // Launchers.  dtype: 0 fp16, 1 bf16.  Return cudaGetLastError() and add the
 // number of kernels enqueued to *launches.
 cudaError_t launch_pt_write(const PtWriteParams &p, cudaStream_t s, long long *launches);

@@ -871,6 +871,60 @@ spd_status fail_message(spd_ctx *c, spd_status s, const char *msg) {
   return c->fail(s, "%s", msg);
 }
 
+void ctx_view(spd_ctx *c, CtxView *v) {
+  v->cfg = &c->cfg;
+  v->buf = &c->buf;
+  v->tm_k = &c->tm_k;
+  v->tm_v = &c->tm_v;
+  v->G = c->dv.G;
+  v->Hd = c->dv.Hd;
+  v->Hs = c->dv.Hs;
+  v->R = c->dv.R;
+  v->max_pp = c->dv.max_pp;
+  v->kv_fp8 = c->dv.kv_fp8;
+  v->device = c->device;
+  v->num_sms = c->num_sms;
+  v->err = c->err_word();
+}
+
+spd_status ctx_device(spd_ctx *c, cudaStream_t st, CtxView *v) {
+  const spd_status r = ensure_device(c, st);
+  ctx_view(c, v);
+  return r;
+}
+
+spd_status check_live(spd_ctx *c, const int *ids, int n) { return check_seqs(c, ids, n); }
+
+long long seq_length(const spd_ctx *c, int id) { return c->seqs[id].L; }
+
+spd_status check_fill(spd_ctx *c, const int *ids, const int *tokens, int n) {
+  long long need = 0;
+  for (int i = 0; i < n; ++i) {
+    if (tokens[i] > c->cfg.max_context)
+      return c->fail(SPD_ERR_CAPACITY, "sequence %d: %d tokens exceed max_context %d", ids[i],
+                     tokens[i], c->cfg.max_context);
+    need += pages_needed(c, c->seqs[ids[i]], tokens[i]);
+  }
+  if (need > (long long)c->free_pages.size())
+    return c->fail(SPD_ERR_NO_PAGES, "need %lld physical pages, %zu free", need,
+                   c->free_pages.size());
+  return SPD_OK;
+}
+
+spd_status fill_pages(spd_ctx *c, const int *ids, const int *tokens, int n, cudaStream_t st) {
+  for (int i = 0; i < n; ++i) take_pages(c, ids[i], tokens[i]);
+  return flush_page_table(c, st);
+}
+
+void set_filled(spd_ctx *c, const int *ids, const int *tokens, int n) {
+  for (int i = 0; i < n; ++i) c->seqs[ids[i]].L = tokens[i];
+}
+
+void note_launches(spd_ctx *c, cudaStream_t st, int n) {
+  c->launches += n;
+  note_launcher(c, st);
+}
+
 }  // namespace spd
 
 extern "C" {
