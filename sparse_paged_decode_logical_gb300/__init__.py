@@ -461,13 +461,17 @@ class SparsePagedKVCache:
             self._stream(stream))
         return out, rm, rs, pages, mass
 
-    def decode_step(self, q, k, v, seq_ids, out=None, stream=None):
+    def _id_array(self, seq_ids):
         key = tuple(seq_ids)
         ids = self._ids_cache.get(key)
         if ids is None:
             ids = _ids(key)
             if len(self._ids_cache) < 1024:
                 self._ids_cache[key] = ids
+        return ids
+
+    def decode_step(self, q, k, v, seq_ids, out=None, stream=None):
+        ids = self._id_array(seq_ids)
         n = ids[1]
         qp = self._ptr(q, (n, self.Hq, self.d), self.dtype)
         kp = self._ptr(k, (n, self.Hkv, self.d), self.dtype)
@@ -492,7 +496,7 @@ class SparsePagedKVCache:
         receives weights_in (None: 0) plus the softmax weight of every own
         token, summed over the query heads of its kv head."""
         t = self.torch
-        ids, n = _ids(seq_ids)
+        ids, n = self._id_array(seq_ids)
         prefix_id = -1 if prefix_id is None else int(prefix_id)
         qp = self._ptr(q, (n, self.Hq, self.d), self.dtype)
         if out_dtype is None:
@@ -535,8 +539,8 @@ class SparsePagedKVCache:
         others by weights fp32 [n][Hkv][>= longest source], `keep` in all.
         Returns (kept int32 [n][Hkv][keep], -1 padded, and their weights)."""
         t = self.torch
-        src, n = _ids(src_ids)
-        dst, nd = _ids(dst_ids)
+        src, n = self._id_array(src_ids)
+        dst, nd = self._id_array(dst_ids)
         if n != nd:
             raise ValueError("as many destinations as sources are needed")
         if weights.dim() != 3:

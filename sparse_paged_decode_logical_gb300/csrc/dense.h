@@ -7,25 +7,43 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "spd.h"
 
 namespace spd {
 
 constexpr int kDenseBlock = 64;      // keys per block of the tensor-core kernel
 constexpr int kDenseRows = 256;      // query rows of one of its CTAs (two matrices of 128)
-constexpr int kDenseSeqs = 1024;     // sequences described per parameter block
+constexpr int kDenseSeqs = 256;      // sequences described per parameter block
 constexpr int kDecodeTile = 16;      // keys per tile of the decode kernel
 constexpr int kDecodeRows = 16;      // query rows of one of its work items
 constexpr int kDenseMaxSplits = 64;  // key splits of one unit
 constexpr int kOwnMaxSplits = 256;   // splits of one sequence's own tokens
+
+// Allows a kernel its dynamic shared memory on the current device, once per
+// device (`ready`: a bit for each of the first 64).
+template <typename K>
+inline cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t> *ready) {
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = device < 64 ? 1ull << device : 0;
+  if (ready->load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) ready->fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // The score of a query row and a key, in base-2 units ready for exp2:
 //   s = scale q.k; softcap: s = cap tanh(s / cap); bias: s -= slope |distance|
 struct ScoreRule {
   float scale_log2;      // scale * log2(e)
   float z_in;            // scale / cap
+  float e_in;            // 2 log2(e) scale / cap
   float small;           // scores q.k up to this are within tanh's short polynomial
   float cap_out;         // cap * log2(e); 0: no cap
+  float poly[5];         // cap_out times tanh(z) / z as a polynomial in z^2, |z| <= 0.6
   const float *slopes;   // [Hq] or null
 };
 
@@ -46,7 +64,7 @@ struct DenseTcParams {
   ScoreRule rule;
   int paged;
   int out_f32;             // type of out
-  int Lq, Lk, Hq, Hkv, G, HP, HG;  // HG = G / HP head groups
+  int Lq, Lk, Hq, Hkv, G, lhp, HG;  // HP = 2^lhp heads per matrix, HG = G / HP head groups
   int tiles, nsplit;
   int dup;                 // both matrices hold the same 128 rows and take turns at the keys
   int P, max_pp, num_phys, box_rows;
@@ -91,6 +109,7 @@ struct DenseDecodeParams {
   int n, Hq, Hkv, G, P, max_pp, num_phys;
   int prefix_slot, prefix_len, prefix_items, prefix_ns, prefix_tpi, prefix_rows;
   int own_items;
+  int follow;              // the kernel before is this call's prefix kernel
   int w_chunks;            // weight CTAs per (sequence, kv head)
   DecodeSeq seqs[kDenseSeqs];
 };

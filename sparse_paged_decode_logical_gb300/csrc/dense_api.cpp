@@ -9,8 +9,8 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <memory>
 #include <new>
-#include <vector>
 
 #include "dense.h"
 #include "spd.h"
@@ -113,8 +113,13 @@ ScoreRule make_rule(const spd_score_rule *r, int d) {
   x.scale_log2 = (float)(scale * kLog2e);
   if (r && r->softcap > 0.f) {
     x.z_in = (float)(scale / r->softcap);
+    x.e_in = (float)(2.0 * kLog2e * scale / r->softcap);
     x.small = (float)(0.5999 * r->softcap / scale);
     x.cap_out = (float)(kLog2e * r->softcap);
+    // tanh(z) / z in z^2, |z| <= 0.6 (dense_math.cuh)
+    constexpr double kTanh[5] = {0.9999999403953552, -0.33332309126853943, 0.13310173153877258,
+                                 -0.05210147798061371, 0.01547542680054903};
+    for (int i = 0; i < 5; ++i) x.poly[i] = (float)(kLog2e * r->softcap * kTanh[i]);
   }
   x.slopes = r ? r->slopes : nullptr;
   return x;
@@ -123,7 +128,7 @@ ScoreRule make_rule(const spd_score_rule *r, int d) {
 // ---- prompt attention ------------------------------------------------------------
 
 struct PromptPlan {
-  int G = 0, HP = 0, HG = 0, tiles = 0, nsplit = 1, dup = 0;
+  int G = 0, HP = 0, lhp = 0, HG = 0, tiles = 0, nsplit = 1, dup = 0;
   bool partial = false;
   size_t po = 0, pml = 0, total = 0;
 };
@@ -147,8 +152,8 @@ spd_status plan_prompt(const spd_dense_config *c, int Lq, int Lk, int sms, Promp
   if (!valid_dense(c) || Lq < 1 || Lk < 1) return SPD_ERR_INVALID_ARG;
   if (Lq > kMaxTokens || Lk > kMaxTokens) return SPD_ERR_CAPACITY;
   z->G = c->num_q_heads / c->num_kv_heads;
-  z->HP = 1;
-  while (z->HP < 8 && z->G % (2 * z->HP) == 0) z->HP *= 2;
+  while (z->lhp < 3 && z->G % (2 << z->lhp) == 0) ++z->lhp;
+  z->HP = 1 << z->lhp;
   z->HG = z->G / z->HP;
   const int blocks = (Lk + kDenseBlock - 1) / kDenseBlock;
   z->dup = (long long)Lq * z->HP <= 128 && blocks >= 8 ? 1 : 0;
@@ -174,7 +179,7 @@ spd_status plan_prompt(const spd_dense_config *c, int Lq, int Lk, int sms, Promp
 
 // At most this many query rows (sequences x heads per kv head) go over the
 // prefix with the decode kernel, more with the tensor-core kernel.
-constexpr int kPrefixRowsDecode = 16;
+constexpr int kPrefixRowsDecode = 32;
 
 struct SharedPlan {
   bool tc = false;
@@ -257,6 +262,20 @@ void plan_shared(const spd_ctx *c, const CtxView &v, int prefix_len, const int *
   z->part_ml = take(own_rows * 8);
   z->logits = take(weights ? (size_t)n * Hkv * v.G * round_up(z->longest, 4) * 4 : 0);
   z->total = off;
+}
+
+// Workspace of a whole call: its launches run one after the other in the same one.
+size_t shared_bytes(const spd_ctx *c, const CtxView &v, int prefix_id, const int *ids, int n,
+                    bool weights) {
+  DecodeSeq seqs[kDenseSeqs];
+  size_t most = 0;
+  for (int b = 0; b < n; b += kDenseSeqs) {
+    SharedPlan z;
+    plan_shared(c, v, prefix_id >= 0 ? (int)seq_length(c, prefix_id) : 0, ids + b,
+                std::min(kDenseSeqs, n - b), weights, seqs, &z);
+    most = std::max(most, z.total);
+  }
+  return most;
 }
 
 spd_status check_shared(spd_ctx *c, const CtxView &v, int prefix_id, const int *ids, int n) {
@@ -347,7 +366,7 @@ spd_status spd_prefill_attention(const spd_dense_config *cfg, int q_len, int kv_
   p.Hq = cfg->num_q_heads;
   p.Hkv = cfg->num_kv_heads;
   p.G = z.G;
-  p.HP = z.HP;
+  p.lhp = z.lhp;
   p.HG = z.HG;
   p.tiles = z.tiles;
   p.nsplit = z.nsplit;
@@ -397,15 +416,7 @@ spd_status spd_shared_prefix_sizes(spd_ctx *c, int prefix_id, const int *seq_ids
   if (r != SPD_OK) return r;
   v.num_sms = sm_count(v.device);
   (void)cudaGetLastError();
-  std::vector<DecodeSeq> seqs(kDenseSeqs);
-  size_t most = 0;
-  for (int b = 0; b < n_seqs; b += kDenseSeqs) {
-    SharedPlan z;
-    plan_shared(c, v, prefix_id >= 0 ? (int)seq_length(c, prefix_id) : 0, seq_ids + b,
-                std::min(kDenseSeqs, n_seqs - b), weights != 0, seqs.data(), &z);
-    most = std::max(most, z.total);
-  }
-  *workspace_bytes = most;
+  *workspace_bytes = shared_bytes(c, v, prefix_id, seq_ids, n_seqs, weights != 0);
   return SPD_OK;
 }
 
@@ -437,11 +448,7 @@ spd_status spd_shared_prefix_attention(spd_ctx *c, const void *q, int prefix_id,
     return fail_message(c, SPD_ERR_INVALID_ARG, "workspace must be a 256-byte aligned pointer");
   cudaStream_t st = (cudaStream_t)stream;
   if ((r = ctx_device(c, st, &v)) != SPD_OK) return r;
-  size_t need = 0;
-  if ((r = spd_shared_prefix_sizes(c, prefix_id, seq_ids, n_seqs, weights_out != nullptr, &need)) !=
-      SPD_OK)
-    return r;
-  if (workspace_bytes < need)
+  if (workspace_bytes < shared_bytes(c, v, prefix_id, seq_ids, n_seqs, weights_out != nullptr))
     return fail_message(c, SPD_ERR_CAPACITY, "workspace is smaller than spd_shared_prefix_sizes");
   DeviceGuard guard;
   if ((r = guard.bind(v.device)) != SPD_OK) return fail_message(c, r, "cudaSetDevice failed");
@@ -488,6 +495,7 @@ spd_status spd_shared_prefix_attention(spd_ctx *c, const void *q, int prefix_id,
     p.prefix_tpi = z.prefix_tpi;
     p.prefix_rows = z.prefix_rows;
     p.own_items = z.own_items;
+    p.follow = z.tc;
     p.w_chunks = (z.longest + 1023) / 1024;
     int launches = 0;
     cudaError_t e = cudaSuccess;
@@ -517,7 +525,8 @@ spd_status spd_shared_prefix_attention(spd_ctx *c, const void *q, int prefix_id,
       t.Lk = lp;
       t.Hq = p.Hq;
       t.Hkv = p.Hkv;
-      t.G = t.HP = v.G;
+      t.G = v.G;
+      t.lhp = v.G == 8 ? 3 : v.G == 4 ? 2 : v.G == 2 ? 1 : 0;
       t.HG = 1;
       t.tiles = z.tiles;
       t.nsplit = z.nsplit;
@@ -560,7 +569,8 @@ spd_status spd_kv_evict(spd_ctx *c, const int *src_ids, const int *dst_ids, int 
   spd_status r = check_live(c, src_ids, n_seqs);
   if (r != SPD_OK) return r;
   if ((r = check_live(c, dst_ids, n_seqs)) != SPD_OK) return r;
-  std::vector<int> m(n_seqs);
+  const std::unique_ptr<int[]> m(new (std::nothrow) int[n_seqs]);
+  if (!m) return fail_message(c, SPD_ERR_CAPACITY, "out of host memory");
   for (int i = 0; i < n_seqs; ++i) {
     for (int j = 0; j < n_seqs; ++j)
       if (src_ids[i] == dst_ids[j])
@@ -576,12 +586,12 @@ spd_status spd_kv_evict(spd_ctx *c, const int *src_ids, const int *dst_ids, int 
   const long long groups = ((long long)keep + 63) / 64;
   if (groups * std::min(n_seqs, kDenseSeqs) * v.Hd > 0x7fffffffLL)
     return fail_message(c, SPD_ERR_CAPACITY, "keep is too large for one launch");
-  if ((r = check_fill(c, dst_ids, m.data(), n_seqs)) != SPD_OK) return r;
+  if ((r = check_fill(c, dst_ids, m.get(), n_seqs)) != SPD_OK) return r;
   cudaStream_t st = (cudaStream_t)stream;
   if ((r = ctx_device(c, st, &v)) != SPD_OK) return r;
   DeviceGuard guard;
   if ((r = guard.bind(v.device)) != SPD_OK) return fail_message(c, r, "cudaSetDevice failed");
-  if ((r = fill_pages(c, dst_ids, m.data(), n_seqs, st)) != SPD_OK) return r;
+  if ((r = fill_pages(c, dst_ids, m.get(), n_seqs, st)) != SPD_OK) return r;
   const spd_config &cfg = *v.cfg;
   static thread_local EvictParams p;
   for (int b = 0; b < n_seqs; b += kDenseSeqs) {
@@ -610,17 +620,17 @@ spd_status spd_kv_evict(spd_ctx *c, const int *src_ids, const int *dst_ids, int 
       p.seqs[i] = EvictSeq{src_ids[b + i], dst_ids[b + i], (int)L, m[b + i]};
       longest = std::max(longest, L);
     }
-    // CTAs per (sequence, kv head): one up to 4,096 tokens, at most eight, and
-    // no more than fill the GPU once
+    // CTAs per (sequence, kv head): at least 2,048 tokens each, at most eight,
+    // and no more than fill the GPU twice
     int cluster = 1;
-    while (cluster < 8 && cluster * 4096LL < longest &&
-           (long long)p.n * v.Hd * cluster * 2 <= v.num_sms)
+    while (cluster < 8 && cluster * 2048LL < longest &&
+           (long long)p.n * v.Hd * cluster * 2 <= 2LL * v.num_sms)
       cluster *= 2;
     const cudaError_t e = launch_evict(p, cfg.dtype, cfg.head_dim, cluster, st);
     note_launches(c, st, 2);
     if (e != cudaSuccess) return fail_message(c, SPD_ERR_CUDA, cudaGetErrorString(e));
   }
-  set_filled(c, dst_ids, m.data(), n_seqs);
+  set_filled(c, dst_ids, m.get(), n_seqs);
   return SPD_OK;
 }
 

@@ -130,7 +130,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     fence_mbar_init();
   }
   __syncwarp();
-  pdl_wait();
+  // behind this call's prefix kernel nothing is waited for: that kernel started
+  // its dependents after its own wait, so all that is read here is there, and
+  // the two write to different places
+  if (!p.follow) pdl_wait();
   pdl_launch_dependents();
 
   const int *table = p.page_table + (size_t)slot * p.max_pp;
@@ -356,76 +359,117 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     *reinterpret_cast<float4 *>(o_out + (size_t)r * D + c) = acc;
     if (c == 0) ml_out[r] = make_float2(M, l);
   }
+  if (p.follow) pdl_wait();  // (done only once the prefix kernel is: the next one reads both)
 }
 
 // ---- joining prefix and own splits ------------------------------------------------
-// CTAs [0, n Hkv): outputs of one (sequence, kv head).  The rest, when asked
-// for: the weights of 1,024 own tokens of one (sequence, kv head),
+// CTAs [0, n Hq): the output of one (sequence, query head), its splits shared
+// out over the CTA's groups of D / 4 threads.  The rest, when asked for: the
+// weights of 1,024 own tokens of one (sequence, kv head),
 // w_out = w_in + sum over the head's G queries of 2^(x - M) / L.
 constexpr int kCombineThreads = 128, kWeightTokens = 1024;
+
+// Where a row's splits lie: own partials first, then the prefix's.
+struct RowSplits {
+  const float2 *own_ml, *pre_ml;
+  const float *own_o, *pre_o;
+  size_t own_step, pre_step;  // rows between two splits
+  int ns, nall;
+};
+__device__ __forceinline__ RowSplits row_splits(const DenseDecodeParams &p, int seq, int hk, int g,
+                                                int D) {
+  const DecodeSeq &s = p.seqs[seq];
+  const int r = seq * p.G + g, tile = p.prefix_ns > 0 ? r / p.prefix_rows : 0;
+  const size_t own = ((size_t)s.item_off + hk * s.ns) * p.G + g,
+               pre = (size_t)(tile * p.Hkv + hk) * p.prefix_ns * p.prefix_rows +
+                     (r - tile * p.prefix_rows);
+  RowSplits x;
+  x.own_ml = p.part_ml + own;
+  x.own_o = p.part_o + own * D;
+  x.pre_ml = p.pre_ml + pre;
+  x.pre_o = p.pre_o + pre * D;
+  x.own_step = p.G;
+  x.pre_step = p.prefix_rows;
+  x.ns = s.ns;
+  x.nall = s.ns + p.prefix_ns;
+  return x;
+}
+// One warp: the row's max (0 if nothing was met) and sum; factors to fac.
+__device__ __forceinline__ float2 row_stats(const RowSplits &x, float *fac) {
+  constexpr int kMax = kOwnMaxSplits + kDenseMaxSplits;
+  const int lane = threadIdx.x & 31;
+  float2 v[kMax / 32];
+  float M = -CUDART_INF_F, L = 0.f;
+#pragma unroll
+  for (int j = 0; j < kMax / 32; ++j) {
+    const int k = lane + 32 * j;
+    v[j] = make_float2(-CUDART_INF_F, 0.f);
+    if (32 * j < x.nall && k < x.nall)
+      v[j] = k < x.ns ? x.own_ml[k * x.own_step] : x.pre_ml[(k - x.ns) * x.pre_step];
+    M = fmaxf(M, v[j].x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float base = M == -CUDART_INF_F ? 0.f : M;
+#pragma unroll
+  for (int j = 0; j < kMax / 32; ++j) {
+    if (32 * j >= x.nall) break;
+    const int k = lane + 32 * j;
+    const float f = exp2f(v[j].x - base);
+    if (fac && k < x.nall) fac[k] = f;
+    L = fmaf(v[j].y, f, L);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  return make_float2(base, L);
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kCombineThreads)
     dense_decode_combine_kernel(const __grid_constant__ DenseDecodeParams p) {
-  constexpr int kMax = kOwnMaxSplits + kDenseMaxSplits;
-  __shared__ float fac[8][kMax];
-  __shared__ float tot_m[8], tot_l[8];
+  constexpr int kCols = D / 4, kGroups = kCombineThreads / kCols;
+  __shared__ float fac[kOwnMaxSplits + kDenseMaxSplits];
+  __shared__ float2 stat[8];
+  __shared__ float4 part[kGroups][kCols];
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int unit = blockIdx.x, chunk = -1;
-  if (unit >= p.n * p.Hkv) {
-    unit -= p.n * p.Hkv;
-    chunk = unit % p.w_chunks;
-    unit /= p.w_chunks;
-  }
-  const int seq = unit / p.Hkv, hk = unit % p.Hkv;
-  const DecodeSeq &s = p.seqs[seq];
-  if (chunk >= 0 && chunk * kWeightTokens >= s.L) return;
-  const int ns = s.ns, nall = ns + p.prefix_ns, rt = p.prefix_rows;
-  // split k of row g: own partials first, then the prefix's
-  auto own_at = [&](int k, int g) { return ((size_t)s.item_off + hk * ns + k) * p.G + g; };
-  auto pre_at = [&](int k, int g) {
-    const int r = seq * p.G + g, tile = r / rt;
-    return ((size_t)(tile * p.Hkv + hk) * p.prefix_ns + k) * rt + r % rt;
-  };
-  for (int g = warp; g < p.G; g += kCombineThreads / 32) {
-    float M = -CUDART_INF_F, L = 0.f;
-    for (int k = lane; k < nall; k += 32)
-      M = fmaxf(M, (k < ns ? p.part_ml[own_at(k, g)] : p.pre_ml[pre_at(k - ns, g)]).x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float base = M == -CUDART_INF_F ? 0.f : M;
-    for (int k = lane; k < nall; k += 32) {
-      const float2 v = k < ns ? p.part_ml[own_at(k, g)] : p.pre_ml[pre_at(k - ns, g)];
-      const float f = exp2f(v.x - base);
-      fac[g][k] = f;
-      L = fmaf(v.y, f, L);
+  if ((int)blockIdx.x < p.n * p.Hq) {
+    const int seq = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
+    const RowSplits x = row_splits(p, seq, h / p.G, h % p.G, D);
+    if (warp == 0) {
+      const float2 st = row_stats(x, fac);
+      if (lane == 0) stat[0] = st;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if (lane == 0) {
-      tot_m[g] = base;
-      tot_l[g] = L;
-    }
-  }
-  __syncthreads();
-  if (chunk < 0) {
-    for (int x = tid; x < p.G * (D / 4); x += kCombineThreads) {
-      const int g = x / (D / 4), c = (x % (D / 4)) * 4;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+    const int grp = tid / kCols, c = (tid % kCols) * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float *src, float f) {
+      const float4 v = __ldcs(reinterpret_cast<const float4 *>(src));
+      acc.x = fmaf(v.x, f, acc.x);
+      acc.y = fmaf(v.y, f, acc.y);
+      acc.z = fmaf(v.z, f, acc.z);
+      acc.w = fmaf(v.w, f, acc.w);
+    };
+    const float *own = x.own_o + c, *pre = x.pre_o + c;
 #pragma unroll 4
-      for (int k = 0; k < nall; ++k) {
-        const float4 v = *reinterpret_cast<const float4 *>(
-            (k < ns ? p.part_o + own_at(k, g) * D : p.pre_o + pre_at(k - ns, g) * D) + c);
-        const float f = fac[g][k];
-        acc.x = fmaf(v.x, f, acc.x);
-        acc.y = fmaf(v.y, f, acc.y);
-        acc.z = fmaf(v.z, f, acc.z);
-        acc.w = fmaf(v.w, f, acc.w);
+    for (int k = grp; k < x.ns; k += kGroups) add(own + k * x.own_step * D, fac[k]);
+#pragma unroll 8
+    for (int k = grp; k < x.nall - x.ns; k += kGroups)
+      add(pre + k * x.pre_step * D, fac[x.ns + k]);
+    part[grp][tid % kCols] = acc;
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+      for (int j = 1; j < kGroups; ++j) {
+        const float4 v = part[j][tid];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
       }
-      const float inv = 1.f / tot_l[g];
-      const size_t at = ((size_t)seq * p.Hq + hk * p.G + g) * D + c;
+      const float inv = 1.f / stat[0].y;
+      const size_t at = ((size_t)seq * p.Hq + h) * D + c;
       if (p.out_f32)
         *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) =
             make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
@@ -434,12 +478,22 @@ __global__ void __launch_bounds__(kCombineThreads)
             make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
     }
   } else {
-    const size_t row = (size_t)(seq * p.Hkv + hk);
-    const int t1 = min(s.L, (chunk + 1) * kWeightTokens);
+    const int b = blockIdx.x - p.n * p.Hq, chunk = b % p.w_chunks, unit = b / p.w_chunks;
+    const int seq = unit / p.Hkv, hk = unit % p.Hkv, L = p.seqs[seq].L;
+    if (chunk * kWeightTokens >= L) return;
+    for (int g = warp; g < p.G; g += kCombineThreads / 32) {
+      const float2 st = row_stats(row_splits(p, seq, hk, g, D), nullptr);
+      if (lane == 0) stat[g] = make_float2(st.x, 1.f / st.y);
+    }
+    __syncthreads();
+    const size_t row = (size_t)unit;
+    const float *lg = p.logits + row * p.G * p.l_stride;
+    const int t1 = min(L, (chunk + 1) * kWeightTokens);
+#pragma unroll 2
     for (int t = chunk * kWeightTokens + tid; t < t1; t += kCombineThreads) {
       float w = 0.f;
       for (int g = 0; g < p.G; ++g)
-        w += ex2_approx(p.logits[(row * p.G + g) * p.l_stride + t] - tot_m[g]) * (1.f / tot_l[g]);
+        w = fmaf(ex2_approx(lg[g * p.l_stride + t] - stat[g].x), stat[g].y, w);
       p.w_out[row * p.w_stride + t] = (p.w_in ? p.w_in[row * p.w_stride + t] : 0.f) + w;
     }
   }
@@ -448,8 +502,8 @@ __global__ void __launch_bounds__(kCombineThreads)
 template <typename T, int D>
 cudaError_t launch_dd(const DenseDecodeParams &p, cudaStream_t st) {
   auto k = dense_decode_kernel<T, D>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       DdSmem<D>::kBytes);
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(k, DdSmem<D>::kBytes, &ready);
   if (e != cudaSuccess) return e;
   return launch_pdl(k, p.prefix_items + p.own_items, kWarps * 32, (size_t)DdSmem<D>::kBytes, st, p);
 }
@@ -463,7 +517,7 @@ cudaError_t launch_dense_decode(const DenseDecodeParams &p, int dtype, int d, cu
 
 cudaError_t launch_dense_decode_combine(const DenseDecodeParams &p, int dtype, int d,
                                         cudaStream_t st) {
-  const int grid = p.n * p.Hkv * (1 + (p.w_out ? p.w_chunks : 0));
+  const int grid = p.n * (p.Hq + (p.w_out ? p.Hkv * p.w_chunks : 0));
   auto go = [&](auto kernel) { return launch_pdl(kernel, grid, kCombineThreads, 0, st, p); };
   if (dtype == 0)
     return d == 64 ? go(dense_decode_combine_kernel<__half, 64>)

@@ -8,18 +8,27 @@
 // One CTA per (head group, kv head, tile, key split): two matrices of 128 query
 // rows, a row being one (token, query head of the group) pair, so that the
 // heads that share K and V share their tiles too.  Keys come in blocks of 64,
-// two blocks (a pair) per stage of a two-stage TMA ring:
-//   S_m = Q_m . K^T     tcgen05.mma M 128 x N 128 (64 for a lone last block),
-//                       fp32 in tensor memory;
+// two blocks (a pair) per stage of two-stage TMA rings of K and of V:
+//   S_m = Q_m . K^T     tcgen05.mma M 128 x N 64 or 128, fp32 in tensor memory,
+//                       block u of a pair in the matrix's buffer u;
 //   softmax             one row per thread: score rule, mask, online max and
 //                       sum in fp32, weights written back over S as 16 bits;
 //   O_m += P_m . V      A = P from tensor memory, fp32 accumulation.
+// An S of N 64 takes as long as one of N 128 (the read of Q's 128 rows bounds
+// both), but two buffers let S of the block after next start as soon as P . V
+// of this one is done: the hand-overs between the roles (about 300 cycles each)
+// and the products of one buffer then pass while the softmax works on the
+// other.  Where the softmax is the longer side (score rules, split weights)
+// that wins: 8,192 capped tokens 790 us against 954, 2,501 tokens of 64
+// channels with a bias and fp32 output 71 against 80.  Plain scores with 16-bit
+// output keep the tensor pipe busy and take one N 128 product per pair (kPairS):
+// 2,048 queries over 49,152 keys 1,402 us against 1,510.
 // Outputs of 32 bits (kSplitP) keep P as a 16-bit high part and the 16-bit
 // rounding of the rest, two products per block: P . V then holds about 16 bits
 // (bf16) or 22 (fp16) of each weight.  Outputs of 16 bits round P once, which
 // is an error of the same size as the rounding of the output.
 //
-// A matrix skips the pairs that none of its rows attends.  With `dup` (at most
+// A matrix leaves out the last pairs when none of its rows attends them.  With `dup` (at most
 // 128 rows) both matrices hold the same rows and take turns at the pairs, so
 // that one's softmax still runs beside the other's products; each then counts
 // as a split of its own.  Splits leave unnormalised sums to a combining kernel.
@@ -57,22 +66,23 @@ struct DtSmem {
   static constexpr int kK = 2 * KB * 16384;       // [stage][KB][block u][64 x 128 B]
   static constexpr int kV = kK + kStages * kStageBytes;  // [stage][block u][KB][64 x 128 B]
   static constexpr int kBars = kV + kStages * kStageBytes;
-  // mbarriers: Q; per stage K full, V full, V scanned, empty; per matrix S
-  // full (per pair), P full (per block of a pair), O done (per block), pair
-  // done, O final, drain; the start of matrix 1.  Every waiter is at most one
-  // completion behind the barrier that it polls by parity.
+  // mbarriers: Q; per stage K full, V full, V scanned, K empty, V empty; per
+  // matrix and buffer S full, P full; per matrix O done (per block), O final,
+  // drain; matrix 0's first softmax.  Every waiter is at most one completion
+  // behind the barrier that it polls by parity.
   static constexpr int kBarQ = 0;
   static constexpr int kBarKF = 1;
   static constexpr int kBarVF = kBarKF + kStages;
   static constexpr int kBarVC = kBarVF + kStages;
   static constexpr int kBarKE = kBarVC + kStages;
-  static constexpr int kBarSF = kBarKE + kStages;
-  static constexpr int kBarPF = kBarSF + 2;
+  static constexpr int kBarVE = kBarKE + kStages;
+  static constexpr int kBarSF = kBarVE + kStages;
+  static constexpr int kBarPF = kBarSF + 4;
   static constexpr int kBarOD = kBarPF + 4;
-  static constexpr int kBarOP = kBarOD + 2;
-  static constexpr int kBarOF = kBarOP + 2;
+  static constexpr int kBarOF = kBarOD + 2;
   static constexpr int kBarDR = kBarOF + 2;
-  static constexpr int kNumBars = kBarDR + 2;
+  static constexpr int kBarLag = kBarDR + 2;
+  static constexpr int kNumBars = kBarLag + 1;
   static constexpr int kMisc = kBars + 8 * kNumBars;  // ints, see below
   static constexpr int kBytes = kMisc + 64 + 1024;    // + alignment slack
   // tensor-memory columns: S / P of matrix m, block u at 128 m + 64 u; O_m at
@@ -139,12 +149,15 @@ template <> struct Weights<__half> {
   static __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 };
 
-// Which 16-bit halves of a word are not finite: (x & exponent) == exponent.
-__device__ __forceinline__ uint32_t nonfinite_halves(uint32_t x, uint32_t exponent) {
-  uint32_t m = 0;
-  if ((x & exponent & 0xffffu) == (exponent & 0xffffu)) m |= 0xffffu;
-  if ((x & exponent & 0xffff0000u) == (exponent & 0xffff0000u)) m |= 0xffff0000u;
-  return m;
+// Bits 15 and 31: the low / high half is not finite (its exponent all ones;
+// `exponent` in both halves, `step` one in the exponent's lowest bit: the sum
+// carries into the half's sign bit exactly then).
+__device__ __forceinline__ uint32_t nonfinite(uint32_t x, uint32_t exponent, uint32_t step) {
+  return ((x & exponent) + step) & 0x80008000u;
+}
+__device__ __forceinline__ uint32_t without_nonfinite(uint32_t x, uint32_t exponent, uint32_t step) {
+  const uint32_t f = nonfinite(x, exponent, step);
+  return x & ~((f >> 15) * 0xffffu);  // (each flagged half's 16 bits)
 }
 
 // Where a prompt call's kernels record a failed check: one word (and details)
@@ -152,11 +165,12 @@ __device__ __forceinline__ uint32_t nonfinite_halves(uint32_t x, uint32_t expone
 // dense_error_word.
 __device__ int g_dense_err[4];
 
-template <typename T, int D, bool kSplitP>
+template <typename T, int D, bool kSplitP, bool kRule>
 __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
     dense_tc_kernel(const __grid_constant__ DenseTcParams p) {
   using Sm = DtSmem<D>;
   constexpr int KB = Sm::KB, S = Sm::kStages;
+  constexpr bool kPairS = !kRule && !kSplitP;
   extern __shared__ uint8_t dt_smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(dt_smem_raw) + 1023) & ~uintptr_t(1023));
@@ -172,15 +186,16 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
   const int hk = hg_hk / p.HG, hg = hg_hk % p.HG;
   const int split = rest % p.nsplit, tile = p.tiles - 1 - rest / p.nsplit;
   const int unit = tile * units_h + hg_hk;
-  const int tpm = 128 / p.HP;                        // tokens per matrix
+  const int lhp = p.lhp, tpm = 128 >> lhp;           // tokens per matrix
   const int tok0 = tile * (p.dup ? tpm : 2 * tpm);   // the unit's first token
-  const int h0 = hk * p.G + hg * p.HP;               // the group's first query head
+  const int h0 = hk * p.G + (hg << lhp);             // the group's first query head
 
   if (warp == Sm::kMmaWarp) tmem_alloc(reinterpret_cast<uint32_t *>(misc), Sm::kAlloc);
   if (tid == Sm::kLoadWarp * 32) {
     for (int x = 0; x < Sm::kNumBars; ++x)
       mbar_init(&bars[x], (x >= Sm::kBarPF && x < Sm::kBarOD)   ? 4  // P: one per softmax warp
                           : (x >= Sm::kBarKE && x < Sm::kBarSF) ? 2  // empty: one per MMA warp
+                          : x == Sm::kBarLag                    ? 4  // matrix 0's softmax warps
                                                                 : 1);
     *fail = 0;
     misc[kMiscBad] = 0;
@@ -205,8 +220,8 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
   // ---- the interval of keys of every row, and of each matrix ----
   int rbeg = 0, rend = 0;  // of softmax thread tid's row (an empty one: 0, 0)
   const int m_row = (warp >> 2) & 1, row = tid & 127;
-  const int tok = tok0 + (p.dup ? 0 : m_row * tpm) + row / p.HP;
-  const int h_row = h0 + row % p.HP;
+  const int tok = tok0 + (p.dup ? 0 : m_row * tpm) + (row >> lhp);
+  const int h_row = h0 + (row & ((1 << lhp) - 1));
   if (warp < 8) {
     if (tok < p.Lq) {
       if (p.paged) {
@@ -245,13 +260,9 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
     n = max(0, min(last - kb0, per));
   }
   const int np = (n + 1) / 2;
-  // the pairs that matrix m computes: [lo_m, hi_m), or with dup every second one
-  auto pair_lo = [&](int m) {
-    return p.dup ? 0 : rg[4 * m] >= rg[4 * m + 1]
-                           ? 0
-                           : min(np, max(0, rg[4 * m] / kDenseBlock - kb0) / 2);
-  };
-  auto pair_hi = [&](int m) {
+  // the pairs that matrix m computes: those before pair_end(m), or with dup
+  // every second one (m's all lie in stage m)
+  auto pair_end = [&](int m) {
     if (p.dup) return np;
     if (rg[4 * m] >= rg[4 * m + 1]) return 0;
     const int last = (rg[4 * m + 1] + kDenseBlock - 1) / kDenseBlock - kb0;  // blocks
@@ -265,7 +276,7 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
   if (warp == Sm::kLoadWarp) {
     // ---- TMA: Q once, then K and V of every pair through the ring ----
     if (lane == 0 && np > 0) {
-      int issued = 0;
+      int k_issued = 0, v_issued = 0;
       bool ok = true;
       mbar_arrive_expect_tx(&bars[Sm::kBarQ], 2 * KB * 16384);
       for (int mm = 0; mm < 2; ++mm)
@@ -277,12 +288,15 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
         if (pp >= S && !(ok = dt_wait(&bars[Sm::kBarKE + s], ((pp / S) - 1) & 1, fail))) break;
         const int key0 = (kb0 + 2 * pp) * kDenseBlock;
         uint8_t *kt = smem + Sm::kK + s * Sm::kStageBytes, *vt = smem + Sm::kV + s * Sm::kStageBytes;
+        auto v_free = [&] { return pp < S || dt_wait(&bars[Sm::kBarVE + s], ((pp / S) - 1) & 1, fail); };
         if (!p.paged) {
           mbar_arrive_expect_tx(&bars[Sm::kBarKF + s], nbk * KB * 8192);
           for (int u = 0; u < nbk; ++u)
             for (int kb = 0; kb < KB; ++kb)
               tma_load_4d(kt + kb * 16384 + u * 8192, &p.tm_k, 0, kb, hk, key0 + 64 * u,
                           &bars[Sm::kBarKF + s]);
+          ++k_issued;
+          if (!(ok = v_free())) break;
           mbar_arrive_expect_tx(&bars[Sm::kBarVF + s], nbk * KB * 8192);
           for (int u = 0; u < nbk; ++u)
             for (int kb = 0; kb < KB; ++kb)
@@ -311,6 +325,8 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
             for (int kb = 0; kb < KB; ++kb)
               tma_load_4d(kt + kb * 16384 + b * br * 128, &p.tm_k, 0, (key0 + b * br) % p.P, kb,
                           planes[b & 7], &bars[Sm::kBarKF + s]);
+          ++k_issued;
+          if (!(ok = v_free())) break;
           mbar_arrive_expect_tx(&bars[Sm::kBarVF + s], nbox * KB * br * 128);
           for (int b = 0; b < nbox; ++b) {
             const int u = b * br / 64, r0 = b * br % 64;
@@ -319,19 +335,20 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
                           kb, planes[b & 7], &bars[Sm::kBarVF + s]);
           }
         }
-        ++issued;
+        ++v_issued;
       }
       // every copy lands before the CTA leaves (other roles may have given up)
       dt_drain(&bars[Sm::kBarQ], 0);
-      for (int pp = max(0, issued - S); pp < issued; ++pp) {
+      for (int pp = max(0, k_issued - S); pp < k_issued; ++pp)
         dt_drain(&bars[Sm::kBarKF + pp % S], (pp / S) & 1);
+      for (int pp = max(0, v_issued - S); pp < v_issued; ++pp)
         dt_drain(&bars[Sm::kBarVF + pp % S], (pp / S) & 1);
-      }
     }
   } else if (warp == Sm::kScanWarp) {
     // ---- V of edge blocks: values that are not finite (and rows behind the
     // sequence's end, whatever they hold) become zero before the products ----
     constexpr uint32_t kExp = Weights<T>::bf16 ? 0x7f807f80u : 0x7c007c00u;
+    constexpr uint32_t kStep = Weights<T>::bf16 ? 0x00800080u : 0x04000400u;
     bool ok = true;
     for (int pp = 0; pp < np && ok; ++pp) {
       const int s = pp % S, nbk = min(2, n - 2 * pp);
@@ -341,99 +358,131 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
       for (int u = 0; u < nbk; ++u) {
         if (!is_edge(2 * pp + u)) continue;
         uint8_t *vt = smem + Sm::kV + s * Sm::kStageBytes + u * KB * 8192;
-        const int keep = p.Lk - (kb0 + 2 * pp + u) * kDenseBlock;  // rows of the sequence
-        for (int c = lane; c < KB * 512; c += 32) {
-          uint4 *w = reinterpret_cast<uint4 *>(vt + c * 16);
-          uint4 x = *w;
-          if (((c & 511) >> 3) >= keep) {
-            *w = make_uint4(0, 0, 0, 0);
-            touched = true;
-            continue;
+        uint4 *w = reinterpret_cast<uint4 *>(vt);
+        if (!p.paged) {
+          constexpr int kBatch = 8;
+#pragma unroll 1
+          for (int c = lane; c < KB * 512; c += 32 * kBatch) {
+            uint4 x[kBatch];
+            uint32_t any = 0;
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) x[e] = w[c + 32 * e];
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e)
+              any |= nonfinite(x[e].x, kExp, kStep) | nonfinite(x[e].y, kExp, kStep) |
+                     nonfinite(x[e].z, kExp, kStep) | nonfinite(x[e].w, kExp, kStep);
+            if (any) {
+              touched = bad = true;
+#pragma unroll
+              for (int e = 0; e < kBatch; ++e)
+                w[c + 32 * e] = make_uint4(without_nonfinite(x[e].x, kExp, kStep),
+                                           without_nonfinite(x[e].y, kExp, kStep),
+                                           without_nonfinite(x[e].z, kExp, kStep),
+                                           without_nonfinite(x[e].w, kExp, kStep));
+            }
           }
-          if (p.paged) continue;
-          const uint32_t m0 = nonfinite_halves(x.x, kExp), m1 = nonfinite_halves(x.y, kExp),
-                         m2 = nonfinite_halves(x.z, kExp), m3 = nonfinite_halves(x.w, kExp);
-          if (m0 | m1 | m2 | m3) {
-            *w = make_uint4(x.x & ~m0, x.y & ~m1, x.z & ~m2, x.w & ~m3);
-            touched = bad = true;
-          }
+        } else {
+          const int keep = p.Lk - (kb0 + 2 * pp + u) * kDenseBlock;  // rows of the sequence
+          for (int c = lane; c < KB * 512; c += 32)
+            if (((c & 511) >> 3) >= keep) {
+              w[c] = make_uint4(0, 0, 0, 0);
+              touched = true;
+            }
         }
       }
       if (bad) misc[kMiscBad] = 1;
       if (touched) fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[Sm::kBarVC + s]);
+      if (lane == 0) {
+        mbar_arrive(&bars[Sm::kBarVC + s]);
+        // a matrix that leaves the pair out frees its stages here
+        for (int m = 0; m < 2; ++m)
+          if (p.dup ? (pp & 1) != m : pp >= pair_end(m)) {
+            mbar_arrive(&bars[Sm::kBarKE + s]);
+            mbar_arrive(&bars[Sm::kBarVE + s]);
+          }
+      }
     }
   } else if (warp >= Sm::kMmaWarp) {
     // ---- MMA issue for matrix m (the whole warp, one elected lane issuing) ----
     const int m = warp - Sm::kMmaWarp;
     const bool bf = Weights<T>::bf16;
-    const uint32_t idesc_s2 = umma_idesc_f16(bf, 128, 128, 0, 0);  // Q . K^T, a pair
-    const uint32_t idesc_s1 = umma_idesc_f16(bf, 128, 64, 0, 0);   // Q . K^T, a lone block
-    const uint32_t idesc_o = umma_idesc_f16(bf, 128, 64, 0, 1);    // P . V: V MN-major
+    const uint32_t idesc_s = umma_idesc_f16(bf, 128, 64, 0, 0);   // Q . K^T, a block
+    const uint32_t idesc_s2 = umma_idesc_f16(bf, 128, 128, 0, 0);  // both blocks of a pair
+    const uint32_t idesc_o = umma_idesc_f16(bf, 128, D, 0, 1);    // P . V: V MN-major
     const uint64_t dq = umma_desc_sw128(smem_u32(smem + Sm::kQ + m * KB * 16384), 16, 1024);
     const uint64_t dk = umma_desc_sw128(smem_u32(smem + Sm::kK), 16, 1024);
-    const uint64_t dv = umma_desc_sw128(smem_u32(smem + Sm::kV), 16, 1024);
+    // (V's 64-channel halves lie 8,192 bytes apart: one product spans all channels)
+    const uint64_t dv = umma_desc_sw128(smem_u32(smem + Sm::kV), 8192, 1024);
     const uint32_t t_o = tmem + 256 + D * m;
-    const int lo = pair_lo(m), hi = pair_hi(m), dup = p.dup;
-    auto mine = [&](int pp) { return pp >= lo && pp < hi && (!dup || (pp & 1) == m); };
+    const int end = pair_end(m), dup = p.dup;
+    auto mine = [&](int pp) { return dup ? (pp & 1) == m : pp < end; };
     auto wwait = [&](uint64_t *bar, uint32_t parity) {
       return __all_sync(0xffffffffu, dt_wait(bar, parity, fail));
     };
-    auto issue_s = [&](int pp) {
-      const uint64_t kt = dk + (uint64_t)(((pp % S) * Sm::kStageBytes) >> 4);
-      const uint32_t idesc = n - 2 * pp >= 2 ? idesc_s2 : idesc_s1;
+    // matrix 1 starts once matrix 0's first softmax is done, so that one's
+    // softmax runs beside the other's products (in step, both wait for the
+    // tensor pipe and then for the special-function units)
+    const bool lag = m == 1 && !dup && pair_end(0) > 0;
+    bool ok = np > 0 && wwait(&bars[Sm::kBarQ], 0), any = false;
+    if (ok && lag && end > 0) ok = wwait(&bars[Sm::kBarLag], 0);
+    const int last = dup ? ((np - 1) & 1) == m ? np - 1 : np - 2 : end - 1;  // its last pair
+    // the S side runs two blocks ahead of the P . V side: block su of pair sp
+    int sp = 0, su = 0;
+    auto issue_s = [&]() {
+      while (sp < np && !mine(sp)) ++sp;
+      if (sp >= np) return;
+      const int s = sp % S;
+      if (su == 0 && !(ok = wwait(&bars[Sm::kBarKF + s], (sp / S) & 1))) return;
+      tc_fence_after();
+      any = true;
+      const bool both = kPairS && 2 * sp + 1 < n;
+      const uint64_t kt = dk + (uint64_t)((s * Sm::kStageBytes + su * 8192) >> 4);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint64_t off = (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-        umma_f16_warp(tmem + 128 * m, dq + off, kt + off, idesc, kk > 0);
+        umma_f16_warp(tmem + 128 * m + 64 * su, dq + off, kt + off, both ? idesc_s2 : idesc_s,
+                      kk > 0);
       }
-      umma_commit_warp(&bars[Sm::kBarSF + m]);
+      umma_commit_warp(&bars[Sm::kBarSF + 2 * m + su]);
+      if (both) umma_commit_warp(&bars[Sm::kBarSF + 2 * m + 1]);
+      if (both || su == 1 || 2 * sp + 1 == n) {
+        umma_commit_warp(&bars[Sm::kBarKE + s]);
+        ++sp;
+        su = 0;
+      } else {
+        su = 1;
+      }
     };
-    bool ok = np > 0 && wwait(&bars[Sm::kBarQ], 0);
-    bool any = false;
-    int i = 0, last = -1;  // pairs of this matrix so far; its last pair
-    for (int pp = lo; pp < hi; ++pp)
-      if (mine(pp)) last = pp;
-    int ready = -1;  // the pair whose S has been issued
+    if (ok) issue_s();
+    if (ok && !kPairS) issue_s();
+    int i = 0, blocks = 0;  // pairs, blocks of this matrix so far
     for (int pp = 0; pp < np && ok; ++pp) {
       const int s = pp % S, nbk = min(2, n - 2 * pp);
-      if (!mine(pp)) {
-        // not this matrix's: the stage is free as far as it is concerned, once
-        // it has been filled
-        if (!(ok = wwait(&bars[Sm::kBarKF + s], (pp / S) & 1))) break;
-        if (!(ok = wwait(&bars[Sm::kBarVC + s], (pp / S) & 1))) break;
-        if (lane == 0) mbar_arrive(&bars[Sm::kBarKE + s]);
-        continue;
-      }
-      if (ready < pp) {
-        if (!(ok = wwait(&bars[Sm::kBarKF + s], (pp / S) & 1))) break;
-        if (i > 0 && !(ok = wwait(&bars[Sm::kBarOP + m], (i - 1) & 1))) break;
-        tc_fence_after();
-        issue_s(pp);
-        any = true;
-      }
+      if (!mine(pp)) continue;
       if (!(ok = wwait(&bars[Sm::kBarVC + s], (pp / S) & 1))) break;
-      for (int u = 0; u < nbk; ++u) {
+      for (int u = 0; u < nbk; ++u, ++blocks) {
         if (!(ok = wwait(&bars[Sm::kBarPF + 2 * m + u], i & 1))) break;
         tc_fence_after();
         const uint64_t vt = dv + (uint64_t)((s * Sm::kStageBytes + u * KB * 8192) >> 4);
         const uint32_t pa = tmem + 128 * m + 64 * u;
 #pragma unroll
-        for (int half = 0; half < KB; ++half)
+        for (int part = 0; part < (kSplitP ? 2 : 1); ++part)
 #pragma unroll
-          for (int part = 0; part < (kSplitP ? 2 : 1); ++part)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_f16_ts_warp(t_o + 64 * half, pa + 32 * part + 8 * kk,
-                               vt + (uint64_t)((half * 8192 + kk * 2048) >> 4), idesc_o,
-                               i > 0 || u > 0 || part > 0 || kk > 0);
+          for (int kk = 0; kk < 4; ++kk)
+            umma_f16_ts_warp(t_o, pa + 32 * part + 8 * kk, vt + (uint64_t)((kk * 2048) >> 4),
+                             idesc_o, blocks > 0 || part > 0 || kk > 0);
         umma_commit_warp(&bars[Sm::kBarOD + m]);
+        if (u == nbk - 1) {
+          umma_commit_warp(&bars[Sm::kBarVE + s]);
+          if (pp == last) umma_commit_warp(&bars[Sm::kBarOF + m]);
+        }
+        if (sp < np && (!kPairS || u == nbk - 1)) {  // the next S goes where this P was
+          if (!(ok = wwait(&bars[Sm::kBarOD + m], blocks & 1))) break;
+          issue_s();
+          if (!ok) break;
+        }
       }
-      if (!ok) break;
-      umma_commit_warp(&bars[Sm::kBarOP + m]);
-      if (pp == last) umma_commit_warp(&bars[Sm::kBarOF + m]);
-      umma_commit_warp(&bars[Sm::kBarKE + s]);
       ++i;
     }
     if (any) {  // every MMA of this warp done before the CTA frees its memory
@@ -445,48 +494,66 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
     const int m = warp >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t t_o = lanes + 256 + D * m;
-    const int lo = pair_lo(m), hi = pair_hi(m), step = p.dup ? 2 : 1;
-    const float slope = p.rule.slopes && tok < p.Lq ? p.rule.slopes[h_row] * 1.4426950408889634f : 0.f;
+    const int end = pair_end(m), step = p.dup ? 2 : 1;
+    const float slope = kRule && p.rule.slopes && tok < p.Lq ? p.rule.slopes[h_row] * 1.4426950408889634f : 0.f;
     // a prompt's distances count from the row's nearest key, so that the bias of
     // the keys that matter keeps its bits however far they are (the nearest key
     // of a decode row is its own newest token, at distance 0)
     const int pos = p.paged ? p.Lk + (tok < p.Lq ? p.lens[tok] : 0) - 1 : p.pos0 + tok;
     const float near = p.paged ? 0.f : (float)max(0, max(pos - rend + 1, rbeg - pos));
-    const bool rule = p.rule.cap_out > 0.f || p.rule.slopes != nullptr;
-    const float sc = rule ? 1.f : p.rule.scale_log2;
+    const float sc = kRule ? 1.f : p.rule.scale_log2;
+    const bool idle = __all_sync(0xffffffffu, rend == 0);  // rows that attend nothing
     float m_run = -CUDART_INF_F, l_run = 0.f;
     bool ok = true;
     int i = 0, blocks = 0;
-    for (int pp = p.dup ? m : lo; pp < hi && ok; pp += step, ++i) {
+    for (int pp = p.dup ? m : 0; pp < end && ok; pp += step, ++i) {
       const int nbk = min(2, n - 2 * pp);
-      ok = dt_wait(&bars[Sm::kBarSF + m], i & 1, fail);
-      if (!(ok = __all_sync(0xffffffffu, ok))) break;  // the tensor-memory accesses are warp-wide
-      tc_fence_after();
 #pragma unroll 1
       for (int u = 0; u < nbk; ++u, ++blocks) {
+        ok = dt_wait(&bars[Sm::kBarSF + 2 * m + u], i & 1, fail);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;  // the tensor-memory accesses are warp-wide
+        tc_fence_after();
+        if (idle) {  // what the products make of these rows is never read
+          if (lane == 0) {
+            mbar_arrive(&bars[Sm::kBarPF + 2 * m + u]);
+            if (m == 0 && blocks == 0) mbar_arrive(&bars[Sm::kBarLag]);
+          }
+          continue;
+        }
         const uint32_t t_s = lanes + 128 * m + 64 * u;
         const int key0 = (kb0 + 2 * pp + u) * kDenseBlock;
         uint32_t s[64];
         tmem_ld64_sync(t_s, s);
-        if (rule) {
+        if constexpr (kRule) {
           if (p.rule.cap_out > 0.f) {
-            // the short polynomial when it holds for the warp's 64 x 32 scores
-            float big = 0.f;
+            if constexpr (kSplitP) {
+              // the short polynomial when it holds for the warp's 64 x 32 scores
+              float big = 0.f;
 #pragma unroll
-            for (int c = 0; c < 64; c += 2)
-              big = fmax3f(big, fabsf(__uint_as_float(s[c])), fabsf(__uint_as_float(s[c + 1])));
-            if (__all_sync(0xffffffffu, big <= p.rule.small)) {
+              for (int c = 0; c < 64; c += 2)
+                big = fmaxf(fmaxf(big, fabsf(__uint_as_float(s[c]))),
+                            fabsf(__uint_as_float(s[c + 1])));
+              if (__all_sync(0xffffffffu, big <= p.rule.small)) {
+#pragma unroll
+                for (int c = 0; c < 64; c += 2) {
+                  const float2 x = cap_small(
+                      p.rule, make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])));
+                  s[c] = __float_as_uint(x.x);
+                  s[c + 1] = __float_as_uint(x.y);
+                }
+              } else {
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                  s[c] = __float_as_uint(cap_any(p.rule, __uint_as_float(s[c])));
+              }
+            } else {
 #pragma unroll
               for (int c = 0; c < 64; c += 2) {
-                const float2 x = cap_small(
+                const float2 x = cap_16bit(
                     p.rule, make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])));
                 s[c] = __float_as_uint(x.x);
                 s[c + 1] = __float_as_uint(x.y);
               }
-            } else {
-#pragma unroll
-              for (int c = 0; c < 64; ++c)
-                s[c] = __float_as_uint(cap_any(p.rule, __uint_as_float(s[c])));
             }
           } else {
 #pragma unroll
@@ -560,21 +627,28 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[Sm::kBarPF + 2 * m + u]);
+        if (lane == 0) {
+          mbar_arrive(&bars[Sm::kBarPF + 2 * m + u]);
+          if (m == 0 && blocks == 0) mbar_arrive(&bars[Sm::kBarLag]);
+        }
       }
     }
-    if (ok && blocks > 0) {
-      ok = dt_wait(&bars[Sm::kBarOF + m], 0, fail);
+    if (ok && np > 0) {  // (without products, Q's copy must have landed: its tile is written next)
+      ok = dt_wait(blocks > 0 ? &bars[Sm::kBarOF + m] : &bars[Sm::kBarQ], 0, fail);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     }
     if (ok) {
+      // ---- the warp's 32 rows, 32 channels at a time, through the matrix's Q
+      // tile (its products are done) so that rows leave in whole lines ----
       const bool live = tok < p.Lq, empty = rend == 0;
       const bool fix = *reinterpret_cast<volatile int *>(misc + kMiscBad) && live && !empty;
       const size_t pr = ((size_t)unit * p.nsplit + split) * kDenseRows + m * 128 + row;
       if (!p.out && live) p.part_ml[pr] = make_float2(m_run, empty ? 0.f : l_run);
       const float inv = empty ? 0.f : p.out ? 1.f / l_run : 1.f;
-      const size_t orow = ((size_t)tok * p.Hq + h_row) * D;
+      const bool f32 = !p.out || p.out_f32;
+      uint8_t *stage = smem + Sm::kQ + m * KB * 16384 + (warp & 3) * 4096;  // [32][128 B]
+      const int row0 = row - lane, tok_m = tok0 + (p.dup ? 0 : m * tpm);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t r[32];
@@ -585,7 +659,6 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) r[e] = 0u;
         }
-        if (!live) continue;
         float f[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) f[e] = empty ? 0.f : __uint_as_float(r[e]) * inv;
@@ -605,26 +678,40 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
             }
           }
         }
-        if (!p.out) {
-          float *o = p.part_o + pr * D + 32 * c;
+        // rows of 128 bytes (32 channels of fp32, or two turns of 16 bits), 16-byte
+        // pieces swizzled by the row
+        if (f32) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4 *>(o + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
-        } else if (p.out_f32) {
-          float *o = static_cast<float *>(p.out) + orow + 32 * c;
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4 *>(o + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4 *>(stage + swz128(lane, e)) =
+                make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
         } else {
-          T *o = static_cast<T *>(p.out) + orow + 32 * c;
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4 *>(o + e) =
-                make_uint4(Weights<T>::round(make_float2(f[e], f[e + 1])),
-                           Weights<T>::round(make_float2(f[e + 2], f[e + 3])),
-                           Weights<T>::round(make_float2(f[e + 4], f[e + 5])),
-                           Weights<T>::round(make_float2(f[e + 6], f[e + 7])));
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4 *>(stage + swz128(lane, 4 * (c & 1) + e)) =
+                make_uint4(Weights<T>::round(make_float2(f[8 * e], f[8 * e + 1])),
+                           Weights<T>::round(make_float2(f[8 * e + 2], f[8 * e + 3])),
+                           Weights<T>::round(make_float2(f[8 * e + 4], f[8 * e + 5])),
+                           Weights<T>::round(make_float2(f[8 * e + 6], f[8 * e + 7])));
+          if (!(c & 1)) continue;
         }
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {  // four rows at once, eight lanes each
+          const int rr = 4 * e + (lane >> 3), ch = lane & 7, rm = row0 + rr;
+          const uint4 x = *reinterpret_cast<const uint4 *>(stage + swz128(rr, ch));
+          const int tk = tok_m + (rm >> lhp);
+          if (tk >= p.Lq) continue;
+          uint8_t *to;
+          if (!p.out)
+            to = reinterpret_cast<uint8_t *>(p.part_o + (pr - lane + rr) * D + 32 * c);
+          else
+            to = static_cast<uint8_t *>(p.out) +
+                 (((size_t)tk * p.Hq + h0 + (rm & ((1 << lhp) - 1))) * D + (f32 ? 32 * c : 32 * (c - 1))) *
+                     (f32 ? 4 : 2);
+          *reinterpret_cast<uint4 *>(to + 16 * ch) = x;
+        }
+        __syncwarp();
       }
     }
   }
@@ -647,10 +734,10 @@ __global__ void __launch_bounds__(256) dense_prompt_combine_kernel(
   const int lane = threadIdx.x & 31;
   if (w >= (long long)p.Lq * p.Hq) return;
   const int tok = (int)(w / p.Hq), h = (int)(w % p.Hq);
-  const int hk = h / p.G, hg = (h % p.G) / p.HP;
+  const int hk = h / p.G, hg = (h % p.G) >> p.lhp;
   const int rt = p.dup ? 128 : kDenseRows, ns = p.nsplit * kDenseRows / rt;
-  const int tpt = rt / p.HP, tile = tok / tpt;
-  const int r = (tok % tpt) * p.HP + h % p.HP;
+  const int tpt = rt >> p.lhp, tile = tok / tpt;  // (heads per matrix: a power of two)
+  const int r = ((tok % tpt) << p.lhp) + (h & ((1 << p.lhp) - 1));
   const size_t unit = (size_t)tile * p.Hkv * p.HG + hk * p.HG + hg;
   const float2 *ml = p.part_ml + unit * ns * rt + r;
   const float *po = p.part_o + (unit * ns * rt + r) * D;
@@ -734,14 +821,20 @@ __global__ void __launch_bounds__(256) document_ranges_kernel(const int *offsets
   ke[t] = e;
 }
 
-template <typename T, int D, bool kSplitP>
-cudaError_t launch_dt(const DenseTcParams &p, cudaStream_t st) {
-  auto k = dense_tc_kernel<T, D, kSplitP>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       DtSmem<D>::kBytes);
+template <typename T, int D, bool kSplitP, bool kRule>
+cudaError_t launch_dt_r(const DenseTcParams &p, cudaStream_t st) {
+  auto k = dense_tc_kernel<T, D, kSplitP, kRule>;
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(k, DtSmem<D>::kBytes, &ready);
   if (e != cudaSuccess) return e;
   return launch_pdl(k, p.tiles * p.nsplit * p.Hkv * p.HG, DtSmem<D>::kThreads,
                     (size_t)DtSmem<D>::kBytes, st, p);
+}
+
+template <typename T, int D, bool kSplitP>
+cudaError_t launch_dt(const DenseTcParams &p, cudaStream_t st) {
+  return p.rule.cap_out > 0.f || p.rule.slopes ? launch_dt_r<T, D, kSplitP, true>(p, st)
+                                               : launch_dt_r<T, D, kSplitP, false>(p, st);
 }
 
 template <typename T>

@@ -25,7 +25,7 @@
 namespace spd {
 namespace {
 
-constexpr int kSelThreads = 512, kPerThread = 4;
+constexpr int kSelThreads = 512;
 constexpr int kBins = 2048;
 constexpr int kCacheKeys = 48 * 1024;  // keys a CTA holds; longer stretches are read again
 
@@ -53,46 +53,52 @@ __device__ __forceinline__ void st_dsmem_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// Inclusive sum over the block's threads in order (two 32-bit counts at once);
-// `tmp` holds one entry per warp.
-__device__ __forceinline__ uint2 block_scan(uint2 v, uint2 *tmp, uint2 *total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t x = __shfl_up_sync(0xffffffffu, v.x, o), y = __shfl_up_sync(0xffffffffu, v.y, o);
-    if (lane >= o) {
-      v.x += x;
-      v.y += y;
-    }
-  }
-  __syncthreads();  // (tmp may still be read from the call before)
-  if (lane == 31) tmp[warp] = v;
-  __syncthreads();
-  uint2 before = make_uint2(0, 0), all = make_uint2(0, 0);
+// Exclusive sums of the warps' two counts and their totals (one entry per warp
+// in `tmp`, written by the callers' lane 0 before a barrier).
+__device__ __forceinline__ void warp_prefix(const uint2 *tmp, uint2 *before, uint2 *all) {
+  const int warp = threadIdx.x >> 5;
+  uint2 b = make_uint2(0, 0), t = make_uint2(0, 0);
 #pragma unroll
   for (int w = 0; w < kSelThreads / 32; ++w) {
-    const uint2 t = tmp[w];
+    const uint2 x = tmp[w];
     if (w < warp) {
-      before.x += t.x;
-      before.y += t.y;
+      b.x += x.x;
+      b.y += x.y;
     }
-    all.x += t.x;
-    all.y += t.y;
+    t.x += x.x;
+    t.y += x.y;
   }
-  *total = all;
-  return make_uint2(v.x + before.x, v.y + before.y);
+  *before = b;
+  *all = t;
+}
+
+// One key into the histogram.  Many tokens share one weight (0 above all): keys
+// that fall into the first active lane's bin are counted at once when they are
+// more than a few.
+__device__ __forceinline__ void count_bin(uint32_t *hist, bool in, uint32_t bin) {
+  const uint32_t act = __ballot_sync(0xffffffffu, in);
+  if (!act) return;
+  const int lead = __ffs(act) - 1;
+  const uint32_t lbin = __shfl_sync(0xffffffffu, bin, lead);
+  const uint32_t same = __ballot_sync(0xffffffffu, in && bin == lbin);
+  if (__popc(same) > 4) {
+    if ((int)(threadIdx.x & 31) == lead) atomicAdd(&hist[lbin], __popc(same));
+    in = in && bin != lbin;
+  }
+  if (in) atomicAdd(&hist[bin], 1u);
 }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
     const __grid_constant__ EvictParams p) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ uint32_t hist[kBins], tot[kBins];
   __shared__ uint2 tmp[kSelThreads / 32];
   __shared__ uint32_t counts[2];       // greater than, equal to the cut in this stretch
   __shared__ uint32_t found[2];        // the round's bin, keys above it
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cs = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
   const int unit = blockIdx.x / cs, seq = unit / p.Hkv;
+  for (int b = tid; b < kBins; b += kSelThreads) hist[b] = 0;
   pdl_wait();
   pdl_launch_dependents();
   const EvictSeq s = p.seqs[seq];
@@ -116,28 +122,41 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
   if (room == 0) return;
   const int seg = ((n_old + cs - 1) / cs + 3) & ~3;
   const int s0 = min(rank * seg, n_old), len = min(seg, n_old - s0);
-  for (int i = tid; i < min(len, kCacheKeys); i += kSelThreads) keys[i] = weight_key(w[s0 + i]);
-  auto key = [&](int i) { return i < kCacheKeys ? keys[i] : weight_key(w[s0 + i]); };
+  const float *ws = w + s0;
+  auto key = [&](int i) { return i < kCacheKeys ? keys[i] : weight_key(ws[i]); };
+  __syncthreads();
+  // ---- the stretch into shared memory, counted by the leading 11 bits ----
+  constexpr int kUnroll = 8;
+  for (int i0 = 0; i0 < len; i0 += kSelThreads * kUnroll) {
+    float x[kUnroll];
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      const int i = i0 + j * kSelThreads + tid;
+      x[j] = i < len ? __ldg(ws + i) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      const int i = i0 + j * kSelThreads + tid;
+      if (i0 + j * kSelThreads >= len) break;  // (the same for the block)
+      const uint32_t k = weight_key(x[j]);
+      if (i < min(len, kCacheKeys)) keys[i] = k;
+      count_bin(hist, i < len, k >> 21);
+    }
+  }
 
   uint32_t prefix = 0, need = (uint32_t)room;  // the cut's leading bits; its rank among them
   for (int round = 0; round < 3; ++round) {
     const int shift = round == 0 ? 21 : round == 1 ? 10 : 0, bits = round == 2 ? 10 : 11;
-    for (int b = tid; b < kBins; b += kSelThreads) hist[b] = 0;
-    __syncthreads();
-    for (int i0 = 0; i0 < len; i0 += kSelThreads) {
-      const int i = i0 + tid;
-      const uint32_t k = i < len ? key(i) : 0u;
-      const bool in = i < len && (round == 0 || (k >> (shift + bits)) == prefix);
-      const uint32_t bin = (k >> shift) & ((1u << bits) - 1);
-      // many tokens share one weight (0 above all): the first lane's bin is
-      // counted once for the warp
-      const uint32_t act = __ballot_sync(0xffffffffu, in);
-      if (!act) continue;
-      const int lead = __ffs(act) - 1;
-      const uint32_t lbin = __shfl_sync(0xffffffffu, bin, lead);
-      const uint32_t same = __ballot_sync(0xffffffffu, in && bin == lbin);
-      if (lane == lead) atomicAdd(&hist[lbin], __popc(same));
-      if (in && bin != lbin) atomicAdd(&hist[bin], 1u);
+    if (round > 0) {
+      for (int b = tid; b < kBins; b += kSelThreads) hist[b] = 0;
+      __syncthreads();
+#pragma unroll 4
+      for (int i0 = 0; i0 < len; i0 += kSelThreads) {
+        const int i = i0 + tid;
+        const uint32_t k = i < len ? key(i) : 0u;
+        count_bin(hist, i < len && (k >> (shift + bits)) == prefix,
+                  (k >> shift) & ((1u << bits) - 1));
+      }
     }
     cluster_sync();  // every CTA's histogram is complete
     const int per = (kBins + cs - 1) / cs;
@@ -150,13 +169,23 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
     cluster_sync();  // the sums are everywhere
     // the bin that holds the need-th greatest key: bins in descending order,
     // four per thread
+    static_assert(kBins == kSelThreads * 4, "four bins per thread");
     uint32_t c[4], mine = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) mine += c[j] = tot[kBins - 1 - (tid * 4 + j)];
-    uint2 all;
-    const uint2 inc = block_scan(make_uint2(mine, 0), tmp, &all);
-    uint32_t above = inc.x - mine;
-    if (above < need && need <= inc.x) {
+    uint32_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) tmp[warp] = make_uint2(inc, 0);
+    __syncthreads();
+    uint2 before, all;
+    warp_prefix(tmp, &before, &all);
+    inc += before.x;
+    uint32_t above = inc - mine;
+    if (above < need && need <= inc) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (above < need && need <= above + c[j]) {
@@ -171,55 +200,84 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
     prefix = (prefix << bits) | found[0];
     need -= found[1];
   }
-  static_assert(kBins == kSelThreads * 4, "four bins per thread");
   // prefix is the cut itself: greater keys all stay, of the equal ones the
-  // first `need`
+  // first `need`.  Every warp counts, then places, a stretch of its own.
+  const int wlen = ((len + kSelThreads / 32 - 1) / (kSelThreads / 32) + 127) & ~127;
+  const int w0 = min(warp * wlen, len), w1 = min(w0 + wlen, len);
+  // four consecutive keys per lane (behind the end: 0, which no key is: the
+  // least, -inf, is 0x007fffff)
+  auto keys4 = [&](int i, uint32_t (&k)[4]) {
+    if (i + 3 < min(w1, kCacheKeys)) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(&keys[i]);
+      k[0] = x.x;
+      k[1] = x.y;
+      k[2] = x.z;
+      k[3] = x.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) k[j] = i + j < w1 ? key(i + j) : 0u;
+    }
+  };
   uint2 cnt = make_uint2(0, 0);
-  for (int i = tid; i < len; i += kSelThreads) {
-    const uint32_t k = key(i);
-    cnt.x += k > prefix;
-    cnt.y += k == prefix;
+#pragma unroll 2
+  for (int i = w0 + 4 * lane; i < w1; i += 128) {
+    uint32_t k[4];
+    keys4(i, k);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      cnt.x += k[j] > prefix;
+      cnt.y += k[j] == prefix;
+    }
   }
-  uint2 total;
-  block_scan(cnt, tmp, &total);
+  cnt.x = __reduce_add_sync(0xffffffffu, cnt.x);
+  cnt.y = __reduce_add_sync(0xffffffffu, cnt.y);
+  if (lane == 0) tmp[warp] = cnt;
+  __syncthreads();
+  uint2 before, total;
+  warp_prefix(tmp, &before, &total);
   if (tid == 0) {
     counts[0] = total.x;
     counts[1] = total.y;
   }
   cluster_sync();
-  uint32_t gt = 0, eq = 0;  // before this stretch
+  uint32_t gt = before.x, eq = before.y;  // before this warp's stretch
   for (int r = 0; r < rank; ++r) {
     gt += ld_dsmem_u32(map_rank(smem_u32(&counts[0]), r));
     eq += ld_dsmem_u32(map_rank(smem_u32(&counts[1]), r));
   }
-  cluster_sync();  // the counts have been read: a CTA may leave
-  for (int i0 = 0; i0 < len; i0 += kSelThreads * kPerThread) {
-    const int i = i0 + tid * kPerThread;
-    uint32_t k[kPerThread];
-    uint2 v = make_uint2(0, 0);
+  cluster_arrive_release();  // the counts have been read: a CTA may leave
+#pragma unroll 1
+  for (int i0 = w0; i0 < w1; i0 += 128) {
+    const int i = i0 + 4 * lane;
+    uint32_t k[4], v = 0;  // (counts of up to 128: both in one word)
+    keys4(i, k);
 #pragma unroll
-    for (int j = 0; j < kPerThread; ++j) {
-      k[j] = i + j < len ? key(i + j) : 0u;
-      v.x += i + j < len && k[j] > prefix;
-      v.y += i + j < len && k[j] == prefix;
+    for (int j = 0; j < 4; ++j) v += (k[j] > prefix ? 1u : 0u) + (k[j] == prefix ? 0x10000u : 0u);
+    if (!__any_sync(0xffffffffu, v != 0)) continue;
+    uint32_t inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
     }
-    const uint2 inc = block_scan(v, tmp, &total);
-    uint32_t g = gt + inc.x - v.x, e = eq + inc.y - v.y;
+    uint32_t g = gt + ((inc - v) & 0xffffu), e = eq + ((inc - v) >> 16);
 #pragma unroll
-    for (int j = 0; j < kPerThread; ++j) {
-      if (i + j >= len) break;
+    for (int j = 0; j < 4; ++j) {
       const bool more = k[j] > prefix, tie = k[j] == prefix;
       if (more || (tie && e < need)) {
         const uint32_t at = g + min(e, need);
         kept[at] = s0 + i + j;
-        if (kw) kw[at] = w[s0 + i + j];
+        if (kw) kw[at] = __ldg(ws + i + j);
       }
       g += more;
       e += tie;
     }
-    gt += total.x;
-    eq += total.y;
+    const uint32_t all = __shfl_sync(0xffffffffu, inc, 31);
+    gt += all & 0xffffu;
+    eq += all >> 16;
   }
+  __syncwarp();
+  cluster_wait();
 }
 
 // ---- gather + metadata ---------------------------------------------------------
@@ -233,12 +291,13 @@ template <typename T> __device__ __forceinline__ float elem_key(T x) { return (f
 template <> __device__ __forceinline__ float elem_key<F8>(F8 x) { return (float)e4m3_key(x.v); }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(
+__global__ void __launch_bounds__(kCopyThreads, 5) evict_copy_kernel(
     const __grid_constant__ EvictParams p) {
   constexpr int kLanes = D * (int)sizeof(T) / 16;       // threads of one row
   constexpr int kStep = kCopyThreads / kLanes;          // rows at once
   constexpr int kIter = kCopyRows / kStep;
   __shared__ uint4 krows[kCopyRows * kLanes];
+  __shared__ T ends[kCopyRows / 16][2][D];
   const int tid = threadIdx.x, groups = (p.keep + kCopyRows - 1) / kCopyRows;
   const int unit = blockIdx.x / groups, r0 = blockIdx.x % groups * kCopyRows;
   const int seq = unit / p.Hkv, hk = unit % p.Hkv;
@@ -253,53 +312,58 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(
   const uint4 *kp = static_cast<const uint4 *>(p.k_pool), *vp = static_cast<const uint4 *>(p.v_pool);
   uint4 *ko = static_cast<uint4 *>(p.k_pool), *vo = static_cast<uint4 *>(p.v_pool);
   const int lane = tid % kLanes, sub = tid / kLanes;
-  // row t of a page list, in units of 16 bytes; negative if the check fails
-  auto row_at = [&](const int *pages, int t, int slot) -> long long {
+  // row t of a page list, or the largest value if the check fails
+  constexpr uint32_t kNone = 0xffffffffu;
+  auto row_at = [&](const int *pages, int t, int slot) -> uint32_t {
     const int blk = t / p.P, phys = t >= 0 && blk < p.max_pp ? pages[blk] : -1;
     if (phys < 0 || phys >= p.num_phys) {
       ev_set_err(p.err, kDevBadPhys, slot, t, phys);
-      return -1;
+      return kNone;
     }
-    return (((long long)phys * p.Hkv + hk) * p.P + t % p.P) * kLanes + lane;
+    return (uint32_t)(phys * p.Hkv + hk) * (uint32_t)p.P + (uint32_t)(t % p.P);
   };
-  long long from[kIter], to[kIter];
-  uint4 kx[kIter], vx[kIter];
+  uint32_t from[kIter], to[kIter];
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
     const int r = i * kStep + sub;
-    from[i] = to[i] = -1;
+    from[i] = to[i] = kNone;
     if (r < n) {
       const int t = kept[r];
-      from[i] = t < s.L ? row_at(src_pages, t, s.src) : -1;
-      to[i] = row_at(dst_pages, r0 + r, s.dst);
+      from[i] = t < s.L ? row_at(src_pages, t, s.src) : kNone;
+      to[i] = from[i] == kNone ? kNone : row_at(dst_pages, r0 + r, s.dst);
     }
   }
+  uint4 kx[kIter], vx[kIter];
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
-    const bool in = from[i] >= 0 && to[i] >= 0;
-    kx[i] = in ? kp[from[i]] : make_uint4(0, 0, 0, 0);
-    vx[i] = in ? vp[from[i]] : make_uint4(0, 0, 0, 0);
+    const bool in = to[i] != kNone;
+    const size_t at = (size_t)from[i] * kLanes + lane;
+    kx[i] = in ? __ldcs(kp + at) : make_uint4(0, 0, 0, 0);
+    vx[i] = in ? __ldcs(vp + at) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
-    if (from[i] >= 0 && to[i] >= 0) {
-      ko[to[i]] = kx[i];
-      vo[to[i]] = vx[i];
+    if (to[i] != kNone) {
+      const size_t at = (size_t)to[i] * kLanes + lane;
+      ko[at] = kx[i];
+      vo[at] = vx[i];
     }
     krows[(i * kStep + sub) * kLanes + lane] = kx[i];
   }
   __syncthreads();
-  // metadata of the logical pages that begin in these rows (64 rows hold whole ones)
+  // metadata of the logical pages that begin in these rows (64 rows hold whole
+  // ones): least and greatest of each channel per 16 rows, then per page
   T *meta = static_cast<T *>(p.meta);
   const T *rows = reinterpret_cast<const T *>(krows);
-  const int pages = (n + p.ell - 1) / p.ell;
-  for (int x = tid; x < pages * D; x += kCopyThreads) {
-    const int j = x / D, c = x % D;
-    const int a = j * p.ell, b = min(a + p.ell, n);
-    T lo = rows[a * D + c], hi = lo;
+  const int parts = (n + 15) / 16;
+  for (int x = tid; x < parts * D; x += kCopyThreads) {
+    const int j = x / D, c = x % D, m = min(16, n - 16 * j);
+    T lo = rows[16 * j * D + c], hi = lo;
     float flo = elem_key(lo), fhi = flo;
-    for (int r = a + 1; r < b; ++r) {
-      const T e = rows[r * D + c];
+#pragma unroll
+    for (int r = 1; r < 16; ++r) {
+      if (r >= m) break;
+      const T e = rows[(16 * j + r) * D + c];
       const float f = elem_key(e);
       if (f < flo) {
         flo = f;
@@ -310,7 +374,19 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(
         hi = e;
       }
     }
-    const int t = r0 + a, blk = t / p.P, phys = dst_pages[blk];
+    ends[j][0][c] = lo;
+    ends[j][1][c] = hi;
+  }
+  __syncthreads();
+  const int pages = (n + p.ell - 1) / p.ell, ppg = p.ell / 16;
+  for (int x = tid; x < pages * D; x += kCopyThreads) {
+    const int j = x / D, c = x % D;
+    T lo = ends[j * ppg][0][c], hi = ends[j * ppg][1][c];
+    for (int r = j * ppg + 1; r < min((j + 1) * ppg, parts); ++r) {
+      if (elem_key(ends[r][0][c]) < elem_key(lo)) lo = ends[r][0][c];
+      if (elem_key(ends[r][1][c]) > elem_key(hi)) hi = ends[r][1][c];
+    }
+    const int t = r0 + j * p.ell, phys = dst_pages[t / p.P];
     if (phys < 0 || phys >= p.num_phys) continue;  // (reported above)
     T *m = meta + (((size_t)phys * p.Hkv + hk) * p.R + t % p.P / p.ell) * 2 * D + c;
     m[0] = lo;
@@ -325,8 +401,8 @@ cudaError_t launch_evict(const EvictParams &p, int dtype, int d, int cluster, cu
   for (int i = 0; i < p.n; ++i) longest = longest > p.seqs[i].L ? longest : p.seqs[i].L;
   int seg = ((longest + cluster - 1) / cluster + 3) & ~3;
   const int smem = 4 * (seg < kCacheKeys ? seg : kCacheKeys);
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kCacheKeys * 4);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(evict_select_kernel, kCacheKeys * 4, &ready);
   if (e != cudaSuccess) return e;
   e = launch_pdl_cluster(evict_select_kernel, p.n * p.Hkv * cluster, kSelThreads, (size_t)smem,
                          cluster, st, p);
