@@ -109,6 +109,7 @@ struct DenseDecodeParams {
   int n, Hq, Hkv, G, P, max_pp, num_phys;
   int prefix_slot, prefix_len, prefix_items, prefix_ns, prefix_tpi, prefix_rows;
   int own_items;
+  int precise;             // outputs that show 2^-22 of the cap (fp32, weights)
   int follow;              // the kernel before is this call's prefix kernel
   int w_chunks;            // weight CTAs per (sequence, kv head)
   DecodeSeq seqs[kDenseSeqs];
@@ -132,6 +133,7 @@ struct EvictParams {
   int *err;
   long long w_stride;
   int n, Hkv, keep, recent, ell, P, R, max_pp, num_phys, kv_fp8;
+  int P_log2;             // log2(P), -1 if P is no power of two
   EvictSeq seqs[kDenseSeqs];
 };
 cudaError_t launch_evict(const EvictParams &p, int dtype, int d, int cluster, cudaStream_t st);

@@ -496,6 +496,7 @@ spd_status spd_shared_prefix_attention(spd_ctx *c, const void *q, int prefix_id,
     p.prefix_rows = z.prefix_rows;
     p.own_items = z.own_items;
     p.follow = z.tc;
+    p.precise = p.out_f32 || weights_out;
     p.w_chunks = (z.longest + 1023) / 1024;
     int launches = 0;
     cudaError_t e = cudaSuccess;
@@ -614,6 +615,9 @@ spd_status spd_kv_evict(spd_ctx *c, const int *src_ids, const int *dst_ids, int 
     p.max_pp = v.max_pp;
     p.num_phys = cfg.num_physical_pages;
     p.kv_fp8 = v.kv_fp8;
+    p.P_log2 = -1;
+    for (int x = 0; x < 31; ++x)
+      if (p.P == 1 << x) p.P_log2 = x;
     long long longest = 0;
     for (int i = 0; i < p.n; ++i) {
       const long long L = seq_length(c, src_ids[b + i]);

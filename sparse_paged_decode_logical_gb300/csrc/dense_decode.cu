@@ -64,11 +64,6 @@ template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t x) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&x));
 }
 
-__device__ __forceinline__ float apply_rule(const ScoreRule &r, float s, float slope, float dist) {
-  const float x = r.cap_out > 0.f ? cap_any(r, s) : s * r.scale_log2;
-  return fmaf(-slope, dist, x);
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     dense_decode_kernel(const __grid_constant__ DenseDecodeParams p) {
@@ -137,11 +132,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   pdl_launch_dependents();
 
   const int *table = p.page_table + (size_t)slot * p.max_pp;
-  const int first = tile0 + warp, ntile = first < tile1 ? (tile1 - first + kWarps - 1) / kWarps : 0;
+  // tiles from the newest to the oldest (a distance bias then finds its largest
+  // scores first, and the running max hardly moves): the warp's i-th is
+  // first - 4 i
+  const int first = tile1 - 1 - warp, ntile = first >= tile0 ? (first - tile0) / kWarps + 1 : 0;
   int issued = 0;
   bool ok = true;
   auto issue = [&](int i) {  // lane 0: the warp's i-th tile into its stage
-    const int t = (first + i * kWarps) * kDecodeTile, blk = t / p.P;
+    const int t = (first - i * kWarps) * kDecodeTile, blk = t / p.P;
     const int phys = blk < p.max_pp ? table[blk] : -1;
     if (phys < 0 || phys >= p.num_phys) {
       dd_set_err(p.err, blk < p.max_pp ? kDevBadPhys : kDevBadPage, slot, blk, phys);
@@ -179,7 +177,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       pos[hrow] = (pre ? L + p.seqs[sq].L : L) - 1;
     }
   }
-  const bool rule = p.rule.cap_out > 0.f || p.rule.slopes != nullptr;
   const bool upper = rows > 8;
 
   float o[NT][4];
@@ -193,7 +190,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
                   : nullptr;
 
   for (int i = 0; i < ntile && ok; ++i) {
-    const int s = i % Sm::kStages, t0 = (first + i * kWarps) * kDecodeTile;
+    const int s = i % Sm::kStages, t0 = (first - i * kWarps) * kDecodeTile;
     ok = __all_sync(0xffffffffu, mbar_wait(&bars[s], (i / Sm::kStages) & 1, kDdWait));
     if (!ok) {
       if (lane == 0) dd_set_err(p.err, kDevTimeout, slot, hk, t0);
@@ -207,6 +204,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         if (((c >> 3) & (kDecodeTile - 1)) >= valid)
           *reinterpret_cast<uint4 *>(vt + c * 16) = make_uint4(0, 0, 0, 0);
       }
+      fence_proxy_async_smem();  // (the stage is filled again later)
       __syncwarp();
     }
     // S = Q . K^T: 16 rows x 16 keys
@@ -227,15 +225,46 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     }
     // scores in base 2, masked behind the end
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int hr = 0; hr < 2; ++hr) {
+      if (hr == 1 && !upper) break;
+      if (p.rule.cap_out > 0.f) {
+        if (p.precise) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int key = 8 * j + 2 * t4 + (e & 1), hr = e >> 1;
-        float x = rule ? apply_rule(p.rule, sc[j][e], slope[hr], (float)(pos[hr] - (t0 + key)))
-                       : sc[j][e] * p.rule.scale_log2;
-        if (key >= valid) x = -CUDART_INF_F;
-        sc[j][e] = x;
+          for (int j = 0; j < 2; ++j) {
+            sc[j][2 * hr] = cap_any(p.rule, sc[j][2 * hr]);
+            sc[j][2 * hr + 1] = cap_any(p.rule, sc[j][2 * hr + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float2 x = cap_16bit(p.rule, make_float2(sc[j][2 * hr], sc[j][2 * hr + 1]));
+            sc[j][2 * hr] = x.x;
+            sc[j][2 * hr + 1] = x.y;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          sc[j][2 * hr] *= p.rule.scale_log2;
+          sc[j][2 * hr + 1] *= p.rule.scale_log2;
+        }
       }
+      if (p.rule.slopes) {
+        const float far = (float)(pos[hr] - t0 - 2 * t4);  // distance of the lane's first key
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            sc[j][2 * hr + e] = fmaf(-slope[hr], far - (float)(8 * j + e), sc[j][2 * hr + e]);
+      }
+    }
+    if (valid < kDecodeTile) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (8 * j + 2 * t4 + (e & 1) >= valid) sc[j][e] = -CUDART_INF_F;
+    }
     if (lg) {
 #pragma unroll
       for (int j = 0; j < 2; ++j)

@@ -124,6 +124,20 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
   const int s0 = min(rank * seg, n_old), len = min(seg, n_old - s0);
   const float *ws = w + s0;
   auto key = [&](int i) { return i < kCacheKeys ? keys[i] : weight_key(ws[i]); };
+  // four consecutive keys, i a multiple of 4 (behind the end: 0, which no key
+  // is: the least, -inf, is 0x007fffff)
+  auto keys4 = [&](int i, int end, uint32_t (&k)[4]) {
+    if (i + 3 < min(end, kCacheKeys)) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(&keys[i]);
+      k[0] = x.x;
+      k[1] = x.y;
+      k[2] = x.z;
+      k[3] = x.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) k[j] = i + j < end ? key(i + j) : 0u;
+    }
+  };
   __syncthreads();
   // ---- the stretch into shared memory, counted by the leading 11 bits ----
   constexpr int kUnroll = 8;
@@ -150,12 +164,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
     if (round > 0) {
       for (int b = tid; b < kBins; b += kSelThreads) hist[b] = 0;
       __syncthreads();
-#pragma unroll 4
-      for (int i0 = 0; i0 < len; i0 += kSelThreads) {
-        const int i = i0 + tid;
-        const uint32_t k = i < len ? key(i) : 0u;
-        count_bin(hist, i < len && (k >> (shift + bits)) == prefix,
-                  (k >> shift) & ((1u << bits) - 1));
+#pragma unroll 2
+      for (int i0 = 0; i0 < len; i0 += 4 * kSelThreads) {
+        uint32_t k[4];
+        keys4(i0 + 4 * tid, len, k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // (0, behind the end, is of no key: it may only be counted where
+          // the cut's leading bits are 0 themselves)
+          const bool in = (k[j] >> (shift + bits)) == prefix && k[j] != 0;
+          const uint32_t bin = (k[j] >> shift) & ((1u << bits) - 1);
+          if (__popc(__ballot_sync(0xffffffffu, in)) > 8) count_bin(hist, in, bin);
+          else if (in) atomicAdd(&hist[bin], 1u);
+        }
       }
     }
     cluster_sync();  // every CTA's histogram is complete
@@ -204,25 +225,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
   // first `need`.  Every warp counts, then places, a stretch of its own.
   const int wlen = ((len + kSelThreads / 32 - 1) / (kSelThreads / 32) + 127) & ~127;
   const int w0 = min(warp * wlen, len), w1 = min(w0 + wlen, len);
-  // four consecutive keys per lane (behind the end: 0, which no key is: the
-  // least, -inf, is 0x007fffff)
-  auto keys4 = [&](int i, uint32_t (&k)[4]) {
-    if (i + 3 < min(w1, kCacheKeys)) {
-      const uint4 x = *reinterpret_cast<const uint4 *>(&keys[i]);
-      k[0] = x.x;
-      k[1] = x.y;
-      k[2] = x.z;
-      k[3] = x.w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) k[j] = i + j < w1 ? key(i + j) : 0u;
-    }
-  };
   uint2 cnt = make_uint2(0, 0);
 #pragma unroll 2
   for (int i = w0 + 4 * lane; i < w1; i += 128) {
     uint32_t k[4];
-    keys4(i, k);
+    keys4(i, w1, k);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       cnt.x += k[j] > prefix;
@@ -250,7 +257,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
   for (int i0 = w0; i0 < w1; i0 += 128) {
     const int i = i0 + 4 * lane;
     uint32_t k[4], v = 0;  // (counts of up to 128: both in one word)
-    keys4(i, k);
+    keys4(i, w1, k);
 #pragma unroll
     for (int j = 0; j < 4; ++j) v += (k[j] > prefix ? 1u : 0u) + (k[j] == prefix ? 0x10000u : 0u);
     if (!__any_sync(0xffffffffu, v != 0)) continue;
@@ -261,13 +268,16 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
       if (lane >= o) inc += x;
     }
     uint32_t g = gt + ((inc - v) & 0xffffu), e = eq + ((inc - v) >> 16);
+    float x[4];  // (all four on their way before the first is stored)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = kw && k[j] >= prefix ? __ldg(ws + i + j) : 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const bool more = k[j] > prefix, tie = k[j] == prefix;
       if (more || (tie && e < need)) {
         const uint32_t at = g + min(e, need);
         kept[at] = s0 + i + j;
-        if (kw) kw[at] = __ldg(ws + i + j);
+        if (kw) kw[at] = x[j];
       }
       g += more;
       e += tie;
@@ -290,6 +300,24 @@ struct F8 {
 template <typename T> __device__ __forceinline__ float elem_key(T x) { return (float)x; }
 template <> __device__ __forceinline__ float elem_key<F8>(F8 x) { return (float)e4m3_key(x.v); }
 
+// Two elements at once, and what no element is above or below.
+template <typename T> struct Pair;
+template <> struct Pair<__half> {
+  using type = __half2;
+  static __device__ __forceinline__ __half2 limit(bool low) {
+    return __half2half2(__ushort_as_half(low ? 0xfc00 : 0x7c00));
+  }
+};
+template <> struct Pair<__nv_bfloat16> {
+  using type = __nv_bfloat162;
+  static __device__ __forceinline__ __nv_bfloat162 limit(bool low) {
+    return __bfloat162bfloat162(__ushort_as_bfloat16(low ? 0xff80 : 0x7f80));
+  }
+};
+template <> struct Pair<F8> {
+  using type = F8;
+};
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kCopyThreads, 5) evict_copy_kernel(
     const __grid_constant__ EvictParams p) {
@@ -297,7 +325,7 @@ __global__ void __launch_bounds__(kCopyThreads, 5) evict_copy_kernel(
   constexpr int kStep = kCopyThreads / kLanes;          // rows at once
   constexpr int kIter = kCopyRows / kStep;
   __shared__ uint4 krows[kCopyRows * kLanes];
-  __shared__ T ends[kCopyRows / 16][2][D];
+  __shared__ __align__(16) T ends[kCopyRows / 16][2][D];
   const int tid = threadIdx.x, groups = (p.keep + kCopyRows - 1) / kCopyRows;
   const int unit = blockIdx.x / groups, r0 = blockIdx.x % groups * kCopyRows;
   const int seq = unit / p.Hkv, hk = unit % p.Hkv;
@@ -315,12 +343,13 @@ __global__ void __launch_bounds__(kCopyThreads, 5) evict_copy_kernel(
   // row t of a page list, or the largest value if the check fails
   constexpr uint32_t kNone = 0xffffffffu;
   auto row_at = [&](const int *pages, int t, int slot) -> uint32_t {
-    const int blk = t / p.P, phys = t >= 0 && blk < p.max_pp ? pages[blk] : -1;
+    const int blk = p.P_log2 >= 0 ? t >> p.P_log2 : t / p.P;
+    const int phys = t >= 0 && blk < p.max_pp ? pages[blk] : -1;
     if (phys < 0 || phys >= p.num_phys) {
       ev_set_err(p.err, kDevBadPhys, slot, t, phys);
       return kNone;
     }
-    return (uint32_t)(phys * p.Hkv + hk) * (uint32_t)p.P + (uint32_t)(t % p.P);
+    return (uint32_t)(phys * p.Hkv + hk) * (uint32_t)p.P + (uint32_t)(t - blk * p.P);
   };
   uint32_t from[kIter], to[kIter];
 #pragma unroll
@@ -348,34 +377,76 @@ __global__ void __launch_bounds__(kCopyThreads, 5) evict_copy_kernel(
       ko[at] = kx[i];
       vo[at] = vx[i];
     }
-    krows[(i * kStep + sub) * kLanes + lane] = kx[i];
   }
-  __syncthreads();
   // metadata of the logical pages that begin in these rows (64 rows hold whole
   // ones): least and greatest of each channel per 16 rows, then per page
   T *meta = static_cast<T *>(p.meta);
-  const T *rows = reinterpret_cast<const T *>(krows);
   const int parts = (n + 15) / 16;
-  for (int x = tid; x < parts * D; x += kCopyThreads) {
-    const int j = x / D, c = x % D, m = min(16, n - 16 * j);
-    T lo = rows[16 * j * D + c], hi = lo;
-    float flo = elem_key(lo), fhi = flo;
+  if constexpr (sizeof(T) == 2) {
+    // rows of a warp first, in registers, then the warps that share a part
+    using T2 = typename Pair<T>::type;
+    constexpr int kWarpRows = 32 / kLanes, kPerPart = 16 / kWarpRows;  // warps per 16 rows
+    const T2 top = Pair<T>::limit(false), bottom = Pair<T>::limit(true);
 #pragma unroll
-    for (int r = 1; r < 16; ++r) {
-      if (r >= m) break;
-      const T e = rows[(16 * j + r) * D + c];
-      const float f = elem_key(e);
-      if (f < flo) {
-        flo = f;
-        lo = e;
+    for (int i = 0; i < kIter; ++i) {
+      const int r = i * kStep + sub;
+      T2 lo[4], hi[4];
+      const T2 *x = reinterpret_cast<const T2 *>(&kx[i]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        lo[e] = r < n ? x[e] : top;
+        hi[e] = r < n ? x[e] : bottom;
+#pragma unroll
+        for (int o = kLanes; o < 32; o <<= 1) {
+          lo[e] = __hmin2(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], o));
+          hi[e] = __hmax2(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], o));
+        }
       }
-      if (f > fhi) {
-        fhi = f;
-        hi = e;
+      if ((tid & 31) < kLanes) {
+        uint4 *to = krows + ((i * (kCopyThreads / 32) + (tid >> 5)) * 2) * kLanes + lane;
+        to[0] = *reinterpret_cast<const uint4 *>(lo);
+        to[kLanes] = *reinterpret_cast<const uint4 *>(hi);
       }
     }
-    ends[j][0][c] = lo;
-    ends[j][1][c] = hi;
+    __syncthreads();
+    // entry w of krows: rows w kWarpRows ..; part j: entries j kPerPart ..
+    for (int x = tid; x < parts * 2 * kLanes; x += kCopyThreads) {
+      const int j = x / (2 * kLanes), which = x / kLanes & 1, ln = x % kLanes;
+      uint4 v = krows[(j * kPerPart * 2 + which) * kLanes + ln];
+      T2 *m = reinterpret_cast<T2 *>(&v);
+#pragma unroll
+      for (int w = 1; w < kPerPart; ++w) {
+        const uint4 y = krows[((j * kPerPart + w) * 2 + which) * kLanes + ln];
+        const T2 *ym = reinterpret_cast<const T2 *>(&y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m[e] = which ? __hmax2(m[e], ym[e]) : __hmin2(m[e], ym[e]);
+      }
+      *reinterpret_cast<uint4 *>(&ends[j][which][ln * 8]) = v;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) krows[(i * kStep + sub) * kLanes + lane] = kx[i];
+    __syncthreads();
+    const T *rows = reinterpret_cast<const T *>(krows);
+    for (int x = tid; x < parts * D; x += kCopyThreads) {
+      const int j = x / D, c = x % D, m = min(16, n - 16 * j);
+      T lo = rows[16 * j * D + c], hi = lo;
+      float flo = elem_key(lo), fhi = flo;
+      for (int r = 1; r < m; ++r) {
+        const T e = rows[(16 * j + r) * D + c];
+        const float f = elem_key(e);
+        if (f < flo) {
+          flo = f;
+          lo = e;
+        }
+        if (f > fhi) {
+          fhi = f;
+          hi = e;
+        }
+      }
+      ends[j][0][c] = lo;
+      ends[j][1][c] = hi;
+    }
   }
   __syncthreads();
   const int pages = (n + p.ell - 1) / p.ell, ppg = p.ell / 16;
