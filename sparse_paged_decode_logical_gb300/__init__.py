@@ -506,7 +506,7 @@ class SparsePagedKVCache:
         if out is None:
             out = t.empty((n, self.Hq, self.d), dtype=out_dtype, device=self.device)
         op = self._ptr(out, (n, self.Hq, self.d), out_dtype)
-        rule = _rule(scale, softcap, slopes, self.Hq, self.device)
+        rule = _rule(scale, softcap, slopes, self.Hq, self._dev_index)
         w_in = w_out = None
         stride = 0
         if weights_out is not None:
@@ -519,16 +519,15 @@ class SparsePagedKVCache:
         elif weights_in is not None:
             raise ValueError("weights_in needs weights_out")
         ws = ctypes.c_size_t()
-        st = lib().spd_shared_prefix_sizes(self.ctx, prefix_id, ids, n, w_out is not None,
-                                           ctypes.byref(ws))
+        L = lib()
+        st = L.spd_shared_prefix_sizes(self.ctx, prefix_id, ids, n, w_out is not None, ws)
         if st != SPD_OK:
             _check(st, "spd_shared_prefix_sizes", self.ctx)
-        raw = self._stream(stream)
-        work = _workspace(t, ws.value, self.device, raw, stream)
-        st = lib().spd_shared_prefix_attention(
-            self.ctx, qp, prefix_id, ids, n, ctypes.byref(rule),
-            0 if out_dtype == t.float32 else 1, op, w_in, w_out, stride, work.data_ptr(),
-            ws.value, raw or None)
+        nbytes, raw = ws.value, self._stream(stream)
+        work = _workspace(t, nbytes, self.device, raw, stream)
+        st = L.spd_shared_prefix_attention(
+            self.ctx, qp, prefix_id, ids, n, rule, 0 if out_dtype == t.float32 else 1, op, w_in,
+            w_out, stride, work.data_ptr(), nbytes, raw or None)
         if st != SPD_OK:
             _check(st, "spd_shared_prefix_attention", self.ctx)
         return out
@@ -614,13 +613,13 @@ def prefill_block_sparse_attention(q, k, v, w_q, w_k, block=64, token_budget=409
 
 # ---- dense attention with score rules ------------------------------------------
 
-def _rule(scale, softcap, slopes, num_q_heads, device):
-    import torch
+def _rule(scale, softcap, slopes, num_q_heads, device_index):
     if slopes is not None:
-        if slopes.dtype != torch.float32 or tuple(slopes.shape) != (num_q_heads,) \
-                or not slopes.is_contiguous() or slopes.device != device:
-            raise ValueError("slopes must be a contiguous fp32 [%d] tensor on %s"
-                             % (num_q_heads, device))
+        import torch
+        if slopes.dtype != torch.float32 or slopes.shape != (num_q_heads,) \
+                or not slopes.is_contiguous() or slopes.get_device() != device_index:
+            raise ValueError("slopes must be a contiguous fp32 [%d] tensor on cuda:%d"
+                             % (num_q_heads, device_index))
         slopes = slopes.data_ptr()
     return spd_score_rule(float(scale or 0.0), float(softcap or 0.0), slopes)
 
@@ -635,13 +634,53 @@ def _workspace(torch, nbytes, device, raw, stream):
     return work
 
 
+# What a prompt call's shapes, types and scalars decide, by them: the checked
+# configuration and the workspace's size.
+_prompt_plans = {}
+
+
+def _prompt_plan(q, k, v, out_dtype, scale, softcap):
+    import torch
+    if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape:
+        raise ValueError("q must be [Lq][Hq][d], k and v [Lk][Hkv][d]")
+    Lq, Hq, d = q.shape
+    Lk, Hkv, dk = k.shape
+    dt = q.dtype
+    if dt not in (torch.float16, torch.bfloat16) or k.dtype != dt or v.dtype != dt or dk != d:
+        raise ValueError("q, k, v must share one dtype, fp16 or bf16, and head_dim")
+    if q.device.type != "cuda":
+        raise ValueError("q, k, v must be on one CUDA device")
+    if out_dtype is None:
+        out_dtype = torch.float32
+    if out_dtype not in (torch.float32, dt):
+        raise ValueError("out_dtype must be torch.float32 or %s" % dt)
+    cfg = spd_dense_config(Hq, Hkv, d, 1 if dt == torch.bfloat16 else 0,
+                           0 if out_dtype == torch.float32 else 1,
+                           _rule(scale, softcap, None, Hq, None))
+    ws = ctypes.c_size_t()
+    with torch.cuda.device(q.device):
+        _check(lib().spd_prefill_attention_sizes(ctypes.byref(cfg), Lq, Lk, ctypes.byref(ws)),
+               "spd_prefill_attention_sizes")
+    return torch, cfg, ws.value, (Lq, Hq, d), out_dtype, Lq, Lk
+
+
+def _raw_stream(torch, device_index, stream):
+    """The address of `stream`, by default of the device's current one."""
+    if stream is None:
+        query = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if query is not None:
+            return query(device_index)
+        stream = torch.cuda.current_stream(device_index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def _token_stride(t, name):
     """Elements between the rows of a [tokens][heads][d] tensor."""
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    n, heads, d = t.shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != d):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
-    if t.shape[0] == 1:
-        return t.shape[1] * t.shape[2]
-    return t.stride(0)
+    return heads * d if n == 1 else s0
 
 
 def prefill_attention(q, k, v, key_begin=None, key_end=None, scale=0.0, softcap=0.0, slopes=None,
@@ -656,50 +695,44 @@ def prefill_attention(q, k, v, key_begin=None, key_end=None, scale=0.0, softcap=
     [Hq] bias them by distance.  Returns out [Lq][Hq][d], fp32 or (out_dtype)
     the type of q.  check=True waits and raises if a kernel's own check
     tripped."""
-    import torch
-    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
-        raise ValueError("q, k, v must be [tokens][heads][head_dim]")
-    Lq, Hq, d = q.shape
-    Lk, Hkv, _ = k.shape
-    dt, dev = q.dtype, q.device
-    if dt not in (torch.float16, torch.bfloat16) or k.dtype != dt or v.dtype != dt:
-        raise ValueError("q, k, v must share one dtype, fp16 or bf16")
-    if dev.type != "cuda" or k.device != dev or v.device != dev:
+    dev = q.get_device()
+    key = (q.shape, k.shape, v.shape, q.dtype, k.dtype, v.dtype, out_dtype, scale, softcap, dev)
+    plan = _prompt_plans.get(key)
+    if plan is None:
+        plan = _prompt_plan(q, k, v, out_dtype, scale, softcap)
+        if len(_prompt_plans) >= 4096:
+            _prompt_plans.clear()
+        _prompt_plans[key] = plan
+    torch, cfg, nbytes, shape, odt, Lq, Lk = plan
+    if k.get_device() != dev or v.get_device() != dev:
         raise ValueError("q, k, v must be on one CUDA device")
-    if tuple(k.shape) != (Lk, Hkv, d) or tuple(v.shape) != (Lk, Hkv, d):
-        raise ValueError("k and v must be [Lk][Hkv][%d]" % d)
-    if (key_begin is None) != (key_end is None):
-        raise ValueError("key_begin and key_end come together")
-    for t in (key_begin, key_end):
-        if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != (Lq,)
-                              or not t.is_contiguous() or t.device != dev):
-            raise ValueError("key_begin and key_end must be contiguous int32 [%d] on %s" % (Lq, dev))
-    if out_dtype is None:
-        out_dtype = torch.float32 if out is None else out.dtype
-    if out_dtype not in (torch.float32, dt):
-        raise ValueError("out_dtype must be torch.float32 or %s" % dt)
+    kb = ke = None
+    if key_begin is not None or key_end is not None:
+        if key_begin is None or key_end is None:
+            raise ValueError("key_begin and key_end come together")
+        for t in (key_begin, key_end):
+            if t.dtype is not torch.int32 or t.shape != (Lq,) or t.get_device() != dev \
+                    or not t.is_contiguous():
+                raise ValueError("key_begin and key_end must be contiguous int32 [%d] on %s"
+                                 % (Lq, q.device))
+        kb, ke = key_begin.data_ptr(), key_end.data_ptr()
     if out is None:
-        out = torch.empty((Lq, Hq, d), dtype=out_dtype, device=dev)
-    elif out.dtype != out_dtype or tuple(out.shape) != (Lq, Hq, d) or not out.is_contiguous() \
-            or out.device != dev:
-        raise ValueError("out must be a contiguous %s tensor (%d, %d, %d) on %s"
-                         % (out_dtype, Lq, Hq, d, dev))
-    cfg = spd_dense_config(Hq, Hkv, d, 1 if dt == torch.bfloat16 else 0,
-                           0 if out_dtype == torch.float32 else 1,
-                           _rule(scale, softcap, slopes, Hq, dev))
-    ws = ctypes.c_size_t()
-    st = lib().spd_prefill_attention_sizes(ctypes.byref(cfg), Lq, Lk, ctypes.byref(ws))
-    if st != SPD_OK:
-        _check(st, "spd_prefill_attention_sizes")
-    raw = torch.cuda.current_stream(dev).cuda_stream if stream is None else (
-        stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
-    work = _workspace(torch, ws.value, dev, raw, stream) if ws.value else None
+        out = torch.empty(shape, dtype=odt, device=q.device)
+    else:
+        if out_dtype is None and out.dtype is not odt:
+            return prefill_attention(q, k, v, key_begin, key_end, scale, softcap, slopes, out.dtype,
+                                     out, stream, check)
+        if out.dtype is not odt or out.shape != shape or not out.is_contiguous() \
+                or out.get_device() != dev:
+            raise ValueError("out must be a contiguous %s tensor %s on %s" % (odt, shape, q.device))
+    if slopes is not None:  # (the kept configuration is shared: this one is the call's own)
+        cfg = spd_dense_config(cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim, cfg.dtype, cfg.out,
+                               _rule(scale, softcap, slopes, cfg.num_q_heads, dev))
+    raw = _raw_stream(torch, dev, stream)
+    work = _workspace(torch, nbytes, q.device, raw, stream).data_ptr() if nbytes else None
     st = lib().spd_prefill_attention(
-        ctypes.byref(cfg), Lq, Lk, q.data_ptr(), _token_stride(q, "q"), k.data_ptr(),
-        _token_stride(k, "k"), v.data_ptr(), _token_stride(v, "v"),
-        key_begin.data_ptr() if key_begin is not None else None,
-        key_end.data_ptr() if key_end is not None else None, out.data_ptr(),
-        work.data_ptr() if work is not None else None, ws.value, raw or None)
+        cfg, Lq, Lk, q.data_ptr(), _token_stride(q, "q"), k.data_ptr(), _token_stride(k, "k"),
+        v.data_ptr(), _token_stride(v, "v"), kb, ke, out.data_ptr(), work, nbytes, raw or None)
     if st != SPD_OK:
         _check(st, "spd_prefill_attention")
     if check:
@@ -722,8 +755,7 @@ def document_key_ranges(offsets, n_tokens, prefix=None, stream=None):
                              "contiguous, on one CUDA device")
     kb = torch.empty(int(n_tokens), dtype=torch.int32, device=dev)
     ke = torch.empty(int(n_tokens), dtype=torch.int32, device=dev)
-    raw = torch.cuda.current_stream(dev).cuda_stream if stream is None else (
-        stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    raw = _raw_stream(torch, dev.index, stream)
     _check(lib().spd_document_key_ranges(
         offsets.data_ptr(), prefix.data_ptr() if prefix is not None else None, n, int(n_tokens),
         kb.data_ptr(), ke.data_ptr(), raw or None), "spd_document_key_ranges")

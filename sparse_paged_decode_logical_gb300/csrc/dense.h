@@ -53,8 +53,10 @@ struct DenseTcParams {
   CUtensorMap tm_q;        // {64, d / 64, Hq, tokens}, box {64, 1, HP, 128 / HP}
   CUtensorMap tm_k, tm_v;  // prompt: {64, d / 64, Hkv, Lk}, box {64, 1, 1, 64};
                            // paged: {64, P, d / 64, planes}, box {64, box_rows, 1, 1}
-  void *out;               // [Lq][Hq][d]; null: partials
-  float *part_o;           // [unit][split][256][d]
+  CUtensorMap tm_out;      // final: {64 (fp32: 32), .., Hq, Lq}, box {.., 1, HP, 32 / HP};
+                           // partials [unit][split][256][d]: {32, d / 32, 1, rows}, box {32, 1, 1, 32}
+  int partial;             // splits: unnormalised sums to tm_out, statistics to part_ml
+  const float *part_o;     // the partials (combining kernel)
   float2 *part_ml;         // [unit][split][256]  (row max in base-2 units, sum)
   const void *v;           // prompt: V itself (rows at v_stride elements), for non-finite values
   long long v_stride;
@@ -66,6 +68,7 @@ struct DenseTcParams {
   int out_f32;             // type of out
   int Lq, Lk, Hq, Hkv, G, lhp, HG;  // HP = 2^lhp heads per matrix, HG = G / HP head groups
   int tiles, nsplit;
+  int pair_s;              // plain scores, 16-bit output: S of two blocks in one product
   int dup;                 // both matrices hold the same 128 rows and take turns at the keys
   int P, max_pp, num_phys, box_rows;
   int pos0;                // prompt: position of query 0 (Lk - Lq)

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -57,9 +58,15 @@ bool device_of(const void *p, int *device) {
 }
 
 int sm_count(int device) {
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n < 1)
-    n = 152;
+  static std::atomic<int> known[64];
+  const bool keep = device >= 0 && device < 64;
+  int n = keep ? known[device].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    return 152;
+  }
+  if (keep) known[device].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -76,26 +83,39 @@ PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   return encode;
 }
 
-// 4-D map of 16-bit elements, 64 channels per row of a box, 128-byte swizzle.
-bool encode4(CUtensorMap *m, spd_dtype t, const void *base, const cuuint64_t (&dims)[4],
+// 4-D map, boxes of 128-byte rows, 128-byte swizzle.
+bool encode4(CUtensorMap *m, CUtensorMapDataType t, const void *base, const cuuint64_t (&dims)[4],
              const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4]) {
   const auto encode = map_encoder();
   if (!encode) return false;
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return encode(m, t == SPD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                4, const_cast<void *>(base), dims, strides, box, estr,
+  return encode(m, t, 4, const_cast<void *>(base), dims, strides, box, estr,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
 
-// Rows [tokens][heads][d] at `stride` elements, boxes of `bh` heads x `bt` tokens.
-bool encode_rows(CUtensorMap *m, spd_dtype t, const void *base, int d, int heads, int tokens,
-                 long long stride, int bh, int bt) {
-  const cuuint64_t dims[4] = {64, (cuuint64_t)d / 64, (cuuint64_t)heads, (cuuint64_t)tokens};
-  const cuuint64_t strides[3] = {128, (cuuint64_t)d * 2, (cuuint64_t)stride * 2};
-  const cuuint32_t box[4] = {64, 1, (cuuint32_t)bh, (cuuint32_t)bt};
+CUtensorMapDataType map_type(spd_dtype t) {
+  return t == SPD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+
+// Rows [tokens][heads][d] at `stride` elements, boxes of `bh` heads x `bt`
+// tokens x 128 bytes of channels.
+bool encode_rows(CUtensorMap *m, CUtensorMapDataType t, const void *base, int d, int heads,
+                 int tokens, long long stride, int bh, int bt) {
+  const cuuint64_t e = t == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2, c = 128 / e;
+  const cuuint64_t dims[4] = {c, (cuuint64_t)d / c, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[3] = {128, (cuuint64_t)d * e, (cuuint64_t)stride * e};
+  const cuuint32_t box[4] = {(cuuint32_t)c, 1, (cuuint32_t)bh, (cuuint32_t)bt};
   return encode4(m, t, base, dims, strides, box);
+}
+
+// Partial sums [rows][d] fp32 in boxes of a warp's 32 rows.
+bool encode_partials(CUtensorMap *m, const float *base, int d, size_t rows) {
+  const cuuint64_t dims[4] = {32, (cuuint64_t)d / 32, 1, (cuuint64_t)rows};
+  const cuuint64_t strides[3] = {128, (cuuint64_t)d * 4, (cuuint64_t)d * 4};
+  const cuuint32_t box[4] = {32, 1, 1, 32};
+  return encode4(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, dims, strides, box);
 }
 
 const char *check_rule(const spd_score_rule *r) {
@@ -124,6 +144,10 @@ ScoreRule make_rule(const spd_score_rule *r, int d) {
   x.slopes = r ? r->slopes : nullptr;
   return x;
 }
+
+// Rows at least this long take S of two blocks in one product (4,096 packed
+// tokens: 67.6 us with, 65.6 without; 49,152 keys: 1,402 and 1,510).
+constexpr int kPairKeys = 8192;
 
 // ---- prompt attention ------------------------------------------------------------
 
@@ -310,9 +334,8 @@ spd_status spd_prefill_attention_sizes(const spd_dense_config *cfg, int q_len, i
                                        size_t *workspace_bytes) {
   PromptPlan z;
   int device = 0;
-  (void)cudaGetDevice(&device);
+  if (cudaGetDevice(&device) != cudaSuccess) (void)cudaGetLastError();
   const spd_status s = plan_prompt(cfg, q_len, kv_len, sm_count(device), &z);
-  (void)cudaGetLastError();
   if (s != SPD_OK) return s;
   if (workspace_bytes) *workspace_bytes = z.total;
   return SPD_OK;
@@ -348,12 +371,18 @@ spd_status spd_prefill_attention(const spd_dense_config *cfg, int q_len, int kv_
   if ((s = guard.bind(device)) != SPD_OK) return s;
   DenseTcParams p{};
   const int d = cfg->head_dim;
-  if (!encode_rows(&p.tm_q, cfg->dtype, q, d, cfg->num_q_heads, q_len, q_stride, z.HP, 128 / z.HP) ||
-      !encode_rows(&p.tm_k, cfg->dtype, k, d, cfg->num_kv_heads, kv_len, k_stride, 1, kDenseBlock) ||
-      !encode_rows(&p.tm_v, cfg->dtype, v, d, cfg->num_kv_heads, kv_len, v_stride, 1, kDenseBlock))
+  const CUtensorMapDataType mt = map_type(cfg->dtype);
+  float *part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + z.po);
+  if (!encode_rows(&p.tm_q, mt, q, d, cfg->num_q_heads, q_len, q_stride, z.HP, 128 / z.HP) ||
+      !encode_rows(&p.tm_k, mt, k, d, cfg->num_kv_heads, kv_len, k_stride, 1, kDenseBlock) ||
+      !encode_rows(&p.tm_v, mt, v, d, cfg->num_kv_heads, kv_len, v_stride, 1, kDenseBlock) ||
+      !(z.partial ? encode_partials(&p.tm_out, part_o, d,
+                                    (size_t)z.tiles * cfg->num_kv_heads * z.HG * z.nsplit * kDenseRows)
+                  : encode_rows(&p.tm_out, cfg->out == SPD_OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : mt,
+                                out, d, cfg->num_q_heads, q_len, qrow, z.HP, 32 / z.HP)))
     return SPD_ERR_CUDA;
-  p.out = z.partial ? nullptr : out;
-  p.part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + z.po);
+  p.partial = z.partial;
+  p.part_o = part_o;
   p.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + z.pml);
   p.v = v;
   p.v_stride = v_stride;
@@ -372,6 +401,7 @@ spd_status spd_prefill_attention(const spd_dense_config *cfg, int q_len, int kv_
   p.nsplit = z.nsplit;
   p.dup = z.dup;
   p.pos0 = kv_len - q_len;
+  p.pair_s = kv_len >= kPairKeys;
   cudaStream_t st = (cudaStream_t)stream;
   if (launch_dense_tc(p, cfg->dtype, d, p.out_f32 != 0, st) != cudaSuccess) return SPD_ERR_CUDA;
   if (z.partial && launch_dense_prompt_combine(p, cfg->dtype, d, out, st) != cudaSuccess)
@@ -415,7 +445,6 @@ spd_status spd_shared_prefix_sizes(spd_ctx *c, int prefix_id, const int *seq_ids
   const spd_status r = check_shared(c, v, prefix_id, seq_ids, n_seqs);
   if (r != SPD_OK) return r;
   v.num_sms = sm_count(v.device);
-  (void)cudaGetLastError();
   *workspace_bytes = shared_bytes(c, v, prefix_id, seq_ids, n_seqs, weights != 0);
   return SPD_OK;
 }
@@ -448,7 +477,9 @@ spd_status spd_shared_prefix_attention(spd_ctx *c, const void *q, int prefix_id,
     return fail_message(c, SPD_ERR_INVALID_ARG, "workspace must be a 256-byte aligned pointer");
   cudaStream_t st = (cudaStream_t)stream;
   if ((r = ctx_device(c, st, &v)) != SPD_OK) return r;
-  if (workspace_bytes < shared_bytes(c, v, prefix_id, seq_ids, n_seqs, weights_out != nullptr))
+  // (a call of one launch is held to the plan that it uses, below)
+  if (n_seqs > kDenseSeqs &&
+      workspace_bytes < shared_bytes(c, v, prefix_id, seq_ids, n_seqs, weights_out != nullptr))
     return fail_message(c, SPD_ERR_CAPACITY, "workspace is smaller than spd_shared_prefix_sizes");
   DeviceGuard guard;
   if ((r = guard.bind(v.device)) != SPD_OK) return fail_message(c, r, "cudaSetDevice failed");
@@ -461,6 +492,8 @@ spd_status spd_shared_prefix_attention(spd_ctx *c, const void *q, int prefix_id,
     const int n = std::min(kDenseSeqs, n_seqs - b);
     SharedPlan z;
     plan_shared(c, v, lp, seq_ids + b, n, weights_out != nullptr, p.seqs, &z);
+    if (workspace_bytes < z.total)
+      return fail_message(c, SPD_ERR_CAPACITY, "workspace is smaller than spd_shared_prefix_sizes");
     const char *qb = static_cast<const char *>(q) + (size_t)b * cfg.num_q_heads * d * 2;
     const size_t oe = out_type == SPD_OUT_F32 ? 4 : 2;
     p.tm_k = *v.tm_k;
@@ -507,12 +540,16 @@ spd_status spd_shared_prefix_attention(spd_ctx *c, const void *q, int prefix_id,
                                   (cuuint64_t)cfg.num_physical_pages * cfg.num_kv_heads};
       const cuuint64_t strides[3] = {(cuuint64_t)d * 2, 128, (cuuint64_t)cfg.physical_page * d * 2};
       const cuuint32_t box[4] = {64, (cuuint32_t)br, 1, 1};
-      if (!encode_rows(&t.tm_q, cfg.dtype, qb, d, cfg.num_q_heads, n,
-                       (long long)cfg.num_q_heads * d, v.G, 128 / v.G) ||
-          !encode4(&t.tm_k, cfg.dtype, v.buf->k_pool, dims, strides, box) ||
-          !encode4(&t.tm_v, cfg.dtype, v.buf->v_pool, dims, strides, box))
+      const CUtensorMapDataType mt = map_type(cfg.dtype);
+      if (!encode_rows(&t.tm_q, mt, qb, d, cfg.num_q_heads, n, (long long)cfg.num_q_heads * d, v.G,
+                       128 / v.G) ||
+          !encode4(&t.tm_k, mt, v.buf->k_pool, dims, strides, box) ||
+          !encode4(&t.tm_v, mt, v.buf->v_pool, dims, strides, box) ||
+          !encode_partials(&t.tm_out, p.pre_o, d,
+                           (size_t)z.tiles * cfg.num_kv_heads * z.nsplit * kDenseRows))
         return fail_message(c, SPD_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-      t.out = nullptr;
+      t.partial = 1;
+      t.pair_s = 0;
       t.part_o = p.pre_o;
       t.part_ml = p.pre_ml;
       t.v = nullptr;

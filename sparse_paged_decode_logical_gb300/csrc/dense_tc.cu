@@ -21,8 +21,8 @@
 // other.  Where the softmax is the longer side (score rules, split weights)
 // that wins: 8,192 capped tokens 790 us against 954, 2,501 tokens of 64
 // channels with a bias and fp32 output 71 against 80.  Plain scores with 16-bit
-// output keep the tensor pipe busy and take one N 128 product per pair (kPairS):
-// 2,048 queries over 49,152 keys 1,402 us against 1,510.
+// output over a long row keep the tensor pipe busy and take one N 128 product
+// per pair (pair_s): 2,048 queries over 49,152 keys 1,402 us against 1,510.
 // Outputs of 32 bits (kSplitP) keep P as a 16-bit high part and the 16-bit
 // rounding of the rest, two products per block: P . V then holds about 16 bits
 // (bf16) or 22 (fp16) of each weight.  Outputs of 16 bits round P once, which
@@ -68,7 +68,7 @@ struct DtSmem {
   static constexpr int kBars = kV + kStages * kStageBytes;
   // mbarriers: Q; per stage K full, V full, V scanned, K empty, V empty; per
   // matrix and buffer S full, P full; per matrix O done (per block), pair done
-  // (kPairS), O final, drain; matrix 0's first softmax.  Every waiter is at most
+  // (pair_s), O final, drain; matrix 0's first softmax.  Every waiter is at most
   // one completion behind the barrier that it polls by parity.
   static constexpr int kBarQ = 0;
   static constexpr int kBarKF = 1;
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
     dense_tc_kernel(const __grid_constant__ DenseTcParams p) {
   using Sm = DtSmem<D>;
   constexpr int KB = Sm::KB, S = Sm::kStages;
-  constexpr bool kPairS = !kRule && !kSplitP;
+  const bool pair_s = !kRule && !kSplitP && p.pair_s;
   extern __shared__ uint8_t dt_smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(dt_smem_raw) + 1023) & ~uintptr_t(1023));
@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
     prefetch_tmap(&p.tm_q);
     prefetch_tmap(&p.tm_k);
     prefetch_tmap(&p.tm_v);
+    prefetch_tmap(&p.tm_out);
   }
   tc_fence_before();
   __syncthreads();
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
       if (su == 0 && !(ok = wwait(&bars[Sm::kBarKF + s], (sp / S) & 1))) return;
       tc_fence_after();
       any = true;
-      const bool both = kPairS && 2 * sp + 1 < n;
+      const bool both = pair_s && 2 * sp + 1 < n;
       const uint64_t kt = dk + (uint64_t)((s * Sm::kStageBytes + su * 8192) >> 4);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
@@ -483,7 +484,7 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
       }
     };
     if (ok) issue_s();
-    if (ok && !kPairS) issue_s();
+    if (ok && !pair_s) issue_s();
     int i = 0, blocks = 0;  // pairs, blocks of this matrix so far
     for (int pp = 0; pp < np && ok; ++pp) {
       const int s = pp % S, nbk = min(2, n - 2 * pp);
@@ -502,12 +503,12 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
                              idesc_o, blocks > 0 || part > 0 || kk > 0);
         umma_commit_warp(&bars[Sm::kBarOD + m]);
         if (u == nbk - 1) {
-          if (kPairS) umma_commit_warp(&bars[Sm::kBarOP + m]);
+          if (pair_s) umma_commit_warp(&bars[Sm::kBarOP + m]);
           umma_commit_warp(&bars[Sm::kBarVE + s]);
           if (pp == last) umma_commit_warp(&bars[Sm::kBarOF + m]);
         }
-        if (sp < np && (!kPairS || u == nbk - 1)) {  // the next S goes where this P was
-          if (!(ok = kPairS ? wwait(&bars[Sm::kBarOP + m], i & 1)
+        if (sp < np && (!pair_s || u == nbk - 1)) {  // the next S goes where this P was
+          if (!(ok = pair_s ? wwait(&bars[Sm::kBarOP + m], i & 1)
                             : wwait(&bars[Sm::kBarOD + m], blocks & 1)))
             break;
           issue_s();
@@ -670,16 +671,19 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
       tc_fence_after();
     }
     if (ok) {
-      // ---- the warp's 32 rows, 32 channels at a time, through the matrix's Q
-      // tile (its products are done) so that rows leave in whole lines ----
+      // ---- the warp's 32 rows, 128 bytes of channels at a time, through the
+      // matrix's Q tile (its products are done) and from there by TMA, which
+      // leaves out the rows behind the last query ----
       const bool live = tok < p.Lq, empty = rend == 0;
       const bool fix = *reinterpret_cast<volatile int *>(misc + kMiscBad) && live && !empty;
       const size_t pr = ((size_t)unit * p.nsplit + split) * kDenseRows + m * 128 + row;
-      if (!p.out && live) p.part_ml[pr] = make_float2(m_run, empty ? 0.f : l_run);
-      const float inv = empty ? 0.f : p.out ? 1.f / l_run : 1.f;
-      const bool f32 = !p.out || p.out_f32;
-      uint8_t *stage = smem + Sm::kQ + m * KB * 16384 + (warp & 3) * 4096;  // [32][128 B]
-      const int row0 = row - lane, tok_m = tok0 + (p.dup ? 0 : m * tpm);
+      if (p.partial && live) p.part_ml[pr] = make_float2(m_run, empty ? 0.f : l_run);
+      const float inv = empty ? 0.f : p.partial ? 1.f : 1.f / l_run;
+      const bool f32 = p.partial || p.out_f32;
+      // two buffers of [32][128 B], 16-byte pieces swizzled by the row
+      uint8_t *stage = smem + Sm::kQ + m * KB * 16384 + (warp & 3) * (KB * 4096);
+      const int at_h = p.partial ? 0 : h0, at_row = p.partial ? (int)(pr - lane) : tok - (lane >> lhp);
+      int turn = 0;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t r[32];
@@ -709,41 +713,38 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
             }
           }
         }
-        // rows of 128 bytes (32 channels of fp32, or two turns of 16 bits), 16-byte
-        // pieces swizzled by the row
+        uint8_t *buf;
         if (f32) {
+          // (D 64 has one buffer of 4,096 bytes per warp)
+          if (turn >= KB) {
+            if (lane == 0) bulk_wait_read<KB - 1>();
+            __syncwarp();
+          }
+          buf = stage + (turn % KB) * 4096;
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<float4 *>(stage + swz128(lane, e)) =
+            *reinterpret_cast<float4 *>(buf + swz128(lane, e)) =
                 make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
         } else {
+          buf = stage + (c >> 1) * 4096;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4 *>(stage + swz128(lane, 4 * (c & 1) + e)) =
+            *reinterpret_cast<uint4 *>(buf + swz128(lane, 4 * (c & 1) + e)) =
                 make_uint4(Weights<T>::round(make_float2(f[8 * e], f[8 * e + 1])),
                            Weights<T>::round(make_float2(f[8 * e + 2], f[8 * e + 3])),
                            Weights<T>::round(make_float2(f[8 * e + 4], f[8 * e + 5])),
                            Weights<T>::round(make_float2(f[8 * e + 6], f[8 * e + 7])));
           if (!(c & 1)) continue;
         }
+        fence_proxy_async_smem();
         __syncwarp();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {  // four rows at once, eight lanes each
-          const int rr = 4 * e + (lane >> 3), ch = lane & 7, rm = row0 + rr;
-          const uint4 x = *reinterpret_cast<const uint4 *>(stage + swz128(rr, ch));
-          const int tk = tok_m + (rm >> lhp);
-          if (tk >= p.Lq) continue;
-          uint8_t *to;
-          if (!p.out)
-            to = reinterpret_cast<uint8_t *>(p.part_o + (pr - lane + rr) * D + 32 * c);
-          else
-            to = static_cast<uint8_t *>(p.out) +
-                 (((size_t)tk * p.Hq + h0 + (rm & ((1 << lhp) - 1))) * D + (f32 ? 32 * c : 32 * (c - 1))) *
-                     (f32 ? 4 : 2);
-          *reinterpret_cast<uint4 *>(to + 16 * ch) = x;
+        if (lane == 0) {
+          tma_store_4d(&p.tm_out, buf, 0, f32 ? c : c >> 1, at_h, at_row);
+          bulk_commit();
         }
-        __syncwarp();
+        ++turn;
       }
+      if (lane == 0) bulk_wait<0>();
     }
   }
   tc_fence_before();
