@@ -18,6 +18,7 @@ constexpr int kDenseRows = 256;      // query rows of one of its CTAs (two matri
 constexpr int kDenseSeqs = 256;      // sequences described per parameter block
 constexpr int kDecodeTile = 16;      // keys per tile of the decode kernel
 constexpr int kDecodeRows = 16;      // query rows of one of its work items
+constexpr int kFewKeys = 128;        // keys per step of dense_few
 constexpr int kDenseMaxSplits = 64;  // key splits of one unit
 constexpr int kOwnMaxSplits = 256;   // splits of one sequence's own tokens
 
@@ -99,8 +100,10 @@ struct DenseDecodeParams {
   void *out;               // [n][Hq][d], fp32 or T
   float *part_o;           // own items: [item][G][d]
   float2 *part_ml;         // [item][G]
-  float *pre_o;            // prefix: [unit][split][rows][d], rows = 256 (tensor cores; unit = kv
-  float2 *pre_ml;          //   head x tile) or 16 (decode kernel; unit = kv head x row group)
+  // prefix: [unit = row tile x kv head][split][prefix_rows][d], prefix_rows =
+  // 256 or 128 (dense_tc), n G (dense_few) or 16 (decode kernel)
+  float *pre_o;
+  float2 *pre_ml;
   float *logits;           // [n][Hkv][G][l_stride] base-2 scores of own tokens, or null
   const float *w_in;       // [n][Hkv][w_stride] or null
   float *w_out;
@@ -113,13 +116,18 @@ struct DenseDecodeParams {
   int prefix_slot, prefix_len, prefix_items, prefix_ns, prefix_tpi, prefix_rows;
   int own_items;
   int precise;             // outputs that show 2^-22 of the cap (fp32, weights)
-  int follow;              // the kernel before is this call's prefix kernel
+  int follow;              // the kernel before is another one of this call
   int w_chunks;            // weight CTAs per (sequence, kv head)
+  int box_rows;            // dense_few: rows of a box
   DecodeSeq seqs[kDenseSeqs];
 };
 static_assert(sizeof(DenseDecodeParams) <= 32764, "parameter block too large");
 
 cudaError_t launch_dense_decode(const DenseDecodeParams &p, int dtype, int d, cudaStream_t st);
+// The prefix's items alone, for 9 to 32 rows (p.prefix_rows = n G of them, one
+// unit per kv head) of 128 channels, on the tensor cores: tm_k, tm_v {64, P, 2,
+// planes}, boxes {64, box_rows, 1, 1}, tiles of kFewKeys.
+cudaError_t launch_dense_few(const DenseDecodeParams &p, int dtype, cudaStream_t st);
 cudaError_t launch_dense_decode_combine(const DenseDecodeParams &p, int dtype, int d,
                                         cudaStream_t st);
 
@@ -139,6 +147,7 @@ struct EvictParams {
   int P_log2;             // log2(P), -1 if P is no power of two
   EvictSeq seqs[kDenseSeqs];
 };
-cudaError_t launch_evict(const EvictParams &p, int dtype, int d, int cluster, cudaStream_t st);
+cudaError_t launch_evict(const EvictParams &p, int dtype, int d, int cluster, int sms,
+                         cudaStream_t st);
 
 }  // namespace spd

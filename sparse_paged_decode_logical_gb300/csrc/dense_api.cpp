@@ -201,30 +201,35 @@ spd_status plan_prompt(const spd_dense_config *c, int Lq, int Lk, int sms, Promp
 
 // ---- shared prefix ------------------------------------------------------------------
 
-// At most this many query rows (sequences x heads per kv head) go over the
-// prefix with the decode kernel, more with the tensor-core kernel.
-constexpr int kPrefixRowsDecode = 32;
+// Query rows (sequences x heads per kv head) of a prefix: up to kFewRows go
+// with the sequences' own tokens (dense_decode), up to kManyRows over dense_few
+// (128 channels; 64 stay with dense_decode), more over dense_tc.
+constexpr int kFewRows = 8, kManyRows = 32;
 
 struct SharedPlan {
-  bool tc = false;
-  int tiles = 0, nsplit = 0, dup = 0;          // tensor-core prefix
+  bool tc = false, few = false;                // the prefix by dense_tc, dense_few
+  bool own_first = false;                      // dense_few after the own tokens
+  int tiles = 0, nsplit = 0, dup = 0;          // dense_tc
   int prefix_items = 0, prefix_ns = 0, prefix_tpi = 1, prefix_rows = 0;
   int own_items = 0, longest = 0;
   size_t pre_o = 0, pre_ml = 0, part_o = 0, part_ml = 0, logits = 0, total = 0;
 };
 
-int tiles_of(long long tokens) { return (int)((tokens + kDecodeTile - 1) / kDecodeTile); }
-
-// The split of one launch's sequences.  The decode kernel runs two CTAs per SM;
-// an item gets the tiles that fill those evenly, at least two per warp.
+// The split of one launch's sequences: an item gets the tiles that fill the
+// CTAs that the GPU holds at once evenly, at least two per warp (of 16 keys) or
+// two (of 128).
 void plan_shared(const spd_ctx *c, const CtxView &v, int prefix_len, const int *ids, int n,
-                 bool weights, DecodeSeq *seqs, SharedPlan *z) {
+                 bool weights, bool f32, DecodeSeq *seqs, SharedPlan *z) {
   const int Hkv = v.cfg->num_kv_heads, d = v.cfg->head_dim, rows = n * v.G;
-  z->tc = prefix_len > 0 && rows > kPrefixRowsDecode;
-  const int pt = prefix_len > 0 && !z->tc ? tiles_of(prefix_len) : 0;
-  const int pu = pt > 0 ? Hkv * ((rows + kDecodeRows - 1) / kDecodeRows) : 0;
-  long long work = (long long)pu * pt;
-  int most = pt;
+  z->tc = prefix_len > 0 && rows > kManyRows;
+  z->few = prefix_len > 0 && !z->tc && rows > kFewRows && d == 128;
+  const int tk = z->few ? kFewKeys : kDecodeTile;  // keys per tile of the prefix
+  z->prefix_rows = z->few ? rows : kDecodeRows;
+  const int pt = prefix_len > 0 && !z->tc ? (prefix_len + tk - 1) / tk : 0;
+  const int pu = pt > 0 ? Hkv * ((rows + z->prefix_rows - 1) / z->prefix_rows) : 0;
+  auto tiles_of = [](int tokens) { return (tokens + kDecodeTile - 1) / kDecodeTile; };
+  int most = 0;
+  long long own_work = 0;
   z->longest = 0;
   for (int i = 0; i < n; ++i) {
     const int L = (int)seq_length(c, ids[i]), t = tiles_of(L);
@@ -232,36 +237,53 @@ void plan_shared(const spd_ctx *c, const CtxView &v, int prefix_len, const int *
     seqs[i].L = L;
     z->longest = std::max(z->longest, L);
     most = std::max(most, t);
-    work += (long long)Hkv * t;
+    own_work += (long long)Hkv * t;
   }
-  const long long slots = 2LL * v.num_sms;
-  auto items_for = [&](long long tpi) {
-    long long k = pu * ((pt + tpi - 1) / tpi);
-    for (int i = 0; i < n; ++i) k += Hkv * ((tiles_of(seqs[i].L) + tpi - 1) / tpi);
+  // the tiles per item: one wave if whole units leave room for it (the least
+  // that fit), else four finer ones
+  auto per_item = [&](long long work, int longest, int per_sm, int least, auto items_for) {
+    const long long slots = (long long)per_sm * v.num_sms;
+    int tpi = (int)std::max<long long>(least, (work + slots - 1) / slots);
+    if (items_for(std::max(longest, 1)) > slots)
+      return (int)std::max<long long>(least, (work + 4 * slots - 1) / (4 * slots));
+    int lo = tpi, hi = std::max(tpi, longest);
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (items_for(mid) <= slots) hi = mid;
+      else lo = mid + 1;
+    }
+    return lo;
+  };
+  auto pre_items = [&](int tpi) { return (long long)pu * ((pt + tpi - 1) / tpi); };
+  auto own_items = [&](int tpi) {
+    long long k = 0;
+    for (int i = 0; i < n; ++i) k += (long long)Hkv * ((tiles_of(seqs[i].L) + tpi - 1) / tpi);
     return k;
   };
-  long long tpi = std::max<long long>(8, (work + slots - 1) / slots);
-  // one wave if whole units leave room for it, else four finer ones
-  if (items_for(std::max(most, 1)) <= slots) {
-    while (tpi < most && items_for(tpi) > slots) tpi += std::max<long long>(1, tpi / 16);
+  const long long pre_work = (long long)pu * pt;
+  int tpi, tpi_pre = 1;
+  if (z->few) {
+    tpi = per_item(own_work, most, 2, 8, own_items);
+    tpi_pre = per_item(pre_work, pt, rows <= 16 && !f32 ? 3 : 2, 2, pre_items);
+    z->own_first = own_work * kDecodeTile < pre_work * kFewKeys;
   } else {
-    tpi = std::max<long long>(8, (work + 4 * slots - 1) / (4 * slots));
+    tpi = tpi_pre = per_item(pre_work + own_work, std::max(pt, most), 2, 8,
+                             [&](int x) { return pre_items(x) + own_items(x); });
   }
-  tpi = std::max<long long>(tpi, (most + kOwnMaxSplits - 1) / kOwnMaxSplits);
-  const long long tpi_pre = std::max<long long>(tpi, (pt + kDenseMaxSplits - 1) / kDenseMaxSplits);
-  z->prefix_tpi = (int)tpi_pre;
-  z->prefix_ns = pt > 0 ? (int)((pt + tpi_pre - 1) / tpi_pre) : 0;
+  tpi = std::max(tpi, (most + kOwnMaxSplits - 1) / kOwnMaxSplits);
+  tpi_pre = std::max(tpi_pre, (pt + kDenseMaxSplits - 1) / kDenseMaxSplits);
+  z->prefix_tpi = tpi_pre;
+  z->prefix_ns = pt > 0 ? (pt + tpi_pre - 1) / tpi_pre : 0;
   z->prefix_items = pu * z->prefix_ns;
-  z->prefix_rows = kDecodeRows;
   z->own_items = 0;
   for (int i = 0; i < n; ++i) {
     const int t = tiles_of(seqs[i].L);
     seqs[i].item_off = z->own_items;
-    seqs[i].ns = (int)((t + tpi - 1) / tpi);
-    seqs[i].tpi = (int)tpi;
+    seqs[i].ns = (t + tpi - 1) / tpi;
+    seqs[i].tpi = tpi;
     z->own_items += Hkv * seqs[i].ns;
   }
-  size_t pre_rows = (size_t)z->prefix_items * kDecodeRows;
+  size_t pre_rows = (size_t)z->prefix_items * z->prefix_rows;
   if (z->tc) {
     const int blocks = (prefix_len + kDenseBlock - 1) / kDenseBlock;
     z->dup = rows <= 128 && blocks >= 8 ? 1 : 0;
@@ -288,17 +310,19 @@ void plan_shared(const spd_ctx *c, const CtxView &v, int prefix_len, const int *
   z->total = off;
 }
 
-// Workspace of a whole call: its launches run one after the other in the same one.
+// Workspace of a whole call: its launches run one after the other in the same
+// one.  The type of the output may change the split: the larger of both.
 size_t shared_bytes(const spd_ctx *c, const CtxView &v, int prefix_id, const int *ids, int n,
                     bool weights) {
   DecodeSeq seqs[kDenseSeqs];
   size_t most = 0;
-  for (int b = 0; b < n; b += kDenseSeqs) {
-    SharedPlan z;
-    plan_shared(c, v, prefix_id >= 0 ? (int)seq_length(c, prefix_id) : 0, ids + b,
-                std::min(kDenseSeqs, n - b), weights, seqs, &z);
-    most = std::max(most, z.total);
-  }
+  for (int b = 0; b < n; b += kDenseSeqs)
+    for (int f32 = 0; f32 < 2; ++f32) {
+      SharedPlan z;
+      plan_shared(c, v, prefix_id >= 0 ? (int)seq_length(c, prefix_id) : 0, ids + b,
+                  std::min(kDenseSeqs, n - b), weights, f32 != 0, seqs, &z);
+      most = std::max(most, z.total);
+    }
   return most;
 }
 
@@ -491,7 +515,8 @@ spd_status spd_shared_prefix_attention(spd_ctx *c, const void *q, int prefix_id,
   for (int b = 0; b < n_seqs; b += kDenseSeqs) {
     const int n = std::min(kDenseSeqs, n_seqs - b);
     SharedPlan z;
-    plan_shared(c, v, lp, seq_ids + b, n, weights_out != nullptr, p.seqs, &z);
+    plan_shared(c, v, lp, seq_ids + b, n, weights_out != nullptr, out_type == SPD_OUT_F32, p.seqs,
+                &z);
     if (workspace_bytes < z.total)
       return fail_message(c, SPD_ERR_CAPACITY, "workspace is smaller than spd_shared_prefix_sizes");
     const char *qb = static_cast<const char *>(q) + (size_t)b * cfg.num_q_heads * d * 2;
@@ -528,23 +553,26 @@ spd_status spd_shared_prefix_attention(spd_ctx *c, const void *q, int prefix_id,
     p.prefix_tpi = z.prefix_tpi;
     p.prefix_rows = z.prefix_rows;
     p.own_items = z.own_items;
-    p.follow = z.tc;
     p.precise = p.out_f32 || weights_out;
     p.w_chunks = (z.longest + 1023) / 1024;
     int launches = 0;
     cudaError_t e = cudaSuccess;
-    if (z.tc) {
-      t.rule = p.rule;
-      const int br = cfg.physical_page % 64 == 0 ? 64 : cfg.physical_page % 32 == 0 ? 32 : 16;
+    const CUtensorMapDataType mt = map_type(cfg.dtype);
+    const int br = cfg.physical_page % 64 == 0 ? 64 : cfg.physical_page % 32 == 0 ? 32 : 16;
+    if (z.tc || z.few) {
       const cuuint64_t dims[4] = {64, (cuuint64_t)cfg.physical_page, (cuuint64_t)d / 64,
                                   (cuuint64_t)cfg.num_physical_pages * cfg.num_kv_heads};
       const cuuint64_t strides[3] = {(cuuint64_t)d * 2, 128, (cuuint64_t)cfg.physical_page * d * 2};
       const cuuint32_t box[4] = {64, (cuuint32_t)br, 1, 1};
-      const CUtensorMapDataType mt = map_type(cfg.dtype);
+      if (!encode4(&t.tm_k, mt, v.buf->k_pool, dims, strides, box) ||
+          !encode4(&t.tm_v, mt, v.buf->v_pool, dims, strides, box))
+        return fail_message(c, SPD_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    }
+    p.box_rows = br;
+    if (z.tc) {
+      t.rule = p.rule;
       if (!encode_rows(&t.tm_q, mt, qb, d, cfg.num_q_heads, n, (long long)cfg.num_q_heads * d, v.G,
                        128 / v.G) ||
-          !encode4(&t.tm_k, mt, v.buf->k_pool, dims, strides, box) ||
-          !encode4(&t.tm_v, mt, v.buf->v_pool, dims, strides, box) ||
           !encode_partials(&t.tm_out, p.pre_o, d,
                            (size_t)z.tiles * cfg.num_kv_heads * z.nsplit * kDenseRows))
         return fail_message(c, SPD_ERR_CUDA, "cuTensorMapEncodeTiled failed");
@@ -578,7 +606,27 @@ spd_status spd_shared_prefix_attention(spd_ctx *c, const void *q, int prefix_id,
       e = launch_dense_tc(t, cfg.dtype, d, p.out_f32 != 0, st);
       ++launches;
     }
-    if (e == cudaSuccess && z.prefix_items + z.own_items > 0) {
+    p.follow = z.tc;
+    if (z.few) {
+      // the shorter one first: the other, which does not wait for it, hides it
+      for (int k = 0; k < 2 && e == cudaSuccess; ++k) {
+        const bool own = (k == 0) == z.own_first;
+        if (own && z.own_items == 0) continue;
+        if (own) {
+          p.tm_k = *v.tm_k;
+          p.tm_v = *v.tm_v;
+          p.prefix_items = 0;  // (the decode kernel takes the own items alone)
+          e = launch_dense_decode(p, cfg.dtype, d, st);
+        } else {
+          p.tm_k = t.tm_k;
+          p.tm_v = t.tm_v;
+          p.prefix_items = z.prefix_items;
+          e = launch_dense_few(p, cfg.dtype, st);
+        }
+        p.follow = 1;
+        ++launches;
+      }
+    } else if (e == cudaSuccess && z.prefix_items + z.own_items > 0) {
       e = launch_dense_decode(p, cfg.dtype, d, st);
       ++launches;
     }
@@ -661,13 +709,15 @@ spd_status spd_kv_evict(spd_ctx *c, const int *src_ids, const int *dst_ids, int 
       p.seqs[i] = EvictSeq{src_ids[b + i], dst_ids[b + i], (int)L, m[b + i]};
       longest = std::max(longest, L);
     }
-    // CTAs per (sequence, kv head): at least 2,048 tokens each, at most eight,
-    // and no more than fill the GPU twice
+    // CTAs per (sequence, kv head): at least 4,096 tokens each, at most eight (a
+    // power of two: clusters of six left SMs of a GPC over and took two rounds),
+    // and no more than one per SM in all (8 x 8 heads of up to 32,768 tokens:
+    // 75 us, with two per SM 83)
     int cluster = 1;
-    while (cluster < 8 && cluster * 2048LL < longest &&
-           (long long)p.n * v.Hd * cluster * 2 <= 2LL * v.num_sms)
+    while (cluster < 8 && cluster * 4096LL < longest &&
+           (long long)p.n * v.Hd * cluster * 2 <= v.num_sms)
       cluster *= 2;
-    const cudaError_t e = launch_evict(p, cfg.dtype, cfg.head_dim, cluster, st);
+    const cudaError_t e = launch_evict(p, cfg.dtype, cfg.head_dim, cluster, v.num_sms, st);
     note_launches(c, st, 2);
     if (e != cudaSuccess) return fail_message(c, SPD_ERR_CUDA, cudaGetErrorString(e));
   }

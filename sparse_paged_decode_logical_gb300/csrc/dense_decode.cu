@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     fence_mbar_init();
   }
   __syncwarp();
-  // behind this call's prefix kernel nothing is waited for: that kernel started
+  // behind another kernel of this call nothing is waited for: that kernel started
   // its dependents after its own wait, so all that is read here is there, and
   // the two write to different places
   if (!p.follow) pdl_wait();
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     *reinterpret_cast<float4 *>(o_out + (size_t)r * D + c) = acc;
     if (c == 0) ml_out[r] = make_float2(M, l);
   }
-  if (p.follow) pdl_wait();  // (done only once the prefix kernel is: the next one reads both)
+  if (p.follow) pdl_wait();  // (done only once that kernel is: the next one reads both)
 }
 
 // ---- joining prefix and own splits ------------------------------------------------
