@@ -22,6 +22,12 @@ constexpr int kFewKeys = 128;        // keys per step of dense_few
 constexpr int kDenseMaxSplits = 64;  // key splits of one unit
 constexpr int kOwnMaxSplits = 256;   // splits of one sequence's own tokens
 
+// Weights are held as 2^(x - m + 7): a running max m may lag 2^8 behind a row's
+// largest score, so that weights stay below fp16's 2^16, and what fp16 loses
+// below its normal range is 2^-32 of the largest weight (without the shift
+// 2^-25).  Sums carry the same factor, and partial sums come with m - 7.
+constexpr float kWeightShift = 7.f;
+
 // Allows a kernel its dynamic shared memory on the current device, once per
 // device (`ready`: a bit for each of the first 64).
 template <typename K>
@@ -108,6 +114,8 @@ struct DenseDecodeParams {
   const float *w_in;       // [n][Hkv][w_stride] or null
   float *w_out;
   const int *page_table;
+  int *tickets;            // [n][Hkv], zero before and after: the last item of a (sequence,
+                           // kv head) joins its splits; null: a combining kernel does
   int *err;
   ScoreRule rule;
   long long w_stride, l_stride;

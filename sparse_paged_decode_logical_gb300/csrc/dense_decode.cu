@@ -64,6 +64,61 @@ template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t x) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&x));
 }
 
+// Where a row's splits lie: own partials first, then the prefix's.
+struct RowSplits {
+  const float2 *own_ml, *pre_ml;
+  const float *own_o, *pre_o;
+  size_t own_step, pre_step;  // rows between two splits
+  int ns, nall;
+};
+__device__ __forceinline__ RowSplits row_splits(const DenseDecodeParams &p, int seq, int hk, int g,
+                                                int D) {
+  const DecodeSeq &s = p.seqs[seq];
+  const int r = seq * p.G + g, tile = p.prefix_ns > 0 ? r / p.prefix_rows : 0;
+  const size_t own = ((size_t)s.item_off + hk * s.ns) * p.G + g,
+               pre = (size_t)(tile * p.Hkv + hk) * p.prefix_ns * p.prefix_rows +
+                     (r - tile * p.prefix_rows);
+  RowSplits x;
+  x.own_ml = p.part_ml + own;
+  x.own_o = p.part_o + own * D;
+  x.pre_ml = p.pre_ml + pre;
+  x.pre_o = p.pre_o + pre * D;
+  x.own_step = p.G;
+  x.pre_step = p.prefix_rows;
+  x.ns = s.ns;
+  x.nall = s.ns + p.prefix_ns;
+  return x;
+}
+// One warp: the row's max (0 if nothing was met) and sum; factors to fac.
+__device__ __forceinline__ float2 row_stats(const RowSplits &x, float *fac) {
+  constexpr int kMax = kOwnMaxSplits + kDenseMaxSplits;
+  const int lane = threadIdx.x & 31;
+  float2 v[kMax / 32];
+  float M = -CUDART_INF_F, L = 0.f;
+#pragma unroll
+  for (int j = 0; j < kMax / 32; ++j) {
+    const int k = lane + 32 * j;
+    v[j] = make_float2(-CUDART_INF_F, 0.f);
+    if (32 * j < x.nall && k < x.nall)
+      v[j] = __ldcg(k < x.ns ? x.own_ml + k * x.own_step : x.pre_ml + (k - x.ns) * x.pre_step);
+    M = fmaxf(M, v[j].x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float base = M == -CUDART_INF_F ? 0.f : M;
+#pragma unroll
+  for (int j = 0; j < kMax / 32; ++j) {
+    if (32 * j >= x.nall) break;
+    const int k = lane + 32 * j;
+    const float f = exp2f(v[j].x - base);
+    if (fac && k < x.nall) fac[k] = f;
+    L = fmaf(v[j].y, f, L);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  return make_float2(base, L);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     dense_decode_kernel(const __grid_constant__ DenseDecodeParams p) {
@@ -310,7 +365,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 #pragma unroll
     for (int hr = 0; hr < 2; ++hr) {
       if (hr == 1 && !upper) break;
-      const float base = m_run[hr] == -CUDART_INF_F ? 0.f : m_run[hr];
+      const float base = m_run[hr] == -CUDART_INF_F ? 0.f : m_run[hr] - kWeightShift;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float a = ex2_approx(sc[j][2 * hr] - base), b = ex2_approx(sc[j][2 * hr + 1] - base);
@@ -386,9 +441,66 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       l = fmaf(msum[w * kDecodeRows + r], f, l);
     }
     *reinterpret_cast<float4 *>(o_out + (size_t)r * D + c) = acc;
-    if (c == 0) ml_out[r] = make_float2(M, l);
+    if (c == 0) ml_out[r] = make_float2(M - kWeightShift, l);
   }
   if (p.follow) pdl_wait();  // (done only once that kernel is: the next one reads both)
+  if (!p.tickets) return;
+  // ---- the last of a (sequence, kv head)'s items joins its splits: a warp per
+  // query head ----
+  __shared__ int mine[kDecodeRows];
+  float *fac = reinterpret_cast<float *>(smem) + warp * (kOwnMaxSplits + kDenseMaxSplits);
+  __threadfence();
+  __syncthreads();  // (and the merge area has been read)
+  const int first_seq = row0 / p.G, seqs = (rows + p.G - 1) / p.G;
+  if (tid < seqs) {
+    const int sq = first_seq + tid, need = p.seqs[sq].ns + p.prefix_ns;
+    int *ticket = p.tickets + sq * p.Hkv + hk;
+    const bool last = atom_add_acq_rel_gpu(ticket, 1) == need - 1;
+    if (last) *ticket = 0;  // as it was found
+    mine[tid] = last;
+  }
+  __syncthreads();
+  for (int i = 0; i < seqs; ++i) {
+    if (!mine[i]) continue;
+    for (int g = warp; g < p.G; g += kWarps) {
+      const RowSplits x = row_splits(p, first_seq + i, hk, g, D);
+      __syncwarp();
+      const float2 st = row_stats(x, fac);
+      __syncwarp();
+      constexpr int E = D / 32;
+      float acc[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = 0.f;
+      auto add = [&](const float *src, float f) {
+        if constexpr (E == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4 *>(src) + lane);
+          acc[0] = fmaf(v.x, f, acc[0]);
+          acc[1] = fmaf(v.y, f, acc[1]);
+          acc[2] = fmaf(v.z, f, acc[2]);
+          acc[3] = fmaf(v.w, f, acc[3]);
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2 *>(src) + lane);
+          acc[0] = fmaf(v.x, f, acc[0]);
+          acc[1] = fmaf(v.y, f, acc[1]);
+        }
+      };
+#pragma unroll 8
+      for (int k = 0; k < x.ns; ++k) add(x.own_o + k * x.own_step * D, fac[k]);
+#pragma unroll 8
+      for (int k = 0; k < x.nall - x.ns; ++k) add(x.pre_o + k * x.pre_step * D, fac[x.ns + k]);
+      const float inv = 1.f / st.y;
+      const size_t at = ((size_t)(first_seq + i) * p.Hq + hk * p.G + g) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        if (p.out_f32)
+          *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + at + e) =
+              make_float2(acc[e] * inv, acc[e + 1] * inv);
+        else
+          *reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + at + e) =
+              pack2<T>(acc[e] * inv, acc[e + 1] * inv);
+      }
+    }
+  }
 }
 
 // ---- joining prefix and own splits ------------------------------------------------
@@ -397,61 +509,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 // weights of 1,024 own tokens of one (sequence, kv head),
 // w_out = w_in + sum over the head's G queries of 2^(x - M) / L.
 constexpr int kCombineThreads = 128, kWeightTokens = 1024;
-
-// Where a row's splits lie: own partials first, then the prefix's.
-struct RowSplits {
-  const float2 *own_ml, *pre_ml;
-  const float *own_o, *pre_o;
-  size_t own_step, pre_step;  // rows between two splits
-  int ns, nall;
-};
-__device__ __forceinline__ RowSplits row_splits(const DenseDecodeParams &p, int seq, int hk, int g,
-                                                int D) {
-  const DecodeSeq &s = p.seqs[seq];
-  const int r = seq * p.G + g, tile = p.prefix_ns > 0 ? r / p.prefix_rows : 0;
-  const size_t own = ((size_t)s.item_off + hk * s.ns) * p.G + g,
-               pre = (size_t)(tile * p.Hkv + hk) * p.prefix_ns * p.prefix_rows +
-                     (r - tile * p.prefix_rows);
-  RowSplits x;
-  x.own_ml = p.part_ml + own;
-  x.own_o = p.part_o + own * D;
-  x.pre_ml = p.pre_ml + pre;
-  x.pre_o = p.pre_o + pre * D;
-  x.own_step = p.G;
-  x.pre_step = p.prefix_rows;
-  x.ns = s.ns;
-  x.nall = s.ns + p.prefix_ns;
-  return x;
-}
-// One warp: the row's max (0 if nothing was met) and sum; factors to fac.
-__device__ __forceinline__ float2 row_stats(const RowSplits &x, float *fac) {
-  constexpr int kMax = kOwnMaxSplits + kDenseMaxSplits;
-  const int lane = threadIdx.x & 31;
-  float2 v[kMax / 32];
-  float M = -CUDART_INF_F, L = 0.f;
-#pragma unroll
-  for (int j = 0; j < kMax / 32; ++j) {
-    const int k = lane + 32 * j;
-    v[j] = make_float2(-CUDART_INF_F, 0.f);
-    if (32 * j < x.nall && k < x.nall)
-      v[j] = k < x.ns ? x.own_ml[k * x.own_step] : x.pre_ml[(k - x.ns) * x.pre_step];
-    M = fmaxf(M, v[j].x);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float base = M == -CUDART_INF_F ? 0.f : M;
-#pragma unroll
-  for (int j = 0; j < kMax / 32; ++j) {
-    if (32 * j >= x.nall) break;
-    const int k = lane + 32 * j;
-    const float f = exp2f(v[j].x - base);
-    if (fac && k < x.nall) fac[k] = f;
-    L = fmaf(v[j].y, f, L);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  return make_float2(base, L);
-}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kCombineThreads)

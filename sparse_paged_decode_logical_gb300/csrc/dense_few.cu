@@ -305,7 +305,8 @@ __global__ void __launch_bounds__(kFewThreads, NR <= 16 ? 3 : 2)
     // where this thread's key lies in a row of P^T: 16-byte piece and place in it
     uint8_t *const prow = smem + Sm::kP + (tid >> 6) * (NR * 128) + (tid & 7) * 2;
     const uint32_t piece = ((tid >> 3) & 7) << 4;
-    // sums, and the rows' references
+    // sums, and what a weight's exponent counts from: the rows' references less
+    // the shift
     float l[NR], rf[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kFewThreads, NR <= 16 ? 3 : 2)
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         if (!in) x[r] = -CUDART_INF_F;
-        grow |= x[r] > rf[r] + 8.f;
+        grow |= x[r] > rf[r] + (8.f + kWeightShift);
       }
       if (few_any(grow || !ok)) {
         if (few_any(!ok)) {
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kFewThreads, NR <= 16 ? 3 : 2)
         for (int r = 0; r < NR; ++r) {
           f[r] = fac[r];
           l[r] *= f[r];
-          rf[r] = ref[r];
+          rf[r] = ref[r] - kWeightShift;
         }
         if (j > 0) {  // (SF of this step: the P . V before is done)
 #pragma unroll
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(kFewThreads, NR <= 16 ? 3 : 2)
     few_sync();
     if (tid < rows)
       ml_out[tid] = make_float2(
-          ref[tid], (wred[tid] + wred[NR + tid]) + (wred[2 * NR + tid] + wred[3 * NR + tid]));
+          ref[tid] - kWeightShift, (wred[tid] + wred[NR + tid]) + (wred[2 * NR + tid] + wred[3 * NR + tid]));
     float o[NR];
     __syncwarp();
     few_load<NR>(lanes + NR, o);

@@ -638,8 +638,9 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
           l_run *= alpha;
           m_run = m_new;
         }
-        // weights 2^(x - m); a row that has met no key yet keeps 2^(-inf - 0) = 0
-        const float base = m_run == -CUDART_INF_F ? 0.f : m_run;
+        // weights 2^(x - m + kWeightShift); a row that has met no key yet keeps
+        // 2^(-inf - 0) = 0
+        const float base = m_run == -CUDART_INF_F ? 0.f : m_run - kWeightShift;
         uint32_t hi_w[32];
         uint32_t lo_w[kSplitP ? 32 : 1];
         const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-base, -base);
@@ -677,7 +678,7 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
       const bool live = tok < p.Lq, empty = rend == 0;
       const bool fix = *reinterpret_cast<volatile int *>(misc + kMiscBad) && live && !empty;
       const size_t pr = ((size_t)unit * p.nsplit + split) * kDenseRows + m * 128 + row;
-      if (p.partial && live) p.part_ml[pr] = make_float2(m_run, empty ? 0.f : l_run);
+      if (p.partial && live) p.part_ml[pr] = make_float2(m_run - kWeightShift, empty ? 0.f : l_run);
       const float inv = empty ? 0.f : p.partial ? 1.f : 1.f / l_run;
       const bool f32 = p.partial || p.out_f32;
       // two buffers of [32][128 B], 16-byte pieces swizzled by the row

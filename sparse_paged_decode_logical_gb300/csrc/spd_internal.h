@@ -221,6 +221,8 @@ struct CtxView {
   int G, Hd, Hs, R, max_pp, kv_fp8;
   int device, num_sms;
   int *err;
+  int *tickets;       // [ticket_seqs][num_kv_heads], zero between launches
+  int ticket_seqs;
 };
 // Host facts only (no device call); ctx_device fills device, num_sms and the
 // tensor maps in, setting the context up on its device the first time.

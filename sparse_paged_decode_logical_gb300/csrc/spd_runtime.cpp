@@ -885,6 +885,8 @@ void ctx_view(spd_ctx *c, CtxView *v) {
   v->device = c->device;
   v->num_sms = c->num_sms;
   v->err = c->err_word();
+  v->tickets = reinterpret_cast<int *>(c->scratch(c->dv.sl.tickets_dec));
+  v->ticket_seqs = c->dv.seqs_per_launch;
 }
 
 spd_status ctx_device(spd_ctx *c, cudaStream_t st, CtxView *v) {
