@@ -218,6 +218,13 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, (uint32_t)misc[0], 0);  // warp-uniform
   pdl_wait();
   pdl_launch_dependents();
+  if (tid == Sm::kLoadWarp * 32) {  // Q is on its way while the intervals are read
+    mbar_arrive_expect_tx(&bars[Sm::kBarQ], 2 * KB * 16384);
+    for (int mm = 0; mm < 2; ++mm)
+      for (int kb = 0; kb < KB; ++kb)
+        tma_load_4d(smem + Sm::kQ + (mm * KB + kb) * 16384, &p.tm_q, 0, kb, h0,
+                    tok0 + (p.dup ? 0 : mm * tpm), &bars[Sm::kBarQ]);
+  }
 
   // ---- the interval of keys of every row, and of each matrix ----
   int rbeg = 0, rend = 0;  // of softmax thread tid's row (an empty one: 0, 0)
@@ -290,15 +297,10 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
   };
 
   if (warp == Sm::kLoadWarp) {
-    // ---- TMA: Q once, then K and V of every pair through the ring ----
-    if (lane == 0 && np > 0) {
+    // ---- TMA: K and V of every pair through the ring ----
+    if (lane == 0) {
       int k_issued = 0, v_issued = 0;
       bool ok = true;
-      mbar_arrive_expect_tx(&bars[Sm::kBarQ], 2 * KB * 16384);
-      for (int mm = 0; mm < 2; ++mm)
-        for (int kb = 0; kb < KB; ++kb)
-          tma_load_4d(smem + Sm::kQ + (mm * KB + kb) * 16384, &p.tm_q, 0, kb, h0,
-                      tok0 + (p.dup ? 0 : mm * tpm), &bars[Sm::kBarQ]);
       for (int pp = 0; pp < np && ok; ++pp) {
         const int s = pp % S, nbk = min(2, n - 2 * pp);
         if (pp >= S && !(ok = dt_wait(&bars[Sm::kBarKE + s], ((pp / S) - 1) & 1, fail))) break;
@@ -666,7 +668,7 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
         }
       }
     }
-    if (ok && np > 0) {  // (without products, Q's copy must have landed: its tile is written next)
+    if (ok) {  // (without products, Q's copy must have landed: its tile is written next)
       ok = dt_wait(blocks > 0 ? &bars[Sm::kBarOF + m] : &bars[Sm::kBarQ], 0, fail);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
