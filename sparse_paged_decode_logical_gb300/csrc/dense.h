@@ -51,6 +51,8 @@ struct ScoreRule {
   float small;           // scores q.k up to this are within tanh's short polynomial
   float cap_out;         // cap * log2(e); 0: no cap
   float poly[5];         // cap_out times tanh(z) / z as a polynomial in z^2, |z| <= 0.6
+  float quick;           // a cap without slopes: scores q.k up to this may take quick_poly; 0: none
+  float quick_poly[5];   // the capped score over q.k as a polynomial in (q.k)^2
   const float *slopes;   // [Hq] or null
 };
 

@@ -142,6 +142,14 @@ ScoreRule make_rule(const spd_score_rule *r, int d) {
     for (int i = 0; i < 5; ++i) x.poly[i] = (float)(kLog2e * r->softcap * kTanh[i]);
   }
   x.slopes = r ? r->slopes : nullptr;
+  if (x.cap_out > 0.f && !x.slopes && x.z_in > 1e-4f) {  // (z_in^8 stays an fp32 number)
+    // tanh(z) / z in z^2, |z| <= 0.75, times scale log2(e) and in (q.k)^2
+    constexpr double kTanh[5] = {0.999999463558197, -0.3332825005054474, 0.13258983194828033, -0.050056301057338715, 0.01292963046580553};
+    double f = scale * kLog2e;
+    const double z2 = scale / r->softcap * (scale / r->softcap);
+    for (int i = 0; i < 5; ++i, f *= z2) x.quick_poly[i] = (float)(f * kTanh[i]);
+    x.quick = (float)(0.7499 * r->softcap / scale);
+  }
   return x;
 }
 

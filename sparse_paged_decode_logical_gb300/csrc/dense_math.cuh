@@ -36,6 +36,16 @@ __device__ __forceinline__ float2 cap_16bit(const ScoreRule &r, float2 s) {
                 f2_dup(r.cap_out));
 }
 
+// cap tanh(s / cap) + add in base-2 units, for |s| <= r.quick (|s / cap| <= 0.75):
+// a polynomial of five terms in s^2 that is 5e-7 of the score off.
+__device__ __forceinline__ float2 cap_quick(const ScoreRule &r, float2 s, float2 add) {
+  const float2 u = f2_mul(s, s);
+  float2 p = f2_dup(r.quick_poly[4]);
+#pragma unroll
+  for (int i = 3; i >= 0; --i) p = f2_fma(p, u, f2_dup(r.quick_poly[i]));
+  return f2_fma(s, p, add);
+}
+
 // The same for any score, precise.
 __device__ __forceinline__ float cap_any(const ScoreRule &r, float s) {
   constexpr float c[7] = {0.9999999403953552f,  -0.33332839608192444f, 0.13325203955173492f,

@@ -558,7 +558,22 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
         const int key0 = key0_of(2 * pp + u);
         uint32_t s[64];
         tmem_ld64_sync(t_s, s);
-        if constexpr (kRule) {
+        const bool edge = is_edge(key0);
+        // a cap alone, 16-bit output, scores within the polynomial's range: the
+        // cap is monotonic, so the row's max is taken first and the polynomial
+        // goes into the exponent (1.5 instructions per score)
+        bool quick = false;
+        if constexpr (kRule && !kSplitP) {
+          if (p.rule.quick > 0.f && !edge) {
+            float big = 0.f;
+#pragma unroll
+            for (int c = 0; c < 64; c += 2)
+              big = fmaxf(fmaxf(big, fabsf(__uint_as_float(s[c]))),
+                          fabsf(__uint_as_float(s[c + 1])));
+            quick = __all_sync(0xffffffffu, big <= p.rule.quick);
+          }
+        }
+        if (kRule && !quick) {
           if (p.rule.cap_out > 0.f) {
             if constexpr (kSplitP) {
               // the short polynomial when it holds for the warp's 64 x 32 scores
@@ -602,7 +617,7 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
                   fmaf(-slope, fabsf(d0 - (float)c) - near, __uint_as_float(s[c])));
           }
         }
-        if (is_edge(key0)) {
+        if (edge) {
           const int c0 = rbeg - key0, c1 = rend - key0;
 #pragma unroll
           for (int c = 0; c < 64; ++c)
@@ -618,7 +633,8 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
             mq[k] = fmax3f(mq[k], __uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1]));
 #pragma unroll
         for (int k = 0; k < 4; ++k) mq[k] = fmaxf(mq[k], __uint_as_float(s[60 + k]));
-        const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * sc;
+        const float top = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+        const float mx = quick ? cap_quick(p.rule, f2_dup(top), f2_dup(0.f)).x : top * sc;
         const bool need = mx > m_run + kDtRescaleAbove;
         if (__any_sync(0xffffffffu, need)) {
           const float m_new = need ? mx : m_run;
@@ -645,17 +661,23 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
         const float base = m_run == -CUDART_INF_F ? 0.f : m_run - kWeightShift;
         uint32_t hi_w[32];
         uint32_t lo_w[kSplitP ? 32 : 1];
-        const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-base, -base);
-        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 sc2 = f2_dup(sc), nm2 = f2_dup(-base);
+        float2 ls[2] = {f2_dup(0.f), f2_dup(0.f)};
+        auto weights = [&](auto exponent) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float2 x = f2_fma(
-              make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sc2, nm2);
-          const float2 w = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-          ls[c & 1] = f2_add(ls[c & 1], w);
-          if constexpr (kSplitP) Weights<T>::split(w, hi_w[c], lo_w[c]);
-          else hi_w[c] = Weights<T>::round(w);
-        }
+          for (int c = 0; c < 32; ++c) {
+            const float2 x = exponent(
+                make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])));
+            const float2 w = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            ls[c & 1] = f2_add(ls[c & 1], w);
+            if constexpr (kSplitP) Weights<T>::split(w, hi_w[c], lo_w[c]);
+            else hi_w[c] = Weights<T>::round(w);
+          }
+        };
+        if (kRule && !kSplitP && quick)
+          weights([&](float2 x) { return cap_quick(p.rule, x, nm2); });
+        else
+          weights([&](float2 x) { return f2_fma(x, sc2, nm2); });
         l_run += (ls[0].x + ls[1].x) + (ls[0].y + ls[1].y);
         tmem_st32(t_s, hi_w);
         if constexpr (kSplitP) tmem_st32(t_s + 32, lo_w);
