@@ -144,7 +144,8 @@ ScoreRule make_rule(const spd_score_rule *r, int d) {
   x.slopes = r ? r->slopes : nullptr;
   if (x.cap_out > 0.f && !x.slopes && x.z_in > 1e-4f) {  // (z_in^8 stays an fp32 number)
     // tanh(z) / z in z^2, |z| <= 0.75, times scale log2(e) and in (q.k)^2
-    constexpr double kTanh[5] = {0.999999463558197, -0.3332825005054474, 0.13258983194828033, -0.050056301057338715, 0.01292963046580553};
+    constexpr double kTanh[5] = {0.999999463558197, -0.3332825005054474, 0.13258983194828033,
+                                 -0.050056301057338715, 0.01292963046580553};
     double f = scale * kLog2e;
     const double z2 = scale / r->softcap * (scale / r->softcap);
     for (int i = 0; i < 5; ++i, f *= z2) x.quick_poly[i] = (float)(f * kTanh[i]);
@@ -153,8 +154,8 @@ ScoreRule make_rule(const spd_score_rule *r, int d) {
   return x;
 }
 
-// Rows at least this long take S of two blocks in one product (4,096 packed
-// tokens: 67.6 us with, 65.6 without; 49,152 keys: 1,402 and 1,510).
+// Rows at least this long take S of two blocks in one product (49,152 keys: 1,318
+// us, with two products 1,345; 4,096 packed tokens 61 either way).
 constexpr int kPairKeys = 8192;
 
 // ---- prompt attention ------------------------------------------------------------
@@ -198,7 +199,7 @@ spd_status plan_prompt(const spd_dense_config *c, int Lq, int Lk, int sms, Promp
   // A few waves of equal units (a chunk over a much longer row) leave the last
   // one part empty: cut into s, they take ceil(units s / SMs) / s unit times, for
   // the price of the partial sums.  (0.9 us per block of a unit, 0.045 us per
-  // cut unit written and read: 256 units of 768 blocks in four cuts 1,325 us, whole
+  // cut unit written and read: 256 units of 768 blocks in four cuts 1,320 us, whole
   // 1,412.  Packed documents, where units are short and uneven, stay whole.)
   if (!z->dup && units > sms && units <= 8LL * sms && Lk >= 4LL * Lq) {
     auto cost = [&](int s) {

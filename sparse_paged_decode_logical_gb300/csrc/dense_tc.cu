@@ -19,10 +19,10 @@
 // of this one is done: the hand-overs between the roles (about 300 cycles each)
 // and the products of one buffer then pass while the softmax works on the
 // other.  Where the softmax is the longer side (score rules, split weights)
-// that wins: 8,192 capped tokens 790 us against 954, 2,501 tokens of 64
-// channels with a bias and fp32 output 71 against 80.  Plain scores with 16-bit
+// that wins: 8,192 capped tokens 678 us against 838, 2,501 tokens of 64
+// channels with a bias and fp32 output 59 against 70.  Plain scores with 16-bit
 // output over a long row keep the tensor pipe busy and take one N 128 product
-// per pair (pair_s): 2,048 queries over 49,152 keys 1,402 us against 1,510.
+// per pair (pair_s): 2,048 queries over 49,152 keys 1,318 us against 1,345.
 // Outputs of 32 bits (kSplitP) keep P as a 16-bit high part and the 16-bit
 // rounding of the rest, two products per block: P . V then holds about 16 bits
 // (bf16) or 22 (fp16) of each weight.  Outputs of 16 bits round P once, which
@@ -271,9 +271,9 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
   const int np = (n + 1) / 2;
   // Blocks in ascending order, so that the CTAs that run together read the same
   // K and V at the same time (descending, where each starts at its own newest
-  // key, took 1,693 us against 1,402 on 2,048 queries over 49,152 keys).  With a
+  // key, took 1,385 us against 1,320 on 2,048 queries over 49,152 keys).  With a
   // distance bias in descending order: the largest scores come first and the
-  // running max hardly moves (2,501 tokens 61.5 us against 71).  Block j of the
+  // running max hardly moves (2,501 tokens 59.5 us against 68.5).  Block j of the
   // split begins at key0_of(j); pair pp holds blocks 2 pp and 2 pp + 1.
   const bool desc = kRule && p.rule.slopes != nullptr;
   auto key0_of = [&](int j) { return (desc ? kb0 + n - 1 - j : kb0 + j) * kDenseBlock; };
@@ -445,10 +445,10 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
     auto wwait = [&](uint64_t *bar, uint32_t parity) {
       return __all_sync(0xffffffffu, dt_wait(bar, parity, fail));
     };
-    // matrix 1 starts once matrix 0's first softmax is done, so that one's
-    // softmax runs beside the other's products (in step, both wait for the
-    // tensor pipe and then for the special-function units)
-    const bool lag = m == 1 && !dup && pair_first(0) == 0 && pair_last(0) > 0;
+    // with one S per pair, matrix 1 starts once matrix 0's first softmax is done,
+    // so that one's softmax runs beside the other's products (in step, both wait
+    // for the tensor pipe and then for the special-function units)
+    const bool lag = pair_s && m == 1 && !dup && pair_first(0) == 0 && pair_last(0) > 0;
     bool ok = begin < end && wwait(&bars[Sm::kBarQ], 0), any = false;
     if (ok && lag) ok = wwait(&bars[Sm::kBarLag], 0);
     for (int pp = 0; pp < begin && ok; ++pp) {  // (every phase is seen, in order)
