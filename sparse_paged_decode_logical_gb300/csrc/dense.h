@@ -157,7 +157,6 @@ struct EvictParams {
   int P_log2;             // log2(P), -1 if P is no power of two
   EvictSeq seqs[kDenseSeqs];
 };
-cudaError_t launch_evict(const EvictParams &p, int dtype, int d, int cluster, int sms,
-                         cudaStream_t st);
+cudaError_t launch_evict(const EvictParams &p, int dtype, int d, int sms, cudaStream_t st);
 
 }  // namespace spd

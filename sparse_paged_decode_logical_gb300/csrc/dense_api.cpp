@@ -728,21 +728,10 @@ spd_status spd_kv_evict(spd_ctx *c, const int *src_ids, const int *dst_ids, int 
     p.P_log2 = -1;
     for (int x = 0; x < 31; ++x)
       if (p.P == 1 << x) p.P_log2 = x;
-    long long longest = 0;
-    for (int i = 0; i < p.n; ++i) {
-      const long long L = seq_length(c, src_ids[b + i]);
-      p.seqs[i] = EvictSeq{src_ids[b + i], dst_ids[b + i], (int)L, m[b + i]};
-      longest = std::max(longest, L);
-    }
-    // CTAs per (sequence, kv head): at least 4,096 tokens each, at most eight (a
-    // power of two: clusters of six left SMs of a GPC over and took two rounds),
-    // and no more than one per SM in all (8 x 8 heads of up to 32,768 tokens:
-    // 75 us, with two per SM 83)
-    int cluster = 1;
-    while (cluster < 8 && cluster * 4096LL < longest &&
-           (long long)p.n * v.Hd * cluster * 2 <= v.num_sms)
-      cluster *= 2;
-    const cudaError_t e = launch_evict(p, cfg.dtype, cfg.head_dim, cluster, v.num_sms, st);
+    for (int i = 0; i < p.n; ++i)
+      p.seqs[i] = EvictSeq{src_ids[b + i], dst_ids[b + i], (int)seq_length(c, src_ids[b + i]),
+                           m[b + i]};
+    const cudaError_t e = launch_evict(p, cfg.dtype, cfg.head_dim, v.num_sms, st);
     note_launches(c, st, 2);
     if (e != cudaSuccess) return fail_message(c, SPD_ERR_CUDA, cudaGetErrorString(e));
   }

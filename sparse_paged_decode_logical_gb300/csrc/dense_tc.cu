@@ -821,12 +821,16 @@ __global__ void __launch_bounds__(256) dense_prompt_combine_kernel(
   float acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
   for (int s = 0; s < ns; ++s) {
     // a split that holds none of the row's keys left zeros (or nothing to weigh)
     const float fs = __shfl_sync(0xffffffffu, s < 32 ? f[0] : f[kDenseMaxSplits / 32 - 1], s & 31);
     const float *o = po + (size_t)s * rt * D + lane * E;
+    float v[E];
+    if constexpr (E == 4) *reinterpret_cast<float4 *>(v) = __ldcs(reinterpret_cast<const float4 *>(o));
+    else *reinterpret_cast<float2 *>(v) = __ldcs(reinterpret_cast<const float2 *>(o));
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(o[e], fs, acc[e]);
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(v[e], fs, acc[e]);
   }
   bool empty;  // (a row whose interval holds no key is zero, one whose weights vanish is not)
   if (p.key_begin) {

@@ -550,15 +550,45 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) evict_copy_kernel(
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictParams &p, int dtype, int d, int cluster, int sms,
-                         cudaStream_t st) {
+// Clusters of `cs` CTAs of evict_select that the current device runs at once.
+static int active_clusters(int cs) {
+  static std::atomic<int> known[64][9];
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return 0;
+  const bool keep = device < 64;
+  int n = keep ? known[device][cs].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n - 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)cs);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = kCacheKeys * 4;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cs;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, evict_select_kernel, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    n = 0;
+  }
+  if (keep) known[device][cs].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+cudaError_t launch_evict(const EvictParams &p, int dtype, int d, int sms, cudaStream_t st) {
   int longest = 0;
   for (int i = 0; i < p.n; ++i) longest = longest > p.seqs[i].L ? longest : p.seqs[i].L;
-  int seg = ((longest + cluster - 1) / cluster + 3) & ~3;
-  const int smem = 4 * (seg < kCacheKeys ? seg : kCacheKeys);
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = allow_smem(evict_select_kernel, kCacheKeys * 4, &ready);
   if (e != cudaSuccess) return e;
+  // CTAs per (sequence, kv head): as many as the GPU runs of such clusters at once
+  // (a GPC holds whole clusters only), with at least 4,096 tokens each
+  int cluster = 1;
+  while (cluster < 8 && cluster * 4096 < longest && active_clusters(cluster + 1) >= p.n * p.Hkv)
+    ++cluster;
+  const int seg = ((longest + cluster - 1) / cluster + 3) & ~3;
+  const int smem = 4 * (seg < kCacheKeys ? seg : kCacheKeys);
   e = launch_pdl_cluster(evict_select_kernel, p.n * p.Hkv * cluster, kSelThreads, (size_t)smem,
                          cluster, st, p);
   if (e != cudaSuccess) return e;
