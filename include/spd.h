@@ -431,8 +431,8 @@ spd_status spd_prefill_check(const void *workspace, spd_stream stream);
  * plain softmax(q . k / sqrt(head_dim)).
  */
 typedef struct {
-  float scale;         /* finite, >= 0 */
-  float softcap;       /* finite, >= 0 */
+  float scale;         /* 0, or in [1e-6, 1e6] */
+  float softcap;       /* 0, or in [1e-6, 1e6] */
   const float *slopes; /* device [num_q_heads], 4-byte aligned, or NULL */
 } spd_score_rule;
 
@@ -518,6 +518,8 @@ spd_status spd_document_key_ranges(const int *offsets, const int *prefix, int n_
  *        array may be both.  weights_stride >= every L_i.
  *   workspace  device, 256-byte aligned, at least spd_shared_prefix_sizes bytes
  *        for the same sequences (host lengths); one call at a time per workspace.
+ * Like every call on a context, calls are issued in order on one stream (tickets
+ * of the split work live in the context's scratch).
  * SPD_ERR_INVALID_ARG for a context with streaming heads or fp8 storage;
  * SPD_ERR_STATE for a prefix without tokens, or a sequence without tokens when
  * there is no prefix.  Device checks are reported by spd_check_status.

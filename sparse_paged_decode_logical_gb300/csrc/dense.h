@@ -50,6 +50,7 @@ struct ScoreRule {
   float e_in;            // 2 log2(e) scale / cap
   float small;           // scores q.k up to this are within tanh's short polynomial
   float cap_out;         // cap * log2(e); 0: no cap
+  int rough;             // 2^-22 of the cap does not show in 16-bit weights
   float poly[5];         // cap_out times tanh(z) / z as a polynomial in z^2, |z| <= 0.6
   float quick;           // a cap without slopes: scores q.k up to this may take quick_poly; 0: none
   float quick_poly[5];   // the capped score over q.k as a polynomial in (q.k)^2
@@ -101,6 +102,7 @@ struct DecodeSeq {
   int item_off;  // first item, relative to the own items
   int ns;        // splits per kv head (0: no tokens)
   int tpi;       // tiles per split
+  long long l_off;  // tokens (rounded up to 4) of the sequences before: its logits' place
 };
 struct DenseDecodeParams {
   CUtensorMap tm_k, tm_v;  // {64, P, d / 64, planes}, box {64, 16, d / 64, 1}
@@ -112,7 +114,8 @@ struct DenseDecodeParams {
   // 256 or 128 (dense_tc), n G (dense_few) or 16 (decode kernel)
   float *pre_o;
   float2 *pre_ml;
-  float *logits;           // [n][Hkv][G][l_stride] base-2 scores of own tokens, or null
+  float *logits;           // per sequence [Hkv][G][own tokens rounded up to 4] from l_off Hkv G:
+                           // base-2 scores of own tokens, or null
   const float *w_in;       // [n][Hkv][w_stride] or null
   float *w_out;
   const int *page_table;
@@ -120,7 +123,7 @@ struct DenseDecodeParams {
                            // kv head) joins its splits; null: a combining kernel does
   int *err;
   ScoreRule rule;
-  long long w_stride, l_stride;
+  long long w_stride;
   int out_f32;
   int n, Hq, Hkv, G, P, max_pp, num_phys;
   int prefix_slot, prefix_len, prefix_items, prefix_ns, prefix_tpi, prefix_rows;

@@ -120,8 +120,11 @@ bool encode_partials(CUtensorMap *m, const float *base, int d, size_t rows) {
 
 const char *check_rule(const spd_score_rule *r) {
   if (!r) return nullptr;
-  if (!(r->scale >= 0.f) || !std::isfinite(r->scale)) return "scale must be finite and >= 0";
-  if (!(r->softcap >= 0.f) || !std::isfinite(r->softcap)) return "softcap must be finite and >= 0";
+  // (between the bounds every constant of the rule is an ordinary fp32 number)
+  if (r->scale != 0.f && !(r->scale >= 1e-6f && r->scale <= 1e6f))
+    return "scale must be 0 or in [1e-6, 1e6]";
+  if (r->softcap != 0.f && !(r->softcap >= 1e-6f && r->softcap <= 1e6f))
+    return "softcap must be 0 or in [1e-6, 1e6]";
   if (r->slopes && !aligned(r->slopes, 4)) return "slopes must be 4-byte aligned";
   return nullptr;
 }
@@ -142,7 +145,8 @@ ScoreRule make_rule(const spd_score_rule *r, int d) {
     for (int i = 0; i < 5; ++i) x.poly[i] = (float)(kLog2e * r->softcap * kTanh[i]);
   }
   x.slopes = r ? r->slopes : nullptr;
-  if (x.cap_out > 0.f && !x.slopes && x.z_in > 1e-4f) {  // (z_in^8 stays an fp32 number)
+  x.rough = x.cap_out <= 256.f;
+  if (x.cap_out > 0.f && !x.slopes && x.z_in > 1e-4f && x.z_in < 1e4f) {  // (z_in^8 fits fp32)
     // tanh(z) / z in z^2, |z| <= 0.75, times scale log2(e) and in (q.k)^2
     constexpr double kTanh[5] = {0.999999463558197, -0.3332825005054474, 0.13258983194828033,
                                  -0.050056301057338715, 0.01292963046580553};
@@ -328,7 +332,12 @@ void plan_shared(const spd_ctx *c, const CtxView &v, int prefix_len, const int *
   z->pre_ml = take(pre_rows * 8);
   z->part_o = take(own_rows * d * 4);
   z->part_ml = take(own_rows * 8);
-  z->logits = take(weights ? (size_t)n * Hkv * v.G * round_up(z->longest, 4) * 4 : 0);
+  long long tokens = 0;
+  for (int i = 0; i < n; ++i) {
+    seqs[i].l_off = tokens;
+    tokens += (long long)round_up(seqs[i].L, 4);
+  }
+  z->logits = take(weights ? (size_t)tokens * Hkv * v.G * 4 : 0);
   z->total = off;
 }
 
@@ -559,7 +568,6 @@ spd_status spd_shared_prefix_attention(spd_ctx *c, const void *q, int prefix_id,
     p.err = v.err;
     p.rule = make_rule(rule, d);
     p.w_stride = weights_stride;
-    p.l_stride = (long long)round_up(z.longest, 4);
     p.out_f32 = out_type == SPD_OUT_F32;
     p.n = n;
     p.Hq = cfg.num_q_heads;
@@ -575,8 +583,10 @@ spd_status spd_shared_prefix_attention(spd_ctx *c, const void *q, int prefix_id,
     p.prefix_tpi = z.prefix_tpi;
     p.prefix_rows = z.prefix_rows;
     p.own_items = z.own_items;
-    p.precise = p.out_f32 || weights_out;
+    p.precise = p.out_f32 || weights_out || !p.rule.rough;
     p.w_chunks = (z.longest + 1023) / 1024;
+    if ((long long)n * (p.Hq + (weights_out ? (long long)p.Hkv * p.w_chunks : 0)) > 0x7fffffffLL)
+      return fail_message(c, SPD_ERR_CAPACITY, "too many weights for one launch");
     int launches = 0;
     cudaError_t e = cudaSuccess;
     const CUtensorMapDataType mt = map_type(cfg.dtype);

@@ -240,8 +240,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
   float m_run[2] = {-CUDART_INF_F, -CUDART_INF_F}, l_run[2] = {0.f, 0.f};
+  const size_t l_stride = (size_t)(L + 3) & ~size_t(3);
   float *lg = !pre && p.logits
-                  ? p.logits + ((size_t)(seq * p.Hkv + hk) * p.G) * p.l_stride
+                  ? p.logits + (size_t)p.seqs[seq].l_off * p.Hkv * p.G + (size_t)hk * p.G * l_stride
                   : nullptr;
 
   for (int i = 0; i < ntile && ok; ++i) {
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int key = 8 * j + 2 * t4 + e;
-          if (g8 < rows && key < valid) lg[(size_t)g8 * p.l_stride + t0 + key] = sc[j][e];
+          if (g8 < rows && key < valid) lg[(size_t)g8 * l_stride + t0 + key] = sc[j][e];
         }
     }
     // running max, moved only when it grows by more than 2^8
@@ -573,13 +574,14 @@ __global__ void __launch_bounds__(kCombineThreads)
     }
     __syncthreads();
     const size_t row = (size_t)unit;
-    const float *lg = p.logits + row * p.G * p.l_stride;
+    const size_t l_stride = (size_t)(L + 3) & ~size_t(3);
+    const float *lg = p.logits + (size_t)p.seqs[seq].l_off * p.Hkv * p.G + (size_t)hk * p.G * l_stride;
     const int t1 = min(L, (chunk + 1) * kWeightTokens);
 #pragma unroll 2
     for (int t = chunk * kWeightTokens + tid; t < t1; t += kCombineThreads) {
       float w = 0.f;
       for (int g = 0; g < p.G; ++g)
-        w = fmaf(ex2_approx(lg[g * p.l_stride + t] - stat[g].x), stat[g].y, w);
+        w = fmaf(ex2_approx(lg[g * l_stride + t] - stat[g].x), stat[g].y, w);
       p.w_out[row * p.w_stride + t] = (p.w_in ? p.w_in[row * p.w_stride + t] : 0.f) + w;
     }
   }

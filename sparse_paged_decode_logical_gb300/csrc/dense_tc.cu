@@ -595,6 +595,10 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
                 for (int c = 0; c < 64; ++c)
                   s[c] = __float_as_uint(cap_any(p.rule, __uint_as_float(s[c])));
               }
+            } else if (!p.rule.rough) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                s[c] = __float_as_uint(cap_any(p.rule, __uint_as_float(s[c])));
             } else {
 #pragma unroll
               for (int c = 0; c < 64; c += 2) {

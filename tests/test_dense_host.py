@@ -28,7 +28,8 @@ INVALID, BAD_SEQ, CAPACITY, STATE, NO_PAGES = 1, 3, 4, 7, 2
     dict(hq=7), dict(hq=0), dict(hkv=0), dict(hkv=129, hq=129), dict(d=96), dict(dtype=2),
     dict(out=2), dict(scale=-1.0), dict(scale=float("inf")), dict(softcap=-3.0),
     dict(softcap=float("nan")), dict(scale=float("nan")), dict(slopes=A + 2),
-    dict(hq=2048, hkv=128)])
+    dict(hq=2048, hkv=128), dict(softcap=1e-7), dict(softcap=2e6), dict(scale=1e-7),
+    dict(scale=1e7)])
 def test_prompt_configs_refused(bad):
     assert sizes(dense_cfg(**bad), 5, 5)[0] == INVALID
 

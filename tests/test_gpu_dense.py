@@ -90,6 +90,15 @@ def test_prompt_large_scores_saturate_the_cap():
     check_prompt(90, 90, 4, 2, 128, "bf16", gain=60.0)
 
 
+@pytest.mark.parametrize("softcap", [1e-6, 1e-3, 300.0, 2e4, 1e6])
+@pytest.mark.parametrize("out", ["same", "fp32"])
+def test_caps_of_every_size(softcap, out):
+    check_prompt(70, 70, 4, 2, 128, "bf16", out=out, softcap=softcap, gain=20.0)
+    check_prompt(70, 70, 4, 2, 64, "fp16", out=out, softcap=softcap, slopes=True)
+    for n in (2, 4, 20):
+        check_shared(n, 150, [9] * n, 8, 2, 128, "fp16", out=out, softcap=softcap, weights=True)
+
+
 def test_prompt_more_queries_than_keys():
     # queries that stand before the first key attend nothing
     check_prompt(200, 120, 4, 2, 64, "bf16")
@@ -358,7 +367,13 @@ def check_evict(lens, keep, recent, hkv, d, dtype="bf16", page=64, logical=16, s
             assert bool((kw_[i, h, m:] == 0).all())
             assert torch.equal(kd[:, h].view(torch.uint8), ks[idx, h].view(torch.uint8))
             assert torch.equal(vd[:, h].view(torch.uint8), vs[idx, h].view(torch.uint8))
-            if fp8:
+            if fp8:  # codes order by sign and magnitude
+                key = kd[:, h].view(torch.float8_e4m3fn).float()
+                for j in range(-(-m // logical)):
+                    rows = key[j * logical:min(m, (j + 1) * logical)]
+                    got = meta[table[j * logical // page], h, j * logical % page // logical]
+                    got = got.contiguous().view(torch.float8_e4m3fn).float()
+                    assert torch.equal(got[0], rows.amin(0)) and torch.equal(got[1], rows.amax(0))
                 continue
             for j in range(-(-m // logical)):
                 rows = kd[j * logical:min(m, (j + 1) * logical), h]
