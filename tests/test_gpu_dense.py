@@ -516,3 +516,101 @@ def test_prompt_decode_and_eviction_together():
         assert c.selection(ids[0], h) == list(range(4))
     ref, ab, mag, _ = shared(q, kk[:0], vv[:0], [kk], [vv], d ** -0.5, 0.0, None)
     assert bool(((got.double() - ref).abs() <= 2e-3).all())
+
+
+# ---- offsets beyond 32 bits ------------------------------------------------------
+
+def test_pools_beyond_four_gigabytes():
+    """Sequences whose pages lie behind the first 4 GB of a pool."""
+    hq, hkv, d, page, dt = 8, 8, 128, 4096, torch.bfloat16
+    pages = 620  # 8 MB of keys each
+    c = spd.SparsePagedKVCache(device="cuda", num_q_heads=hq, num_kv_heads=hkv, head_dim=d,
+                               dtype="bf16", logical_page=64, physical_page=page,
+                               num_physical_pages=pages, max_seqs=48, max_context=page * pages)
+    low = c.seq_create()
+    c.seq_reserve(low, (pages - 46) * page)
+    doc = c.seq_create()
+    kp, vp = normal(1, 3000, hkv, d, dtype=dt), normal(2, 3000, hkv, d, dtype=dt)
+    c.kv_append([doc], kp[None], vp[None])
+    assert min(c.page_table(doc)) * page * hkv * d * 2 > 1 << 32
+    for n in (2, 12, 40):  # each of the prefix's kernels
+        ids = [c.seq_create() for _ in range(n)]
+        ko, vo = normal(3, n, 20, hkv, d, dtype=dt), normal(4, n, 20, hkv, d, dtype=dt)
+        c.kv_append(ids, ko, vo)
+        q = normal(5, n, hq, d, dtype=dt)
+        got = c.shared_prefix_attention(q, doc, ids)
+        c.check_status()
+        ref, ab, mag, _ = shared(q, kp, vp, list(ko), list(vo), d ** -0.5, 0.0, None)
+        assert bool(((got.double() - ref).abs() <=
+                     tolerance(ref, ab, mag, d, 3020, dt, torch.float32, 0.0)).all())
+        for i in ids:
+            c.seq_free(i)
+    w = normal(6, 1, hkv, 3000).abs()
+    dst = c.seq_create()
+    kept, _ = c.kv_evict([doc], [dst], 500, 20, w)
+    c.check_status()
+    for h in range(hkv):
+        assert kept[0, h].tolist() == kept_positions(w[0, h].cpu(), 3000, 500, 20)
+        assert torch.equal(cache_rows(c, dst, hkv, d, dt, page)[:, h], kp[kept[0, h].long(), h])
+
+
+def test_keys_beyond_four_gigabytes():
+    n, hkv, d = 2_200_000, 8, 128
+    k = torch.empty(n, hkv, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    for a in range(0, n, 200_000):
+        k[a:a + 200_000] = normal(a, min(200_000, n - a), hkv, d, dtype=torch.bfloat16)
+        v[a:a + 200_000] = normal(a + 1, min(200_000, n - a), hkv, d, dtype=torch.bfloat16)
+    q = normal(9, 3, hkv, d, dtype=torch.bfloat16)
+    at = [2_199_990, 2_150_000, 17]  # each query's own needle, two of them behind 4 GB
+    for i, t in enumerate(at):
+        k[t] = q[i] * 4
+    got = spd.prefill_attention(q, k, v, check=True)
+    for i, t in enumerate(at):
+        assert (got[i] - v[t].float()).abs().max() < 1e-2
+
+
+# ---- calls in a row --------------------------------------------------------------
+
+def test_calls_of_every_kind_in_a_row_on_one_stream():
+    """Kernels start before the ones before them have ended: calls whose inputs the
+    call before wrote, without a pause, give what they give alone."""
+    hq, hkv, d, dt = 8, 2, 128, torch.bfloat16
+    c = new_cache(hq, hkv, d, "bf16", 64, 16, 200, 60, 4096)
+    doc = c.seq_create()
+    c.kv_append([doc], normal(1, 1, 700, hkv, d, dtype=dt), normal(2, 1, 700, hkv, d, dtype=dt))
+    sizes = [1, 3, 9]
+    groups = [[c.seq_create() for _ in range(n)] for n in sizes]
+    for g in groups:
+        c.kv_append(g, normal(3, len(g), 40, hkv, d, dtype=dt), normal(4, len(g), 40, hkv, d, dtype=dt))
+    long_k, long_v = normal(7, 3000, hkv, d, dtype=dt), normal(8, 3000, hkv, d, dtype=dt)
+
+    def chain(wait):
+        outs, x = [], normal(5, 30, hq, d, dtype=dt)
+        for r in range(6):
+            x = spd.prefill_attention(x, long_k, long_v, out_dtype=dt)
+            if wait:
+                torch.cuda.synchronize()
+            for n, g in zip(sizes, groups):
+                y = c.shared_prefix_attention(x[:n], doc, g, out_dtype=dt)
+                if wait:
+                    torch.cuda.synchronize()
+                x[:n] += y
+                w = torch.zeros(n, hkv, 64, device="cuda")
+                c.shared_prefix_attention(x[:n], doc, g, weights_in=w, weights_out=w, out_dtype=dt)
+                dst = [c.seq_create() for _ in g]
+                kept, kw = c.kv_evict(g, dst, 24, 4, w)
+                y = c.shared_prefix_attention(x[:n], doc, dst, out_dtype=dt)
+                if wait:
+                    torch.cuda.synchronize()
+                x[:n] -= y
+                for i in reversed(dst):
+                    c.seq_free(i)
+                outs += [w, kept, kw]
+            outs.append(x.clone())
+        return outs
+
+    alone, row = chain(True), chain(False)
+    c.check_status()
+    for a, b in zip(alone, row):
+        assert torch.equal(a, b)
