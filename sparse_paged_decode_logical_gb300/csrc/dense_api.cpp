@@ -230,7 +230,7 @@ spd_status plan_prompt(const spd_dense_config *c, int Lq, int Lk, int sms, Promp
 // Query rows (sequences x heads per kv head) of a prefix: up to kFewRows go
 // with the sequences' own tokens (dense_decode), up to kManyRows over dense_few
 // (128 channels; 64 stay with dense_decode), more over dense_tc.
-constexpr int kFewRows = 8, kManyRows = 32;
+constexpr int kFewRows = 8, kManyRows = 32, kFewTile = 32;
 
 struct SharedPlan {
   bool tc = false, few = false;                // the prefix by dense_tc, dense_few
@@ -247,10 +247,10 @@ struct SharedPlan {
 void plan_shared(const spd_ctx *c, const CtxView &v, int prefix_len, const int *ids, int n,
                  bool weights, bool f32, DecodeSeq *seqs, SharedPlan *z) {
   const int Hkv = v.cfg->num_kv_heads, d = v.cfg->head_dim, rows = n * v.G;
-  z->tc = prefix_len > 0 && rows > kManyRows;
+  z->tc = prefix_len > 0 && rows > (d == 128 ? kManyRows : 32);
   z->few = prefix_len > 0 && !z->tc && rows > kFewRows && d == 128;
   const int tk = z->few ? kFewKeys : kDecodeTile;  // keys per tile of the prefix
-  z->prefix_rows = z->few ? rows : kDecodeRows;
+  z->prefix_rows = z->few ? std::min(rows, kFewTile) : kDecodeRows;
   const int pt = prefix_len > 0 && !z->tc ? (prefix_len + tk - 1) / tk : 0;
   const int pu = pt > 0 ? Hkv * ((rows + z->prefix_rows - 1) / z->prefix_rows) : 0;
   auto tiles_of = [](int tokens) { return (tokens + kDecodeTile - 1) / kDecodeTile; };

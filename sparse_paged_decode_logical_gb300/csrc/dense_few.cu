@@ -160,11 +160,16 @@ __global__ void __launch_bounds__(kFewThreads, NR <= 16 ? 3 : 2)
   constexpr int kCols = 2 * NR < 32 ? 32 : 2 * NR;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  // ---- the item: kv head, split, its tiles of 128 keys ----
-  const int hk = blockIdx.x / p.prefix_ns, split = blockIdx.x % p.prefix_ns;
-  const int rows = p.prefix_rows, slot = p.prefix_slot, L = p.prefix_len;
+  // ---- the item: row tile, kv head, split, its tiles of 128 keys.  Row tiles of
+  // the same keys lie next to one another: the second finds them in L2 ----
+  const int row_tiles = (p.n * p.G + p.prefix_rows - 1) / p.prefix_rows;
+  const int row_tile = blockIdx.x % row_tiles, rest = blockIdx.x / row_tiles;
+  const int hk = rest / p.prefix_ns, split = rest % p.prefix_ns;
+  const int row0 = row_tile * p.prefix_rows, rows = min(p.prefix_rows, p.n * p.G - row0);
+  const int slot = p.prefix_slot, L = p.prefix_len;
   const int tile0 = split * p.prefix_tpi;
-  const size_t at_row = (size_t)blockIdx.x * p.prefix_rows;
+  const size_t at_row =
+      ((size_t)(row_tile * p.Hkv + hk) * p.prefix_ns + split) * p.prefix_rows;
   float2 *ml_out = p.pre_ml + at_row;
   float *o_out = p.pre_o + at_row * kFewD;
   const int tile1 = min(tile0 + p.prefix_tpi, (L + kFewKeys - 1) / kFewKeys);
@@ -283,7 +288,7 @@ __global__ void __launch_bounds__(kFewThreads, NR <= 16 ? 3 : 2)
       const int r = x >> 4, ch = x & 15;
       uint4 v = make_uint4(0, 0, 0, 0);
       if (r < rows) {
-        const int sq = r / p.G, h = hk * p.G + r % p.G;
+        const int sq = (row0 + r) / p.G, h = hk * p.G + (row0 + r) % p.G;
         v = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) +
                                              ((size_t)sq * p.Hq + h) * kFewD + ch * 8);
       }
@@ -292,7 +297,7 @@ __global__ void __launch_bounds__(kFewThreads, NR <= 16 ? 3 : 2)
     for (int x = tid; x < (kSplitP ? 4 : 2) * NR * 8; x += 128)
       *reinterpret_cast<uint4 *>(smem + Sm::kP + x * 16) = make_uint4(0, 0, 0, 0);
     if (tid < NR) {
-      const int sq = tid / p.G, h = hk * p.G + tid % p.G;
+      const int sq = (row0 + tid) / p.G, h = hk * p.G + (row0 + tid) % p.G;
       const bool live = tid < rows;
       rowc[tid] = make_float2(
           live && p.rule.slopes ? p.rule.slopes[h] * 1.4426950408889634f : 0.f,

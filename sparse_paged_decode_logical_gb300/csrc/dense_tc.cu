@@ -28,10 +28,10 @@
 // (bf16) or 22 (fp16) of each weight.  Outputs of 16 bits round P once, which
 // is an error of the same size as the rounding of the output.
 //
-// A matrix leaves out the pairs before and behind its rows' keys.  With `dup` (at most
-// 128 rows) both matrices hold the same rows and take turns at the pairs, so
-// that one's softmax still runs beside the other's products; each then counts
-// as a split of its own.  Splits leave unnormalised sums to a combining kernel.
+// A matrix leaves out the pairs before and behind its rows' keys.  With `dup` (at
+// most 128 rows) both matrices hold the same rows, and matrix m takes block m of
+// every pair; each then counts as a split of its own.  Splits leave unnormalised
+// sums to a combining kernel.
 //
 // Blocks that some row attends only in part ("edge" blocks) are masked, and
 // their V tile is scanned: a value that is not finite is replaced by zero in
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
     dense_tc_kernel(const __grid_constant__ DenseTcParams p) {
   using Sm = DtSmem<D>;
   constexpr int KB = Sm::KB, S = Sm::kStages;
-  const bool pair_s = !kRule && !kSplitP && p.pair_s;
+  const bool pair_s = !kRule && !kSplitP && p.pair_s && !p.dup;
   extern __shared__ uint8_t dt_smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(dt_smem_raw) + 1023) & ~uintptr_t(1023));
@@ -277,15 +277,14 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
   // split begins at key0_of(j); pair pp holds blocks 2 pp and 2 pp + 1.
   const bool desc = kRule && p.rule.slopes != nullptr;
   auto key0_of = [&](int j) { return (desc ? kb0 + n - 1 - j : kb0 + j) * kDenseBlock; };
-  // the pairs [first, last) that matrix m computes, or with dup every second
-  // one (m's all lie in stage m)
+  // the pairs [first, last) that matrix m computes (with dup its block m of each)
   auto pair_first = [&](int m) {
     const int past = desc ? kb0 + n - (rg[4 * m + 1] + kDenseBlock - 1) / kDenseBlock
                           : rg[4 * m] / kDenseBlock - kb0;  // blocks before its keys
     return p.dup ? 0 : min(np, max(0, past) / 2);
   };
   auto pair_last = [&](int m) {
-    if (p.dup) return np;
+    if (p.dup) return (n + 1 - m) / 2;
     if (rg[4 * m] >= rg[4 * m + 1]) return 0;
     const int blocks = desc ? kb0 + n - rg[4 * m] / kDenseBlock  // up to its last key's
                             : (rg[4 * m + 1] + kDenseBlock - 1) / kDenseBlock - kb0;
@@ -419,10 +418,10 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&bars[Sm::kBarVC + s]);
-        // a matrix that has no more pairs (or with dup not this one) frees the
-        // stages here; the pairs before its first it frees itself
+        // a matrix that has no more pairs frees the stages here; the pairs before
+        // its first it frees itself
         for (int m = 0; m < 2; ++m)
-          if (p.dup ? (pp & 1) != m : pp >= pair_last(m)) {
+          if (pp >= pair_last(m)) {
             mbar_arrive(&bars[Sm::kBarKE + s]);
             mbar_arrive(&bars[Sm::kBarVE + s]);
           }
@@ -441,7 +440,6 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
     const uint64_t dv = umma_desc_sw128(smem_u32(smem + Sm::kV), 8192, 1024);
     const uint32_t t_o = tmem + 256 + D * m;
     const int begin = pair_first(m), end = pair_last(m), dup = p.dup;
-    auto mine = [&](int pp) { return dup ? (pp & 1) == m : pp >= begin && pp < end; };
     auto wwait = [&](uint64_t *bar, uint32_t parity) {
       return __all_sync(0xffffffffu, dt_wait(bar, parity, fail));
     };
@@ -457,14 +455,13 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
       if (!(ok = wwait(&bars[Sm::kBarVC + pp % S], (pp / S) & 1))) break;
       if (lane == 0) mbar_arrive(&bars[Sm::kBarVE + pp % S]);
     }
-    const int last = dup ? ((np - 1) & 1) == m ? np - 1 : np - 2 : end - 1;  // its last pair
-    // the S side runs two blocks ahead of the P . V side: block su of pair sp
-    int sp = begin, su = 0;
+    // the S side runs two blocks ahead of the P . V side: block su of pair sp, the
+    // matrix's block sb (buffer sb & 1)
+    int sp = begin, su = dup ? m : 0, sb = 0;
     auto issue_s = [&]() {
-      while (sp < np && !mine(sp)) ++sp;
-      if (sp >= np) return;
+      if (sp >= end) return;
       const int s = sp % S;
-      if (su == 0 && !(ok = wwait(&bars[Sm::kBarKF + s], (sp / S) & 1))) return;
+      if ((dup || su == 0) && !(ok = wwait(&bars[Sm::kBarKF + s], (sp / S) & 1))) return;
       tc_fence_after();
       any = true;
       const bool both = pair_s && 2 * sp + 1 < n;
@@ -472,31 +469,32 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint64_t off = (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-        umma_f16_warp(tmem + 128 * m + 64 * su, dq + off, kt + off, both ? idesc_s2 : idesc_s,
-                      kk > 0);
+        umma_f16_warp(tmem + 128 * m + 64 * (sb & 1), dq + off, kt + off,
+                      both ? idesc_s2 : idesc_s, kk > 0);
       }
-      umma_commit_warp(&bars[Sm::kBarSF + 2 * m + su]);
+      umma_commit_warp(&bars[Sm::kBarSF + 2 * m + (sb & 1)]);
       if (both) umma_commit_warp(&bars[Sm::kBarSF + 2 * m + 1]);
-      if (both || su == 1 || 2 * sp + 1 == n) {
+      sb += both ? 2 : 1;
+      if (dup || both || su == 1 || 2 * sp + 1 == n) {
         umma_commit_warp(&bars[Sm::kBarKE + s]);
         ++sp;
-        su = 0;
+        su = dup ? m : 0;
       } else {
         su = 1;
       }
     };
     if (ok) issue_s();
     if (ok && !pair_s) issue_s();
-    int i = 0, blocks = 0;  // pairs, blocks of this matrix so far
-    for (int pp = 0; pp < np && ok; ++pp) {
-      const int s = pp % S, nbk = min(2, n - 2 * pp);
-      if (!mine(pp)) continue;
+    int blocks = 0;  // of this matrix so far
+    for (int pp = begin; pp < end && ok; ++pp) {
+      const int s = pp % S, u0 = dup ? m : 0, u1 = dup ? m + 1 : min(2, n - 2 * pp);
       if (!(ok = wwait(&bars[Sm::kBarVC + s], (pp / S) & 1))) break;
-      for (int u = 0; u < nbk; ++u, ++blocks) {
-        if (!(ok = wwait(&bars[Sm::kBarPF + 2 * m + u], i & 1))) break;
+      for (int u = u0; u < u1; ++u, ++blocks) {
+        const int buf = blocks & 1;
+        if (!(ok = wwait(&bars[Sm::kBarPF + 2 * m + buf], (blocks >> 1) & 1))) break;
         tc_fence_after();
         const uint64_t vt = dv + (uint64_t)((s * Sm::kStageBytes + u * KB * 8192) >> 4);
-        const uint32_t pa = tmem + 128 * m + 64 * u;
+        const uint32_t pa = tmem + 128 * m + 64 * buf;
 #pragma unroll
         for (int part = 0; part < (kSplitP ? 2 : 1); ++part)
 #pragma unroll
@@ -504,20 +502,19 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
             umma_f16_ts_warp(t_o, pa + 32 * part + 8 * kk, vt + (uint64_t)((kk * 2048) >> 4),
                              idesc_o, blocks > 0 || part > 0 || kk > 0);
         umma_commit_warp(&bars[Sm::kBarOD + m]);
-        if (u == nbk - 1) {
+        if (u == u1 - 1) {
           if (pair_s) umma_commit_warp(&bars[Sm::kBarOP + m]);
           umma_commit_warp(&bars[Sm::kBarVE + s]);
-          if (pp == last) umma_commit_warp(&bars[Sm::kBarOF + m]);
+          if (pp == end - 1) umma_commit_warp(&bars[Sm::kBarOF + m]);
         }
-        if (sp < np && (!pair_s || u == nbk - 1)) {  // the next S goes where this P was
-          if (!(ok = pair_s ? wwait(&bars[Sm::kBarOP + m], i & 1)
+        if (sp < end && (!pair_s || u == u1 - 1)) {  // the next S goes where this P was
+          if (!(ok = pair_s ? wwait(&bars[Sm::kBarOP + m], (pp - begin) & 1)
                             : wwait(&bars[Sm::kBarOD + m], blocks & 1)))
             break;
           issue_s();
           if (!ok) break;
         }
       }
-      ++i;
     }
     if (any) {  // every MMA of this warp done before the CTA frees its memory
       umma_commit_warp(&bars[Sm::kBarDR + m]);
@@ -528,7 +525,7 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
     const int m = warp >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t t_o = lanes + 256 + D * m;
-    const int begin = p.dup ? m : pair_first(m), end = pair_last(m), step = p.dup ? 2 : 1;
+    const int begin = pair_first(m), end = pair_last(m);
     const float slope = kRule && p.rule.slopes && tok < p.Lq ? p.rule.slopes[h_row] * 1.4426950408889634f : 0.f;
     // a prompt's distances count from the row's nearest key, so that the bias of
     // the keys that matter keeps its bits however far they are (the nearest key
@@ -539,22 +536,23 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
     const bool idle = __all_sync(0xffffffffu, rend == 0);  // rows that attend nothing
     float m_run = -CUDART_INF_F, l_run = 0.f;
     bool ok = true;
-    int i = 0, blocks = 0;
-    for (int pp = begin; pp < end && ok; pp += step, ++i) {
-      const int nbk = min(2, n - 2 * pp);
+    int blocks = 0;
+    for (int pp = begin; pp < end && ok; ++pp) {
+      const int u1 = p.dup ? m + 1 : min(2, n - 2 * pp);
 #pragma unroll 1
-      for (int u = 0; u < nbk; ++u, ++blocks) {
-        ok = dt_wait(&bars[Sm::kBarSF + 2 * m + u], i & 1, fail);
+      for (int u = p.dup ? m : 0; u < u1; ++u, ++blocks) {
+        const int buf = blocks & 1;
+        ok = dt_wait(&bars[Sm::kBarSF + 2 * m + buf], (blocks >> 1) & 1, fail);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;  // the tensor-memory accesses are warp-wide
         tc_fence_after();
         if (idle) {  // what the products make of these rows is never read
           if (lane == 0) {
-            mbar_arrive(&bars[Sm::kBarPF + 2 * m + u]);
+            mbar_arrive(&bars[Sm::kBarPF + 2 * m + buf]);
             if (m == 0 && blocks == 0) mbar_arrive(&bars[Sm::kBarLag]);
           }
           continue;
         }
-        const uint32_t t_s = lanes + 128 * m + 64 * u;
+        const uint32_t t_s = lanes + 128 * m + 64 * buf;
         const int key0 = key0_of(2 * pp + u);
         uint32_t s[64];
         tmem_ld64_sync(t_s, s);
@@ -608,17 +606,28 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
                 s[c + 1] = __float_as_uint(x.y);
               }
             }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              s[c] = __float_as_uint(__uint_as_float(s[c]) * p.rule.scale_log2);
           }
           if (p.rule.slopes) {
+            // keys at or before every row of the warp: the distance needs no
+            // absolute value, and the bias is a line over the block
             const float d0 = (float)(pos - key0);
+            const float2 sc2 = f2_dup(p.rule.cap_out > 0.f ? 1.f : p.rule.scale_log2);
+            if (__all_sync(0xffffffffu, d0 >= 63.f)) {
+              const float2 up = f2_dup(slope), b0 = f2_dup(-slope * (d0 - near));
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              s[c] = __float_as_uint(
-                  fmaf(-slope, fabsf(d0 - (float)c) - near, __uint_as_float(s[c])));
+              for (int c = 0; c < 64; c += 2) {
+                const float2 t = f2_fma(make_float2((float)c, (float)(c + 1)), up, b0);
+                const float2 x = f2_fma(
+                    make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, t);
+                s[c] = __float_as_uint(x.x);
+                s[c + 1] = __float_as_uint(x.y);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                s[c] = __float_as_uint(fmaf(-slope, fabsf(d0 - (float)c) - near,
+                                            __uint_as_float(s[c]) * sc2.x));
+            }
           }
         }
         if (edge) {
@@ -689,7 +698,7 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&bars[Sm::kBarPF + 2 * m + u]);
+          mbar_arrive(&bars[Sm::kBarPF + 2 * m + buf]);
           if (m == 0 && blocks == 0) mbar_arrive(&bars[Sm::kBarLag]);
         }
       }
