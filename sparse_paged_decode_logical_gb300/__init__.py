@@ -717,7 +717,7 @@ def prefill_attention(q, k, v, key_begin=None, key_end=None, scale=0.0, softcap=
                                  % (Lq, q.device))
         kb, ke = key_begin.data_ptr(), key_end.data_ptr()
     if out is None:
-        out = torch.empty(shape, dtype=odt, device=q.device)
+        out = q.new_empty(shape, dtype=odt)
     else:
         if out_dtype is None and out.dtype is not odt:
             return prefill_attention(q, k, v, key_begin, key_end, scale, softcap, slopes, out.dtype,

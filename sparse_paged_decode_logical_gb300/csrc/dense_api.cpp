@@ -230,7 +230,10 @@ spd_status plan_prompt(const spd_dense_config *c, int Lq, int Lk, int sms, Promp
 // Query rows (sequences x heads per kv head) of a prefix: up to kFewRows go
 // with the sequences' own tokens (dense_decode), up to kManyRows over dense_few
 // (128 channels; 64 stay with dense_decode), more over dense_tc.
-constexpr int kFewRows = 8, kManyRows = 32, kFewTile = 32;
+// A brief prefix (tokens times groups of 16 rows) goes with the own tokens
+// whatever its rows: one kernel (12 and 48 rows over 1,000 tokens 14 and 16 us
+// against 16 and 19; 96 over 1,000 23 against 20, 12 over 4,099 20 against 18).
+constexpr int kFewRows = 8, kManyRows = 32, kFewTile = 32, kBriefWork = 4000;
 
 struct SharedPlan {
   bool tc = false, few = false;                // the prefix by dense_tc, dense_few
@@ -247,8 +250,9 @@ struct SharedPlan {
 void plan_shared(const spd_ctx *c, const CtxView &v, int prefix_len, const int *ids, int n,
                  bool weights, bool f32, DecodeSeq *seqs, SharedPlan *z) {
   const int Hkv = v.cfg->num_kv_heads, d = v.cfg->head_dim, rows = n * v.G;
-  z->tc = prefix_len > 0 && rows > (d == 128 ? kManyRows : 32);
-  z->few = prefix_len > 0 && !z->tc && rows > kFewRows && d == 128;
+  const bool brief = (long long)((rows + kDecodeRows - 1) / kDecodeRows) * prefix_len <= kBriefWork;
+  z->tc = !brief && rows > kManyRows;
+  z->few = !brief && !z->tc && rows > kFewRows && d == 128;
   const int tk = z->few ? kFewKeys : kDecodeTile;  // keys per tile of the prefix
   z->prefix_rows = z->few ? std::min(rows, kFewTile) : kDecodeRows;
   const int pt = prefix_len > 0 && !z->tc ? (prefix_len + tk - 1) / tk : 0;

@@ -530,7 +530,7 @@ def test_pools_beyond_four_gigabytes():
     low = c.seq_create()
     c.seq_reserve(low, (pages - 46) * page)
     doc = c.seq_create()
-    kp, vp = normal(1, 3000, hkv, d, dtype=dt), normal(2, 3000, hkv, d, dtype=dt)
+    kp, vp = normal(1, 4100, hkv, d, dtype=dt), normal(2, 4100, hkv, d, dtype=dt)
     c.kv_append([doc], kp[None], vp[None])
     assert min(c.page_table(doc)) * page * hkv * d * 2 > 1 << 32
     for n in (2, 12, 40):  # each of the prefix's kernels
@@ -542,15 +542,15 @@ def test_pools_beyond_four_gigabytes():
         c.check_status()
         ref, ab, mag, _ = shared(q, kp, vp, list(ko), list(vo), d ** -0.5, 0.0, None)
         assert bool(((got.double() - ref).abs() <=
-                     tolerance(ref, ab, mag, d, 3020, dt, torch.float32, 0.0)).all())
+                     tolerance(ref, ab, mag, d, 4120, dt, torch.float32, 0.0)).all())
         for i in ids:
             c.seq_free(i)
-    w = normal(6, 1, hkv, 3000).abs()
+    w = normal(6, 1, hkv, 4100).abs()
     dst = c.seq_create()
     kept, _ = c.kv_evict([doc], [dst], 500, 20, w)
     c.check_status()
     for h in range(hkv):
-        assert kept[0, h].tolist() == kept_positions(w[0, h].cpu(), 3000, 500, 20)
+        assert kept[0, h].tolist() == kept_positions(w[0, h].cpu(), 4100, 500, 20)
         assert torch.equal(cache_rows(c, dst, hkv, d, dt, page)[:, h], kp[kept[0, h].long(), h])
 
 
@@ -614,3 +614,41 @@ def test_calls_of_every_kind_in_a_row_on_one_stream():
     c.check_status()
     for a, b in zip(alone, row):
         assert torch.equal(a, b)
+
+
+# ---- every kernel of a prefix, by its rows ----------------------------------------
+
+@pytest.mark.parametrize("n,hq,hkv", [(3, 4, 1), (4, 8, 2), (5, 4, 1), (8, 8, 2), (31, 1, 1),
+                                      (33, 1, 1), (8, 8, 1), (25, 4, 1), (32, 8, 2), (33, 4, 1),
+                                      (65, 4, 1)])
+@pytest.mark.parametrize("lp,page", [(4500, 256), (5009, 16), (4160, 48)])
+@pytest.mark.parametrize("kind", [dict(), dict(out="same", weights=True),
+                                  dict(softcap=25.0, gain=5.0, slopes=True),
+                                  dict(softcap=25.0, out="same", gain=5.0)])
+def test_shared_prefix_kernels(n, hq, hkv, lp, page, kind):
+    lens = [(7 * i) % 40 for i in range(n)]
+    check_shared(n, lp, lens, hq, hkv, 128, "bf16" if page == 16 else "fp16", page=page, **kind)
+
+
+@pytest.mark.parametrize("n", [4, 40])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_shared_rows_behind_the_end_hold_anything(n, bad):
+    """Pages are NaN before they are filled; here the rows behind the prefix's end
+    are overwritten too."""
+    hq, hkv, d, page, dt = 4, 1, 128, 64, torch.bfloat16
+    c = new_cache(hq, hkv, d, "bf16", page, 16, 200, n + 1, 8192)
+    kp, vp = normal(1, 4501, hkv, d, dtype=dt), normal(2, 4501, hkv, d, dtype=dt)
+    doc = c.seq_create()
+    c.kv_append([doc], kp[None], vp[None])
+    last = c.page_table(doc)[-1]
+    for f in ("k_pool", "v_pool"):
+        c.buffers[f].view(dt).view(-1, hkv, page, d)[last, :, 4501 % page:] = bad
+    ids = [c.seq_create() for _ in range(n)]
+    ko, vo = normal(3, n, 3, hkv, d, dtype=dt), normal(4, n, 3, hkv, d, dtype=dt)
+    c.kv_append(ids, ko, vo)
+    q = normal(5, n, hq, d, dtype=dt)
+    got = c.shared_prefix_attention(q, doc, ids)
+    c.check_status()
+    ref, ab, mag, _ = shared(q, kp, vp, list(ko), list(vo), d ** -0.5, 0.0, None)
+    assert bool(((got.double() - ref).abs() <=
+                 tolerance(ref, ab, mag, d, 4504, dt, torch.float32, 0.0)).all())
