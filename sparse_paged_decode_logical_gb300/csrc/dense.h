@@ -52,7 +52,8 @@ struct ScoreRule {
   float cap_out;         // cap * log2(e); 0: no cap
   int rough;             // 2^-22 of the cap does not show in 16-bit weights
   float poly[5];         // cap_out times tanh(z) / z as a polynomial in z^2, |z| <= 0.6
-  float quick;           // a cap without slopes: scores q.k up to this may take quick_poly; 0: none
+  float quick, quick_floor;  // a cap of 30 or more without slopes: rows whose largest q.k lies
+                             // between these may take quick_poly; quick 0: none
   float quick_poly[5];   // the capped score over q.k as a polynomial in (q.k)^2
   const float *slopes;   // [Hq] or null
 };

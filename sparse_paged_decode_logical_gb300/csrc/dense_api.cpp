@@ -146,7 +146,8 @@ ScoreRule make_rule(const spd_score_rule *r, int d) {
   }
   x.slopes = r ? r->slopes : nullptr;
   x.rough = x.cap_out <= 256.f;
-  if (x.cap_out > 0.f && !x.slopes && x.z_in > 1e-4f && x.z_in < 1e4f) {  // (z_in^8 fits fp32)
+  if (x.cap_out > 0.f && r->softcap >= 30.f && !x.slopes && x.z_in > 1e-4f && x.z_in < 1e4f) {
+    // (z_in^8 fits fp32)
     // tanh(z) / z in z^2, |z| <= 0.75, times scale log2(e) and in (q.k)^2
     constexpr double kTanh[5] = {0.999999463558197, -0.3332825005054474, 0.13258983194828033,
                                  -0.050056301057338715, 0.01292963046580553};
@@ -154,6 +155,7 @@ ScoreRule make_rule(const spd_score_rule *r, int d) {
     const double z2 = scale / r->softcap * (scale / r->softcap);
     for (int i = 0; i < 5; ++i, f *= z2) x.quick_poly[i] = (float)(f * kTanh[i]);
     x.quick = (float)(0.7499 * r->softcap / scale);
+    x.quick_floor = (float)(-0.25 * r->softcap / scale);
   }
   return x;
 }

@@ -557,18 +557,28 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
         uint32_t s[64];
         tmem_ld64_sync(t_s, s);
         const bool edge = is_edge(key0);
-        // a cap alone, 16-bit output, scores within the polynomial's range: the
-        // cap is monotonic, so the row's max is taken first and the polynomial
-        // goes into the exponent (1.5 instructions per score)
+        auto row_max = [&] {
+          float mq[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mq[k] = __uint_as_float(s[k]);
+#pragma unroll
+          for (int c = 4; c < 60; c += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mq[k] = fmax3f(mq[k], __uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1]));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mq[k] = fmaxf(mq[k], __uint_as_float(s[60 + k]));
+          return fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+        };
+        // a cap alone, 16-bit output, largest scores within the polynomial's range:
+        // the cap is monotonic, so the row's max is taken first and the polynomial
+        // goes into the exponent
         bool quick = false;
+        float top = 0.f;
         if constexpr (kRule && !kSplitP) {
           if (p.rule.quick > 0.f && !edge) {
-            float big = 0.f;
-#pragma unroll
-            for (int c = 0; c < 64; c += 2)
-              big = fmaxf(fmaxf(big, fabsf(__uint_as_float(s[c]))),
-                          fabsf(__uint_as_float(s[c + 1])));
-            quick = __all_sync(0xffffffffu, big <= p.rule.quick);
+            top = row_max();
+            quick = __all_sync(0xffffffffu, top <= p.rule.quick && top >= p.rule.quick_floor);
           }
         }
         if (kRule && !quick) {
@@ -636,17 +646,7 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
           for (int c = 0; c < 64; ++c)
             if (c < c0 || c >= c1) s[c] = 0xff800000u;  // -inf
         }
-        float mq[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mq[k] = __uint_as_float(s[k]);
-#pragma unroll
-        for (int c = 4; c < 60; c += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mq[k] = fmax3f(mq[k], __uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1]));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mq[k] = fmaxf(mq[k], __uint_as_float(s[60 + k]));
-        const float top = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+        if (!quick) top = row_max();
         const float mx = quick ? cap_quick(p.rule, f2_dup(top), f2_dup(0.f)).x : top * sc;
         const bool need = mx > m_run + kDtRescaleAbove;
         if (__any_sync(0xffffffffu, need)) {

@@ -652,3 +652,17 @@ def test_shared_rows_behind_the_end_hold_anything(n, bad):
     ref, ab, mag, _ = shared(q, kp, vp, list(ko), list(vo), d ** -0.5, 0.0, None)
     assert bool(((got.double() - ref).abs() <=
                  tolerance(ref, ab, mag, d, 4504, dt, torch.float32, 0.0)).all())
+
+
+@pytest.mark.parametrize("level", [-1.2, -0.8, -0.26, 0.0, 0.6, 0.74, 0.8, 1.5])
+def test_capped_scores_around_every_level(level):
+    """All of a row's scores near one part of the cap's curve."""
+    d, dt, cap, n = 128, torch.bfloat16, 30.0, 500
+    q, k, v = (normal(i, n, h, d, dtype=dt) for i, h in ((1, 4), (2, 2), (3, 2)))
+    q[..., 0], k[..., 0] = 16.0, level * cap * d ** 0.5 / 16.0
+    b, e = intervals("causal", n, n)
+    for out in (dt, torch.float32):
+        got = spd.prefill_attention(q, k, v, softcap=cap, out_dtype=out, check=True)
+        ref, ab, mag = prompt(q, k, v, b, e, d ** -0.5, cap, None)
+        assert bool(((got.double() - ref).abs() <=
+                     tolerance(ref, ab, mag, d, n, dt, out, cap)).all())
