@@ -39,9 +39,9 @@ __device__ __forceinline__ float2 cap_16bit(const ScoreRule &r, float2 s) {
 // cap tanh(s / cap) + add in base-2 units by a polynomial of five terms in s^2 that
 // is 5e-7 of the score off for |s / cap| <= 0.75, for the scores of a row whose
 // largest lies in [-0.25, 0.75] cap, cap >= 30.  What lies below -0.75 cap has a
-// weight under e^(-0.39 cap) = 8e-6 of the largest; there the polynomial stays
-// monotonic and on the lower side (8e-4 of the score at -cap, then falling away
-// to 0 weight), which 8,192 such keys show as 2e-5 of the sum.
+// weight under e^(-0.39 cap) of the largest; there the polynomial stays monotonic
+// and on the lower side (8e-4 of the score at -cap, then falling away to 0 weight),
+// an error of at most 5e-9 of the largest weight.
 __device__ __forceinline__ float2 cap_quick(const ScoreRule &r, float2 s, float2 add) {
   const float2 u = f2_mul(s, s);
   float2 p = f2_dup(r.quick_poly[4]);
