@@ -79,7 +79,6 @@ struct DenseTcParams {
   int out_f32;             // type of out
   int Lq, Lk, Hq, Hkv, G, lhp, HG;  // HP = 2^lhp heads per matrix, HG = G / HP head groups
   int tiles, nsplit;
-  int pair_s;              // plain scores, 16-bit output: S of two blocks in one product
   int dup;                 // both matrices hold the same 128 rows, each takes every second block
   int P, max_pp, num_phys, box_rows;
   int pos0;                // prompt: position of query 0 (Lk - Lq)

@@ -160,10 +160,6 @@ ScoreRule make_rule(const spd_score_rule *r, int d) {
   return x;
 }
 
-// Rows at least this long take S of two blocks in one product (49,152 keys: 1,318
-// us, with two products 1,345; 4,096 packed tokens 61 either way).
-constexpr int kPairKeys = 8192;
-
 // ---- prompt attention ------------------------------------------------------------
 
 struct PromptPlan {
@@ -204,12 +200,12 @@ spd_status plan_prompt(const spd_dense_config *c, int Lq, int Lk, int sms, Promp
       1, std::min<long long>(most, std::min<long long>(sms / units, blocks / 4)));
   // A few waves of equal units (a chunk over a much longer row) leave the last
   // one part empty: cut into s, they take ceil(units s / SMs) / s unit times, for
-  // the price of the partial sums.  (0.9 us per block of a unit, 0.045 us per
+  // the price of the partial sums.  (0.85 us per block of a unit, 0.045 us per
   // cut unit written and read: 256 units of 768 blocks in four cuts 1,320 us, whole
   // 1,412.  Packed documents, where units are short and uneven, stay whole.)
   if (!z->dup && units > sms && units <= 8LL * sms && Lk >= 4LL * Lq) {
     auto cost = [&](int s) {
-      return (double)((units * s + sms - 1) / sms) / s * blocks * 0.9 +
+      return (double)((units * s + sms - 1) / sms) / s * blocks * 0.85 +
              (s > 1 ? units * s * 0.045 + 10.0 : 0.0);
     };
     for (int s = 2; s <= 8 && s * 16 <= blocks; ++s)
@@ -462,7 +458,6 @@ spd_status spd_prefill_attention(const spd_dense_config *cfg, int q_len, int kv_
   p.nsplit = z.nsplit;
   p.dup = z.dup;
   p.pos0 = kv_len - q_len;
-  p.pair_s = kv_len >= kPairKeys;
   cudaStream_t st = (cudaStream_t)stream;
   if (launch_dense_tc(p, cfg->dtype, d, p.out_f32 != 0, st) != cudaSuccess) return SPD_ERR_CUDA;
   if (z.partial && launch_dense_prompt_combine(p, cfg->dtype, d, out, st) != cudaSuccess)
@@ -615,7 +610,6 @@ spd_status spd_shared_prefix_attention(spd_ctx *c, const void *q, int prefix_id,
                            (size_t)z.tiles * cfg.num_kv_heads * z.nsplit * kDenseRows))
         return fail_message(c, SPD_ERR_CUDA, "cuTensorMapEncodeTiled failed");
       t.partial = 1;
-      t.pair_s = 0;
       t.part_o = p.pre_o;
       t.part_ml = p.pre_ml;
       t.v = nullptr;

@@ -9,20 +9,20 @@
 // rows, a row being one (token, query head of the group) pair, so that the
 // heads that share K and V share their tiles too.  Keys come in blocks of 64,
 // two blocks (a pair) per stage of two-stage TMA rings of K and of V:
-//   S_m = Q_m . K^T     tcgen05.mma M 128 x N 64 or 128, fp32 in tensor memory,
-//                       block u of a pair in the matrix's buffer u;
+//   S_m = Q_m . K^T     tcgen05.mma M 128 x N 64, fp32 in tensor memory, the
+//                       matrix's blocks in two buffers in turn;
 //   softmax             one row per thread: score rule, mask, online max and
 //                       sum in fp32, weights written back over S as 16 bits;
 //   O_m += P_m . V      A = P from tensor memory, fp32 accumulation.
-// An S of N 64 takes as long as one of N 128 (the read of Q's 128 rows bounds
-// both), but two buffers let S of the block after next start as soon as P . V
-// of this one is done: the hand-overs between the roles (about 300 cycles each)
-// and the products of one buffer then pass while the softmax works on the
-// other.  Where the softmax is the longer side (score rules, split weights)
-// that wins: 8,192 capped tokens 678 us against 838, 2,501 tokens of 64
-// channels with a bias and fp32 output 59 against 70.  Plain scores with 16-bit
-// output over a long row keep the tensor pipe busy and take one N 128 product
-// per pair (pair_s): 2,048 queries over 49,152 keys 1,318 us against 1,345.
+// An S of N 64 takes longer than half of one of N 128 (the read of Q's 128 rows
+// bounds it), but two buffers let S of the block after next start as soon as
+// P . V of this one is done: the hand-overs between the roles (about 300 cycles
+// each) and the products of one buffer then pass while the softmax works on the
+// other.  One product of N 128 per pair, with the next S behind the whole pair's
+// P . V, took 1,319 us against 1,209 (2,048 queries over 49,152 keys), 461 against
+// 423 (8,192 causal), 2,307 against 2,052 (8,192 over 16,384, 64 channels), 831
+// against 635 (8,192 capped) and 67 against 54 (2,501 tokens with a bias and fp32
+// output, 64 channels).
 // Outputs of 32 bits (kSplitP) keep P as a 16-bit high part and the 16-bit
 // rounding of the rest, two products per block: P . V then holds about 16 bits
 // (bf16) or 22 (fp16) of each weight.  Outputs of 16 bits round P once, which
@@ -67,9 +67,9 @@ struct DtSmem {
   static constexpr int kV = kK + kStages * kStageBytes;  // [stage][block u][KB][64 x 128 B]
   static constexpr int kBars = kV + kStages * kStageBytes;
   // mbarriers: Q; per stage K full, V full, V scanned, K empty, V empty; per
-  // matrix and buffer S full, P full; per matrix O done (per block), pair done
-  // (pair_s), O final, drain; matrix 0's first softmax.  Every waiter is at most
-  // one completion behind the barrier that it polls by parity.
+  // matrix and buffer S full, P full; per matrix O done (per block), O final,
+  // drain.  Every waiter is at most one completion behind the barrier that it
+  // polls by parity.
   static constexpr int kBarQ = 0;
   static constexpr int kBarKF = 1;
   static constexpr int kBarVF = kBarKF + kStages;
@@ -79,11 +79,9 @@ struct DtSmem {
   static constexpr int kBarSF = kBarVE + kStages;
   static constexpr int kBarPF = kBarSF + 4;
   static constexpr int kBarOD = kBarPF + 4;
-  static constexpr int kBarOP = kBarOD + 2;
-  static constexpr int kBarOF = kBarOP + 2;
+  static constexpr int kBarOF = kBarOD + 2;
   static constexpr int kBarDR = kBarOF + 2;
-  static constexpr int kBarLag = kBarDR + 2;
-  static constexpr int kNumBars = kBarLag + 1;
+  static constexpr int kNumBars = kBarDR + 2;
   static constexpr int kMisc = kBars + 8 * kNumBars;  // ints, see below
   static constexpr int kBytes = kMisc + 64 + 1024;    // + alignment slack
   // tensor-memory columns: S / P of matrix m, block u at 128 m + 64 u; O_m at
@@ -171,7 +169,6 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
     dense_tc_kernel(const __grid_constant__ DenseTcParams p) {
   using Sm = DtSmem<D>;
   constexpr int KB = Sm::KB, S = Sm::kStages;
-  const bool pair_s = !kRule && !kSplitP && p.pair_s && !p.dup;
   extern __shared__ uint8_t dt_smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(dt_smem_raw) + 1023) & ~uintptr_t(1023));
@@ -196,7 +193,6 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
     for (int x = 0; x < Sm::kNumBars; ++x)
       mbar_init(&bars[x], (x >= Sm::kBarPF && x < Sm::kBarOD)   ? 4  // P: one per softmax warp
                           : (x >= Sm::kBarKE && x < Sm::kBarSF) ? 2  // empty: one per MMA warp
-                          : x == Sm::kBarLag                    ? 4  // matrix 0's softmax warps
                                                                 : 1);
     *fail = 0;
     misc[kMiscBad] = 0;
@@ -431,9 +427,8 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
     // ---- MMA issue for matrix m (the whole warp, one elected lane issuing) ----
     const int m = warp - Sm::kMmaWarp;
     const bool bf = Weights<T>::bf16;
-    const uint32_t idesc_s = umma_idesc_f16(bf, 128, 64, 0, 0);   // Q . K^T, a block
-    const uint32_t idesc_s2 = umma_idesc_f16(bf, 128, 128, 0, 0);  // both blocks of a pair
-    const uint32_t idesc_o = umma_idesc_f16(bf, 128, D, 0, 1);    // P . V: V MN-major
+    const uint32_t idesc_s = umma_idesc_f16(bf, 128, 64, 0, 0);  // Q . K^T, a block
+    const uint32_t idesc_o = umma_idesc_f16(bf, 128, D, 0, 1);   // P . V: V MN-major
     const uint64_t dq = umma_desc_sw128(smem_u32(smem + Sm::kQ + m * KB * 16384), 16, 1024);
     const uint64_t dk = umma_desc_sw128(smem_u32(smem + Sm::kK), 16, 1024);
     // (V's 64-channel halves lie 8,192 bytes apart: one product spans all channels)
@@ -443,12 +438,7 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
     auto wwait = [&](uint64_t *bar, uint32_t parity) {
       return __all_sync(0xffffffffu, dt_wait(bar, parity, fail));
     };
-    // with one S per pair, matrix 1 starts once matrix 0's first softmax is done,
-    // so that one's softmax runs beside the other's products (in step, both wait
-    // for the tensor pipe and then for the special-function units)
-    const bool lag = pair_s && m == 1 && !dup && pair_first(0) == 0 && pair_last(0) > 0;
     bool ok = begin < end && wwait(&bars[Sm::kBarQ], 0), any = false;
-    if (ok && lag) ok = wwait(&bars[Sm::kBarLag], 0);
     for (int pp = 0; pp < begin && ok; ++pp) {  // (every phase is seen, in order)
       if (!(ok = wwait(&bars[Sm::kBarKF + pp % S], (pp / S) & 1))) break;
       if (lane == 0) mbar_arrive(&bars[Sm::kBarKE + pp % S]);
@@ -464,18 +454,15 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
       if ((dup || su == 0) && !(ok = wwait(&bars[Sm::kBarKF + s], (sp / S) & 1))) return;
       tc_fence_after();
       any = true;
-      const bool both = pair_s && 2 * sp + 1 < n;
       const uint64_t kt = dk + (uint64_t)((s * Sm::kStageBytes + su * 8192) >> 4);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint64_t off = (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-        umma_f16_warp(tmem + 128 * m + 64 * (sb & 1), dq + off, kt + off,
-                      both ? idesc_s2 : idesc_s, kk > 0);
+        umma_f16_warp(tmem + 128 * m + 64 * (sb & 1), dq + off, kt + off, idesc_s, kk > 0);
       }
       umma_commit_warp(&bars[Sm::kBarSF + 2 * m + (sb & 1)]);
-      if (both) umma_commit_warp(&bars[Sm::kBarSF + 2 * m + 1]);
-      sb += both ? 2 : 1;
-      if (dup || both || su == 1 || 2 * sp + 1 == n) {
+      ++sb;
+      if (dup || su == 1 || 2 * sp + 1 == n) {
         umma_commit_warp(&bars[Sm::kBarKE + s]);
         ++sp;
         su = dup ? m : 0;
@@ -484,7 +471,7 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
       }
     };
     if (ok) issue_s();
-    if (ok && !pair_s) issue_s();
+    if (ok) issue_s();
     int blocks = 0;  // of this matrix so far
     for (int pp = begin; pp < end && ok; ++pp) {
       const int s = pp % S, u0 = dup ? m : 0, u1 = dup ? m + 1 : min(2, n - 2 * pp);
@@ -503,14 +490,11 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
                              idesc_o, blocks > 0 || part > 0 || kk > 0);
         umma_commit_warp(&bars[Sm::kBarOD + m]);
         if (u == u1 - 1) {
-          if (pair_s) umma_commit_warp(&bars[Sm::kBarOP + m]);
           umma_commit_warp(&bars[Sm::kBarVE + s]);
           if (pp == end - 1) umma_commit_warp(&bars[Sm::kBarOF + m]);
         }
-        if (sp < end && (!pair_s || u == u1 - 1)) {  // the next S goes where this P was
-          if (!(ok = pair_s ? wwait(&bars[Sm::kBarOP + m], (pp - begin) & 1)
-                            : wwait(&bars[Sm::kBarOD + m], blocks & 1)))
-            break;
+        if (sp < end) {  // the next S goes where this P was
+          if (!(ok = wwait(&bars[Sm::kBarOD + m], blocks & 1))) break;
           issue_s();
           if (!ok) break;
         }
@@ -546,10 +530,7 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
         if (!(ok = __all_sync(0xffffffffu, ok))) break;  // the tensor-memory accesses are warp-wide
         tc_fence_after();
         if (idle) {  // what the products make of these rows is never read
-          if (lane == 0) {
-            mbar_arrive(&bars[Sm::kBarPF + 2 * m + buf]);
-            if (m == 0 && blocks == 0) mbar_arrive(&bars[Sm::kBarLag]);
-          }
+          if (lane == 0) mbar_arrive(&bars[Sm::kBarPF + 2 * m + buf]);
           continue;
         }
         const uint32_t t_s = lanes + 128 * m + 64 * buf;
@@ -697,10 +678,7 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bars[Sm::kBarPF + 2 * m + buf]);
-          if (m == 0 && blocks == 0) mbar_arrive(&bars[Sm::kBarLag]);
-        }
+        if (lane == 0) mbar_arrive(&bars[Sm::kBarPF + 2 * m + buf]);
       }
     }
     if (ok) {  // (without products, Q's copy must have landed: its tile is written next)
