@@ -196,21 +196,28 @@ spd_status plan_prompt(const spd_dense_config *c, int Lq, int Lk, int sms, Promp
   z->tiles = (Lq + per - 1) / per;
   const long long units = (long long)z->tiles * c->num_kv_heads * z->HG;
   const int most = kDenseMaxSplits / (z->dup ? 2 : 1);
-  z->nsplit = (int)std::max<long long>(
-      1, std::min<long long>(most, std::min<long long>(sms / units, blocks / 4)));
-  // A few waves of equal units (a chunk over a much longer row) leave the last
-  // one part empty: cut into s, they take ceil(units s / SMs) / s unit times, for
-  // the price of the partial sums.  (0.85 us per block of a unit, 0.045 us per
-  // cut unit written and read: 256 units of 768 blocks in four cuts 1,320 us, whole
-  // 1,412.  Packed documents, where units are short and uneven, stay whole.)
-  if (!z->dup && units > sms && units <= 8LL * sms && Lk >= 4LL * Lq) {
-    auto cost = [&](int s) {
-      return (double)((units * s + sms - 1) / sms) / s * blocks * 0.85 +
-             (s > 1 ? units * s * 0.045 + 10.0 : 0.0);
-    };
-    for (int s = 2; s <= 8 && s * 16 <= blocks; ++s)
-      if (cost(s) < cost(z->nsplit)) z->nsplit = s;
-  }
+  // Cuts along the keys.  A block takes 0.85 us, a CTA 8 us besides; where the CTAs
+  // of a full GPU leave partial sums, 5.2 more, and as much to join them (a fit to
+  // about 30 shapes).  Over a much longer row the units are even and run in whole
+  // rounds; a square causal prompt's run longest first, and either the longest or
+  // the average bounds them.  (Whole and in the cuts taken: 2,048 queries over 49,152
+  // keys with 32 heads 1,292 and 1,202 us, 8,192 causal with 4 heads 114 and 75,
+  // 4,096 with 8 heads 62 and 53, 128 over 1,024 keys 20 and 15.  Kept whole: 7,000
+  // with 8 heads 101, in two cuts 123; 2,048 with 32 heads 38 and 76; 512 13.6 and
+  // 18.7.)
+  const double work = Lk > Lq ? 1.0 - 0.5 * Lq / Lk : 0.5;  // of units x blocks
+  auto cost = [&](long long s) {
+    const bool cut = z->dup || s > 1;
+    const double part = cut ? 5.2 * std::min(1.0, (double)(units * s) / sms) : 0.0;
+    const double block = 0.85, fixed = 8.0 + part, join = part;
+    const double one = block * blocks / (double)s + fixed;
+    if (Lk >= 4LL * Lq) return (double)((units * s + sms - 1) / sms) * one + join;
+    const double all = block * work * blocks * (double)units / sms +
+                       (cut ? fixed * (double)(units * s) / sms : 0.0);
+    return std::max(one, all) + join;
+  };
+  for (int s = 2; s <= most && s * 4 <= blocks && units <= 8LL * sms; ++s)
+    if (cost(s) < cost(z->nsplit)) z->nsplit = s;
   z->partial = z->dup || z->nsplit > 1;
   if (units * z->nsplit > 0x7fffffffLL || (long long)Lq * c->num_q_heads > 0x7fffffffLL * 8)
     return SPD_ERR_CAPACITY;
