@@ -85,6 +85,18 @@ def test_prompt_masks_and_rules(mask, rule, lq, lk, heads):
     check_prompt(lq, lk, *heads, 128, "bf16", out="same", mask=mask, **rule)
 
 
+@pytest.mark.parametrize("mask", [None, "random", "window", "far"])
+@pytest.mark.parametrize("lq,lk,heads,d,dtype,out,rule", [
+    (2600, 2600, (8, 8), 128, "bf16", "same", dict()),
+    (2600, 2600, (8, 8), 64, "fp16", "fp32", dict(slopes=True)),
+    (3300, 3300, (4, 2), 128, "fp16", "same", dict(softcap=30.0)),
+    (600, 3000, (16, 4), 128, "bf16", "fp32", dict()),
+])
+def test_prompts_cut_along_the_keys(mask, lq, lk, heads, d, dtype, out, rule):
+    """Uneven causal tiles and rows that some cuts hold no key of."""
+    check_prompt(lq, lk, *heads, d, dtype, out=out, mask=mask, **rule)
+
+
 def test_prompt_large_scores_saturate_the_cap():
     check_prompt(90, 90, 4, 2, 128, "bf16", softcap=5.0, gain=300.0)
     check_prompt(90, 90, 4, 2, 128, "bf16", gain=60.0)
