@@ -11,7 +11,8 @@
 // A decode step reads each own key once for G <= 8 rows, 2 G flops per byte:
 // memory is the bound, and mma.sync's rate is far above it.  Weights are split
 // into a 16-bit high part and the rounding of the rest (two products), so that
-// the fp32 result keeps about 16 bits (bf16) or 22 (fp16) of each.
+// the fp32 result keeps about 16 bits (bf16) or 22 (fp16) of each; fp32
+// outputs of bf16 take a third part and keep 24.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         o[n][3] *= al[1];
       }
     }
-    uint32_t ph[4] = {0, 0, 0, 0}, pl[4] = {0, 0, 0, 0};
+    uint32_t ph[4] = {0, 0, 0, 0}, pl[4] = {0, 0, 0, 0}, px[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int hr = 0; hr < 2; ++hr) {
       if (hr == 1 && !upper) break;
@@ -374,7 +375,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         const uint32_t h = pack2<T>(a, b);
         const float2 f = unpack2<T>(h);
         ph[2 * j + hr] = h;
-        pl[2 * j + hr] = pack2<T>(a - f.x, b - f.y);
+        const uint32_t lo = pack2<T>(a - f.x, b - f.y);
+        pl[2 * j + hr] = lo;
+        if (kBf) {
+          const float2 f2 = unpack2<T>(lo);
+          px[2 * j + hr] = pack2<T>(a - f.x - f2.x, b - f.y - f2.y);
+        }
       }
     }
     // O += P . V
@@ -388,6 +394,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       mma_16816<kBf>(o[n], pl, b0, b1);
       mma_16816<kBf>(o[n + 1], ph, b2, b3);
       mma_16816<kBf>(o[n + 1], pl, b2, b3);
+      if (kBf && p.out_f32) {
+        mma_16816<kBf>(o[n], px, b0, b1);
+        mma_16816<kBf>(o[n + 1], px, b2, b3);
+      }
     }
     __syncwarp();
     if (issued < ntile) {

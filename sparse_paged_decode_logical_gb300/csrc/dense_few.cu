@@ -10,8 +10,8 @@
 //                      step needs one vote and no reduction over the keys; sums
 //                      per thread, joined at the end;
 //   O^T += V^T . P^T   M 128 channels x N rows: A is V read transposed, P^T goes
-//                      through shared memory (16 bits, with kSplitP a second
-//                      product for the rounding of the first).
+//                      through shared memory (16 bits, with kSplitP one or
+//                      two more products for what the rounding left).
 // A step of 128 keys moves 64 KB and takes 1,024 cycles of the tensor pipe (64
 // bytes per cycle; an SM's share of HBM is 23), whatever the rows: memory is the
 // bound.  K and V are single buffers, freed as soon as their product is done;
@@ -44,12 +44,13 @@ constexpr int kFewD = 128, kFewThreads = 192;
 constexpr float kFewNone = -FLT_MAX;  // the reference of a row that has met no key
 
 // NR: rows of the products (a multiple of 16).
-template <int NR, bool kSplitP> struct FewSmem {
+// kParts: 16-bit parts that a weight is kept in.
+template <int NR, int kParts> struct FewSmem {
   static constexpr int kK = 0;                    // [2 x 64 channels][128 keys][128 B]
   static constexpr int kV = 32768;
   static constexpr int kQ = 65536;                // [2 x 64 channels][NR][128 B]
-  static constexpr int kP = kQ + 2 * NR * 128;    // [high, low][2 x 64 keys][NR][128 B]
-  static constexpr int kRow = kP + (kSplitP ? 4 : 2) * NR * 128;
+  static constexpr int kP = kQ + 2 * NR * 128;    // [part][2 x 64 keys][NR][128 B]
+  static constexpr int kRow = kP + 2 * kParts * NR * 128;
   // per row: slope, tokens behind the keys; reference, factor; per warp and row:
   // max / sum
   static constexpr int kRef = kRow + NR * 8;
@@ -123,6 +124,11 @@ template <> struct FewT<__half> {
   }
 };
 
+// Outputs of 32 bits: 22 bits of a weight in two fp16 parts, 24 in three of bf16
+// (two hold 16).
+template <typename T, bool kSplitP>
+constexpr int kFewParts = !kSplitP ? 1 : FewT<T>::bf16 ? 3 : 2;
+
 // NR columns of the warp's 32 lanes.
 template <int NR>
 __device__ __forceinline__ void few_load(uint32_t taddr, float (&x)[NR]) {
@@ -149,7 +155,8 @@ __device__ __forceinline__ void few_load(uint32_t taddr, float (&x)[NR]) {
 template <typename T, int NR, bool kSplitP>
 __global__ void __launch_bounds__(kFewThreads, NR <= 16 ? 3 : 2)
     dense_few_kernel(const __grid_constant__ DenseDecodeParams p) {
-  using Sm = FewSmem<NR, kSplitP>;
+  constexpr int kParts = kFewParts<T, kSplitP>;
+  using Sm = FewSmem<NR, kParts>;
   extern __shared__ uint8_t few_smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(few_smem_raw) + 1023) & ~uintptr_t(1023));
@@ -265,7 +272,7 @@ __global__ void __launch_bounds__(kFewThreads, NR <= 16 ? 3 : 2)
       if (!(ok = wwait(kFewPF, j & 1))) break;
       tc_fence_after();
 #pragma unroll
-      for (int part = 0; part < (kSplitP ? 2 : 1); ++part)
+      for (int part = 0; part < kParts; ++part)
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           umma_f16_warp(tmem + NR, dv + (uint64_t)((kk * 2048) >> 4),
@@ -294,7 +301,7 @@ __global__ void __launch_bounds__(kFewThreads, NR <= 16 ? 3 : 2)
       }
       *reinterpret_cast<uint4 *>(smem + Sm::kQ + (ch >> 3) * NR * 128 + swz128(r, ch & 7)) = v;
     }
-    for (int x = tid; x < (kSplitP ? 4 : 2) * NR * 8; x += 128)
+    for (int x = tid; x < 2 * kParts * NR * 8; x += 128)
       *reinterpret_cast<uint4 *>(smem + Sm::kP + x * 16) = make_uint4(0, 0, 0, 0);
     if (tid < NR) {
       const int sq = (row0 + tid) / p.G, h = hk * p.G + (row0 + tid) % p.G;
@@ -418,6 +425,12 @@ __global__ void __launch_bounds__(kFewThreads, NR <= 16 ? 3 : 2)
           const uint32_t lo = FewT<T>::pack(a - g.x, b - g.y);
           *reinterpret_cast<uint16_t *>(at0 + 2 * NR * 128) = (uint16_t)lo;
           *reinterpret_cast<uint16_t *>(at1 + 2 * NR * 128) = (uint16_t)(lo >> 16);
+          if constexpr (kParts == 3) {
+            const float2 g2 = FewT<T>::unpack(lo);
+            const uint32_t rest = FewT<T>::pack(a - g.x - g2.x, b - g.y - g2.y);
+            *reinterpret_cast<uint16_t *>(at0 + 4 * NR * 128) = (uint16_t)rest;
+            *reinterpret_cast<uint16_t *>(at1 + 4 * NR * 128) = (uint16_t)(rest >> 16);
+          }
         }
       }
       if (L - key0 < kFewKeys) {
@@ -471,7 +484,8 @@ __global__ void __launch_bounds__(kFewThreads, NR <= 16 ? 3 : 2)
 
 template <typename T, int NR, bool kSplitP>
 cudaError_t launch_few_t(const DenseDecodeParams &p, cudaStream_t st) {
-  using Sm = FewSmem<NR, kSplitP>;
+  constexpr int kParts = kFewParts<T, kSplitP>;
+  using Sm = FewSmem<NR, kParts>;
   auto k = dense_few_kernel<T, NR, kSplitP>;
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = allow_smem(k, Sm::kBytes, &ready);

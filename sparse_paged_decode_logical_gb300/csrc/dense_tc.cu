@@ -24,8 +24,9 @@
 // against 635 (8,192 capped) and 67 against 54 (2,501 tokens with a bias and fp32
 // output, 64 channels).
 // Outputs of 32 bits (kSplitP) keep P as a 16-bit high part and the 16-bit
-// rounding of the rest, two products per block: P . V then holds about 16 bits
-// (bf16) or 22 (fp16) of each weight.  Outputs of 16 bits round P once, which
+// rounding of the rest, with bf16 of the rest's rest too (through shared memory:
+// tensor memory is full), a product each: P . V then holds 22 bits (fp16) or 24
+// (bf16; two parts hold 16) of each weight.  Outputs of 16 bits round P once, which
 // is an error of the same size as the rounding of the output.
 //
 // A matrix leaves out the pairs before and behind its rows' keys.  With `dup` (at
@@ -57,7 +58,7 @@ namespace {
 constexpr uint32_t kDtWait = 1u << 22;  // bounded mbarrier polls
 constexpr float kDtRescaleAbove = 8.f;  // log2 growth of a row max that moves it
 
-template <int D>
+template <int D, bool kThird>
 struct DtSmem {
   static constexpr int KB = D / 64;               // 64-column sub-tiles of a row
   static constexpr int kStages = 2;               // K / V ring, a pair of blocks per stage
@@ -65,7 +66,8 @@ struct DtSmem {
   static constexpr int kQ = 0;                    // [2][KB][128 x 128 B]
   static constexpr int kK = 2 * KB * 16384;       // [stage][KB][block u][64 x 128 B]
   static constexpr int kV = kK + kStages * kStageBytes;  // [stage][block u][KB][64 x 128 B]
-  static constexpr int kBars = kV + kStages * kStageBytes;
+  static constexpr int kL = kV + kStages * kStageBytes;  // P's third part [2][128 x 128 B]
+  static constexpr int kBars = kL + (kThird ? 2 * 16384 : 0);
   // mbarriers: Q; per stage K full, V full, V scanned, K empty, V empty; per
   // matrix and buffer S full, P full; per matrix O done (per block), O final,
   // drain.  Every waiter is at most one completion behind the barrier that it
@@ -132,6 +134,12 @@ template <> struct Weights<__nv_bfloat16> {
     lo = round(f2_sub(p, make_float2(__uint_as_float(hi << 16),
                                      __uint_as_float(hi & 0xffff0000u))));
   }
+  static __device__ __forceinline__ uint32_t third(float2 p, uint32_t hi, uint32_t lo) {
+    const float2 r = f2_sub(p, make_float2(__uint_as_float(hi << 16),
+                                           __uint_as_float(hi & 0xffff0000u)));
+    return round(f2_sub(r, make_float2(__uint_as_float(lo << 16),
+                                       __uint_as_float(lo & 0xffff0000u))));
+  }
   static __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 };
 template <> struct Weights<__half> {
@@ -165,9 +173,10 @@ __device__ __forceinline__ uint32_t without_nonfinite(uint32_t x, uint32_t expon
 __device__ int g_dense_err[4];
 
 template <typename T, int D, bool kSplitP, bool kRule>
-__global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
+__global__ void __launch_bounds__(DtSmem<D, false>::kThreads, 1)
     dense_tc_kernel(const __grid_constant__ DenseTcParams p) {
-  using Sm = DtSmem<D>;
+  constexpr bool kThird = kSplitP && Weights<T>::bf16;
+  using Sm = DtSmem<D, kThird>;
   constexpr int KB = Sm::KB, S = Sm::kStages;
   extern __shared__ uint8_t dt_smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -433,6 +442,7 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
     const uint64_t dk = umma_desc_sw128(smem_u32(smem + Sm::kK), 16, 1024);
     // (V's 64-channel halves lie 8,192 bytes apart: one product spans all channels)
     const uint64_t dv = umma_desc_sw128(smem_u32(smem + Sm::kV), 8192, 1024);
+    const uint64_t dl = umma_desc_sw128(smem_u32(smem + Sm::kL + m * 16384), 16, 1024);
     const uint32_t t_o = tmem + 256 + D * m;
     const int begin = pair_first(m), end = pair_last(m), dup = p.dup;
     auto wwait = [&](uint64_t *bar, uint32_t parity) {
@@ -488,6 +498,12 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
           for (int kk = 0; kk < 4; ++kk)
             umma_f16_ts_warp(t_o, pa + 32 * part + 8 * kk, vt + (uint64_t)((kk * 2048) >> 4),
                              idesc_o, blocks > 0 || part > 0 || kk > 0);
+        if constexpr (kThird) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_f16_warp(t_o, dl + (uint64_t)((kk * 32) >> 4), vt + (uint64_t)((kk * 2048) >> 4),
+                          idesc_o, true);
+        }
         umma_commit_warp(&bars[Sm::kBarOD + m]);
         if (u == u1 - 1) {
           umma_commit_warp(&bars[Sm::kBarVE + s]);
@@ -657,6 +673,11 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
         uint32_t lo_w[kSplitP ? 32 : 1];
         const float2 sc2 = f2_dup(sc), nm2 = f2_dup(-base);
         float2 ls[2] = {f2_dup(0.f), f2_dup(0.f)};
+        uint32_t third[kThird ? 4 : 1];
+        if (kThird && blocks > 0) {  // the block before has been read from there
+          ok = dt_wait(&bars[Sm::kBarOD + m], (blocks - 1) & 1, fail);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        }
         auto weights = [&](auto exponent) {
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
@@ -666,6 +687,12 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
             ls[c & 1] = f2_add(ls[c & 1], w);
             if constexpr (kSplitP) Weights<T>::split(w, hi_w[c], lo_w[c]);
             else hi_w[c] = Weights<T>::round(w);
+            if constexpr (kThird) {
+              third[c & 3] = Weights<T>::third(w, hi_w[c], lo_w[c]);
+              if ((c & 3) == 3)
+                *reinterpret_cast<uint4 *>(smem + Sm::kL + m * 16384 + swz128(row, c >> 2)) =
+                    make_uint4(third[0], third[1], third[2], third[3]);
+            }
           }
         };
         if (kRule && !kSplitP && quick)
@@ -676,6 +703,7 @@ __global__ void __launch_bounds__(DtSmem<D>::kThreads, 1)
         tmem_st32(t_s, hi_w);
         if constexpr (kSplitP) tmem_st32(t_s + 32, lo_w);
         tmem_wait_st();
+        if constexpr (kThird) fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[Sm::kBarPF + 2 * m + buf]);
@@ -877,10 +905,10 @@ template <typename T, int D, bool kSplitP, bool kRule>
 cudaError_t launch_dt_r(const DenseTcParams &p, cudaStream_t st) {
   auto k = dense_tc_kernel<T, D, kSplitP, kRule>;
   static std::atomic<uint64_t> ready{0};
-  const cudaError_t e = allow_smem(k, DtSmem<D>::kBytes, &ready);
+  using Sm = DtSmem<D, kSplitP && Weights<T>::bf16>;
+  const cudaError_t e = allow_smem(k, Sm::kBytes, &ready);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, p.tiles * p.nsplit * p.Hkv * p.HG, DtSmem<D>::kThreads,
-                    (size_t)DtSmem<D>::kBytes, st, p);
+  return launch_pdl(k, p.tiles * p.nsplit * p.Hkv * p.HG, Sm::kThreads, (size_t)Sm::kBytes, st, p);
 }
 
 template <typename T, int D, bool kSplitP>

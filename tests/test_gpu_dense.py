@@ -301,6 +301,48 @@ def test_shared_long_own_tokens():
     check_shared(2, 0, [5000, 20001], 4, 1, 64, "bf16", page=512, weights=True)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("kind,d", [("prompt", 64), ("prompt", 128), (2, 64), (2, 128), (5, 128),
+                                    (20, 64), (20, 128)])
+def test_fp32_outputs_hold_the_weights_to_22_bits(kind, d, dtype):
+    """16 keys count, each with a channel of V of its own, so that an output is
+    one weight.  Scores are exact products of two numbers, |x| < 3 in base 2: the
+    exponent (x by a rounded constant, less at most 13 in magnitude) is off by
+    2.9 x 2^-24 + 2^-21, e^ln2 of that 4.5e-7, 2^x by 2^-22, fp16's parts by 2^-22;
+    numerator and sum 9.3e-7 each, the sum of 16 and the joins 20 x 2^-24, the
+    division 2^-23: 3.2e-6.  (Two parts of bf16: 2^-18 = 3.8e-6 more.)"""
+    dt = DT[dtype]
+    n_keys, hq, hkv = 4500, 8, 2
+    at = torch.randperm(n_keys, generator=torch.Generator().manual_seed(3))[:16].cuda()
+    rows = 30 if kind == "prompt" else kind
+    q = torch.zeros(rows, hq, d, device="cuda", dtype=dt)
+    q[..., 0], q[..., 1] = normal(1, rows, hq).abs().clamp_max(2).to(dt), 1
+    k = torch.zeros(n_keys, hkv, d, device="cuda", dtype=dt)
+    k[..., 1] = -1000
+    k[at, :, 0], k[at, :, 1] = normal(2, 16, hkv).clamp(-1, 1).to(dt), 0
+    v = torch.zeros(n_keys, hkv, d, device="cuda", dtype=dt)
+    v[at, :, torch.arange(16, device="cuda")] = 1
+    if kind == "prompt":
+        b, e = torch.zeros(rows, dtype=torch.int32, device="cuda"), \
+            torch.full((rows,), n_keys, dtype=torch.int32, device="cuda")
+        got = spd.prefill_attention(q, k, v, key_begin=b, key_end=e, scale=1.0, check=True,
+                                    out_dtype=torch.float32)
+    else:
+        c = new_cache(hq, hkv, d, dtype, 256, 16, 18 + 2 * rows, rows + 1, 4600)
+        pid, ids = c.seq_create(), [c.seq_create() for _ in range(rows)]
+        c.kv_append([pid], k[None], v[None])
+        own = torch.zeros(rows, 3, hkv, d, device="cuda", dtype=dt)
+        own[..., 1] = -1000
+        c.kv_append(ids, own, torch.zeros_like(own))
+        got = c.shared_prefix_attention(q, pid, ids, scale=1.0, out_dtype=torch.float32)
+        c.check_status()
+    x = torch.einsum("rhg,thg->rht", q[..., :1].double(),
+                     k[at, :, :1].double().repeat_interleave(hq // hkv, 1))
+    want = torch.softmax(x, -1)
+    assert float(((got[..., :16].double() - want) / want).abs().max()) < 3.2e-6
+    assert bool((got[..., 16:] == 0).all())
+
+
 def test_shared_streams_graph_and_another_workspace():
     c, q, pid, ids, got = check_shared(9, 400, [30] * 9, 8, 2, 128, "bf16")
     s = torch.cuda.Stream()
