@@ -436,8 +436,9 @@ typedef struct {
   const float *slopes; /* device [num_q_heads], 4-byte aligned, or NULL */
 } spd_score_rule;
 
-/* Type of the output: fp32 (softmax weights enter the products with v with
- * about 16 bits for bf16 inputs, 22 for fp16), or the type of the inputs
+/* Type of the output: fp32 (softmax weights enter the products with v with 22 to
+ * 24 bits, 16 in prompts of bf16 where a query attends more than about 1,000 keys;
+ * there the tensor cores' fp32 sums are off by as much), or the type of the inputs
  * (weights rounded to it once, the fp32 sums rounded to it at the end). */
 typedef enum { SPD_OUT_F32 = 0, SPD_OUT_DTYPE = 1 } spd_out;
 

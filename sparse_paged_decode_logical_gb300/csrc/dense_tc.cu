@@ -23,10 +23,14 @@
 // 423 (8,192 causal), 2,307 against 2,052 (8,192 over 16,384, 64 channels), 831
 // against 635 (8,192 capped) and 67 against 54 (2,501 tokens with a bias and fp32
 // output, 64 channels).
-// Outputs of 32 bits (kSplitP) keep P as a 16-bit high part and the 16-bit
-// rounding of the rest, with bf16 of the rest's rest too (through shared memory:
-// tensor memory is full), a product each: P . V then holds 22 bits (fp16) or 24
-// (bf16; two parts hold 16) of each weight.  Outputs of 16 bits round P once, which
+// Outputs of 32 bits keep P in kParts 16-bit parts, each the rounding of what the
+// ones before left, a product each: two hold 22 bits of each weight with fp16 and
+// 16 with bf16, which takes a third part (through shared memory: tensor memory is
+// full) where a CTA meets at most kThirdKeys keys (kParts 3).  Over longer stretches
+// the tensor cores' own sums, which round towards 0 at every 16 keys, are off by as
+// much (two parts a relative 2e-6, the sums 2.9e-6 at 1,100 keys), and a third part
+// everywhere costs 40% of the time (2,048 biased queries over 16,384 keys 662 and
+// 935 us, 742 as it is).  Outputs of 16 bits round P once, which
 // is an error of the same size as the rounding of the output.
 //
 // A matrix leaves out the pairs before and behind its rows' keys.  With `dup` (at
@@ -56,6 +60,7 @@ namespace spd {
 namespace {
 
 constexpr uint32_t kDtWait = 1u << 22;  // bounded mbarrier polls
+constexpr int kThirdKeys = 1024;        // a CTA's keys up to which bf16 weights take three parts
 constexpr float kDtRescaleAbove = 8.f;  // log2 growth of a row max that moves it
 
 template <int D, bool kThird>
@@ -134,7 +139,7 @@ template <> struct Weights<__nv_bfloat16> {
     lo = round(f2_sub(p, make_float2(__uint_as_float(hi << 16),
                                      __uint_as_float(hi & 0xffff0000u))));
   }
-  static __device__ __forceinline__ uint32_t third(float2 p, uint32_t hi, uint32_t lo) {
+  static __device__ __forceinline__ uint32_t rest(float2 p, uint32_t hi, uint32_t lo) {
     const float2 r = f2_sub(p, make_float2(__uint_as_float(hi << 16),
                                            __uint_as_float(hi & 0xffff0000u)));
     return round(f2_sub(r, make_float2(__uint_as_float(lo << 16),
@@ -172,10 +177,10 @@ __device__ __forceinline__ uint32_t without_nonfinite(uint32_t x, uint32_t expon
 // dense_error_word.
 __device__ int g_dense_err[4];
 
-template <typename T, int D, bool kSplitP, bool kRule>
+template <typename T, int D, int kParts, bool kRule>
 __global__ void __launch_bounds__(DtSmem<D, false>::kThreads, 1)
     dense_tc_kernel(const __grid_constant__ DenseTcParams p) {
-  constexpr bool kThird = kSplitP && Weights<T>::bf16;
+  constexpr bool kSplitP = kParts > 1, kThird = kParts == 3;
   using Sm = DtSmem<D, kThird>;
   constexpr int KB = Sm::KB, S = Sm::kStages;
   extern __shared__ uint8_t dt_smem_raw[];
@@ -274,6 +279,7 @@ __global__ void __launch_bounds__(DtSmem<D, false>::kThreads, 1)
     n = max(0, min(last - kb0, per));
   }
   const int np = (n + 1) / 2;
+  const bool third = kThird && n * kDenseBlock <= kThirdKeys;
   // Blocks in ascending order, so that the CTAs that run together read the same
   // K and V at the same time (descending, where each starts at its own newest
   // key, took 1,385 us against 1,320 on 2,048 queries over 49,152 keys).  With a
@@ -498,7 +504,7 @@ __global__ void __launch_bounds__(DtSmem<D, false>::kThreads, 1)
           for (int kk = 0; kk < 4; ++kk)
             umma_f16_ts_warp(t_o, pa + 32 * part + 8 * kk, vt + (uint64_t)((kk * 2048) >> 4),
                              idesc_o, blocks > 0 || part > 0 || kk > 0);
-        if constexpr (kThird) {
+        if (third) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             umma_f16_warp(t_o, dl + (uint64_t)((kk * 32) >> 4), vt + (uint64_t)((kk * 2048) >> 4),
@@ -673,8 +679,8 @@ __global__ void __launch_bounds__(DtSmem<D, false>::kThreads, 1)
         uint32_t lo_w[kSplitP ? 32 : 1];
         const float2 sc2 = f2_dup(sc), nm2 = f2_dup(-base);
         float2 ls[2] = {f2_dup(0.f), f2_dup(0.f)};
-        uint32_t third[kThird ? 4 : 1];
-        if (kThird && blocks > 0) {  // the block before has been read from there
+        uint32_t rest[kThird ? 4 : 1];
+        if (third && blocks > 0) {  // the block before has been read from there
           ok = dt_wait(&bars[Sm::kBarOD + m], (blocks - 1) & 1, fail);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
         }
@@ -688,10 +694,12 @@ __global__ void __launch_bounds__(DtSmem<D, false>::kThreads, 1)
             if constexpr (kSplitP) Weights<T>::split(w, hi_w[c], lo_w[c]);
             else hi_w[c] = Weights<T>::round(w);
             if constexpr (kThird) {
-              third[c & 3] = Weights<T>::third(w, hi_w[c], lo_w[c]);
-              if ((c & 3) == 3)
-                *reinterpret_cast<uint4 *>(smem + Sm::kL + m * 16384 + swz128(row, c >> 2)) =
-                    make_uint4(third[0], third[1], third[2], third[3]);
+              if (third) {
+                rest[c & 3] = Weights<T>::rest(w, hi_w[c], lo_w[c]);
+                if ((c & 3) == 3)
+                  *reinterpret_cast<uint4 *>(smem + Sm::kL + m * 16384 + swz128(row, c >> 2)) =
+                      make_uint4(rest[0], rest[1], rest[2], rest[3]);
+              }
             }
           }
         };
@@ -703,7 +711,7 @@ __global__ void __launch_bounds__(DtSmem<D, false>::kThreads, 1)
         tmem_st32(t_s, hi_w);
         if constexpr (kSplitP) tmem_st32(t_s + 32, lo_w);
         tmem_wait_st();
-        if constexpr (kThird) fence_proxy_async_smem();
+        if (third) fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[Sm::kBarPF + 2 * m + buf]);
@@ -901,26 +909,34 @@ __global__ void __launch_bounds__(256) document_ranges_kernel(const int *offsets
   ke[t] = e;
 }
 
-template <typename T, int D, bool kSplitP, bool kRule>
+template <typename T, int D, int kParts, bool kRule>
 cudaError_t launch_dt_r(const DenseTcParams &p, cudaStream_t st) {
-  auto k = dense_tc_kernel<T, D, kSplitP, kRule>;
+  auto k = dense_tc_kernel<T, D, kParts, kRule>;
   static std::atomic<uint64_t> ready{0};
-  using Sm = DtSmem<D, kSplitP && Weights<T>::bf16>;
+  using Sm = DtSmem<D, kParts == 3>;
   const cudaError_t e = allow_smem(k, Sm::kBytes, &ready);
   if (e != cudaSuccess) return e;
   return launch_pdl(k, p.tiles * p.nsplit * p.Hkv * p.HG, Sm::kThreads, (size_t)Sm::kBytes, st, p);
 }
 
-template <typename T, int D, bool kSplitP>
+template <typename T, int D, int kParts>
 cudaError_t launch_dt(const DenseTcParams &p, cudaStream_t st) {
-  return p.rule.cap_out > 0.f || p.rule.slopes ? launch_dt_r<T, D, kSplitP, true>(p, st)
-                                               : launch_dt_r<T, D, kSplitP, false>(p, st);
+  return p.rule.cap_out > 0.f || p.rule.slopes ? launch_dt_r<T, D, kParts, true>(p, st)
+                                               : launch_dt_r<T, D, kParts, false>(p, st);
+}
+
+template <typename T, int D>
+cudaError_t launch_dt_p(const DenseTcParams &p, bool split_p, cudaStream_t st) {
+  if (!split_p) return launch_dt<T, D, 1>(p, st);
+  if constexpr (Weights<T>::bf16)
+    return launch_dt<T, D, 3>(p, st);
+  else
+    return launch_dt<T, D, 2>(p, st);
 }
 
 template <typename T>
 cudaError_t launch_dt_d(const DenseTcParams &p, int d, bool split_p, cudaStream_t st) {
-  if (d == 64) return split_p ? launch_dt<T, 64, true>(p, st) : launch_dt<T, 64, false>(p, st);
-  return split_p ? launch_dt<T, 128, true>(p, st) : launch_dt<T, 128, false>(p, st);
+  return d == 64 ? launch_dt_p<T, 64>(p, split_p, st) : launch_dt_p<T, 128>(p, split_p, st);
 }
 
 }  // namespace
