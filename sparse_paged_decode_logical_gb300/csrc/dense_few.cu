@@ -16,8 +16,8 @@
 // bytes per cycle; an SM's share of HBM is 23), whatever the rows: memory is the
 // bound.  K and V are single buffers, freed as soon as their product is done;
 // two or three CTAs per SM overlap one another's waits.  5 sequences (20 rows)
-// over 120,001 tokens with cap and bias: 156 us with mma.sync tiles of 16 rows,
-// 165 with the kernel whose rows are queries.  Up to 8 rows (a sequence's own
+// over 120,001 tokens with cap and bias: 98 us, 158 with mma.sync tiles of 16
+// rows, 141 with the kernel whose rows are queries.  Up to 8 rows (a sequence's own
 // tokens) the mma.sync kernel is as fast or faster: its warps start without the
 // set-up of tensor memory and hand-overs between roles (64 sequences' own
 // tokens 51 us against 54, one sequence's 6 against 11).

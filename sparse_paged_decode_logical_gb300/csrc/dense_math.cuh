@@ -22,8 +22,8 @@ __device__ __forceinline__ float2 cap_small(const ScoreRule &r, float2 s) {
 
 // The same for any score, by 2^x and a reciprocal: off by about 2^-22 of the cap
 // near 0, which 16-bit weights (2^-9 and 2^-12 of each) do not show.
-// cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)).  (8,192 capped tokens: 772
-// us with this alone, 678 with cap_quick where it holds.)
+// cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)).  (8,192 capped tokens: 770
+// us with this alone, 625 with cap_quick where it holds.)
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -19,9 +19,9 @@
 // P . V of this one is done: the hand-overs between the roles (about 300 cycles
 // each) and the products of one buffer then pass while the softmax works on the
 // other.  One product of N 128 per pair, with the next S behind the whole pair's
-// P . V, took 1,319 us against 1,209 (2,048 queries over 49,152 keys), 461 against
-// 423 (8,192 causal), 2,307 against 2,052 (8,192 over 16,384, 64 channels), 831
-// against 635 (8,192 capped) and 67 against 54 (2,501 tokens with a bias and fp32
+// P . V, took 1,319 us against 1,202 (2,048 queries over 49,152 keys), 461 against
+// 420 (8,192 causal), 2,307 against 2,020 (8,192 over 16,384, 64 channels), 831
+// against 623 (8,192 capped) and 67 against 55 (2,501 tokens with a bias and fp32
 // output, 64 channels).
 // Outputs of 32 bits keep P in kParts 16-bit parts, each the rounding of what the
 // ones before left, a product each: two hold 22 bits of each weight with fp16 and
@@ -30,8 +30,8 @@
 // the tensor cores' own sums, which round towards 0 at every 16 keys, are off by as
 // much (two parts a relative 2e-6, the sums 2.9e-6 at 1,100 keys), and a third part
 // everywhere costs 40% of the time (2,048 biased queries over 16,384 keys 662 and
-// 935 us, 742 as it is).  Outputs of 16 bits round P once, which
-// is an error of the same size as the rounding of the output.
+// 935 us, 742 as it is).  Outputs of 16 bits round P once, which is an error of the
+// same size as the rounding of the output.
 //
 // A matrix leaves out the pairs before and behind its rows' keys.  With `dup` (at
 // most 128 rows) both matrices hold the same rows, and matrix m takes block m of
@@ -282,9 +282,9 @@ __global__ void __launch_bounds__(DtSmem<D, false>::kThreads, 1)
   const bool third = kThird && n * kDenseBlock <= kThirdKeys;
   // Blocks in ascending order, so that the CTAs that run together read the same
   // K and V at the same time (descending, where each starts at its own newest
-  // key, took 1,385 us against 1,320 on 2,048 queries over 49,152 keys).  With a
+  // key, 1,227 us against 1,216 on 2,048 queries over 49,152 keys).  With a
   // distance bias in descending order: the largest scores come first and the
-  // running max hardly moves (2,501 tokens 59.5 us against 68.5).  Block j of the
+  // running max hardly moves (2,501 tokens 55 us against 66).  Block j of the
   // split begins at key0_of(j); pair pp holds blocks 2 pp and 2 pp + 1.
   const bool desc = kRule && p.rule.slopes != nullptr;
   auto key0_of = [&](int j) { return (desc ? kb0 + n - 1 - j : kb0 + j) * kDenseBlock; };
