@@ -587,8 +587,9 @@ __global__ void __launch_bounds__(DtSmem<D, false>::kThreads, 1)
         if (kRule && !quick) {
           if (p.rule.cap_out > 0.f) {
             if constexpr (kSplitP) {
-              // the short polynomial when it holds for the warp's 64 x 32 scores
-              float big = 0.f;
+              // the short polynomial when it holds for the warp's 64 x 32 scores (not
+              // in edge blocks, where keys that no row attends would have a say)
+              float big = edge ? CUDART_INF_F : 0.f;
 #pragma unroll
               for (int c = 0; c < 64; c += 2)
                 big = fmaxf(fmaxf(big, fabsf(__uint_as_float(s[c]))),

@@ -301,6 +301,22 @@ def test_shared_long_own_tokens():
     check_shared(2, 0, [5000, 20001], 4, 1, 64, "bf16", page=512, weights=True)
 
 
+@pytest.mark.parametrize("n,d", [(14, 128), (14, 64), (3, 128), (1, 128)])
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+@pytest.mark.parametrize("out", ["same", "fp32"])
+def test_shared_results_do_not_depend_on_what_ran_before(n, d, softcap, out):
+    """Rows behind the prefix's end are whatever shared memory held."""
+    c, q, pid, ids, got = check_shared(n, 4937, [9] * n, 8, 1, d, "bf16", page=32, out=out,
+                                       softcap=softcap, slopes=True)
+    sl = torch.linspace(0.01, 0.6, 8, device="cuda")
+    for gain in (1e-3, 1e4):
+        k = normal(8, 20000, 8, d, dtype=torch.bfloat16, gain=gain)
+        for rows in (1, 512):
+            spd.prefill_attention(normal(9, rows, 8, d, dtype=torch.bfloat16), k, k, check=True)
+        x = c.shared_prefix_attention(q, pid, ids, softcap=softcap, slopes=sl, out_dtype=got.dtype)
+        assert torch.equal(x, got)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("kind,d", [("prompt", 64), ("prompt", 128), (2, 64), (2, 128), (5, 128),
                                     (20, 64), (20, 128)])
