@@ -729,10 +729,12 @@ def prefill_attention(q, k, v, key_begin=None, key_end=None, scale=0.0, softcap=
         cfg = spd_dense_config(cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim, cfg.dtype, cfg.out,
                                _rule(scale, softcap, slopes, cfg.num_q_heads, dev))
     raw = _raw_stream(torch, dev, stream)
-    work = _workspace(torch, nbytes, q.device, raw, stream).data_ptr() if nbytes else None
+    # (held until the kernels are enqueued: a block given back before could go to another call)
+    work = _workspace(torch, nbytes, q.device, raw, stream) if nbytes else None
     st = lib().spd_prefill_attention(
         cfg, Lq, Lk, q.data_ptr(), _token_stride(q, "q"), k.data_ptr(), _token_stride(k, "k"),
-        v.data_ptr(), _token_stride(v, "v"), kb, ke, out.data_ptr(), work, nbytes, raw or None)
+        v.data_ptr(), _token_stride(v, "v"), kb, ke, out.data_ptr(),
+        None if work is None else work.data_ptr(), nbytes, raw or None)
     if st != SPD_OK:
         _check(st, "spd_prefill_attention")
     if check:

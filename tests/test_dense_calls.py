@@ -1,0 +1,96 @@
+"""How the dense operators' Python calls handle memory and arguments, on the CPU:
+the library's entry points are replaced by recorders, tensors live in host
+memory and streams are stand-ins."""
+import contextlib
+import ctypes
+import types
+import weakref
+
+import pytest
+import torch
+
+import sparse_paged_decode_logical_gb300 as spd
+
+
+class Recorder:
+    """Stands in for torch and for the library: every buffer that a call
+    allocates, the stream whose pool it came from and the streams it was
+    recorded on, and which of the buffers live when the library is called."""
+
+    def __init__(self):
+        self.buffers = {}  # address: (weak reference, stream it was allocated under)
+        self.recorded = {}
+        self.current = "caller"
+        self.calls = []
+        self.torch = types.SimpleNamespace(
+            empty=self.empty, float32=torch.float32, int32=torch.int32, uint8=torch.uint8,
+            cuda=types.SimpleNamespace(stream=self.stream, Stream=Stream, ExternalStream=Stream,
+                                       current_stream=lambda device=None: self.current))
+
+    def empty(self, shape, dtype=None, device=None):
+        t = Buffer(torch.empty(shape, dtype=dtype))
+        t.recorder = self
+        self.buffers[t.data_ptr()] = (weakref.ref(t), self.current)
+        return t
+
+    @contextlib.contextmanager
+    def stream(self, s):
+        held, self.current = self.current, s
+        yield
+        self.current = held
+
+    def __getattr__(self, name):  # a library entry point
+        def call(*args):
+            addresses = [a for a in args if isinstance(a, int) and a in self.buffers]
+            self.calls.append((name, args, [(self.buffers[a][0]() is not None, self.buffers[a][1])
+                                            for a in addresses]))
+            if name.endswith("_sizes"):
+                args[-1].value = 4096
+            return 0
+        return call
+
+
+class Stream:
+    def __init__(self, address=77, device=None):
+        self.cuda_stream = address
+
+    def __eq__(self, other):
+        return isinstance(other, Stream) and other.cuda_stream == self.cuda_stream
+
+
+class Buffer(torch.Tensor):
+    @staticmethod
+    def __new__(cls, t):
+        return torch.Tensor._make_subclass(cls, t)
+
+    def record_stream(self, s):
+        self.recorder.recorded.setdefault(self.data_ptr(), []).append(s)
+
+
+@pytest.fixture
+def rec(monkeypatch):
+    r = Recorder()
+    monkeypatch.setattr(spd, "lib", lambda: r)
+    monkeypatch.setattr(spd, "_prompt_plans", {})
+    return r
+
+
+def prompt_operands(rec, monkeypatch):
+    """A prompt call whose plan needs a workspace."""
+    cfg = spd.spd_dense_config(4, 2, 64, 1, 0, spd.spd_score_rule(0.0, 0.0, None))
+    monkeypatch.setattr(spd, "_prompt_plan", lambda q, k, v, out_dtype, scale, softcap: (
+        rec.torch, cfg, 4096, tuple(q.shape), torch.float32, q.shape[0], k.shape[0]))
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    k = torch.zeros(9, 2, 64, dtype=torch.bfloat16)
+    return q, k
+
+
+@pytest.mark.parametrize("stream", [None, Stream()])
+def test_prompt_workspace_lives_until_the_kernels_are_enqueued(rec, monkeypatch, stream):
+    q, k = prompt_operands(rec, monkeypatch)
+    monkeypatch.setattr(spd, "_raw_stream", lambda *a: 77)
+    spd.prefill_attention(q, k, k, stream=stream)
+    (name, args, held), = rec.calls
+    work = args[-3]
+    assert name == "spd_prefill_attention" and work in rec.buffers and args[-2] == 4096
+    assert held and all(alive for alive, _ in held)
