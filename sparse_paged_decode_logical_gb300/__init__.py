@@ -494,7 +494,8 @@ class SparsePagedKVCache:
         1/sqrt(d); softcap caps the scores by a tanh; slopes fp32 [Hq] bias
         them by distance.  weights_out fp32 [n][Hkv][>= longest own length]
         receives weights_in (None: 0) plus the softmax weight of every own
-        token, summed over the query heads of its kv head."""
+        token, summed over the query heads of its kv head.  `stream` as in
+        :func:`prefill_attention`."""
         t = self.torch
         ids, n = self._id_array(seq_ids)
         prefix_id = -1 if prefix_id is None else int(prefix_id)
@@ -504,7 +505,7 @@ class SparsePagedKVCache:
         if out_dtype not in (t.float32, self.dtype):
             raise ValueError("out_dtype must be torch.float32 or %s" % self.dtype)
         if out is None:
-            out = t.empty((n, self.Hq, self.d), dtype=out_dtype, device=self.device)
+            out = _empty(t, (n, self.Hq, self.d), out_dtype, self.device, stream)
         op = self._ptr(out, (n, self.Hq, self.d), out_dtype)
         rule = _rule(scale, softcap, slopes, self.Hq, self._dev_index)
         w_in = w_out = None
@@ -524,7 +525,7 @@ class SparsePagedKVCache:
         if st != SPD_OK:
             _check(st, "spd_shared_prefix_sizes", self.ctx)
         nbytes, raw = ws.value, self._stream(stream)
-        work = _workspace(t, nbytes, self.device, raw, stream)
+        work = _empty(t, nbytes, t.uint8, self.device, stream)
         st = L.spd_shared_prefix_attention(
             self.ctx, qp, prefix_id, ids, n, rule, 0 if out_dtype == t.float32 else 1, op, w_in,
             w_out, stride, work.data_ptr(), nbytes, raw or None)
@@ -536,7 +537,8 @@ class SparsePagedKVCache:
         """Compact each source sequence into an empty destination sequence:
         every kv head keeps its `recent` newest tokens and the best of the
         others by weights fp32 [n][Hkv][>= longest source], `keep` in all.
-        Returns (kept int32 [n][Hkv][keep], -1 padded, and their weights)."""
+        Returns (kept int32 [n][Hkv][keep], -1 padded, and their weights).
+        `stream` as in :func:`prefill_attention`."""
         t = self.torch
         src, n = self._id_array(src_ids)
         dst, nd = self._id_array(dst_ids)
@@ -548,8 +550,8 @@ class SparsePagedKVCache:
         if keep < 1:
             raise ValueError("keep must be >= 1")
         wp = self._ptr(weights, (n, self.Hkv, weights.shape[2]), t.float32)
-        kept = t.empty((n, self.Hkv, keep), dtype=t.int32, device=self.device)
-        kw = t.empty((n, self.Hkv, keep), dtype=t.float32, device=self.device)
+        kept = _empty(t, (n, self.Hkv, keep), t.int32, self.device, stream)
+        kw = _empty(t, (n, self.Hkv, keep), t.float32, self.device, stream)
         raw = self._stream(stream)
         _check(lib().spd_kv_evict(self.ctx, src, dst, n, keep, int(recent), wp, weights.shape[2],
                                   kept.data_ptr(), kw.data_ptr(), raw or None), "spd_kv_evict",
@@ -624,14 +626,19 @@ def _rule(scale, softcap, slopes, num_q_heads, device_index):
     return spd_score_rule(float(scale or 0.0), float(softcap or 0.0), slopes)
 
 
-def _workspace(torch, nbytes, device, raw, stream):
-    """A call's workspace, not reused by the allocator before the stream that
-    the call runs on has done with it."""
-    work = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-    if stream is not None:
-        work.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                           else torch.cuda.ExternalStream(raw, device=device))
-    return work
+def _empty(torch, shape, dtype, device, stream):
+    """A buffer of a call on `stream`, from that stream's pool: the kernels that used
+    its memory before are then ahead of the call's, and those that use it next
+    behind.  (None: the current stream.)  What the caller's stream does with it
+    before it is given back is waited for too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 # What a prompt call's shapes, types and scalars decide, by them: the checked
@@ -717,7 +724,7 @@ def prefill_attention(q, k, v, key_begin=None, key_end=None, scale=0.0, softcap=
                                  % (Lq, q.device))
         kb, ke = key_begin.data_ptr(), key_end.data_ptr()
     if out is None:
-        out = q.new_empty(shape, dtype=odt)
+        out = _empty(torch, shape, odt, q.device, stream)
     else:
         if out_dtype is None and out.dtype is not odt:
             return prefill_attention(q, k, v, key_begin, key_end, scale, softcap, slopes, out.dtype,
@@ -730,7 +737,7 @@ def prefill_attention(q, k, v, key_begin=None, key_end=None, scale=0.0, softcap=
                                _rule(scale, softcap, slopes, cfg.num_q_heads, dev))
     raw = _raw_stream(torch, dev, stream)
     # (held until the kernels are enqueued: a block given back before could go to another call)
-    work = _workspace(torch, nbytes, q.device, raw, stream) if nbytes else None
+    work = _empty(torch, nbytes, torch.uint8, q.device, stream) if nbytes else None
     st = lib().spd_prefill_attention(
         cfg, Lq, Lk, q.data_ptr(), _token_stride(q, "q"), k.data_ptr(), _token_stride(k, "k"),
         v.data_ptr(), _token_stride(v, "v"), kb, ke, out.data_ptr(),
@@ -746,7 +753,8 @@ def prefill_attention(q, k, v, key_begin=None, key_end=None, scale=0.0, softcap=
 def document_key_ranges(offsets, n_tokens, prefix=None, stream=None):
     """Key intervals of packed documents (spd_document_key_ranges): offsets
     int32 [documents + 1], prefix int32 [documents] or None (causal).  Returns
-    (key_begin, key_end) int32 [n_tokens] for :func:`prefill_attention`."""
+    (key_begin, key_end) int32 [n_tokens] for :func:`prefill_attention`, whose
+    rule for `stream` holds here too."""
     import torch
     dev = offsets.device
     n = offsets.shape[0] - 1 if offsets.dim() == 1 else 0
@@ -755,8 +763,7 @@ def document_key_ranges(offsets, n_tokens, prefix=None, stream=None):
                               or not t.is_contiguous() or t.device != dev or dev.type != "cuda"):
             raise ValueError("offsets int32 [documents + 1] and prefix int32 [documents], "
                              "contiguous, on one CUDA device")
-    kb = torch.empty(int(n_tokens), dtype=torch.int32, device=dev)
-    ke = torch.empty(int(n_tokens), dtype=torch.int32, device=dev)
+    kb, ke = (_empty(torch, int(n_tokens), torch.int32, dev, stream) for _ in range(2))
     raw = _raw_stream(torch, dev.index, stream)
     _check(lib().spd_document_key_ranges(
         offsets.data_ptr(), prefix.data_ptr() if prefix is not None else None, n, int(n_tokens),

@@ -2,7 +2,6 @@
 the library's entry points are replaced by recorders, tensors live in host
 memory and streams are stand-ins."""
 import contextlib
-import ctypes
 import types
 import weakref
 
@@ -23,15 +22,18 @@ class Recorder:
         self.current = "caller"
         self.calls = []
         self.torch = types.SimpleNamespace(
-            empty=self.empty, float32=torch.float32, int32=torch.int32, uint8=torch.uint8,
+            empty=self.empty_of(torch.empty), float32=torch.float32, int32=torch.int32, uint8=torch.uint8,
             cuda=types.SimpleNamespace(stream=self.stream, Stream=Stream, ExternalStream=Stream,
                                        current_stream=lambda device=None: self.current))
 
-    def empty(self, shape, dtype=None, device=None):
-        t = Buffer(torch.empty(shape, dtype=dtype))
-        t.recorder = self
-        self.buffers[t.data_ptr()] = (weakref.ref(t), self.current)
-        return t
+    def empty_of(self, real):
+        """`empty`, from the allocator `real` (to stand in for it)."""
+        def empty(shape, dtype=None, device=None):
+            t = Buffer(real(shape, dtype=dtype))
+            t.recorder = self
+            self.buffers[t.data_ptr()] = (weakref.ref(t), self.current)
+            return t
+        return empty
 
     @contextlib.contextmanager
     def stream(self, s):
@@ -54,6 +56,8 @@ class Stream:
     def __init__(self, address=77, device=None):
         self.cuda_stream = address
 
+    __hash__ = None
+
     def __eq__(self, other):
         return isinstance(other, Stream) and other.cuda_stream == self.cuda_stream
 
@@ -64,7 +68,7 @@ class Buffer(torch.Tensor):
         return torch.Tensor._make_subclass(cls, t)
 
     def record_stream(self, s):
-        self.recorder.recorded.setdefault(self.data_ptr(), []).append(s)
+        self.recorder.recorded.setdefault(self.data_ptr(), set()).add(s)
 
 
 @pytest.fixture
@@ -94,3 +98,48 @@ def test_prompt_workspace_lives_until_the_kernels_are_enqueued(rec, monkeypatch,
     work = args[-3]
     assert name == "spd_prefill_attention" and work in rec.buffers and args[-2] == 4096
     assert held and all(alive for alive, _ in held)
+
+
+def stand_in_cache(rec):
+    c = object.__new__(spd.SparsePagedKVCache)
+    c.torch, c.ctx, c.device = rec.torch, None, torch.device("cpu")
+    c.Hq, c.Hkv, c.d, c.dtype = 4, 2, 64, torch.bfloat16
+    c._dev_index, c._raw_stream, c._ids_cache = -1, lambda device: 77, {}
+    return c
+
+
+@pytest.mark.parametrize("stream", [Stream(), 77])
+def test_buffers_of_a_call_on_a_stream_come_from_its_pool(rec, monkeypatch, stream):
+    """Memory from the caller's pool may still be in use there when the call's
+    stream writes it, and the other way round when it is given back."""
+    q, k = prompt_operands(rec, monkeypatch)
+    c = stand_in_cache(rec)
+    outs = [spd.prefill_attention(q, k, k, stream=stream),
+            c.shared_prefix_attention(q, 5, [0, 1, 2], stream=stream),
+            *c.kv_evict([0], [1], 7, 2, torch.zeros(1, 2, 9), stream=stream)]
+    offsets = types.SimpleNamespace(device=types.SimpleNamespace(type="cuda", index=0), shape=(3,),
+                                    dtype=torch.int32, dim=lambda: 1, is_contiguous=lambda: True,
+                                    data_ptr=lambda: 4096)
+    monkeypatch.setattr(torch, "empty", rec.empty_of(torch.empty))
+    monkeypatch.setattr(torch, "cuda", rec.torch.cuda)
+    outs += spd.document_key_ranges(offsets, 9, stream=stream)
+    assert [n for n, _, _ in rec.calls] == ["spd_prefill_attention", "spd_shared_prefix_sizes",
+                                            "spd_shared_prefix_attention", "spd_kv_evict",
+                                            "spd_document_key_ranges"]
+    for name, _, held in rec.calls:
+        assert len(held) == (0 if name.endswith("_sizes") else 2), name
+        assert all(alive and under == Stream(77) for alive, under in held), name
+    for t in outs:  # the caller reads them on its own stream
+        assert rec.recorded[t.data_ptr()] == {"caller"}
+
+
+def test_buffers_of_a_call_without_a_stream(rec, monkeypatch):
+    q, k = prompt_operands(rec, monkeypatch)
+    monkeypatch.setattr(spd, "_raw_stream", lambda *a: 0)
+    c = stand_in_cache(rec)
+    spd.prefill_attention(q, k, k)
+    c.shared_prefix_attention(q, 5, [0, 1, 2])
+    c.kv_evict([0], [1], 7, 2, torch.zeros(1, 2, 9))
+    for _, _, held in rec.calls:
+        assert all(alive and under == "caller" for alive, under in held)
+    assert not rec.recorded

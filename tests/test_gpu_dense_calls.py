@@ -1,0 +1,81 @@
+"""Calls of the dense operators as programs make them: beside one another on
+streams, on uneven key intervals, with operands that share a warp or a batch
+with others; against the 64-bit implementations of dense_ref.py or against the
+same call alone."""
+import math
+
+import pytest
+import torch
+
+import sparse_paged_decode_logical_gb300 as spd
+from dense_ref import prompt, tolerance
+from test_gpu_dense import DT, check_shared, new_cache, normal
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- streams ---------------------------------------------------------------------
+
+def test_cut_prompts_on_two_streams_at_once():
+    """Both calls have a workspace of the same size, and their buffers are given
+    back and taken again while they run."""
+    hq, hkv, d, lk = 16, 8, 128, 20000
+    k, v = (normal(i, lk, hkv, d, dtype=torch.bfloat16) for i in (1, 2))
+    qs = [normal(10 + i, 40, hq, d, dtype=torch.bfloat16) for i in range(12)]
+    want = [spd.prefill_attention(q, k, v, check=True) for q in qs]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        got, fill = [], []
+        for i, q in enumerate(qs):
+            got.append(spd.prefill_attention(q, k, v, stream=stream if i % 2 else None))
+            # blocks of the workspace's and the output's sizes, written at once
+            for n in (want[0].numel() * 4, 1 << 21, 1 << 22, 1 << 23):
+                fill.append(torch.full((n // 4,), 7.0, device="cuda"))
+            if i % 3 == 2:
+                fill.clear()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_cache_calls_on_a_stream_beside_other_work():
+    """The cache's calls all on one stream, the caller's stream busy with memory of
+    its own; results read there after a wait and given back at once."""
+    hq, hkv, d, dt = 8, 2, 128, torch.bfloat16
+    c = new_cache(hq, hkv, d, "bf16", 64, 16, 300, 40, 6000)
+    doc = c.seq_create()
+    c.kv_append([doc], normal(1, 1, 5000, hkv, d, dtype=dt), normal(2, 1, 5000, hkv, d, dtype=dt))
+    ids = [c.seq_create() for _ in range(9)]
+    c.kv_append(ids, normal(3, 9, 30, hkv, d, dtype=dt), normal(4, 9, 30, hkv, d, dtype=dt))
+    q = normal(5, 9, hq, d, dtype=dt)
+    w = normal(6, 9, hkv, 30).abs()
+    want = c.shared_prefix_attention(q, doc, ids)
+    dst = [c.seq_create() for _ in ids]
+    kept = c.kv_evict(ids, dst, 12, 3, w)
+    kept = kept[0].clone(), kept[1].clone()
+    for i in reversed(dst):
+        c.seq_free(i)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    here = torch.cuda.current_stream()
+    sums = []
+    for _ in range(20):
+        busy = torch.full((want.numel(),), 3.0, device="cuda") * 2
+        x = c.shared_prefix_attention(q, doc, ids, stream=s)
+        dst = [c.seq_create() for _ in ids]
+        a, b = c.kv_evict(ids, dst, 12, 3, w, stream=s)
+        for i in reversed(dst):
+            c.seq_free(i)
+        here.wait_stream(s)
+        sums.append((x - want).abs().max() + (a - kept[0]).abs().max() + (b - kept[1]).abs().max()
+                    + (busy - 6).abs().max())
+        del x, a, b, busy
+    assert float(torch.stack(sums).max()) == 0.0
+    c.check_status(stream=s)
+    off = torch.tensor([0, 5, 70, 83], dtype=torch.int32, device="cuda")
+    b0, e0 = spd.document_key_ranges(off, 90)
+    torch.cuda.synchronize()
+    b1, e1 = spd.document_key_ranges(off, 90, stream=s)
+    here.wait_stream(s)
+    assert torch.equal(b0, b1) and torch.equal(e0, e1)
