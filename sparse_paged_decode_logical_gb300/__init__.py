@@ -407,8 +407,7 @@ class SparsePagedKVCache:
         n = len(seq_ids)
         qp = self._ptr(q, (n, self.Hq, self.d), self.dtype)
         if out is None:
-            out = self.torch.empty((n, self.Hq, self.d), dtype=self.torch.float32,
-                                   device=self.device)
+            out = _empty(self.torch, (n, self.Hq, self.d), self.torch.float32, self.device, stream)
         op = self._ptr(out, (n, self.Hq, self.d), self.torch.float32)
         spd_sparse_decode_attention(self.ctx, qp, seq_ids, op, self._stream(stream))
         return out
@@ -419,13 +418,14 @@ class SparsePagedKVCache:
         exp(logit - row_max) over the attended tokens, [n][Hq] fp32."""
         n = len(seq_ids)
         qp = self._ptr(q, (n, self.Hq, self.d), self.dtype)
-        out = self.torch.empty((n, self.Hq, self.d), dtype=self.torch.float32, device=self.device)
-        rm = self.torch.empty((n, self.Hq), dtype=self.torch.float32, device=self.device)
-        rs = self.torch.empty((n, self.Hq), dtype=self.torch.float32, device=self.device)
+        t, f32 = self.torch, self.torch.float32
+        out = _empty(t, (n, self.Hq, self.d), f32, self.device, stream)
+        rm = _empty(t, (n, self.Hq), f32, self.device, stream)
+        rs = _empty(t, (n, self.Hq), f32, self.device, stream)
         spd_sparse_decode_attention_stats(self.ctx, qp, seq_ids,
-                                          self._ptr(out, (n, self.Hq, self.d), self.torch.float32),
-                                          self._ptr(rm, (n, self.Hq), self.torch.float32),
-                                          self._ptr(rs, (n, self.Hq), self.torch.float32),
+                                          self._ptr(out, (n, self.Hq, self.d), f32),
+                                          self._ptr(rm, (n, self.Hq), f32),
+                                          self._ptr(rs, (n, self.Hq), f32),
                                           self._stream(stream))
         return out, rm, rs
 
@@ -449,11 +449,11 @@ class SparsePagedKVCache:
             max_pages = max([self.attended_page_count(s) for s in seq_ids] + [1]) if Hd else 1
         qp = self._ptr(q, (n, self.Hq, self.d), self.dtype)
         t, f32 = self.torch, self.torch.float32
-        out = t.empty((n, self.Hq, self.d), dtype=f32, device=self.device)
-        rm = t.empty((n, self.Hq), dtype=f32, device=self.device)
-        rs = t.empty((n, self.Hq), dtype=f32, device=self.device)
-        pages = t.empty((n, Hd, max_pages), dtype=t.int32, device=self.device)
-        mass = t.empty((n, Hd, G, max_pages), dtype=f32, device=self.device)
+        out = _empty(t, (n, self.Hq, self.d), f32, self.device, stream)
+        rm = _empty(t, (n, self.Hq), f32, self.device, stream)
+        rs = _empty(t, (n, self.Hq), f32, self.device, stream)
+        pages = _empty(t, (n, Hd, max_pages), t.int32, self.device, stream)
+        mass = _empty(t, (n, Hd, G, max_pages), f32, self.device, stream)
         spd_sparse_decode_attention_page_mass(
             self.ctx, qp, seq_ids, self._ptr(out, (n, self.Hq, self.d), f32),
             self._ptr(rm, (n, self.Hq), f32), self._ptr(rs, (n, self.Hq), f32),
@@ -477,8 +477,7 @@ class SparsePagedKVCache:
         kp = self._ptr(k, (n, self.Hkv, self.d), self.dtype)
         vp = self._ptr(v, (n, self.Hkv, self.d), self.dtype)
         if out is None:
-            out = self.torch.empty((n, self.Hq, self.d), dtype=self.torch.float32,
-                                   device=self.device)
+            out = _empty(self.torch, (n, self.Hq, self.d), self.torch.float32, self.device, stream)
         op = self._ptr(out, (n, self.Hq, self.d), self.torch.float32)
         st = self._step_fn(self.ctx, qp, kp, vp, ids[0], n, op, self._stream(stream) or None)
         if st != SPD_OK:
@@ -598,9 +597,9 @@ def prefill_block_sparse_attention(q, k, v, w_q, w_k, block=64, token_budget=409
     _check(lib().spd_prefill_sizes(ctypes.byref(cfg), L, ctypes.byref(kb), ctypes.byref(ws)),
            "spd_prefill_sizes")
     nb = -(-L // block)
-    out = torch.empty((L, Hq, d), dtype=torch.float32, device=q.device)
-    blocks = torch.empty((Hkv, nb, kb.value), dtype=torch.int32, device=q.device)
-    work = torch.empty(ws.value, dtype=torch.uint8, device=q.device)
+    out = _empty(torch, (L, Hq, d), torch.float32, q.device, stream)
+    blocks = _empty(torch, (Hkv, nb, kb.value), torch.int32, q.device, stream)
+    work = _empty(torch, ws.value, torch.uint8, q.device, stream)
     if stream is None:
         stream = torch.cuda.current_stream(q.device)
     st = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)

@@ -47,7 +47,10 @@ class Recorder:
             self.calls.append((name, args, [(self.buffers[a][0]() is not None, self.buffers[a][1])
                                             for a in addresses]))
             if name.endswith("_sizes"):
-                args[-1].value = 4096
+                for a in args:  # (by reference, or the object itself)
+                    a = getattr(a, "_obj", a)
+                    if hasattr(a, "value"):
+                        a.value = 4096
             return 0
         return call
 
@@ -143,3 +146,28 @@ def test_buffers_of_a_call_without_a_stream(rec, monkeypatch):
     for _, _, held in rec.calls:
         assert all(alive and under == "caller" for alive, under in held)
     assert not rec.recorded
+
+
+@pytest.mark.parametrize("stream", [None, Stream(), 77])
+def test_sparse_calls_allocate_under_their_stream(rec, monkeypatch, stream):
+    c = stand_in_cache(rec)
+    c.cfg_dict = {"streaming": [True, False]}
+    c._step_fn = rec.spd_decode_step
+    q, k = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    c.sparse_decode_attention(q, [0, 1, 2], stream=stream)
+    c.sparse_decode_attention_stats(q, [0, 1, 2], stream=stream)
+    c.sparse_decode_attention_page_mass(q, [0, 1, 2], max_pages=4, stream=stream)
+    c.decode_step(q, k, k, [0, 1, 2], stream=stream)
+    monkeypatch.setattr(torch, "empty", rec.empty_of(torch.empty))
+    monkeypatch.setattr(torch, "cuda", rec.torch.cuda)
+    monkeypatch.setattr(rec.torch.cuda, "current_stream", lambda device=None: Stream(5))
+    w = torch.zeros(2, 64, 8)
+    spd.prefill_block_sparse_attention(torch.zeros(9, 4, 64, dtype=torch.bfloat16),
+                                       *[torch.zeros(9, 2, 64, dtype=torch.bfloat16)] * 2, w, w,
+                                       stream=stream, check=False)
+    under = "caller" if stream is None else Stream(77)
+    buffers = {name: held for name, _, held in rec.calls}
+    for name, n in (("spd_sparse_decode_attention", 1), ("spd_sparse_decode_attention_stats", 3),
+                    ("spd_sparse_decode_attention_page_mass", 5), ("spd_decode_step", 1),
+                    ("spd_prefill_block_sparse_attention", 3)):
+        assert len(buffers[name]) == n and all(x == (True, under) for x in buffers[name]), name
