@@ -59,7 +59,8 @@ class Stream:
     def __init__(self, address=77, device=None):
         self.cuda_stream = address
 
-    __hash__ = None
+    def __hash__(self):
+        return self.cuda_stream
 
     def __eq__(self, other):
         return isinstance(other, Stream) and other.cuda_stream == self.cuda_stream
@@ -116,10 +117,11 @@ def test_buffers_of_a_call_on_a_stream_come_from_its_pool(rec, monkeypatch, stre
     """Memory from the caller's pool may still be in use there when the call's
     stream writes it, and the other way round when it is given back."""
     q, k = prompt_operands(rec, monkeypatch)
-    c = stand_in_cache(rec)
+    c, w = stand_in_cache(rec), torch.zeros(1, 2, 9)
     outs = [spd.prefill_attention(q, k, k, stream=stream),
             c.shared_prefix_attention(q, 5, [0, 1, 2], stream=stream),
-            *c.kv_evict([0], [1], 7, 2, torch.zeros(1, 2, 9), stream=stream)]
+            *c.kv_evict([0], [1], 7, 2, w, stream=stream)]
+    rec.buffers = {t.data_ptr(): rec.buffers[t.data_ptr()] for t in outs}
     offsets = types.SimpleNamespace(device=types.SimpleNamespace(type="cuda", index=0), shape=(3,),
                                     dtype=torch.int32, dim=lambda: 1, is_contiguous=lambda: True,
                                     data_ptr=lambda: 4096)
@@ -139,10 +141,10 @@ def test_buffers_of_a_call_on_a_stream_come_from_its_pool(rec, monkeypatch, stre
 def test_buffers_of_a_call_without_a_stream(rec, monkeypatch):
     q, k = prompt_operands(rec, monkeypatch)
     monkeypatch.setattr(spd, "_raw_stream", lambda *a: 0)
-    c = stand_in_cache(rec)
+    c, w = stand_in_cache(rec), torch.zeros(1, 2, 9)
     spd.prefill_attention(q, k, k)
     c.shared_prefix_attention(q, 5, [0, 1, 2])
-    c.kv_evict([0], [1], 7, 2, torch.zeros(1, 2, 9))
+    c.kv_evict([0], [1], 7, 2, w)
     for _, _, held in rec.calls:
         assert all(alive and under == "caller" for alive, under in held)
     assert not rec.recorded
@@ -161,10 +163,10 @@ def test_sparse_calls_allocate_under_their_stream(rec, monkeypatch, stream):
     monkeypatch.setattr(torch, "empty", rec.empty_of(torch.empty))
     monkeypatch.setattr(torch, "cuda", rec.torch.cuda)
     monkeypatch.setattr(rec.torch.cuda, "current_stream", lambda device=None: Stream(5))
-    w = torch.zeros(2, 64, 8)
-    spd.prefill_block_sparse_attention(torch.zeros(9, 4, 64, dtype=torch.bfloat16),
-                                       *[torch.zeros(9, 2, 64, dtype=torch.bfloat16)] * 2, w, w,
-                                       stream=stream, check=False)
+    q, k, w = torch.zeros(9, 4, 64, dtype=torch.bfloat16), torch.zeros(
+        9, 2, 64, dtype=torch.bfloat16), torch.zeros(2, 64, 8)
+    rec.buffers.clear()  # (operands may lie where a result given back was)
+    spd.prefill_block_sparse_attention(q, k, k, w, w, stream=stream, check=False)
     under = "caller" if stream is None else Stream(77)
     buffers = {name: held for name, _, held in rec.calls}
     for name, n in (("spd_sparse_decode_attention", 1), ("spd_sparse_decode_attention_stats", 3),
