@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(DtSmem<D, false>::kThreads, 1)
   }
   __syncthreads();
   const int *rg = misc + kMiscRange;
-  // the split's blocks [kb0, kb0 + n) of the CTA's range, in pairs [0, np)
+  // the split's blocks [kb0, kb0 + n) of the CTA's range, in pairs [0, pairs)
   const int all_beg = min(rg[0], rg[4]), all_end = max(rg[1], rg[5]);
   const int full_beg = max(rg[2], rg[6]), full_end = min(rg[3], rg[7]);
   int kb0 = 0, n = 0;
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(DtSmem<D, false>::kThreads, 1)
     kb0 = first + split * per;
     n = max(0, min(last - kb0, per));
   }
-  const int np = (n + 1) / 2;
+  const int pairs = (n + 1) / 2;
   const bool third = kThird && n * kDenseBlock <= kThirdKeys;
   // Blocks in ascending order, so that the CTAs that run together read the same
   // K and V at the same time (descending, where each starts at its own newest
@@ -292,16 +292,21 @@ __global__ void __launch_bounds__(DtSmem<D, false>::kThreads, 1)
   auto pair_first = [&](int m) {
     const int past = desc ? kb0 + n - (rg[4 * m + 1] + kDenseBlock - 1) / kDenseBlock
                           : rg[4 * m] / kDenseBlock - kb0;  // blocks before its keys
-    return p.dup ? 0 : min(np, max(0, past) / 2);
+    return p.dup ? 0 : min(pairs, max(0, past) / 2);
   };
   auto pair_last = [&](int m) {
     if (p.dup) return (n + 1 - m) / 2;
     if (rg[4 * m] >= rg[4 * m + 1]) return 0;
     const int blocks = desc ? kb0 + n - rg[4 * m] / kDenseBlock  // up to its last key's
                             : (rg[4 * m + 1] + kDenseBlock - 1) / kDenseBlock - kb0;
-    const int last = min(np, max(0, blocks + 1) / 2);
+    const int last = min(pairs, max(0, blocks + 1) / 2);
     return last > pair_first(m) ? last : 0;  // (0: none of the split's keys)
   };
+  // the pairs [0, np) that are loaded: up to the last one that a matrix computes.  (The
+  // rows of one matrix may lie far from those of the other, with whole splits between
+  // them.  A stage's K counts as read once both matrices say so, and only one that
+  // computes the pair or a later one has waited for the copy.)
+  const int np = max(pair_last(0), pair_last(1));
   auto is_edge = [&](int key0) {  // some row attends only a part of the block
     return key0 < full_beg || key0 + kDenseBlock > full_end;
   };
@@ -429,8 +434,8 @@ __global__ void __launch_bounds__(DtSmem<D, false>::kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&bars[Sm::kBarVC + s]);
-        // a matrix that has no more pairs frees the stages here; the pairs before
-        // its first it frees itself
+        // a matrix that has no more pairs frees the stages here (the other one has
+        // this pair or a later one); the pairs before its first it frees itself
         for (int m = 0; m < 2; ++m)
           if (pp >= pair_last(m)) {
             mbar_arrive(&bars[Sm::kBarKE + s]);

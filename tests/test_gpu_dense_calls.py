@@ -79,3 +79,31 @@ def test_cache_calls_on_a_stream_beside_other_work():
     b1, e1 = spd.document_key_ranges(off, 90, stream=s)
     here.wait_stream(s)
     assert torch.equal(b0, b1) and torch.equal(e0, e1)
+
+
+# ---- key intervals of one tile's rows far apart ------------------------------------
+
+@pytest.mark.parametrize("near,far", [(64, 40), (700, 1500), (1, 1), (5000, 9000)])
+@pytest.mark.parametrize("hq,hkv,d,dtype,out", [(1, 1, 64, "fp16", "same"), (2, 1, 128, "bf16", "fp32"),
+                                                (3, 3, 128, "fp16", "fp32"), (2, 2, 64, "bf16", "same")])
+@pytest.mark.parametrize("slopes", [False, True])
+def test_prompt_rows_that_attend_the_first_keys_beside_rows_that_attend_the_last(near, far, hq, hkv, d,
+                                                                                 dtype, out, slopes):
+    """Cut prompts with whole cuts between the keys of a tile's two halves; in the
+    last rows the halves come the other way round, with rows that attend nothing."""
+    lq, lk, dt = 700, 40000, DT[dtype]
+    q, k, v = normal(1, lq, hq, d, dtype=dt), normal(2, lk, hkv, d, dtype=dt), normal(3, lk, hkv, d, dtype=dt)
+    half = 128 // math.gcd(hq // hkv, 8)
+    at = torch.arange(lq, device="cuda")
+    first = (at // half % 2 == 0) ^ (at >= 4 * half)
+    b = torch.where(first, 0, lk - far)
+    e = torch.where(first, near, lk)
+    e = torch.where(at % 97 == 5, b, e)
+    sl = torch.linspace(0.001, 0.2, hq, device="cuda") if slopes else None
+    od = torch.float32 if out == "fp32" else dt
+    got = spd.prefill_attention(q, k, v, key_begin=b.int(), key_end=e.int(), slopes=sl, out_dtype=od,
+                                check=True)
+    ref, ab, mag = prompt(q, k, v, b, e, d ** -0.5, 0.0, sl)
+    assert bool(((got.double() - ref).abs() <=
+                 tolerance(ref, ab, mag, d, max(near, far, 1025), dt, od, 0.0)).all())
+    assert bool((got[b >= e] == 0).all())
