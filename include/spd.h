@@ -543,7 +543,7 @@ spd_status spd_shared_prefix_attention(spd_ctx *ctx, const void *q, int prefix_i
  * Every kv head keeps its own tokens.  The source stays as it was (free it, or
  * keep it as a prefix); the destination must be empty and takes pages as in
  * spd_kv_append (all or nothing: SPD_ERR_NO_PAGES / SPD_ERR_CAPACITY change
- * nothing).
+ * nothing).  keep <= 2^28 (SPD_ERR_CAPACITY), which is more than any sequence holds.
  *   weights  device fp32 [n_seqs][Hkv][weights_stride], weights_stride >= every L
  *   kept     device int32 [n_seqs][Hkv][keep]: the kept positions, ascending, -1
  *            behind the m-th

@@ -22,6 +22,7 @@ using namespace spd;
 namespace {
 
 constexpr int kMaxTokens = 1 << 28;
+constexpr int kMaxKeep = 1 << 28;  // no sequence is longer (max_context is bounded by it)
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned(const void *p, uintptr_t a) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -688,6 +689,7 @@ spd_status spd_kv_evict(spd_ctx *c, const int *src_ids, const int *dst_ids, int 
   if (!c) return SPD_ERR_INVALID_ARG;
   if (keep < 1 || recent < 0 || recent > keep)
     return fail_message(c, SPD_ERR_INVALID_ARG, "keep >= 1 and 0 <= recent <= keep required");
+  if (keep > kMaxKeep) return fail_message(c, SPD_ERR_CAPACITY, "keep exceeds 2^28");
   if (!aligned(weights, 4) || !aligned(kept, 4) || (kept_weights && !aligned(kept_weights, 4)))
     return fail_message(c, SPD_ERR_INVALID_ARG, "weights and kept must be 4-byte aligned pointers");
   CtxView v;
@@ -711,8 +713,9 @@ spd_status spd_kv_evict(spd_ctx *c, const int *src_ids, const int *dst_ids, int 
       return fail_message(c, SPD_ERR_CAPACITY, "weights_stride is below a sequence's length");
     m[i] = (int)std::min<long long>(keep, L);
   }
+  // (below 2^30: the copying CTAs count on by the grid behind the last group)
   const long long groups = ((long long)keep + 63) / 64;
-  if (groups * std::min(n_seqs, kDenseSeqs) * v.Hd > 0x7fffffffLL)
+  if (groups * std::min(n_seqs, kDenseSeqs) * v.Hd > (1LL << 30))
     return fail_message(c, SPD_ERR_CAPACITY, "keep is too large for one launch");
   if ((r = check_fill(c, dst_ids, m.get(), n_seqs)) != SPD_OK) return r;
   cudaStream_t st = (cudaStream_t)stream;

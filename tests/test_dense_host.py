@@ -192,3 +192,13 @@ def test_python_argument_checks_need_no_gpu():
     row = torch.zeros(4, 12, 128)
     assert spd._token_stride(row[:, :8], "q") == 12 * 128
     assert spd._token_stride(row[:1, :8], "q") == 8 * 128
+
+
+@pytest.mark.parametrize("keep", [(1 << 28) + 1, (1 << 31) - 64, (1 << 31) - 1])
+def test_evict_refuses_a_keep_that_no_sequence_holds(keep):
+    """Before anything is looked at (the source is empty here, too), so that no page is taken."""
+    _, ctx = context()
+    for _ in range(2):
+        spd.spd_seq_create(ctx)
+    assert evict(ctx, keep=keep, recent=0) == CAPACITY
+    assert evict(ctx, keep=1 << 28, recent=0) == STATE
