@@ -27,6 +27,9 @@ BUFFER_FIELDS = ("k_pool", "v_pool", "meta", "stream_k", "stream_v",
                  "page_table", "selection", "scratch")
 
 
+_MAX_TOKENS = 1 << 28  # of a row or a sequence; what is larger would not fit the ABI's ints
+
+
 class SpdError(RuntimeError):
     def __init__(self, status, where, detail=""):
         self.status = status
@@ -548,11 +551,14 @@ class SparsePagedKVCache:
         keep = int(keep)
         if keep < 1:
             raise ValueError("keep must be >= 1")
+        if keep > _MAX_TOKENS:
+            raise SpdError(4, "spd_kv_evict", "keep exceeds 2^28")
+        recent = min(max(int(recent), -1), _MAX_TOKENS + 1)  # (refused below, and never wrapped)
         wp = self._ptr(weights, (n, self.Hkv, weights.shape[2]), t.float32)
         kept = _empty(t, (n, self.Hkv, keep), t.int32, self.device, stream)
         kw = _empty(t, (n, self.Hkv, keep), t.float32, self.device, stream)
         raw = self._stream(stream)
-        _check(lib().spd_kv_evict(self.ctx, src, dst, n, keep, int(recent), wp, weights.shape[2],
+        _check(lib().spd_kv_evict(self.ctx, src, dst, n, keep, recent, wp, weights.shape[2],
                                   kept.data_ptr(), kw.data_ptr(), raw or None), "spd_kv_evict",
                self.ctx)
         return kept, kw
@@ -762,9 +768,12 @@ def document_key_ranges(offsets, n_tokens, prefix=None, stream=None):
                               or not t.is_contiguous() or t.device != dev or dev.type != "cuda"):
             raise ValueError("offsets int32 [documents + 1] and prefix int32 [documents], "
                              "contiguous, on one CUDA device")
-    kb, ke = (_empty(torch, int(n_tokens), torch.int32, dev, stream) for _ in range(2))
+    n_tokens = int(n_tokens)
+    if not 1 <= n_tokens <= _MAX_TOKENS:
+        raise SpdError(1, "spd_document_key_ranges", "n_tokens must be in [1, 2^28]")
+    kb, ke = (_empty(torch, n_tokens, torch.int32, dev, stream) for _ in range(2))
     raw = _raw_stream(torch, dev.index, stream)
     _check(lib().spd_document_key_ranges(
-        offsets.data_ptr(), prefix.data_ptr() if prefix is not None else None, n, int(n_tokens),
+        offsets.data_ptr(), prefix.data_ptr() if prefix is not None else None, n, n_tokens,
         kb.data_ptr(), ke.data_ptr(), raw or None), "spd_document_key_ranges")
     return kb, ke

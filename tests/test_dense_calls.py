@@ -173,3 +173,26 @@ def test_sparse_calls_allocate_under_their_stream(rec, monkeypatch, stream):
                     ("spd_sparse_decode_attention_page_mass", 5), ("spd_decode_step", 1),
                     ("spd_prefill_block_sparse_attention", 3)):
         assert len(buffers[name]) == n and all(x == (True, under) for x in buffers[name]), name
+
+
+# ---- numbers beyond the ABI's 32 bits --------------------------------------------
+
+def test_numbers_that_32_bits_would_wrap_are_refused(rec):
+    """Nothing is allocated and nothing called: as 32 bits, 2^32 + 5 would be 5."""
+    c, w = stand_in_cache(rec), torch.zeros(1, 2, 9)
+    for keep in (2 ** 28 + 1, 2 ** 31 + 5, 2 ** 32 + 5):
+        with pytest.raises(spd.SpdError) as e:
+            c.kv_evict([0], [1], keep, 2, w)
+        assert e.value.name == "SPD_ERR_CAPACITY"
+    for n in (0, -1, 2 ** 28 + 1, 2 ** 32 + 5):
+        offsets = types.SimpleNamespace(device=types.SimpleNamespace(type="cuda", index=0), shape=(3,),
+                                        dtype=torch.int32, dim=lambda: 1, is_contiguous=lambda: True,
+                                        data_ptr=lambda: 4096)
+        with pytest.raises(spd.SpdError) as e:
+            spd.document_key_ranges(offsets, n, stream=77)
+        assert e.value.name == "SPD_ERR_INVALID_ARG"
+    assert not rec.calls and not rec.buffers
+    for recent in (-1, -2 ** 32 + 2, 2 ** 32, 2 ** 32 + 2):
+        c.kv_evict([0], [1], 7, recent, w)
+        passed = rec.calls[-1][1][5]
+        assert passed == (-1 if recent < 0 else 2 ** 28 + 1)  # (neither is a number that is taken)
