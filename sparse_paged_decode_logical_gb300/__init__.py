@@ -708,6 +708,8 @@ def prefill_attention(q, k, v, key_begin=None, key_end=None, scale=0.0, softcap=
     the type of q.  check=True waits and raises if a kernel's own check
     tripped."""
     dev = q.get_device()
+    # (the plan is found by values: a number that a tensor holds may have changed)
+    scale, softcap = float(scale or 0.0), float(softcap or 0.0)
     key = (q.shape, k.shape, v.shape, q.dtype, k.dtype, v.dtype, out_dtype, scale, softcap, dev)
     plan = _prompt_plans.get(key)
     if plan is None:

@@ -196,3 +196,28 @@ def test_numbers_that_32_bits_would_wrap_are_refused(rec):
         c.kv_evict([0], [1], 7, recent, w)
         passed = rec.calls[-1][1][5]
         assert passed == (-1 if recent < 0 else 2 ** 28 + 1)  # (neither is a number that is taken)
+
+
+def test_a_scale_that_a_tensor_holds_is_read_at_every_call(rec, monkeypatch):
+    """The plans of prompt calls are kept by the numbers, not by what held them."""
+    made = []
+
+    def plan(q, k, v, out_dtype, scale, softcap):
+        cfg = spd.spd_dense_config(4, 2, 64, 1, 0, spd._rule(scale, softcap, None, 4, None))
+        made.append((float(scale), float(softcap)))
+        return rec.torch, cfg, 0, tuple(q.shape), torch.float32, q.shape[0], k.shape[0]
+
+    monkeypatch.setattr(spd, "_prompt_plan", plan)
+    monkeypatch.setattr(spd, "_raw_stream", lambda *a: 0)
+    q, k = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(9, 2, 64, dtype=torch.bfloat16)
+    scale, cap = torch.tensor(0.5), torch.tensor(30.0)
+    seen = []
+    for _ in range(3):
+        spd.prefill_attention(q, k, k, scale=scale, softcap=cap)
+        rule = rec.calls[-1][1][0].rule
+        seen.append((rule.scale, rule.softcap))
+        scale *= 0.5
+        cap += 1
+    assert seen == [(0.5, 30.0), (0.25, 31.0), (0.125, 32.0)]
+    spd.prefill_attention(q, k, k, scale=0.5, softcap=30)  # the first again, by its numbers
+    assert len(made) == 3
