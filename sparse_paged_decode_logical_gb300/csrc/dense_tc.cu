@@ -26,11 +26,12 @@
 // Outputs of 32 bits keep P in kParts 16-bit parts, each the rounding of what the
 // ones before left, a product each: two hold 22 bits of each weight with fp16 and
 // 16 with bf16, which takes a third part (through shared memory: tensor memory is
-// full) where a CTA meets at most kThirdKeys keys (kParts 3).  Over longer stretches
-// the tensor cores' own sums, which round towards 0 at every 16 keys, are off by as
-// much (two parts a relative 2e-6, the sums 2.9e-6 at 1,100 keys), and a third part
+// full): over a shared prefix always, in prompts where a CTA meets at most kThirdKeys
+// keys (kParts 3).  Over longer stretches the tensor cores' own sums, which round
+// towards 0 at every 16 keys, are off by as much where many keys count (two parts a
+// relative 2e-6, the sums 2.9e-6 at 1,100 keys), and in prompts a third part
 // everywhere costs 40% of the time (2,048 biased queries over 16,384 keys 662 and
-// 935 us, 742 as it is).  Outputs of 16 bits round P once, which is an error of the
+// 935 us, 742 as it is; 64 sequences over 32,768 shared keys 86 and 97).  Outputs of 16 bits round P once, which is an error of the
 // same size as the rounding of the output.
 //
 // A matrix leaves out the pairs before and behind its rows' keys.  With `dup` (at
@@ -60,7 +61,7 @@ namespace spd {
 namespace {
 
 constexpr uint32_t kDtWait = 1u << 22;  // bounded mbarrier polls
-constexpr int kThirdKeys = 1024;        // a CTA's keys up to which bf16 weights take three parts
+constexpr int kThirdKeys = 1024;        // a prompt CTA's keys up to which bf16 weights take three parts
 constexpr float kDtRescaleAbove = 8.f;  // log2 growth of a row max that moves it
 
 template <int D, bool kThird>
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(DtSmem<D, false>::kThreads, 1)
     n = max(0, min(last - kb0, per));
   }
   const int pairs = (n + 1) / 2;
-  const bool third = kThird && n * kDenseBlock <= kThirdKeys;
+  const bool third = kThird && (p.paged || n * kDenseBlock <= kThirdKeys);
   // Blocks in ascending order, so that the CTAs that run together read the same
   // K and V at the same time (descending, where each starts at its own newest
   // key, 1,227 us against 1,216 on 2,048 queries over 49,152 keys).  With a

@@ -107,3 +107,34 @@ def test_prompt_rows_that_attend_the_first_keys_beside_rows_that_attend_the_last
     assert bool(((got.double() - ref).abs() <=
                  tolerance(ref, ab, mag, d, max(near, far, 1025), dt, od, 0.0)).all())
     assert bool((got[b >= e] == 0).all())
+
+
+# ---- precision ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n,d", [(2, 128), (9, 128), (20, 128), (20, 64), (70, 128)])
+def test_fp32_outputs_hold_the_weights_over_a_long_prefix(n, d, dtype):
+    """As test_fp32_outputs_hold_the_weights_to_22_bits (which derives the bound), where
+    a CTA meets more keys than in prompts whose bf16 weights take a third part."""
+    dt, lp, hq, hkv = DT[dtype], 60000, 16, 8
+    at = torch.randperm(lp, generator=torch.Generator().manual_seed(3))[:16].cuda()
+    q = torch.zeros(n, hq, d, device="cuda", dtype=dt)
+    q[..., 0], q[..., 1] = normal(1, n, hq).abs().clamp_max(2).to(dt), 1
+    k = torch.zeros(lp, hkv, d, device="cuda", dtype=dt)
+    k[..., 1] = -1000
+    k[at, :, 0], k[at, :, 1] = normal(2, 16, hkv).clamp(-1, 1).to(dt), 0
+    v = torch.zeros(lp, hkv, d, device="cuda", dtype=dt)
+    v[at, :, torch.arange(16, device="cuda")] = 1
+    c = new_cache(hq, hkv, d, dtype, 1024, 16, 59 + n, n + 1, lp)
+    pid, ids = c.seq_create(), [c.seq_create() for _ in range(n)]
+    c.kv_append([pid], k[None], v[None])
+    own = torch.zeros(n, 3, hkv, d, device="cuda", dtype=dt)
+    own[..., 1] = -1000
+    c.kv_append(ids, own, torch.zeros_like(own))
+    got = c.shared_prefix_attention(q, pid, ids, scale=1.0)
+    c.check_status()
+    x = torch.einsum("rhg,thg->rht", q[..., :1].double(),
+                     k[at, :, :1].double().repeat_interleave(hq // hkv, 1))
+    want = torch.softmax(x, -1)
+    assert float(((got[..., :16].double() - want) / want).abs().max()) < 3.2e-6
+    assert bool((got[..., 16:] == 0).all())
