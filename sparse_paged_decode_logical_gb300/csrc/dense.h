@@ -76,7 +76,7 @@ struct DenseTcParams {
   int *err;                // error word, or null: the library's own
   ScoreRule rule;
   int paged;
-  int out_f32;             // type of out
+  int out_f32;             // type of out (paged: of what the splits become)
   int Lq, Lk, Hq, Hkv, G, lhp, HG;  // HP = 2^lhp heads per matrix, HG = G / HP head groups
   int tiles, nsplit;
   int dup;                 // both matrices hold the same 128 rows, each takes every second block

@@ -626,7 +626,7 @@ spd_status spd_shared_prefix_attention(spd_ctx *c, const void *q, int prefix_id,
       t.page_row = p.page_table + (size_t)prefix_id * v.max_pp;
       t.err = v.err;
       t.paged = 1;
-      t.out_f32 = 1;
+      t.out_f32 = p.out_f32;
       t.Lq = n;
       t.Lk = lp;
       t.Hq = p.Hq;
@@ -643,7 +643,10 @@ spd_status spd_shared_prefix_attention(spd_ctx *c, const void *q, int prefix_id,
       t.box_rows = br;
       t.pos0 = 0;
       for (int i = 0; i < n; ++i) t.lens[i] = p.seqs[i].L;
-      e = launch_dense_tc(t, cfg.dtype, d, p.out_f32 != 0, st);
+      // weights that are kept show the cap in their denominator: the precise form, which
+      // is the split one's (64 sequences over 32,768 tokens with a cap 86 -> 113 us)
+      const bool fine = p.out_f32 || (weights_out && p.rule.cap_out > 0.f);
+      e = launch_dense_tc(t, cfg.dtype, d, fine, st);
       ++launches;
     }
     p.follow = z.tc;

@@ -31,8 +31,9 @@
 // towards 0 at every 16 keys, are off by as much where many keys count (two parts a
 // relative 2e-6, the sums 2.9e-6 at 1,100 keys), and in prompts a third part
 // everywhere costs 40% of the time (2,048 biased queries over 16,384 keys 662 and
-// 935 us, 742 as it is; 64 sequences over 32,768 shared keys 86 and 97).  Outputs of 16 bits round P once, which is an error of the
-// same size as the rounding of the output.
+// 935 us, 742 as it is; 64 sequences over 32,768 shared keys 86 and 97).  Outputs of
+// 16 bits round P once, which is an error of the same size as the rounding of the
+// output.
 //
 // A matrix leaves out the pairs before and behind its rows' keys.  With `dup` (at
 // most 128 rows) both matrices hold the same rows, and matrix m takes block m of
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(DtSmem<D, false>::kThreads, 1)
     n = max(0, min(last - kb0, per));
   }
   const int pairs = (n + 1) / 2;
-  const bool third = kThird && (p.paged || n * kDenseBlock <= kThirdKeys);
+  const bool third = kThird && p.out_f32 && (p.paged || n * kDenseBlock <= kThirdKeys);
   // Blocks in ascending order, so that the CTAs that run together read the same
   // K and V at the same time (descending, where each starts at its own newest
   // key, 1,227 us against 1,216 on 2,048 queries over 49,152 keys).  With a

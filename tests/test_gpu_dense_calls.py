@@ -138,3 +138,35 @@ def test_fp32_outputs_hold_the_weights_over_a_long_prefix(n, d, dtype):
     want = torch.softmax(x, -1)
     assert float(((got[..., :16].double() - want) / want).abs().max()) < 3.2e-6
     assert bool((got[..., 16:] == 0).all())
+
+
+@pytest.mark.parametrize("out", ["same", "fp32"])
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("n", [5, 20, 40, 200])
+def test_kept_weights_over_a_capped_prefix_show_no_rough_cap(n, slopes, out):
+    """Every key of the prefix has one score s per query, |s| < 2, an exact product of
+    two numbers, the own tokens' scores are 0, and the cap is 170: a form that is off
+    by 2^-22 of the cap (1.9e-5 here) shows in every own token's weight,
+    1 / (own + Lp e^x).  Allowed, relative: scores 2 x 4 x 2^-24 |s| = 16 x 2^-24, their
+    exponents (|x| < 3 in base 2) 6 x 2^-24, 2^x 2 x 2^-22, sums of a thread's 15 equal
+    weights, of up to 30 blocks and 19 splits 64 x 2^-24, joins, quotient and product
+    8 x 2^-24: 102 x 2^-24 = 6.1e-6."""
+    d, lp, own, cap, dt = 128, 4500, 3, 170.0, torch.bfloat16
+    c = new_cache(1, 1, d, "bf16", 256, 16, 18 + n + 1, n + 1, 4600)
+    k = torch.zeros(lp, 1, d, dtype=dt, device="cuda")
+    k[..., 0] = 1.0
+    v = normal(2, lp, 1, d, dtype=dt)
+    pid, ids = c.seq_create(), [c.seq_create() for _ in range(n)]
+    c.kv_append([pid], k[None], v[None])
+    c.kv_append(ids, torch.zeros(n, own, 1, d, dtype=dt, device="cuda"),
+                normal(3, n, own, 1, d, dtype=dt))
+    q = torch.zeros(n, 1, d, dtype=dt, device="cuda")
+    q[:, 0, 0] = (torch.rand(n, device="cuda", generator=torch.Generator("cuda").manual_seed(4)) * 4 - 2).to(dt)
+    w = torch.zeros(n, 1, own, device="cuda")
+    c.shared_prefix_attention(q, pid, ids, scale=1.0, softcap=cap, weights_out=w,
+                              slopes=torch.zeros(1, device="cuda") if slopes else None,
+                              out_dtype=torch.float32 if out == "fp32" else dt)
+    c.check_status()
+    x = cap * torch.tanh(q[:, 0, 0].double() / cap)
+    want = 1.0 / (own + lp * x.exp())
+    assert float(((w[:, 0].double() - want[:, None]) / want[:, None]).abs().max()) < 102 * 2.0 ** -24
