@@ -582,13 +582,15 @@ __global__ void __launch_bounds__(DtSmem<D, false>::kThreads, 1)
         };
         // a cap alone, 16-bit output, largest scores within the polynomial's range:
         // the cap is monotonic, so the row's max is taken first and the polynomial
-        // goes into the exponent
+        // goes into the exponent (rows that attend nothing have no say in it: what
+        // they become is never read)
         bool quick = false;
         float top = 0.f;
         if constexpr (kRule && !kSplitP) {
           if (p.rule.quick > 0.f && !edge) {
             top = row_max();
-            quick = __all_sync(0xffffffffu, top <= p.rule.quick && top >= p.rule.quick_floor);
+            quick = __all_sync(0xffffffffu, rend == 0 || (top <= p.rule.quick &&
+                                                          top >= p.rule.quick_floor));
           }
         }
         if (kRule && !quick) {
@@ -601,7 +603,7 @@ __global__ void __launch_bounds__(DtSmem<D, false>::kThreads, 1)
               for (int c = 0; c < 64; c += 2)
                 big = fmaxf(fmaxf(big, fabsf(__uint_as_float(s[c]))),
                             fabsf(__uint_as_float(s[c + 1])));
-              if (__all_sync(0xffffffffu, big <= p.rule.small)) {
+              if (__all_sync(0xffffffffu, rend == 0 || big <= p.rule.small)) {
 #pragma unroll
                 for (int c = 0; c < 64; c += 2) {
                   const float2 x = cap_small(

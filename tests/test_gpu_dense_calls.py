@@ -170,3 +170,27 @@ def test_kept_weights_over_a_capped_prefix_show_no_rough_cap(n, slopes, out):
     x = cap * torch.tanh(q[:, 0, 0].double() / cap)
     want = 1.0 / (own + lp * x.exp())
     assert float(((w[:, 0].double() - want[:, None]) / want[:, None]).abs().max()) < 102 * 2.0 ** -24
+
+
+# ---- rows that attend nothing --------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp16", 64)])
+@pytest.mark.parametrize("out", ["same", "fp32"])
+@pytest.mark.parametrize("softcap", [30.0, 300.0])
+@pytest.mark.parametrize("lq,lk,hq,hkv", [(300, 300, 4, 2), (300, 300, 8, 1), (60, 3000, 4, 2)])
+def test_queries_that_attend_nothing_have_no_say(lq, lk, hq, hkv, d, dtype, out, softcap):
+    """Not even in the last bits: padding rows between others hold small numbers, large
+    ones or none at all."""
+    dt = DT[dtype]
+    q, k, v = normal(1, lq, hq, d, dtype=dt, gain=3.0), normal(2, lk, hkv, d, dtype=dt), \
+        normal(3, lk, hkv, d, dtype=dt)
+    pad = torch.arange(lq, device="cuda") % 7 == 2
+    b = torch.zeros(lq, dtype=torch.int32, device="cuda")
+    e = torch.where(pad, 0, lk).int()
+    got = []
+    for what in (1e-3, 300.0, -300.0, math.nan, math.inf):
+        q[pad] = what
+        got.append(spd.prefill_attention(q, k, v, key_begin=b, key_end=e, softcap=softcap, check=True,
+                                         out_dtype=torch.float32 if out == "fp32" else dt))
+    for x in got:
+        assert torch.equal(x, got[0]) and bool((x[pad] == 0).all())
