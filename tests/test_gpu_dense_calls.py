@@ -194,3 +194,38 @@ def test_queries_that_attend_nothing_have_no_say(lq, lk, hq, hkv, d, dtype, out,
                                          out_dtype=torch.float32 if out == "fp32" else dt))
     for x in got:
         assert torch.equal(x, got[0]) and bool((x[pad] == 0).all())
+
+
+# ---- a prompt call between a context's own calls -----------------------------------
+
+@pytest.mark.parametrize("lq,lk", [(6, 6), (6, 30000), (6000, 6000)])
+def test_early_staging_waits_for_a_prompt_call_in_between(lq, lk):
+    """Selection, then a prompt whose output is the decode call's q: streaming heads, which
+    may run without a wait behind their context's own selection, have to wait here."""
+    hq, hkv, d, dt, n = 8, 2, 128, torch.bfloat16, 6
+    c = new_cache(hq, hkv, d, "bf16", 64, 16, 200, n, 2048, streaming=[True, False], sink=16, window=256,
+                  token_budget=256)
+    ids = [c.seq_create() for _ in range(n)]
+    c.kv_append(ids, normal(1, n, 900, hkv, d, dtype=dt), normal(2, n, 900, hkv, d, dtype=dt))
+    q0 = normal(3, n, hq, d, dtype=dt)
+    k, v = normal(4, lk, hkv, d, dtype=dt), normal(5, lk, hkv, d, dtype=dt)
+    qs = [normal(10 + i, lq, hq, d, dtype=dt) for i in range(6)]
+    q = torch.zeros(lq, hq, d, dtype=dt, device="cuda")
+
+    def chain(wait):
+        outs = []
+        for x in qs:
+            c.select_pages(q0, ids, force=True)
+            spd.prefill_attention(x, k, v, out_dtype=dt, out=q)
+            if wait:
+                torch.cuda.synchronize()
+            outs.append(c.sparse_decode_attention(q[-n:], ids))
+        return outs
+
+    want = chain(True)
+    c.set_early_kv_staging(True)
+    for _ in range(5):
+        q.zero_()
+        for a, b in zip(chain(False), want):
+            assert torch.equal(a, b)
+    c.check_status()
