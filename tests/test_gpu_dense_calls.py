@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import sparse_paged_decode_logical_gb300 as spd
-from dense_ref import prompt, tolerance
+from dense_ref import attend, prompt, tolerance
 from test_gpu_dense import DT, check_shared, new_cache, normal
 
 pytestmark = pytest.mark.gpu
@@ -229,3 +229,36 @@ def test_early_staging_waits_for_a_prompt_call_in_between(lq, lk):
         for a, b in zip(chain(False), want):
             assert torch.equal(a, b)
     c.check_status()
+
+
+# ---- distances beyond fp32's integers ---------------------------------------------
+
+@pytest.mark.parametrize("out", ["same", "fp32"])
+@pytest.mark.parametrize("lq", [3, 300])
+def test_distance_bias_of_keys_far_from_the_query(lq, out):
+    """Queries behind 34 million keys (distances of 2^25, where fp32's integers are 4
+    apart), that attend a few of the first ones."""
+    lk, hq, hkv, d, dt = 34_000_003, 4, 1, 64, torch.float16
+    k = torch.zeros(lk, hkv, d, dtype=dt, device="cuda")
+    v = torch.zeros(lk, hkv, d, dtype=dt, device="cuda")
+    q = normal(1, lq, hq, d, dtype=dt)
+    sl = torch.tensor([0.01, 0.3, 1.0, 2.0], device="cuda")
+    od = torch.float32 if out == "fp32" else dt
+    at = torch.arange(lk - lq, lk, device="cuda")
+    for a, n in ((0, 90), (77, 500), (lk - (1 << 25) - 250, 500)):
+        k[a:a + n], v[a:a + n] = normal(2, n, hkv, d, dtype=dt), normal(3, n, hkv, d, dtype=dt)
+        b, e = torch.full((lq,), a, device="cuda"), torch.full((lq,), a + n, device="cuda")
+        e[1::3] -= 7
+        got = spd.prefill_attention(q, k, v, key_begin=b.int(), key_end=e.int(), slopes=sl, out_dtype=od,
+                                    check=True)
+        # the same with the queries right behind their keys: one bias less for a whole row
+        ref = torch.zeros(lq, hq, d, dtype=torch.float64, device="cuda")
+        t = torch.arange(a, a + n, device="cuda")
+        seen = (t >= b[:, None]) & (t < e[:, None])
+        far = (at[:, None] - t).double() - (at - e + 1)[:, None].double()
+        ab, mag = torch.zeros(2, lq, hq, d, dtype=torch.float64, device="cuda"), 0.0
+        for h in range(hq):
+            o, x, _, m = attend(q[:, h], k[a:a + n, 0], v[a:a + n, 0], h, far, seen, d ** -0.5, 0.0, sl)
+            ref[:, h], ab[:, :, h], mag = o, x, max(mag, m)
+        tol = tolerance(ref, ab, mag, d, n, dt, od, 0.0)
+        assert bool(((got.double() - ref).abs() <= tol).all())
