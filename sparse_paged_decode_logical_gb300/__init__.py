@@ -527,7 +527,7 @@ class SparsePagedKVCache:
         if st != SPD_OK:
             _check(st, "spd_shared_prefix_sizes", self.ctx)
         nbytes, raw = ws.value, self._stream(stream)
-        work = _empty(t, nbytes, t.uint8, self.device, stream)
+        work = _empty(t, nbytes, t.uint8, self.device, stream, result=False)
         st = L.spd_shared_prefix_attention(
             self.ctx, qp, prefix_id, ids, n, rule, 0 if out_dtype == t.float32 else 1, op, w_in,
             w_out, stride, work.data_ptr(), nbytes, raw or None)
@@ -605,7 +605,7 @@ def prefill_block_sparse_attention(q, k, v, w_q, w_k, block=64, token_budget=409
     nb = -(-L // block)
     out = _empty(torch, (L, Hq, d), torch.float32, q.device, stream)
     blocks = _empty(torch, (Hkv, nb, kb.value), torch.int32, q.device, stream)
-    work = _empty(torch, ws.value, torch.uint8, q.device, stream)
+    work = _empty(torch, ws.value, torch.uint8, q.device, stream, result=False)
     if stream is None:
         stream = torch.cuda.current_stream(q.device)
     st = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -631,10 +631,10 @@ def _rule(scale, softcap, slopes, num_q_heads, device_index):
     return spd_score_rule(float(scale or 0.0), float(softcap or 0.0), slopes)
 
 
-def _empty(torch, shape, dtype, device, stream):
+def _empty(torch, shape, dtype, device, stream, result=True):
     """A buffer of a call on `stream`, from that stream's pool: the kernels that used
     its memory before are then ahead of the call's, and those that use it next
-    behind.  (None: the current stream.)  What the caller's stream does with it
+    behind.  (None: the current stream.)  What the caller's stream does with a result
     before it is given back is waited for too."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
@@ -642,7 +642,8 @@ def _empty(torch, shape, dtype, device, stream):
         stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=device)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(device))
+    if result:
+        t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
@@ -744,7 +745,7 @@ def prefill_attention(q, k, v, key_begin=None, key_end=None, scale=0.0, softcap=
                                _rule(scale, softcap, slopes, cfg.num_q_heads, dev))
     raw = _raw_stream(torch, dev, stream)
     # (held until the kernels are enqueued: a block given back before could go to another call)
-    work = _empty(torch, nbytes, torch.uint8, q.device, stream) if nbytes else None
+    work = _empty(torch, nbytes, torch.uint8, q.device, stream, result=False) if nbytes else None
     st = lib().spd_prefill_attention(
         cfg, Lq, Lk, q.data_ptr(), _token_stride(q, "q"), k.data_ptr(), _token_stride(k, "k"),
         v.data_ptr(), _token_stride(v, "v"), kb, ke, out.data_ptr(),

@@ -134,8 +134,8 @@ def test_buffers_of_a_call_on_a_stream_come_from_its_pool(rec, monkeypatch, stre
     for name, _, held in rec.calls:
         assert len(held) == (0 if name.endswith("_sizes") else 2), name
         assert all(alive and under == Stream(77) for alive, under in held), name
-    for t in outs:  # the caller reads them on its own stream
-        assert rec.recorded[t.data_ptr()] == {"caller"}
+    # the caller reads the results on its own stream, and nobody but the call a workspace
+    assert rec.recorded == {t.data_ptr(): {"caller"} for t in outs}
 
 
 def test_buffers_of_a_call_without_a_stream(rec, monkeypatch):

@@ -81,6 +81,31 @@ def test_cache_calls_on_a_stream_beside_other_work():
     assert torch.equal(b0, b1) and torch.equal(e0, e1)
 
 
+def test_calls_on_a_stream_inside_a_capture_and_on_the_default_stream():
+    hq, hkv, d, lk = 16, 8, 128, 20000
+    k, v = (normal(i, lk, hkv, d, dtype=torch.bfloat16) for i in (1, 2))
+    q, q2 = normal(3, 40, hq, d, dtype=torch.bfloat16), normal(4, 40, hq, d, dtype=torch.bfloat16)
+    want = [spd.prefill_attention(x, k, v, check=True) for x in (q, q2)]
+    torch.cuda.synchronize()
+    got = spd.prefill_attention(q, k, v, stream=0)  # the legacy default stream
+    torch.cuda.synchronize()
+    assert torch.equal(got, want[0])
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g):
+        here = torch.cuda.current_stream()
+        s.wait_stream(here)
+        a = spd.prefill_attention(q, k, v, stream=s)
+        b = spd.prefill_attention(q2, k, v)  # beside it: neither has the other's workspace
+        c = spd.prefill_attention(q2, k, v, stream=s)
+        here.wait_stream(s)
+    for _ in range(3):
+        for x in (a, b, c):
+            x.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1]) and torch.equal(c, want[1])
+
+
 # ---- key intervals of one tile's rows far apart ------------------------------------
 
 @pytest.mark.parametrize("near,far", [(64, 40), (700, 1500), (1, 1), (5000, 9000)])
