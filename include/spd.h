@@ -32,10 +32,13 @@
  *     order on one stream.  A context is not thread-safe.
  *   - Argument errors are detected on the host before anything is enqueued
  *     and leave the context unchanged.
- *   - Kernels are launched with programmatic dependent launch: each waits
- *     for the preceding kernel on the stream before touching global memory
- *     and only then lets the next kernel start (see
- *     spd_set_early_kv_staging for the one exception).
+ *   - Kernels are launched with programmatic dependent launch: the first
+ *     kernel of a call waits for the preceding kernel on the stream before
+ *     touching global memory and only then lets the next kernel start (see
+ *     spd_set_early_kv_staging for the one exception), and so does the last
+ *     one, which is done only when the others are.  In between, kernels of
+ *     one call that write to different places may run at the same time
+ *     (spd_shared_prefix_attention: the prefix's and the own tokens').
  */
 #ifndef SPD_H
 #define SPD_H
@@ -348,8 +351,11 @@ const char *spd_status_string(spd_status s);
  * Turn it on only if (a) nothing but this library's calls on this context
  * writes its KV-cache buffers, and (b) other code's kernels on the stream do
  * not release their dependents (programmatic dependent launch) before they
- * have waited for their own predecessor.  All of this library's kernels
- * meet (b).  SPD_ERR_INVALID_ARG for a NULL context.
+ * have waited for their own predecessor.  All of this library's calls meet
+ * (b): where two kernels of one run at the same time, the call's last one
+ * waits for both before it releases anything.  A prompt call (which has no
+ * context) between two calls of this context counts as other code.
+ * SPD_ERR_INVALID_ARG for a NULL context.
  */
 spd_status spd_set_early_kv_staging(spd_ctx *ctx, int enable);
 
@@ -436,10 +442,12 @@ typedef struct {
   const float *slopes; /* device [num_q_heads], 4-byte aligned, or NULL */
 } spd_score_rule;
 
-/* Type of the output: fp32 (softmax weights enter the products with v with 22 to
- * 24 bits, 16 in prompts of bf16 where a query attends more than about 1,000 keys;
- * there the tensor cores' fp32 sums are off by as much), or the type of the inputs
- * (weights rounded to it once, the fp32 sums rounded to it at the end). */
+/* Type of the output: fp32 (softmax weights enter the products with v with 22 bits
+ * (fp16) or 24 (bf16), but 16 in prompts of bf16 where the queries of one tile (up to
+ * 256 rows of tokens and heads that share K and V) attend a stretch of more than about
+ * 1,000 keys; the tensor cores' fp32 sums over so many keys are off by as much), or
+ * the type of the inputs (weights rounded to it once, or kept longer with few rows;
+ * the fp32 sums rounded to it at the end). */
 typedef enum { SPD_OUT_F32 = 0, SPD_OUT_DTYPE = 1 } spd_out;
 
 typedef struct {
@@ -504,7 +512,9 @@ spd_status spd_document_key_ranges(const int *offsets, const int *prefix, int n_
  * every token of both (no page selection; step counters and selections stay as
  * they are).  The prefix is a sequence of the context like any other, filled
  * once by spd_kv_append; each listed sequence holds only its own tokens.  The
- * prefix's keys and values are read once for the batch.
+ * prefix's keys and values are read once per 256 query rows of a kv head (sequences
+ * x Hq / Hkv; per 16 rows where rows / 16 x tokens is at most 4,000, or with up to 32
+ * rows of head_dim 64), at most 256 sequences at a time.
  *   out[i][h] = sum_t softmax_t(s) v_t over the prefix's Lp tokens (positions
  *               0 .. Lp - 1) and the sequence's own L_i (Lp .. Lp + L_i - 1);
  *               the query stands at the newest, Lp + L_i - 1

@@ -6,8 +6,8 @@
 namespace spd {
 
 // tanh(z) = z T(z^2).  T as polynomials fitted for least relative error:
-// |z| <= 0.6, 5 terms (7e-8; 3 x 2^-24 with fp32 arithmetic), and |z| <= 1, 7
-// terms (5e-8; 3 x 2^-24).  Beyond 1, 1 - 2 / (1 + e^2z) has no cancellation
+// |z| <= 0.6, 5 terms (9.1e-8; 4.3 x 2^-24 with fp32 arithmetic), and |z| <= 1, 7
+// terms (6.9e-8; 4.3 x 2^-24).  Beyond 1, 1 - 2 / (1 + e^2z) has no cancellation
 // left (2 / (1 + e^2) = 0.24).
 __device__ __forceinline__ float2 f2_dup(float x) { return make_float2(x, x); }
 
@@ -22,8 +22,8 @@ __device__ __forceinline__ float2 cap_small(const ScoreRule &r, float2 s) {
 
 // The same for any score, by 2^x and a reciprocal: off by about 2^-22 of the cap
 // near 0, which 16-bit weights (2^-9 and 2^-12 of each) do not show.
-// cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)).  (8,192 capped tokens: 770
-// us with this alone, 625 with cap_quick where it holds.)
+// cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)).  (8,192 capped tokens with a
+// prefix of 30%: 804 us with this alone, 614 with cap_quick where it holds.)
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -37,7 +37,7 @@ __device__ __forceinline__ float2 cap_16bit(const ScoreRule &r, float2 s) {
 }
 
 // cap tanh(s / cap) + add in base-2 units by a polynomial of five terms in s^2 that
-// is 5e-7 of the score off for |s / cap| <= 0.75, for the scores of a row whose
+// is 6.1e-7 of the score off for |s / cap| <= 0.75, for the scores of a row whose
 // largest lies in [-0.25, 0.75] cap, cap >= 30.  What lies below -0.75 cap has a
 // weight under e^(-0.39 cap) of the largest; there the polynomial stays monotonic
 // and on the lower side (8e-4 of the score at -cap, then falling away to 0 weight),

@@ -30,8 +30,8 @@
 // keys (kParts 3).  Over longer stretches the tensor cores' own sums, which round
 // towards 0 at every 16 keys, are off by as much where many keys count (two parts a
 // relative 2e-6, the sums 2.9e-6 at 1,100 keys), and in prompts a third part
-// everywhere costs 40% of the time (2,048 biased queries over 16,384 keys 662 and
-// 935 us, 742 as it is; 64 sequences over 32,768 shared keys 86 and 97).  Outputs of
+// everywhere costs 40% of the time (2,048 biased queries over 16,384 keys 650 and
+// 929 us, 759 as it is; 64 sequences over 32,768 shared keys 86 and 97).  Outputs of
 // 16 bits round P once, which is an error of the same size as the rounding of the
 // output.
 //
