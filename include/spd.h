@@ -353,8 +353,8 @@ const char *spd_status_string(spd_status s);
  * not release their dependents (programmatic dependent launch) before they
  * have waited for their own predecessor.  All of this library's calls meet
  * (b): where two kernels of one run at the same time, the call's last one
- * waits for both before it releases anything.  A prompt call (which has no
- * context) between two calls of this context counts as other code.
+ * waits for both before it releases anything.  Behind a prompt call (which has
+ * no context) that follows this context's own kernel, nothing starts early.
  * SPD_ERR_INVALID_ARG for a NULL context.
  */
 spd_status spd_set_early_kv_staging(spd_ctx *ctx, int enable);

@@ -467,7 +467,7 @@ spd_status spd_prefill_attention(const spd_dense_config *cfg, int q_len, int kv_
   p.dup = z.dup;
   p.pos0 = kv_len - q_len;
   cudaStream_t st = (cudaStream_t)stream;
-  note_foreign_launch(st);
+  note_prompt_launch(st);
   if (launch_dense_tc(p, cfg->dtype, d, p.out_f32 != 0, st) != cudaSuccess) return SPD_ERR_CUDA;
   if (z.partial && launch_dense_prompt_combine(p, cfg->dtype, d, out, st) != cudaSuccess)
     return SPD_ERR_CUDA;
@@ -496,7 +496,7 @@ spd_status spd_document_key_ranges(const int *offsets, const int *prefix, int n_
   DeviceGuard guard;
   const spd_status s = guard.bind(device);
   if (s != SPD_OK) return s;
-  note_foreign_launch((cudaStream_t)stream);
+  note_prompt_launch((cudaStream_t)stream);
   return launch_document_ranges(offsets, prefix, n_docs, n_tokens, key_begin, key_end,
                                 (cudaStream_t)stream) == cudaSuccess
              ? SPD_OK

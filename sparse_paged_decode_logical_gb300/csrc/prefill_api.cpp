@@ -169,7 +169,7 @@ spd_status enqueue(const spd_prefill_config *cfg, int seq_len, const PrefillLayo
       (!encode_map(&p.tm_q, q, cfg, p.Hq, seq_len) || !encode_map(&p.tm_k, k, cfg, p.Hkv, seq_len) ||
        !encode_map(&p.tm_v, v, cfg, p.Hkv, seq_len)))
     return SPD_ERR_CUDA;
-  spd::note_foreign_launch(st);
+  spd::note_prompt_launch(st);
   return spd::launch_prefill(p, cfg->dtype, cfg->head_dim, st) == cudaSuccess ? SPD_OK
                                                                               : SPD_ERR_CUDA;
 }

@@ -237,9 +237,9 @@ spd_status fill_pages(spd_ctx *c, const int *ids, const int *tokens, int n, cuda
 void set_filled(spd_ctx *c, const int *ids, const int *tokens, int n);
 // The context enqueued n kernels on the stream.
 void note_launches(spd_ctx *c, cudaStream_t st, int n);
-// A call without a context enqueued kernels on the stream: what a context's last
-// kernel there allows to start early no longer holds.
-void note_foreign_launch(cudaStream_t st);
+// A prompt call, which has no context, enqueues kernels on the stream: the kernel
+// behind them waits, whatever the context's own last one there would have allowed.
+void note_prompt_launch(cudaStream_t st);
 
 // Launchers.  dtype: 0 fp16, 1 bf16.  Return cudaGetLastError() and add the
 // number of kernels enqueued to *launches.

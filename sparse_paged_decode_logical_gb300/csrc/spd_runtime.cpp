@@ -206,8 +206,8 @@ namespace {
 // it reads: a kernel of another context (or other code) writes nothing of
 // this cache; this context's selection kernel writes only the selection, and
 // its page-table flush only the page table, neither of which a streaming
-// head reads.  (ctx null: a prompt call, which has no context.  Its kernels let the
-// next one start before their outputs, which may be its q, are there.)
+// head reads.  A prompt call, which has no context, takes that allowance back: its
+// kernels let the next one start before their outputs, which may be its q, are there.
 enum LaunchKind { kKindOther = 0, kKindSelect = 1, kKindPageTable = 2 };
 struct LastLaunch {
   const spd_ctx *ctx;
@@ -928,7 +928,11 @@ void note_launches(spd_ctx *c, cudaStream_t st, int n) {
   note_launcher(c, st);
 }
 
-void note_foreign_launch(cudaStream_t st) { note_launcher(nullptr, st); }
+void note_prompt_launch(cudaStream_t st) {
+  std::lock_guard<std::mutex> lock(g_last_mu);
+  const auto it = g_last_launcher.find(st);
+  if (it != g_last_launcher.end()) it->second.kind = kKindOther;
+}
 
 }  // namespace spd
 
