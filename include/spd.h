@@ -101,6 +101,19 @@ typedef struct {
   int kv_fp8;
   const float *k_scale;
   const float *v_scale;
+  /* Storage in 8 or 4 bits whose scales follow the data.  kv_quant = 8 or 4:
+   * a group of channels of a token -- of each kv head's key row and value row,
+   * all of them (8) or runs of 32 (4) -- is held as value = lo + step * code:
+   * lo the group's lowest value, step the least number of `dtype` with
+   * (2^kv_quant - 1) step >= highest - lowest, code = (x - lo) / step rounded
+   * to nearest, 0 .. 2^kv_quant - 1.  A group that holds a value that is not
+   * finite, or whose span exceeds fp32, reads back as NaN throughout.  q, k and
+   * v of the calls stay `dtype`.  Such a context has no page metadata: it is
+   * written by spd_kv_append and spd_kv_append_rotary, read by spd_kv_read and
+   * spd_quant_decode_attention, and takes part in neither page selection nor
+   * the calls of the 16-bit cache (SPD_ERR_INVALID_ARG).  No streaming heads,
+   * no kv_fp8.  0 (a zero-initialised config): 16-bit or fp8 storage. */
+  int kv_quant;
 } spd_config;
 
 /*
@@ -123,6 +136,10 @@ typedef struct {
  *   selection      int32 [max_seqs][Hd][KS]  kept logical pages, ascending.
  *   scratch        split partials, tickets, page scores and the device error
  *                   word; contents need no initialisation.
+ * With kv_quant, k_pool holds keys and values, [num_physical_pages][Hkv][P / 16]
+ * tiles of 16 tokens of 32 (d + 4) bytes (kv_quant 8) or 20 d (4), in an order
+ * of the library's own (spd_kv_read gives rows), and v_pool, meta and selection
+ * are not used.
  * Every buffer must be 256-byte aligned.  Sizes of 0 mean "not used".
  */
 typedef struct {
@@ -566,6 +583,113 @@ spd_status spd_shared_prefix_attention(spd_ctx *ctx, const void *q, int prefix_i
 spd_status spd_kv_evict(spd_ctx *ctx, const int *src_ids, const int *dst_ids, int n_seqs, int keep,
                         int recent, const float *weights, long long weights_stride, int *kept,
                         float *kept_weights, spd_stream stream);
+
+/* ---- rotary positions ------------------------------------------------------ */
+/*
+ * The pair i of channels, (x, y), of a token becomes
+ *   (x cos a - y sin a, x sin a + y cos a),  a = position[axis(i)] * frequency(i)
+ * for 0 <= i < rotary_dim / 2; channels from rotary_dim on stay.  Text has one
+ * axis; images and video give time, height and width axes of their own.
+ */
+typedef struct {
+  int head_dim;     /* d in {64, 128}                                         */
+  int rotary_dim;   /* a multiple of 16, at most head_dim                     */
+  int axes;         /* 1..4                                                   */
+  int sections[4];  /* pairs of each axis, >= 0, rotary_dim / 2 in all        */
+  int axes_in_turn; /* 0: sections lie one behind the other; 1: the axes take
+                       pairs in turn (0, 1, 2, 0, 1, 2, ...) while they have any */
+  int neighbours;   /* 0: pair i is channels i and i + rotary_dim / 2;
+                       1: channels 2i and 2i + 1                              */
+  double base;      /* frequency(i) = base^(-2i / rotary_dim), base >= 1      */
+  const double *inv_freq; /* host [rotary_dim / 2], 0 <= x <= 1000: used instead
+                             of base; or NULL                                  */
+} spd_rotary_rule;
+
+/* A rule worked out, once per model: `turns` are frequencies in turns, in units
+ * of 2^-64 (so that position * turns is the angle's fraction of a turn, exactly,
+ * however far the position).  Filled by spd_rotary_make. */
+typedef struct {
+  int head_dim, rotary_dim, axes, neighbours;
+  unsigned char axis[64];
+  unsigned long long turns[64];
+} spd_rotary_table;
+
+/* Host only.  SPD_ERR_INVALID_ARG on a bad rule. */
+spd_status spd_rotary_make(const spd_rotary_rule *rule, spd_rotary_table *out);
+
+/*
+ * Rotates q and k of n_tokens tokens.
+ *   dtype      of q and k
+ *   positions  device int32 [axes][n_tokens], any value
+ *   q, q_out   device [n_tokens][q_heads][d], rows q_stride / q_out_stride elements
+ *              apart (strides multiples of 8, at least a row; 16-byte aligned)
+ *   k, k_out   device [n_tokens][kv_heads][d] likewise; both NULL: q alone
+ *              (kv_heads is then ignored)
+ *   inverse    1: by -a (back; also the gradient of the rotation)
+ * An output may be its input (same pointer and stride), and overlap nothing else.
+ * Computed in fp32, rounded to dtype once.  All pointers are of one device; the
+ * call runs on it whichever is current.  SPD_ERR_INVALID_ARG on bad arguments,
+ * SPD_ERR_CAPACITY beyond 2^28 tokens (nothing enqueued).
+ */
+spd_status spd_rotary(const spd_rotary_table *table, spd_dtype dtype, int n_tokens,
+                      const int *positions, const void *q, long long q_stride, int q_heads,
+                      const void *k, long long k_stride, int kv_heads, void *q_out,
+                      long long q_out_stride, void *k_out, long long k_out_stride, int inverse,
+                      spd_stream stream);
+
+/* ---- a cache in 8 or 4 bits ------------------------------------------------- */
+/*
+ * spd_kv_append of a context with kv_quant whose keys are rotated on the way,
+ * and the queries of the same tokens with them.  Same results as spd_rotary
+ * followed by spd_kv_append.
+ *   positions  device int32 [axes][n_seqs][n_tokens], or NULL: a token's place in
+ *              its sequence, on every axis
+ *   q          device [n_seqs * n_tokens][Hq][d], k, v [n_seqs * n_tokens][Hkv][d]:
+ *              rows at strides as in spd_rotary (a fused projection's rows)
+ *   q_out      device [n_seqs * n_tokens][Hq][d], contiguous; may be q where
+ *              q_stride = Hq d
+ */
+spd_status spd_kv_append_rotary(spd_ctx *ctx, const spd_rotary_table *table, const int *seq_ids,
+                                int n_seqs, int n_tokens, const int *positions, const void *q,
+                                long long q_stride, const void *k, long long k_stride,
+                                const void *v, long long v_stride, void *q_out,
+                                spd_stream stream);
+
+/*
+ * Reads n_tokens tokens of each listed sequence back as the values that they
+ * stand for, from position `begin` on, or, begin < 0, from -begin tokens before
+ * each sequence's end (so that -1 is the newest).  Contexts with kv_quant.
+ *   k, v  device [n_seqs][n_tokens][Hkv][d] of dtype, 16-byte aligned
+ * Values are rounded to dtype once (those of finite groups to a finite number).
+ * SPD_ERR_CAPACITY (nothing enqueued) where a
+ * sequence does not hold all of them.
+ */
+spd_status spd_kv_read(spd_ctx *ctx, const int *seq_ids, int n_seqs, int begin, int n_tokens,
+                       void *k, void *v, spd_stream stream);
+
+/*
+ * Takes a sequence of a context with kv_quant back to its first n_tokens tokens
+ * (a draft that was rejected); pages behind them return to the pool.  Host only.
+ * SPD_ERR_CAPACITY beyond its length.
+ */
+spd_status spd_seq_truncate(spd_ctx *ctx, int seq_id, int n_tokens);
+
+/*
+ * Attention of one token of each listed sequence over its cache in 8 or 4 bits.
+ *   out[i][h] = sum_t softmax_t(s) v_t over the sequence's newest min(window, L)
+ *               tokens (window 0: all L); the query stands at the newest, L - 1
+ *   q    device [n_seqs][Hq][d];  out device [n_seqs][Hq][d], fp32 or dtype
+ *   rule NULL: plain
+ * Softmax weights enter the products with 22 bits (11 where out is bf16) and the
+ * codes exactly; sums are fp32.  Keys or values outside the window never reach
+ * the output, finite or not.
+ * Like every call on a context, calls are issued in order on one stream (partial
+ * sums and tickets lie in the context's scratch).  SPD_ERR_STATE for a sequence
+ * without tokens.  Device checks are reported by spd_check_status.
+ */
+spd_status spd_quant_decode_attention(spd_ctx *ctx, const void *q, const int *seq_ids, int n_seqs,
+                                      int window, const spd_score_rule *rule, spd_out out_type,
+                                      void *out, spd_stream stream);
 
 #ifdef __cplusplus
 }

@@ -14,7 +14,8 @@ import ctypes
 import os
 
 __all__ = ["SpdError", "SparsePagedKVCache", "lib", "LIB_PATH", "make_config",
-           "prefill_block_sparse_attention", "prefill_attention", "document_key_ranges"]
+           "prefill_block_sparse_attention", "prefill_attention", "document_key_ranges",
+           "Rotary", "rotary"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libspd.so")
 
@@ -49,7 +50,20 @@ class spd_config(ctypes.Structure):
                 ("token_budget", ctypes.c_int), ("reuse_interval", ctypes.c_int),
                 ("free_list_seed", ctypes.c_ulonglong), ("kv_fp8", ctypes.c_int),
                 ("k_scale", ctypes.POINTER(ctypes.c_float)),
-                ("v_scale", ctypes.POINTER(ctypes.c_float))]
+                ("v_scale", ctypes.POINTER(ctypes.c_float)), ("kv_quant", ctypes.c_int)]
+
+
+class spd_rotary_rule(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int), ("rotary_dim", ctypes.c_int), ("axes", ctypes.c_int),
+                ("sections", ctypes.c_int * 4), ("axes_in_turn", ctypes.c_int),
+                ("neighbours", ctypes.c_int), ("base", ctypes.c_double),
+                ("inv_freq", ctypes.POINTER(ctypes.c_double))]
+
+
+class spd_rotary_table(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int), ("rotary_dim", ctypes.c_int), ("axes", ctypes.c_int),
+                ("neighbours", ctypes.c_int), ("axis", ctypes.c_ubyte * 64),
+                ("turns", ctypes.c_ulonglong * 64)]
 
 
 class spd_prefill_config(ctypes.Structure):
@@ -128,6 +142,14 @@ def lib():
         "spd_shared_prefix_attention": [vp, vp, i, ip, i, ctypes.POINTER(spd_score_rule), i, vp,
                                         vp, vp, i64, vp, ctypes.c_size_t, vp],
         "spd_kv_evict": [vp, ip, ip, i, i, i, vp, i64, vp, vp, vp],
+        "spd_rotary_make": [ctypes.POINTER(spd_rotary_rule), ctypes.POINTER(spd_rotary_table)],
+        "spd_rotary": [ctypes.POINTER(spd_rotary_table), i, i, vp, vp, i64, i, vp, i64, i, vp, i64,
+                       vp, i64, i, vp],
+        "spd_kv_append_rotary": [vp, ctypes.POINTER(spd_rotary_table), ip, i, i, vp, vp, i64, vp,
+                                 i64, vp, i64, vp, vp],
+        "spd_kv_read": [vp, ip, i, i, i, vp, vp, vp],
+        "spd_seq_truncate": [vp, i, i],
+        "spd_quant_decode_attention": [vp, vp, ip, i, i, ctypes.POINTER(spd_score_rule), i, vp, vp],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -149,10 +171,11 @@ def make_config(num_q_heads, num_kv_heads, head_dim, dtype, logical_page,
                 physical_page, num_physical_pages, max_seqs, max_context,
                 streaming=None, sink=0, window=0, token_budget=0,
                 reuse_interval=4, free_list_seed=0, kv_fp8=False, k_scale=None,
-                v_scale=None):
+                v_scale=None, kv_quant=0):
     """Build an ``spd_config`` (the streaming mask and scale arrays are kept
     alive on it).  kv_fp8: store K/V as fp8 E4M3 codes of value / scale, with
-    per-kv-head k_scale / v_scale (default 1)."""
+    per-kv-head k_scale / v_scale (default 1).  kv_quant: store K/V in 8 or 4
+    bits with scales that follow the data."""
     c = spd_config()
     c.num_q_heads, c.num_kv_heads, c.head_dim = num_q_heads, num_kv_heads, head_dim
     c.dtype = DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
@@ -165,6 +188,7 @@ def make_config(num_q_heads, num_kv_heads, head_dim, dtype, logical_page,
     c.sink, c.window, c.token_budget = sink, window, token_budget
     c.reuse_interval, c.free_list_seed = reuse_interval, free_list_seed
     c.kv_fp8 = 1 if kv_fp8 else 0
+    c.kv_quant = int(kv_quant)
     for name, vals in (("k_scale", k_scale), ("v_scale", v_scale)):
         if vals is not None:
             arr = (ctypes.c_float * num_kv_heads)(*[float(x) for x in vals])
@@ -242,6 +266,11 @@ def spd_free_pages(ctx):
     n = ctypes.c_int()
     _check(lib().spd_free_pages(ctx, ctypes.byref(n)), "spd_free_pages", ctx)
     return n.value
+
+
+def spd_seq_truncate(ctx, seq_id, n_tokens):
+    n_tokens = min(max(int(n_tokens), -1), _MAX_TOKENS + 1)  # (refused below, and never wrapped)
+    _check(lib().spd_seq_truncate(ctx, int(seq_id), n_tokens), "spd_seq_truncate", ctx)
 
 
 def spd_kv_append(ctx, seq_ids, n_tokens, k_ptr, v_ptr, stream=0):
@@ -563,6 +592,110 @@ class SparsePagedKVCache:
                self.ctx)
         return kept, kw
 
+    # -- a cache in 8 or 4 bits (kv_quant) --
+
+    def seq_truncate(self, seq_id, n_tokens):
+        """Back to the sequence's first n_tokens tokens (kv_quant)."""
+        spd_seq_truncate(self.ctx, seq_id, n_tokens)
+
+    def kv_append_rotary(self, seq_ids, table, q, k, v, positions=None, out=None, stream=None):
+        """Append k, v [n][tokens][Hkv][d], the keys rotated on the way, and rotate
+        q [n][tokens][Hq][d] of the same tokens: returns the rotated q (`out`: a
+        contiguous tensor for it, or q itself).  Rows may be strided, as in a fused
+        projection's output.  positions int32 [axes][n][tokens] ([n][tokens] with
+        one axis); None: a token's place in its sequence.  `stream` as in
+        :func:`prefill_attention`."""
+        t = self.torch
+        ids, n = self._id_array(seq_ids)
+        if k.dim() != 4:
+            raise ValueError("k must be [n][tokens][Hkv][d]")
+        tokens = k.shape[1]
+        qs, ks, vs = (self._rows(x, (n, tokens, h, self.d), name)
+                      for x, h, name in ((q, self.Hq, "q"), (k, self.Hkv, "k"), (v, self.Hkv, "v")))
+        pos = None
+        if positions is not None:
+            shape = (table.axes, n, tokens)
+            if positions.shape != shape and not (table.axes == 1 and positions.shape == shape[1:]):
+                raise ValueError("positions must be int32 %s" % (shape,))
+            pos = self._ptr(positions, positions.shape, t.int32)
+        if out is None:
+            out = _empty(t, (n, tokens, self.Hq, self.d), self.dtype, self.device, stream)
+        op = self._ptr(out, (n, tokens, self.Hq, self.d), self.dtype)
+        st = lib().spd_kv_append_rotary(self.ctx, table.table, ids, n, tokens, pos, q.data_ptr(), qs,
+                                        k.data_ptr(), ks, v.data_ptr(), vs, op,
+                                        self._stream(stream) or None)
+        if st != SPD_OK:
+            _check(st, "spd_kv_append_rotary", self.ctx)
+        return out
+
+    def _rows(self, x, shape, name):
+        """Elements between the tokens of [n][tokens][heads][d]."""
+        if x.shape != shape or x.dtype != self.dtype or x.get_device() != self._dev_index:
+            raise ValueError("%s: expected a %s tensor %s on %s, got %s %s on %s"
+                             % (name, self.dtype, shape, self.device, x.dtype, tuple(x.shape), x.device))
+        n, tokens, heads, d = shape
+        s = x.stride()
+        if s[3] != 1 or (heads > 1 and s[2] != d):
+            raise ValueError("%s: the heads of a token must be contiguous" % name)
+        stride = s[1] if tokens > 1 else s[0] if n > 1 else heads * d
+        if n > 1 and tokens > 1 and s[0] != tokens * stride:
+            raise ValueError("%s: all tokens must lie at one stride" % name)
+        return stride
+
+    def kv_read(self, seq_ids, begin=0, n_tokens=None, stream=None):
+        """Tokens of a cache with kv_quant as the values that they stand for: (k, v)
+        [n][n_tokens][Hkv][d] of the cache's type, from position `begin` on, or, below
+        0, from -begin tokens before each sequence's end.  n_tokens None: all that
+        the shortest sequence holds from there.  `stream` as in
+        :func:`prefill_attention`."""
+        t = self.torch
+        ids, n = self._id_array(seq_ids)
+        begin = int(begin)
+        if n_tokens is None:
+            if not n:
+                raise ValueError("no sequences")
+            n_tokens = -begin if begin < 0 else min(self.seq_info(s)["length"] for s in seq_ids) - begin
+        n_tokens = int(n_tokens)
+        if n_tokens < 1 or n_tokens > _MAX_TOKENS or abs(begin) > _MAX_TOKENS:
+            raise SpdError(4, "spd_kv_read", "begin and n_tokens must lie within the sequences")
+        shape = (n, n_tokens, self.Hkv, self.d)
+        longest = max((self.seq_info(s)["length"] for s in seq_ids), default=0)
+        if n_tokens > longest:  # (refused before a buffer is made)
+            raise SpdError(4, "spd_kv_read", "a sequence does not hold all of these tokens")
+        k, v = (_empty(t, shape, self.dtype, self.device, stream) for _ in range(2))
+        st = lib().spd_kv_read(self.ctx, ids, n, begin, n_tokens, k.data_ptr(), v.data_ptr(),
+                               self._stream(stream) or None)
+        if st != SPD_OK:
+            _check(st, "spd_kv_read", self.ctx)
+        return k, v
+
+    def quant_decode_attention(self, q, seq_ids, window=0, scale=0.0, softcap=0.0, slopes=None,
+                               out_dtype=None, out=None, stream=None):
+        """Attention of one token of each sequence over its cache in 8 or 4 bits
+        (kv_quant): the newest `window` tokens, or all (0).  Returns out [n][Hq][d],
+        fp32 or (out_dtype) the cache's type; scale, softcap and slopes as in
+        :func:`prefill_attention`, and `stream`."""
+        t = self.torch
+        ids, n = self._id_array(seq_ids)
+        qp = self._ptr(q, (n, self.Hq, self.d), self.dtype)
+        if out_dtype is None:
+            out_dtype = t.float32 if out is None else out.dtype
+        if out_dtype not in (t.float32, self.dtype):
+            raise ValueError("out_dtype must be torch.float32 or %s" % self.dtype)
+        window = int(window)
+        if window < 0:
+            raise ValueError("window must be >= 0")
+        if out is None:
+            out = _empty(t, (n, self.Hq, self.d), out_dtype, self.device, stream)
+        op = self._ptr(out, (n, self.Hq, self.d), out_dtype)
+        rule = _rule(scale, softcap, slopes, self.Hq, self._dev_index)
+        st = lib().spd_quant_decode_attention(self.ctx, qp, ids, n, min(window, _MAX_TOKENS), rule,
+                                              0 if out_dtype == t.float32 else 1, op,
+                                              self._stream(stream) or None)
+        if st != SPD_OK:
+            _check(st, "spd_quant_decode_attention", self.ctx)
+        return out
+
     def selection(self, seq_id, kv_head, stream=None):
         return spd_get_selection(self.ctx, seq_id, kv_head, self._stream(stream))
 
@@ -780,3 +913,81 @@ def document_key_ranges(offsets, n_tokens, prefix=None, stream=None):
         offsets.data_ptr(), prefix.data_ptr() if prefix is not None else None, n, n_tokens,
         kb.data_ptr(), ke.data_ptr(), raw or None), "spd_document_key_ranges")
     return kb, ke
+
+
+# ---- rotary positions --------------------------------------------------------------
+
+class Rotary:
+    """A rotary rule worked out, once per model (spd_rotary_make): pair i of a
+    token's channels turns by position[axis(i)] * base^(-2i / rotary_dim), or
+    inv_freq[i].
+
+    rotary_dim (default head_dim) channels turn, the others stay.  sections: how
+    many pairs each axis has (default: one axis has all); axes_in_turn: the axes
+    take pairs in turn instead of one section behind the other.  neighbours: pair i
+    is channels 2i and 2i + 1 instead of i and i + rotary_dim / 2."""
+
+    def __init__(self, head_dim, rotary_dim=None, sections=None, axes_in_turn=False,
+                 neighbours=False, base=10000.0, inv_freq=None):
+        rotary_dim = head_dim if rotary_dim is None else int(rotary_dim)
+        sections = [rotary_dim // 2] if sections is None else [int(s) for s in sections]
+        if not 1 <= len(sections) <= 4:
+            raise ValueError("1 to 4 axes")
+        freq = None
+        if inv_freq is not None:
+            if len(inv_freq) != rotary_dim // 2:
+                raise ValueError("inv_freq must have rotary_dim / 2 entries")
+            freq = (ctypes.c_double * max(len(inv_freq), 1))(*[float(f) for f in inv_freq])
+        rule = spd_rotary_rule(int(head_dim), rotary_dim, len(sections),
+                               (ctypes.c_int * 4)(*sections), 1 if axes_in_turn else 0,
+                               1 if neighbours else 0, float(base),
+                               ctypes.cast(freq, ctypes.POINTER(ctypes.c_double)) if freq else None)
+        self.table = spd_rotary_table()
+        _check(lib().spd_rotary_make(ctypes.byref(rule), ctypes.byref(self.table)),
+               "spd_rotary_make")
+        self.head_dim, self.rotary_dim, self.axes = int(head_dim), rotary_dim, len(sections)
+
+
+def rotary(table, positions, q, k=None, inverse=False, out=None, stream=None):
+    """Rotate q [n][Hq][d] and k [n][Hk][d] (or q alone) by the :class:`Rotary`
+    rule `table` (spd_rotary).  positions int32 [axes][n] ([n] with one axis).
+    q and k are fp16 or bf16 on one CUDA device; rows may be strided, as in a fused
+    projection's output.  inverse: back, which is also the rotation's gradient.
+    out: a tensor for the rotated q, or a pair of them; they may be q and k
+    themselves.  Returns (q, k) rotated, or q.  `stream` as in
+    :func:`prefill_attention`."""
+    import torch
+    dev = q.get_device()
+    if q.dim() != 3 or q.shape[2] != table.head_dim or q.shape[0] < 1:
+        raise ValueError("q must be [n][heads][%d]" % table.head_dim)
+    dt = q.dtype
+    if dt not in (torch.float16, torch.bfloat16) or dev < 0:
+        raise ValueError("q and k must be fp16 or bf16, on one CUDA device")
+    n = q.shape[0]
+    if k is not None and (k.dim() != 3 or k.shape[0] != n or k.shape[2] != table.head_dim
+                          or k.dtype != dt or k.get_device() != dev):
+        raise ValueError("k must be [n][heads][%d] of q's type, on its device" % table.head_dim)
+    if positions.dtype != torch.int32 or not positions.is_contiguous() \
+            or positions.get_device() != dev or not (
+                positions.shape == (table.axes, n) or (table.axes == 1 and positions.shape == (n,))):
+        raise ValueError("positions must be contiguous int32 [%d][%d] on cuda:%d"
+                         % (table.axes, n, dev))
+    xs = (q,) if k is None else (q, k)
+    if out is None:
+        ys = tuple(_empty(torch, tuple(x.shape), dt, x.device, stream) for x in xs)
+    else:
+        ys = tuple(out) if isinstance(out, (tuple, list)) else (out,)
+        if len(ys) != len(xs) or any(y.shape != x.shape or y.dtype != dt or y.get_device() != dev
+                                     for x, y in zip(xs, ys)):
+            raise ValueError("out must have the shapes and type of q and k")
+    args = []
+    for group in (xs, ys):
+        for i in range(2):
+            args.append((group[i].data_ptr(), _token_stride(group[i], "qk"[i]))
+                        if i < len(xs) else (None, 0))
+    raw = _raw_stream(torch, dev, stream)
+    (qp, qs), (kp, ks), (qo, qos), (ko, kos) = args
+    _check(lib().spd_rotary(table.table, 1 if dt == torch.bfloat16 else 0, n, positions.data_ptr(),
+                            qp, qs, q.shape[1], kp, ks, 0 if k is None else k.shape[1], qo, qos, ko,
+                            kos, 1 if inverse else 0, raw or None), "spd_rotary")
+    return ys[0] if k is None else ys

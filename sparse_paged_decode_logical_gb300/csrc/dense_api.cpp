@@ -13,6 +13,7 @@
 #include <memory>
 #include <new>
 
+#include "api_util.h"
 #include "dense.h"
 #include "spd.h"
 #include "spd_internal.h"
@@ -26,50 +27,6 @@ constexpr int kMaxKeep = 1 << 28;  // no sequence is longer (max_context is boun
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned(const void *p, uintptr_t a) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-// The device of a pointer made current for a call, the caller's afterwards.
-class DeviceGuard {
- public:
-  spd_status bind(int device) {
-    if (cudaGetDevice(&prev_) != cudaSuccess) return SPD_ERR_CUDA;
-    if (prev_ != device) {
-      if (cudaSetDevice(device) != cudaSuccess) return SPD_ERR_CUDA;
-      moved_ = true;
-    }
-    return SPD_OK;
-  }
-  ~DeviceGuard() {
-    if (moved_) (void)cudaSetDevice(prev_);
-  }
-
- private:
-  int prev_ = -1;
-  bool moved_ = false;
-};
-
-bool device_of(const void *p, int *device) {
-  cudaPointerAttributes a{};
-  if (cudaPointerGetAttributes(&a, p) != cudaSuccess ||
-      (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged)) {
-    (void)cudaGetLastError();
-    return false;
-  }
-  *device = a.device;
-  return true;
-}
-
-int sm_count(int device) {
-  static std::atomic<int> known[64];
-  const bool keep = device >= 0 && device < 64;
-  int n = keep ? known[device].load(std::memory_order_relaxed) : 0;
-  if (n > 0) return n;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n < 1) {
-    (void)cudaGetLastError();
-    return 152;
-  }
-  if (keep) known[device].store(n, std::memory_order_relaxed);
-  return n;
-}
 
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
@@ -117,48 +74,6 @@ bool encode_partials(CUtensorMap *m, const float *base, int d, size_t rows) {
   const cuuint64_t strides[3] = {128, (cuuint64_t)d * 4, (cuuint64_t)d * 4};
   const cuuint32_t box[4] = {32, 1, 1, 32};
   return encode4(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, dims, strides, box);
-}
-
-const char *check_rule(const spd_score_rule *r) {
-  if (!r) return nullptr;
-  // (between the bounds every constant of the rule is an ordinary fp32 number)
-  if (r->scale != 0.f && !(r->scale >= 1e-6f && r->scale <= 1e6f))
-    return "scale must be 0 or in [1e-6, 1e6]";
-  if (r->softcap != 0.f && !(r->softcap >= 1e-6f && r->softcap <= 1e6f))
-    return "softcap must be 0 or in [1e-6, 1e6]";
-  if (r->slopes && !aligned(r->slopes, 4)) return "slopes must be 4-byte aligned";
-  return nullptr;
-}
-
-ScoreRule make_rule(const spd_score_rule *r, int d) {
-  constexpr double kLog2e = 1.4426950408889634;
-  ScoreRule x{};
-  const double scale = r && r->scale > 0.f ? (double)r->scale : 1.0 / std::sqrt((double)d);
-  x.scale_log2 = (float)(scale * kLog2e);
-  if (r && r->softcap > 0.f) {
-    x.z_in = (float)(scale / r->softcap);
-    x.e_in = (float)(2.0 * kLog2e * scale / r->softcap);
-    x.small = (float)(0.5999 * r->softcap / scale);
-    x.cap_out = (float)(kLog2e * r->softcap);
-    // tanh(z) / z in z^2, |z| <= 0.6 (dense_math.cuh)
-    constexpr double kTanh[5] = {0.9999999403953552, -0.33332309126853943, 0.13310173153877258,
-                                 -0.05210147798061371, 0.01547542680054903};
-    for (int i = 0; i < 5; ++i) x.poly[i] = (float)(kLog2e * r->softcap * kTanh[i]);
-  }
-  x.slopes = r ? r->slopes : nullptr;
-  x.rough = x.cap_out <= 256.f;
-  if (x.cap_out > 0.f && r->softcap >= 30.f && !x.slopes && x.z_in > 1e-4f && x.z_in < 1e4f) {
-    // (z_in^8 fits fp32)
-    // tanh(z) / z in z^2, |z| <= 0.75, times scale log2(e) and in (q.k)^2
-    constexpr double kTanh[5] = {0.999999463558197, -0.3332825005054474, 0.13258983194828033,
-                                 -0.050056301057338715, 0.01292963046580553};
-    double f = scale * kLog2e;
-    const double z2 = scale / r->softcap * (scale / r->softcap);
-    for (int i = 0; i < 5; ++i, f *= z2) x.quick_poly[i] = (float)(f * kTanh[i]);
-    x.quick = (float)(0.7499 * r->softcap / scale);
-    x.quick_floor = (float)(-0.25 * r->softcap / scale);
-  }
-  return x;
 }
 
 // ---- prompt attention ------------------------------------------------------------
@@ -371,6 +286,8 @@ spd_status check_shared(spd_ctx *c, const CtxView &v, int prefix_id, const int *
   if (v.Hs > 0)
     return fail_message(c, SPD_ERR_INVALID_ARG, "a context with streaming heads keeps no whole cache");
   if (v.kv_fp8) return fail_message(c, SPD_ERR_INVALID_ARG, "fp8 KV storage is not supported here");
+  if (v.quant)
+    return fail_message(c, SPD_ERR_INVALID_ARG, "a cache with kv_quant is attended by spd_quant_decode_attention");
   spd_status r = check_live(c, ids, n);
   if (r != SPD_OK) return r;
   long long lp = 0;
@@ -701,6 +618,7 @@ spd_status spd_kv_evict(spd_ctx *c, const int *src_ids, const int *dst_ids, int 
   ctx_view(c, &v);
   if (v.Hs > 0)
     return fail_message(c, SPD_ERR_INVALID_ARG, "a context with streaming heads keeps no whole cache");
+  if (v.quant) return fail_message(c, SPD_ERR_INVALID_ARG, "a cache with kv_quant is not evicted from");
   spd_status r = check_live(c, src_ids, n_seqs);
   if (r != SPD_OK) return r;
   if ((r = check_live(c, dst_ids, n_seqs)) != SPD_OK) return r;

@@ -1,0 +1,380 @@
+// C ABI of rotary positions and of the cache in 8 or 4 bits (declared in
+// spd.h): argument checks, the split of the work over the GPU and launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "api_util.h"
+#include "quant.h"
+#include "spd.h"
+#include "spd_internal.h"
+
+using namespace spd;
+
+namespace {
+
+constexpr int kMaxTokens = 1 << 28;
+constexpr long long kMaxPlaces = 1LL << 30;  // tiles of one attention launch
+
+bool aligned(const void *p, uintptr_t a) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; }
+bool bad_stride(long long s, long long row) { return s < row || s % 8 || s > (1LL << 31); }
+
+const char *check_table(const spd_rotary_table *t) {
+  if (!t) return "the rotary table is NULL";
+  if ((t->head_dim != 64 && t->head_dim != 128) || t->rotary_dim < 16 || t->rotary_dim % 16 ||
+      t->rotary_dim > t->head_dim || t->axes < 1 || t->axes > 4 ||
+      (t->neighbours != 0 && t->neighbours != 1))
+    return "the rotary table was not made by spd_rotary_make";
+  for (int i = 0; i < t->rotary_dim / 2; ++i)
+    if (t->axis[i] >= t->axes) return "the rotary table was not made by spd_rotary_make";
+  return nullptr;
+}
+
+spd_status need_quant(spd_ctx *c, const CtxView &v) {
+  if (v.quant) return SPD_OK;
+  return fail_message(c, SPD_ERR_INVALID_ARG, "the context has no kv_quant");
+}
+
+// Tiles that tokens [first, first + n) touch.
+long long tiles_of(long long first, long long n) {
+  return (first + n + kQuantTile - 1) / kQuantTile - first / kQuantTile;
+}
+
+}  // namespace
+
+namespace spd {
+
+// Writes n_tokens tokens of each listed sequence (their pages are there); lengths are the
+// caller's to set.
+spd_status quant_append(spd_ctx *c, const QuantWrite &w, const int *ids, int n, int n_tokens,
+                        cudaStream_t st) {
+  CtxView v;
+  spd_status r = ctx_device(c, st, &v);
+  if (r != SPD_OK) return r;
+  const spd_config &cfg = *v.cfg;
+  DeviceGuard guard;
+  if ((r = guard.bind(v.device)) != SPD_OK) return fail_message(c, r, "cudaSetDevice failed");
+  for (int b = 0; b < n; b += kQuantSeqs) {
+    static thread_local QuantAppendParams p;
+    p.n_seqs = std::min(kQuantSeqs, n - b);
+    long long tiles = 0;
+    for (int i = 0; i < p.n_seqs; ++i) {
+      const long long L = seq_length(c, ids[b + i]);
+      p.seqs[i] = QuantSeq{ids[b + i], (int)L, (int)tiles};
+      tiles += tiles_of(L, n_tokens);
+    }
+    const int works = 2 * cfg.num_kv_heads + (w.table ? cfg.num_q_heads : 0);
+    // few tiles: their heads go to several CTAs, each of which makes the sines again
+    const int most = (works + 7) / 8;
+    p.parts = (int)std::max<long long>(1, std::min<long long>(most, 2LL * v.num_sms / std::max(tiles, 1LL)));
+    if (tiles * p.parts > 0x7fffffffLL)
+      return fail_message(c, SPD_ERR_CAPACITY, "append too large for one launch");
+    if (w.table) p.table = *w.table;
+    p.rotate = w.table != nullptr;
+    p.k = w.k;
+    p.v = w.v;
+    p.q = w.q;
+    p.q_out = w.q_out;
+    p.k_stride = w.k_stride;
+    p.v_stride = w.v_stride;
+    p.q_stride = w.q_stride;
+    p.positions = w.positions;
+    p.pool = v.buf->k_pool;
+    p.page_table = static_cast<const int *>(v.buf->page_table);
+    p.err = v.err;
+    p.n_tokens = n_tokens;
+    p.hq = cfg.num_q_heads;
+    p.hkv = cfg.num_kv_heads;
+    p.P = cfg.physical_page;
+    p.max_pp = v.max_pp;
+    p.num_phys = cfg.num_physical_pages;
+    p.total_seqs = n;
+    p.seq0 = b;
+    p.tiles = (int)tiles;
+    const cudaError_t e = launch_quant_append(p, cfg.dtype, cfg.head_dim, v.quant, st);
+    note_launches(c, st, 1);
+    if (e != cudaSuccess) return fail_message(c, SPD_ERR_CUDA, cudaGetErrorString(e));
+  }
+  return SPD_OK;
+}
+
+}  // namespace spd
+
+extern "C" {
+
+spd_status spd_rotary_make(const spd_rotary_rule *r, spd_rotary_table *out) {
+  if (!r || !out) return SPD_ERR_INVALID_ARG;
+  if ((r->head_dim != 64 && r->head_dim != 128) || r->rotary_dim < 16 || r->rotary_dim % 16 ||
+      r->rotary_dim > r->head_dim || r->axes < 1 || r->axes > 4)
+    return SPD_ERR_INVALID_ARG;
+  if ((r->axes_in_turn != 0 && r->axes_in_turn != 1) || (r->neighbours != 0 && r->neighbours != 1))
+    return SPD_ERR_INVALID_ARG;
+  const int pairs = r->rotary_dim / 2;
+  int left[4] = {0, 0, 0, 0}, sum = 0;
+  for (int a = 0; a < r->axes; ++a) {
+    if (r->sections[a] < 0 || r->sections[a] > pairs) return SPD_ERR_INVALID_ARG;
+    sum += left[a] = r->sections[a];
+  }
+  if (sum != pairs) return SPD_ERR_INVALID_ARG;
+  if (!r->inv_freq && !(r->base >= 1.0 && r->base <= 1e300)) return SPD_ERR_INVALID_ARG;
+  if (r->inv_freq)
+    for (int i = 0; i < pairs; ++i)
+      if (!(r->inv_freq[i] >= 0.0 && r->inv_freq[i] <= 1000.0)) return SPD_ERR_INVALID_ARG;
+  spd_rotary_table t;
+  memset(&t, 0, sizeof t);
+  t.head_dim = r->head_dim;
+  t.rotary_dim = r->rotary_dim;
+  t.axes = r->axes;
+  t.neighbours = r->neighbours;
+  int a = 0;
+  for (int i = 0; i < pairs; ++i) {
+    while (left[a] == 0) a = (a + 1) % r->axes;
+    t.axis[i] = (unsigned char)a;
+    --left[a];
+    if (r->axes_in_turn) a = (a + 1) % r->axes;
+    const double f = r->inv_freq ? r->inv_freq[i] : std::pow(r->base, -2.0 * i / r->rotary_dim);
+    const double turns = f / 6.283185307179586476925286766559;
+    const double x = std::nearbyint(std::ldexp(turns - std::floor(turns), 64));
+    t.turns[i] = x >= 18446744073709551616.0 ? 0ull : (unsigned long long)x;
+  }
+  *out = t;
+  return SPD_OK;
+}
+
+spd_status spd_rotary(const spd_rotary_table *table, spd_dtype dtype, int n_tokens,
+                      const int *positions, const void *q, long long q_stride, int q_heads,
+                      const void *k, long long k_stride, int kv_heads, void *q_out,
+                      long long q_out_stride, void *k_out, long long k_out_stride, int inverse,
+                      spd_stream stream) {
+  if (check_table(table) || (dtype != SPD_F16 && dtype != SPD_BF16) || n_tokens < 1 ||
+      !aligned(positions, 4) || (inverse != 0 && inverse != 1))
+    return SPD_ERR_INVALID_ARG;
+  const bool has_k = k || k_out;
+  const int hkv = has_k ? kv_heads : 0;
+  if (q_heads < 1 || q_heads > 1024 || (has_k && (kv_heads < 1 || kv_heads > 1024)))
+    return SPD_ERR_INVALID_ARG;
+  const long long qr = (long long)q_heads * table->head_dim, kr = (long long)hkv * table->head_dim;
+  if (!aligned(q, 16) || !aligned(q_out, 16) || bad_stride(q_stride, qr) ||
+      bad_stride(q_out_stride, qr))
+    return SPD_ERR_INVALID_ARG;
+  if (has_k && (!aligned(k, 16) || !aligned(k_out, 16) || bad_stride(k_stride, kr) ||
+                bad_stride(k_out_stride, kr)))
+    return SPD_ERR_INVALID_ARG;
+  if ((q == q_out && q_stride != q_out_stride) || (has_k && k == k_out && k_stride != k_out_stride))
+    return SPD_ERR_INVALID_ARG;
+  if (n_tokens > kMaxTokens) return SPD_ERR_CAPACITY;
+  int device = 0;
+  if (!device_of(q_out, &device)) return SPD_ERR_INVALID_ARG;
+  DeviceGuard guard;
+  const spd_status s = guard.bind(device);
+  if (s != SPD_OK) return s;
+  static thread_local RotaryParams p;
+  p.table = *table;
+  p.q = q;
+  p.k = k;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.q_out_stride = q_out_stride;
+  p.k_out_stride = k_out_stride;
+  p.positions = positions;
+  p.n = n_tokens;
+  p.hq = q_heads;
+  p.hkv = hkv;
+  p.inverse = inverse;
+  // few tokens: one per CTA; many: up to 8, which share the set-up
+  p.tokens_per_cta = std::max(1, std::min(8, n_tokens / (4 * sm_count(device))));
+  const cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e = launch_rotary(p, dtype, st);
+  note_prompt_launch(st);
+  return e == cudaSuccess ? SPD_OK : SPD_ERR_CUDA;
+}
+
+spd_status spd_kv_append_rotary(spd_ctx *c, const spd_rotary_table *table, const int *seq_ids,
+                                int n_seqs, int n_tokens, const int *positions, const void *q,
+                                long long q_stride, const void *k, long long k_stride,
+                                const void *v, long long v_stride, void *q_out,
+                                spd_stream stream) {
+  if (!c) return SPD_ERR_INVALID_ARG;
+  CtxView w;
+  ctx_view(c, &w);
+  spd_status r = need_quant(c, w);
+  if (r != SPD_OK) return r;
+  const spd_config &cfg = *w.cfg;
+  if (const char *bad = check_table(table)) return fail_message(c, SPD_ERR_INVALID_ARG, bad);
+  if (table->head_dim != cfg.head_dim)
+    return fail_message(c, SPD_ERR_INVALID_ARG, "the rotary table is of another head_dim");
+  const long long qr = (long long)cfg.num_q_heads * cfg.head_dim,
+                  kr = (long long)cfg.num_kv_heads * cfg.head_dim;
+  if (!aligned(q, 16) || !aligned(q_out, 16) || bad_stride(q_stride, qr) ||
+      bad_stride(k_stride, kr) || bad_stride(v_stride, kr))
+    return fail_message(c, SPD_ERR_INVALID_ARG,
+                        "q, k, v and q_out must be 16-byte aligned, strides multiples of 8 and at "
+                        "least a row");
+  if (q == q_out && q_stride != qr)
+    return fail_message(c, SPD_ERR_INVALID_ARG, "q_out may be q only where its rows are contiguous");
+  if (positions && !aligned(positions, 4))
+    return fail_message(c, SPD_ERR_INVALID_ARG, "positions must be 4-byte aligned");
+  QuantWrite x{};
+  x.table = table;
+  x.k = k;
+  x.v = v;
+  x.q = q;
+  x.q_out = q_out;
+  x.k_stride = k_stride;
+  x.v_stride = v_stride;
+  x.q_stride = q_stride;
+  x.positions = positions;
+  return append_quantised(c, x, seq_ids, n_seqs, n_tokens, (cudaStream_t)stream);
+}
+
+spd_status spd_kv_read(spd_ctx *c, const int *seq_ids, int n_seqs, int begin, int n_tokens,
+                       void *k, void *v, spd_stream stream) {
+  if (!c) return SPD_ERR_INVALID_ARG;
+  CtxView w;
+  ctx_view(c, &w);
+  spd_status r = need_quant(c, w);
+  if (r != SPD_OK) return r;
+  if (n_tokens < 1 || !aligned(k, 16) || !aligned(v, 16))
+    return fail_message(c, SPD_ERR_INVALID_ARG,
+                        "n_tokens >= 1 and 16-byte aligned k and v required");
+  if ((r = check_live(c, seq_ids, n_seqs)) != SPD_OK) return r;
+  for (int i = 0; i < n_seqs; ++i) {
+    const long long L = seq_length(c, seq_ids[i]), first = begin < 0 ? L + begin : begin;
+    if (first < 0 || first + n_tokens > L)
+      return fail_message(c, SPD_ERR_CAPACITY, "a sequence does not hold all of these tokens");
+  }
+  const cudaStream_t st = (cudaStream_t)stream;
+  if ((r = ctx_device(c, st, &w)) != SPD_OK) return r;
+  DeviceGuard guard;
+  if ((r = guard.bind(w.device)) != SPD_OK) return fail_message(c, r, "cudaSetDevice failed");
+  const spd_config &cfg = *w.cfg;
+  const size_t row = (size_t)n_tokens * cfg.num_kv_heads * cfg.head_dim * 2;  // of a sequence
+  for (int b = 0; b < n_seqs; b += kQuantSeqs) {
+    static thread_local QuantReadParams p;
+    p.n_seqs = std::min(kQuantSeqs, n_seqs - b);
+    long long tiles = 0;
+    for (int i = 0; i < p.n_seqs; ++i) {
+      const long long L = seq_length(c, seq_ids[b + i]), first = begin < 0 ? L + begin : begin;
+      p.seqs[i] = QuantSeq{seq_ids[b + i], (int)first, (int)tiles};
+      tiles += tiles_of(first, n_tokens);
+    }
+    if (tiles * 2 * cfg.num_kv_heads > 0x7fffffffLL)
+      return fail_message(c, SPD_ERR_CAPACITY, "read too large for one launch");
+    p.pool = w.buf->k_pool;
+    p.k = static_cast<char *>(k) + (size_t)b * row;
+    p.v = static_cast<char *>(v) + (size_t)b * row;
+    p.page_table = static_cast<const int *>(w.buf->page_table);
+    p.err = w.err;
+    p.n_tokens = n_tokens;
+    p.hkv = cfg.num_kv_heads;
+    p.P = cfg.physical_page;
+    p.max_pp = w.max_pp;
+    p.num_phys = cfg.num_physical_pages;
+    p.tiles = (int)tiles;
+    const cudaError_t e = launch_quant_read(p, cfg.dtype, cfg.head_dim, w.quant, st);
+    note_launches(c, st, 1);
+    if (e != cudaSuccess) return fail_message(c, SPD_ERR_CUDA, cudaGetErrorString(e));
+  }
+  return SPD_OK;
+}
+
+spd_status spd_quant_decode_attention(spd_ctx *c, const void *q, const int *seq_ids, int n_seqs,
+                                      int window, const spd_score_rule *rule, spd_out out_type,
+                                      void *out, spd_stream stream) {
+  if (!c) return SPD_ERR_INVALID_ARG;
+  CtxView v;
+  ctx_view(c, &v);
+  spd_status r = need_quant(c, v);
+  if (r != SPD_OK) return r;
+  if (!aligned(q, 16) || !aligned(out, 16))
+    return fail_message(c, SPD_ERR_INVALID_ARG, "q and out must be 16-byte aligned pointers");
+  if (out_type != SPD_OUT_F32 && out_type != SPD_OUT_DTYPE)
+    return fail_message(c, SPD_ERR_INVALID_ARG, "out_type must be SPD_OUT_F32 or SPD_OUT_DTYPE");
+  if (window < 0) return fail_message(c, SPD_ERR_INVALID_ARG, "window must be >= 0");
+  if (const char *bad = check_rule(rule)) return fail_message(c, SPD_ERR_INVALID_ARG, bad);
+  if ((r = check_live(c, seq_ids, n_seqs)) != SPD_OK) return r;
+  for (int i = 0; i < n_seqs; ++i)
+    if (seq_length(c, seq_ids[i]) < 1)
+      return fail_message(c, SPD_ERR_STATE, "a sequence has no tokens");
+  const cudaStream_t st = (cudaStream_t)stream;
+  if ((r = ctx_device(c, st, &v)) != SPD_OK) return r;
+  DeviceGuard guard;
+  if ((r = guard.bind(v.device)) != SPD_OK) return fail_message(c, r, "cudaSetDevice failed");
+  const spd_config &cfg = *v.cfg;
+  const size_t oe = out_type == SPD_OUT_F32 ? 4 : 2, row = (size_t)cfg.num_q_heads * cfg.head_dim;
+  const int Hkv = cfg.num_kv_heads, most_ctas = std::min(kQuantCtas, 2 * v.num_sms);
+  for (int b = 0; b < n_seqs;) {
+    static thread_local QuantAttendParams p;
+    // as many sequences as fit one launch
+    int n = 0, most = 0;
+    long long total = 0;
+    while (n < kQuantSeqs && b + n < n_seqs) {
+      const int L = (int)seq_length(c, seq_ids[b + n]);
+      const int first = window > 0 && window < L ? L - window : 0;
+      const int tiles = (int)tiles_of(first, L - first);
+      if (n > 0 && total + (long long)tiles * Hkv > kMaxPlaces) break;
+      p.seqs[n] = QuantAttendSeq{seq_ids[b + n], L, first, tiles, tiles, 0};
+      total += (long long)tiles * Hkv;
+      most = std::max(most, tiles);
+      ++n;
+    }
+    if (total > kMaxPlaces)
+      return fail_message(c, SPD_ERR_CAPACITY, "a sequence is too long for one launch");
+    // Every warp takes per_warp tiles.  Where all units can begin at a CTA of their own
+    // without another tile per warp they do, so that no unit has a stray part elsewhere.
+    const long long warps = (long long)most_ctas * kQuantWarps;
+    p.per_warp = (int)std::max<long long>(1, (total + warps - 1) / warps);
+    auto ctas_of = [&](int per_warp) {  // with units that begin at CTAs
+      long long k = 0;
+      for (int i = 0; i < n; ++i)
+        k += (long long)Hkv * ((p.seqs[i].tiles + per_warp * kQuantWarps - 1) /
+                               (per_warp * kQuantWarps));
+      return k;
+    };
+    int whole = p.per_warp;
+    const int give = std::max(whole + whole / 16, whole + 1);
+    while (whole < give && ctas_of(whole) > most_ctas) ++whole;
+    if (ctas_of(whole) <= most_ctas) {
+      p.per_warp = whole;
+      const int per_cta = whole * kQuantWarps;
+      for (int i = 0; i < n; ++i)
+        p.seqs[i].stride = (p.seqs[i].tiles + per_cta - 1) / per_cta * per_cta;
+    }
+    long long places = 0;
+    for (int i = 0; i < n; ++i) {
+      p.seqs[i].off = (int)places;
+      places += (long long)p.seqs[i].stride * Hkv;
+    }
+    p.total = (int)places;
+    p.ctas = (int)((places + (long long)p.per_warp * kQuantWarps - 1) /
+                   ((long long)p.per_warp * kQuantWarps));
+    p.pool = v.buf->k_pool;
+    p.q = static_cast<const char *>(q) + (size_t)b * row * 2;
+    p.out = static_cast<char *>(out) + (size_t)b * row * oe;
+    p.page_table = static_cast<const int *>(v.buf->page_table);
+    p.part_o = v.part_o;
+    p.part_ml = v.part_ml;
+    p.tickets = v.tickets;
+    p.err = v.err;
+    p.rule = make_rule(rule, cfg.head_dim);
+    p.out_f32 = out_type == SPD_OUT_F32;
+    p.precise_cap = p.out_f32 || cfg.dtype == SPD_F16 || !p.rule.rough;
+    p.n = n;
+    p.hkv = Hkv;
+    p.P = cfg.physical_page;
+    p.max_pp = v.max_pp;
+    p.num_phys = cfg.num_physical_pages;
+    const cudaError_t e = launch_quant_attend(p, cfg.dtype, cfg.head_dim, v.quant, v.G, st);
+    note_launches(c, st, 1);
+    if (e != cudaSuccess) return fail_message(c, SPD_ERR_CUDA, cudaGetErrorString(e));
+    b += n;
+  }
+  return SPD_OK;
+}
+
+}  // extern "C"

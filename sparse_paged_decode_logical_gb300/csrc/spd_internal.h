@@ -223,6 +223,9 @@ struct CtxView {
   int *err;
   int *tickets;       // [ticket_seqs][num_kv_heads], zero between launches
   int ticket_seqs;
+  int quant;          // bits of a quantised cache, or 0
+  float *part_o;      // quantised: partial sums (kQuantCtas x 2)
+  float2 *part_ml;
 };
 // Host facts only (no device call); ctx_device fills device, num_sms and the
 // tensor maps in, setting the context up on its device the first time.
@@ -235,6 +238,19 @@ long long seq_length(const spd_ctx *c, int id);
 spd_status check_fill(spd_ctx *c, const int *ids, const int *tokens, int n);
 spd_status fill_pages(spd_ctx *c, const int *ids, const int *tokens, int n, cudaStream_t st);
 void set_filled(spd_ctx *c, const int *ids, const int *tokens, int n);
+// New tokens of a quantised cache (quant_api.cpp): `table` null writes keys as they are.
+struct QuantWrite {
+  const spd_rotary_table *table;
+  const void *k, *v, *q;
+  void *q_out;
+  long long k_stride, v_stride, q_stride;  // elements between tokens
+  const int *positions;
+};
+spd_status quant_append(spd_ctx *c, const QuantWrite &w, const int *ids, int n, int n_tokens,
+                        cudaStream_t st);
+// Checks, pages, quant_append and the new lengths.
+spd_status append_quantised(spd_ctx *c, const QuantWrite &w, const int *ids, int n, int n_tokens,
+                            cudaStream_t st);
 // The context enqueued n kernels on the stream.
 void note_launches(spd_ctx *c, cudaStream_t st, int n);
 // A prompt call, which has no context, enqueues kernels on the stream: the kernel

@@ -22,6 +22,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "quant.h"
 #include "spd.h"
 #include "spd_internal.h"
 
@@ -59,6 +60,7 @@ struct Derived {
       seqs_per_launch = 0;
   int mass_pages = 0, mass_tiles = 0;  // per-page mass: attended pages / tiles per unit
   int kv_fp8 = 0;                       // K/V stored as E4M3 codes of value / scale
+  int quant = 0;                        // K/V stored in this many bits, scales by the data
   float k_scale[kMaxKvHeads] = {}, v_scale[kMaxKvHeads] = {};
   unsigned char kv_kind[kMaxKvHeads] = {}, kv_sub[kMaxKvHeads] = {},
                 dyn_kv[kMaxKvHeads] = {}, str_kv[kMaxKvHeads] = {};
@@ -96,6 +98,9 @@ const char *derive(const spd_config *c, Derived *d) {
   if (c->reuse_interval < 1) return "reuse_interval must be >= 1";
   if (c->kv_fp8 != 0 && c->kv_fp8 != 1) return "kv_fp8 must be 0 or 1";
   d->kv_fp8 = c->kv_fp8;
+  if (c->kv_quant != 0 && c->kv_quant != 4 && c->kv_quant != 8) return "kv_quant must be 0, 4 or 8";
+  d->quant = c->kv_quant;
+  if (d->quant && d->kv_fp8) return "kv_quant and kv_fp8 exclude each other";
   if (d->kv_fp8 && c->head_dim != 128) return "fp8 KV storage needs head_dim 128";
   for (int h = 0; h < c->num_kv_heads; ++h) {
     d->k_scale[h] = d->kv_fp8 && c->k_scale ? c->k_scale[h] : 1.f;
@@ -116,6 +121,7 @@ const char *derive(const spd_config *c, Derived *d) {
       d->dyn_kv[d->Hd++] = (unsigned char)h;
     }
   }
+  if (d->quant && d->Hs > 0) return "kv_quant has no streaming heads";
   if (d->Hs > 0 && (c->sink < 0 || c->window < 1 || (long long)c->sink + c->window > (1 << 24)))
     return "streaming heads need sink >= 0 and window >= 1";
   if (d->Hd > 0 && c->num_physical_pages < 1) return "num_physical_pages must be >= 1";
@@ -136,6 +142,24 @@ const char *derive(const spd_config *c, Derived *d) {
   if (d->Hs > 0 && (long long)c->max_seqs * d->Hs * (c->sink + c->window) >= (1LL << 31))
     return "streaming buffers exceed 2^31 rows";
 
+  if (d->quant) {
+    spd_sizes &z = d->sizes;
+    z.k_pool = (size_t)c->num_physical_pages * d->Hd * (c->physical_page / kQuantTile) *
+               quant_tile_bytes(c->head_dim, d->quant);
+    z.page_table = (size_t)c->max_seqs * d->max_pp * 4;
+    ScratchLayout &sl = d->sl;
+    d->seqs_per_launch = std::min(c->max_seqs, kQuantSeqs);
+    size_t off = kScratchHeader;
+    sl.tickets_dec = off;
+    off = round_up(off + (size_t)d->seqs_per_launch * c->num_kv_heads * 4, 256);
+    sl.part_ml = off;
+    off = round_up(off + (size_t)kQuantCtas * 2 * d->G * 8, 256);
+    sl.part_o = off;
+    off = round_up(off + (size_t)kQuantCtas * 2 * d->G * c->head_dim * 4, 256);
+    sl.total = off;
+    z.scratch = off;
+    return nullptr;
+  }
   const size_t e = d->kv_fp8 ? 1 : 2, dim = (size_t)c->head_dim;
   const int S = d->Hs ? c->sink : 0, W = d->Hs ? c->window : 0;
   spd_sizes &z = d->sizes;
@@ -287,6 +311,7 @@ spd_status encode_map(spd_ctx *c, CUtensorMap *m, void *base, uint64_t rows_per_
 
 spd_status make_tensor_maps(spd_ctx *c) {
   const Derived &dv = c->dv;
+  if (dv.quant) return SPD_OK;  // (its tiles are copied whole)
   spd_status r;
   if (dv.Hd > 0) {
     const uint64_t planes = (uint64_t)c->cfg.num_physical_pages * dv.Hd;
@@ -844,8 +869,15 @@ spd_status check_attend_state(spd_ctx *c, const int *ids, int n, bool will_appen
 
 namespace spd {
 
+spd_status refuse_quant(spd_ctx *c) {
+  if (!c->dv.quant) return SPD_OK;
+  return c->fail(SPD_ERR_INVALID_ARG, "the context's cache is in %d bits (kv_quant): it is read by "
+                 "spd_quant_decode_attention and spd_kv_read", c->dv.quant);
+}
+
 spd_status check_attention_call(spd_ctx *c, const void *q, const int *ids, int n,
                                 const float *out) {
+  if (refuse_quant(c) != SPD_OK) return SPD_ERR_INVALID_ARG;
   if (!q || !out || !aligned16(q) || !aligned16(out))
     return c->fail(SPD_ERR_INVALID_ARG, "q and out must be 16-byte aligned pointers");
   spd_status r = check_seqs(c, ids, n);
@@ -888,6 +920,9 @@ void ctx_view(spd_ctx *c, CtxView *v) {
   v->err = c->err_word();
   v->tickets = reinterpret_cast<int *>(c->scratch(c->dv.sl.tickets_dec));
   v->ticket_seqs = c->dv.seqs_per_launch;
+  v->quant = c->dv.quant;
+  v->part_o = c->dv.quant ? reinterpret_cast<float *>(c->scratch(c->dv.sl.part_o)) : nullptr;
+  v->part_ml = c->dv.quant ? reinterpret_cast<float2 *>(c->scratch(c->dv.sl.part_ml)) : nullptr;
 }
 
 spd_status ctx_device(spd_ctx *c, cudaStream_t st, CtxView *v) {
@@ -932,6 +967,38 @@ void note_prompt_launch(cudaStream_t st) {
   std::lock_guard<std::mutex> lock(g_last_mu);
   const auto it = g_last_launcher.find(st);
   if (it != g_last_launcher.end()) it->second.kind = kKindOther;
+}
+
+static spd_status check_append(spd_ctx *c, const int *ids, int n, int n_tokens, const void *k,
+                               const void *v) {
+  if (n_tokens < 1 || !k || !v) return c->fail(SPD_ERR_INVALID_ARG, "n_tokens >= 1 and k, v required");
+  if (!aligned16(k) || !aligned16(v)) return c->fail(SPD_ERR_INVALID_ARG, "k, v must be 16-byte aligned");
+  spd_status r = check_seqs(c, ids, n);
+  if (r != SPD_OK) return r;
+  long long need = 0;
+  for (int i = 0; i < n; ++i) {
+    const Seq &s = c->seqs[ids[i]];
+    if (s.L + n_tokens > c->cfg.max_context)
+      return c->fail(SPD_ERR_CAPACITY, "sequence %d: %lld + %d tokens exceed max_context %d",
+                     ids[i], s.L, n_tokens, c->cfg.max_context);
+    need += pages_needed(c, s, n_tokens);
+  }
+  if (need > (long long)c->free_pages.size())
+    return c->fail(SPD_ERR_NO_PAGES, "need %lld physical pages, %zu free", need,
+                   c->free_pages.size());
+  return SPD_OK;
+}
+
+spd_status append_quantised(spd_ctx *c, const QuantWrite &w, const int *ids, int n, int n_tokens,
+                            cudaStream_t st) {
+  spd_status r = check_append(c, ids, n, n_tokens, w.k, w.v);
+  if (r != SPD_OK) return r;
+  if ((r = ensure_device(c, st)) != SPD_OK) return r;
+  for (int i = 0; i < n; ++i) take_pages(c, ids[i], n_tokens);
+  if ((r = flush_page_table(c, st)) != SPD_OK) return r;
+  if ((r = quant_append(c, w, ids, n, n_tokens, st)) != SPD_OK) return r;
+  for (int i = 0; i < n; ++i) c->seqs[ids[i]].L += n_tokens;
+  return SPD_OK;
 }
 
 }  // namespace spd
@@ -1015,6 +1082,28 @@ spd_status spd_seq_free(spd_ctx *c, int seq_id) {
   return SPD_OK;
 }
 
+spd_status spd_seq_truncate(spd_ctx *c, int seq_id, int n_tokens) {
+  if (!c) return SPD_ERR_INVALID_ARG;
+  if (!c->dv.quant)
+    return c->fail(SPD_ERR_INVALID_ARG, "the context has no kv_quant (page metadata would be stale)");
+  if (n_tokens < 0) return c->fail(SPD_ERR_INVALID_ARG, "n_tokens must be >= 0");
+  const spd_status r = check_seqs(c, &seq_id, 1);
+  if (r != SPD_OK) return r;
+  Seq &s = c->seqs[seq_id];
+  if (n_tokens > s.L)
+    return c->fail(SPD_ERR_CAPACITY, "sequence %d holds %lld tokens", seq_id, s.L);
+  const size_t keep = ((size_t)n_tokens + c->cfg.physical_page - 1) / c->cfg.physical_page;
+  for (; s.pages.size() > keep; s.pages.pop_back()) c->free_pages.push_back(s.pages.back());
+  // (page-table writes of what is left are still due, those of returned pages no longer)
+  c->pending_pt.erase(std::remove_if(c->pending_pt.begin(), c->pending_pt.end(),
+                                     [&](const PtUpdate &u) {
+                                       return u.slot == seq_id && (size_t)u.index >= keep;
+                                     }),
+                      c->pending_pt.end());
+  s.L = n_tokens;
+  return SPD_OK;
+}
+
 spd_status spd_seq_reserve(spd_ctx *c, int seq_id, int n_tokens) {
   if (!c || n_tokens < 0) return SPD_ERR_INVALID_ARG;
   spd_status r = check_seqs(c, &seq_id, 1);
@@ -1061,29 +1150,16 @@ spd_status spd_free_pages(spd_ctx *c, int *n_free) {
   return SPD_OK;
 }
 
-static spd_status check_append(spd_ctx *c, const int *ids, int n, int n_tokens, const void *k,
-                               const void *v) {
-  if (n_tokens < 1 || !k || !v) return c->fail(SPD_ERR_INVALID_ARG, "n_tokens >= 1 and k, v required");
-  if (!aligned16(k) || !aligned16(v)) return c->fail(SPD_ERR_INVALID_ARG, "k, v must be 16-byte aligned");
-  spd_status r = check_seqs(c, ids, n);
-  if (r != SPD_OK) return r;
-  long long need = 0;
-  for (int i = 0; i < n; ++i) {
-    const Seq &s = c->seqs[ids[i]];
-    if (s.L + n_tokens > c->cfg.max_context)
-      return c->fail(SPD_ERR_CAPACITY, "sequence %d: %lld + %d tokens exceed max_context %d",
-                     ids[i], s.L, n_tokens, c->cfg.max_context);
-    need += pages_needed(c, s, n_tokens);
-  }
-  if (need > (long long)c->free_pages.size())
-    return c->fail(SPD_ERR_NO_PAGES, "need %lld physical pages, %zu free", need,
-                   c->free_pages.size());
-  return SPD_OK;
-}
-
 spd_status spd_kv_append(spd_ctx *c, const int *seq_ids, int n_seqs, int n_tokens, const void *k,
                          const void *v, spd_stream stream) {
   if (!c) return SPD_ERR_INVALID_ARG;
+  if (c->dv.quant) {
+    QuantWrite w{};
+    w.k = k;
+    w.v = v;
+    w.k_stride = w.v_stride = (long long)c->cfg.num_kv_heads * c->cfg.head_dim;
+    return append_quantised(c, w, seq_ids, n_seqs, n_tokens, (cudaStream_t)stream);
+  }
   spd_status r = check_append(c, seq_ids, n_seqs, n_tokens, k, v);
   if (r != SPD_OK) return r;
   return append_impl(c, seq_ids, n_seqs, n_tokens, k, v, (cudaStream_t)stream);
@@ -1091,7 +1167,7 @@ spd_status spd_kv_append(spd_ctx *c, const int *seq_ids, int n_seqs, int n_token
 
 spd_status spd_select_pages(spd_ctx *c, const void *q, const int *seq_ids, int n_seqs, int force,
                             spd_stream stream) {
-  if (!c) return SPD_ERR_INVALID_ARG;
+  if (!c || refuse_quant(c) != SPD_OK) return SPD_ERR_INVALID_ARG;
   if (!q || !aligned16(q)) return c->fail(SPD_ERR_INVALID_ARG, "q must be a 16-byte aligned pointer");
   spd_status r = check_seqs(c, seq_ids, n_seqs);
   if (r != SPD_OK) return r;
@@ -1103,7 +1179,7 @@ spd_status spd_select_pages(spd_ctx *c, const void *q, const int *seq_ids, int n
 
 spd_status spd_sparse_decode_attention(spd_ctx *c, const void *q, const int *seq_ids, int n_seqs,
                                        float *out, spd_stream stream) {
-  if (!c) return SPD_ERR_INVALID_ARG;
+  if (!c || refuse_quant(c) != SPD_OK) return SPD_ERR_INVALID_ARG;
   if (!q || !out || !aligned16(q) || !aligned16(out))
     return c->fail(SPD_ERR_INVALID_ARG, "q and out must be 16-byte aligned pointers");
   spd_status r = check_seqs(c, seq_ids, n_seqs);
@@ -1167,7 +1243,7 @@ spd_status spd_sparse_decode_attention_page_mass(spd_ctx *c, const void *q, cons
 
 spd_status spd_decode_step(spd_ctx *c, const void *q, const void *k, const void *v,
                            const int *seq_ids, int n_seqs, float *out, spd_stream stream) {
-  if (!c) return SPD_ERR_INVALID_ARG;
+  if (!c || refuse_quant(c) != SPD_OK) return SPD_ERR_INVALID_ARG;
   if (!q || !out || !aligned16(q) || !aligned16(out))
     return c->fail(SPD_ERR_INVALID_ARG, "q and out must be 16-byte aligned pointers");
   spd_status r = check_append(c, seq_ids, n_seqs, 1, k, v);
