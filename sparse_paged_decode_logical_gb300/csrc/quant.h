@@ -46,8 +46,12 @@ inline size_t quant_tile_bytes(int d, int bits) {
 }
 
 constexpr int kQuantSeqs = 256;  // sequences described per parameter block
-constexpr int kQuantCtas = 512;  // most CTAs of an attention launch
-constexpr int kQuantWarps = 8;   // per CTA
+constexpr int kQuantCtas = 256;  // most CTAs of an attention launch
+constexpr int kQuantWarps = 12;  // per CTA
+constexpr int kQuantPerSm = 1;   // CTAs that an SM holds
+
+// A warp's share of a unit: [G][d] sums, [G] (reference, sum of weights).
+constexpr int quant_slot_bytes(int d, int G) { return (G * d * 4 + G * 8 + 15) / 16 * 16; }
 
 // ---- rotary ------------------------------------------------------------------------
 struct RotaryParams {
@@ -116,6 +120,7 @@ struct QuantAttendParams {
   const int *page_table;
   float *part_o;    // [2 x CTAs][G][d]
   float2 *part_ml;  // [2 x CTAs][G]
+  char *firsts;     // [CTAs][warps][quant_slot_bytes]: what a warp starts with
   int *tickets;     // [n][hkv], zero before and after
   int *err;
   ScoreRule rule;
@@ -127,7 +132,5 @@ struct QuantAttendParams {
 };
 cudaError_t launch_quant_attend(const QuantAttendParams &p, int dtype, int d, int bits, int G,
                                 cudaStream_t st);
-// CTAs of an attention launch that an SM holds at once.
-int quant_attend_ctas_per_sm(int d, int bits, int G);
 
 }  // namespace spd

@@ -307,7 +307,7 @@ spd_status spd_quant_decode_attention(spd_ctx *c, const void *q, const int *seq_
   if ((r = guard.bind(v.device)) != SPD_OK) return fail_message(c, r, "cudaSetDevice failed");
   const spd_config &cfg = *v.cfg;
   const size_t oe = out_type == SPD_OUT_F32 ? 4 : 2, row = (size_t)cfg.num_q_heads * cfg.head_dim;
-  const int Hkv = cfg.num_kv_heads, most_ctas = std::min(kQuantCtas, 2 * v.num_sms);
+  const int Hkv = cfg.num_kv_heads, most_ctas = std::min(kQuantCtas, kQuantPerSm * v.num_sms);
   for (int b = 0; b < n_seqs;) {
     static thread_local QuantAttendParams p;
     // as many sequences as fit one launch
@@ -328,7 +328,8 @@ spd_status spd_quant_decode_attention(spd_ctx *c, const void *q, const int *seq_
     // Every warp takes per_warp tiles.  Where all units can begin at a CTA of their own
     // without another tile per warp they do, so that no unit has a stray part elsewhere.
     const long long warps = (long long)most_ctas * kQuantWarps;
-    p.per_warp = (int)std::max<long long>(1, (total + warps - 1) / warps);
+    p.per_warp = (int)std::max<long long>(2, (total + warps - 1) / warps);
+    p.per_warp += p.per_warp & 1;  // (a step takes two)
     auto ctas_of = [&](int per_warp) {  // with units that begin at CTAs
       long long k = 0;
       for (int i = 0; i < n; ++i)
@@ -337,8 +338,8 @@ spd_status spd_quant_decode_attention(spd_ctx *c, const void *q, const int *seq_
       return k;
     };
     int whole = p.per_warp;
-    const int give = std::max(whole + whole / 16, whole + 1);
-    while (whole < give && ctas_of(whole) > most_ctas) ++whole;
+    const int give = std::max(whole + whole / 16, whole + 2);
+    while (whole < give && ctas_of(whole) > most_ctas) whole += 2;
     if (ctas_of(whole) <= most_ctas) {
       p.per_warp = whole;
       const int per_cta = whole * kQuantWarps;
@@ -359,6 +360,7 @@ spd_status spd_quant_decode_attention(spd_ctx *c, const void *q, const int *seq_
     p.page_table = static_cast<const int *>(v.buf->page_table);
     p.part_o = v.part_o;
     p.part_ml = v.part_ml;
+    p.firsts = v.firsts;
     p.tickets = v.tickets;
     p.err = v.err;
     p.rule = make_rule(rule, cfg.head_dim);

@@ -25,6 +25,7 @@
 #include <math_constants.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "dense_math.cuh"
 #include "ptx.cuh"
@@ -38,10 +39,10 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr uint32_t kWaitPolls = 1u << 22;
 constexpr int kThreads = kQuantWarps * 32;
 
-// A weight enters the product as 2^(z - m' + 11) (mantissa of its step), z = score + exponent
-// of the step, m' the largest z so far or at most 2^3 behind it: at most 2^15, and what fp16
-// loses below its normal range is 2^-36 of the largest.
-constexpr float kShift = 11.f, kLag = 3.f;
+// A weight enters the product as p 2^k step, p = 2^(score - m): 2^k moves the largest p step of
+// a column to between 2^10 and 2^12, and a new k is taken where one would pass 2^15.  What fp16
+// loses below its normal range is then 2^-35 of the largest.
+constexpr int kRoom = 11;
 
 __device__ __forceinline__ void qd_set_err(int *err, int code, int a, int b, int c) {
   if (atomicCAS(err, 0, code) == 0) {
@@ -55,6 +56,16 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+// D = A B + C in fp16 with fp32 sums; not volatile, so that a tile's scores and the weighted sum
+// of the one before are scheduled into one another.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
+      " {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
+        "f"(c3));
 }
 __device__ __forceinline__ uint32_t pack_rz(float a, float b) {
   uint32_t r;
@@ -70,18 +81,18 @@ __device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(
 template <int D, int BITS, int G>
 struct Shape {
   using Q = QuantTile<D, BITS>;
-  static constexpr int kSlot = (G * D * 4 + G * 8 + 15) / 16 * 16;  // bytes of one partial
-  static constexpr int kFirst = kQuantWarps * kSlot;
-  // two CTAs of an SM share its 227 KB; the ring holds the partials at the end, too
-  static constexpr int kRoom = 112 * 1024 - 1024 - kFirst;
-  static constexpr int kFit = kRoom / (kQuantWarps * Q::kBytes);
-  static constexpr int kStages = kFit < 2 ? 2 : kFit > 6 ? 6 : kFit;
-  static constexpr int kRing = kQuantWarps * kStages * Q::kBytes;
+  static constexpr int kSlot = quant_slot_bytes(D, G);  // one warp's partial
+  static constexpr int kStage = 2 * Q::kBytes;          // a step's two tiles
+  // the CTAs of an SM share its 227 KB; the ring holds the partials at the end, too
+  static constexpr int kRoom = (227 / kQuantPerSm - 2) * 1024;
+  static constexpr int kFit = kRoom / (kQuantWarps * kStage);
+  static constexpr int kStages = kFit > 4 ? 4 : kFit;
   static constexpr int kLast = kQuantWarps * kSlot;
-  static constexpr int kJoin = kQuantCtas * G * 4;  // weights of a unit's partials
-  static constexpr int kRingOrJoin = kRing > kLast + kJoin ? kRing : kLast + kJoin;
-  static constexpr int kBars = kQuantWarps * kStages * 8;
-  static constexpr int kSmem = kRingOrJoin + kFirst + kBars;
+  static constexpr int kRing = kQuantWarps * kStages * kStage;
+  static constexpr int kJoin = kLast + kQuantWarps * 32 * 24;  // and a unit's partials' sums
+  static constexpr int kBars = kRing > kJoin ? kRing : kJoin;
+  static constexpr int kSmem = kBars + kQuantWarps * kStages * 8;
+  static_assert(kStages >= 2 && kSmem <= kRoom + 1024, "the CTAs of an SM share its memory");
 };
 
 // Where a warp is in the row of tiles.
@@ -124,10 +135,11 @@ struct Cursor {
     }
     seek(p);
   }
-  __device__ __forceinline__ void step(const QuantAttendParams &p) {
-    ++at;
-    ++tile;
-    if (--left == 0) seek(p);
+  __device__ __forceinline__ void advance(const QuantAttendParams &p, int n) {  // n <= left
+    at += n;
+    tile += n;
+    left -= n;
+    if (left == 0) seek(p);
   }
 };
 
@@ -138,14 +150,26 @@ struct Warp {
   static constexpr int NG = Q::kGroups;
   static constexpr bool kTwo = SPLIT && G == 8;   // low halves need products of their own
   static constexpr bool kLanes = SPLIT && G < 8;  // low halves in the columns 4 .. 7
+  // Codes as fp16 numbers.  Outputs in bf16: as they lie, a subnormal number, code 2^-24 (2^-20
+  // in a high nibble).  The tensor cores cut sums off where their largest term, or what its
+  // exponent could hold, ends; the others therefore take ordinary numbers around 0, code - 2^(b-1)
+  // (11 instructions a word of 4 bits instead of 5, 5 for 4 codes of 8 bits instead of 3), and add
+  // products over more than two operands in fp32 outside.  (fp32 outputs 5.5e-6 off without.)
+  static constexpr bool kNibbles = BITS == 4 && !SPLIT;  // high nibbles 2^4 as large
+  static constexpr int kUnit = SPLIT ? 0 : 24;           // a code of 1 is 2^-kUnit
+  static constexpr float kMid = SPLIT ? (BITS == 4 ? 8.f : 128.f) : 0.f;
 
   uint32_t qb[KS][2];  // q as the second operand of S
   float qs[2][NG];     // sums of q over the groups, of the lane's two columns
-  float fac[2];        // of the columns: 2^e of q (and 2^24 is applied before)
+  float fac[2];        // of the columns: from sums to scores
   float slope[2];
-  float m[2], mz[2], l[2];
+  float m[2], l[2];    // reference of the weights, their sum
+  float up[2];         // 2^k
+  int k2[2];           // k
   float lo[2][NG];     // sum of p lo over the lane's tokens
   float o[KS][4];
+  bool vast;           // a query beyond 2^100: its factor comes in two
+  bool plain;          // neither vast nor capped nor biased
 
   __device__ __forceinline__ void begin(const QuantAttendParams &p, int i, int h, int lane) {
     const int g = lane >> 2, t = lane & 3;
@@ -174,27 +198,31 @@ struct Warp {
         x[s][c] *= down;
         sum[s * NG / KS] += x[s][c];
       }
-      // (codes of 4 bits: channels 2 and 3 come from high nibbles, 16 times as large)
-      const float hi = BITS == 4 ? 0.0625f : 1.f;
+      // (channels 2 and 3 come from high nibbles)
+      const float hi = kNibbles ? 0.0625f : 1.f;
       qb[s][0] = pack2<__half>(x[s][0], x[s][1]);
       qb[s][1] = pack2<__half>(x[s][2] * hi, x[s][3] * hi);
     }
     const float sl = p.rule.slopes ? p.rule.slopes[h * G + g % G] * 1.4426950408889634f : 0.f;
-    const float up = pow2(e);
+    vast = __any_sync(kFull, e > 86);
+    plain = !vast && p.rule.cap_out == 0.f && !p.rule.slopes;
+    const float f = pow2(vast ? e : e + kUnit) * (p.rule.cap_out == 0.f ? p.rule.scale_log2 : 1.f);
 #pragma unroll
     for (int a = 0; a < NG; ++a) {
       sum[a] += __shfl_xor_sync(kFull, sum[a], 1);
       sum[a] += __shfl_xor_sync(kFull, sum[a], 2);
-      sum[a] *= 0x1p-24f;
+      sum[a] *= pow2(-kUnit);
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int from = 4 * (2 * t + c);  // a lane of the column
-      fac[c] = __shfl_sync(kFull, up, from);
+      fac[c] = __shfl_sync(kFull, f, from);
       slope[c] = __shfl_sync(kFull, sl, from);
 #pragma unroll
       for (int a = 0; a < NG; ++a) qs[c][a] = __shfl_sync(kFull, sum[a], from);
-      m[c] = mz[c] = -CUDART_INF_F;
+      m[c] = -CUDART_INF_F;
+      up[c] = 1.f;
+      k2[c] = 0;
       l[c] = 0.f;
 #pragma unroll
       for (int a = 0; a < NG; ++a) lo[c][a] = 0.f;
@@ -225,187 +253,274 @@ struct Warp {
   }
 
   // Operand registers of a k-step (K) or an m-tile (V) from its codes.
+  static __device__ __forceinline__ uint32_t centred(uint32_t x) {  // code in the low bits
+    x |= 0x64006400u;                                               // 1024 + code
+    const __half2 y = __hsub2(*reinterpret_cast<__half2 *>(&x), __float2half2_rn(1024.f + kMid));
+    return *reinterpret_cast<const uint32_t *>(&y);
+  }
   static __device__ __forceinline__ void widen(const uint32_t *w, bool is_v, uint32_t (&a)[4]) {
-    if constexpr (BITS == 4) {
+    // 4 bits.  K: low nibbles k, high ones k + 8; V: low ones row g, high ones row g + 8
+    const int n1 = is_v ? 1 : 2, n2 = is_v ? 2 : 1;
+    if constexpr (kNibbles) {
       const uint32_t x = w[0], y = w[0] >> 8;
-      // K: low nibbles k, high ones k + 8; V: low ones row g, high ones row g + 8
       a[0] = x & 0x000f000fu;
-      a[is_v ? 1 : 2] = x & 0x00f000f0u;
-      a[is_v ? 2 : 1] = y & 0x000f000fu;
+      a[n1] = x & 0x00f000f0u;
+      a[n2] = y & 0x000f000fu;
       a[3] = y & 0x00f000f0u;
+    } else if constexpr (BITS == 4) {
+      a[0] = centred(w[0] & 0x000f000fu);
+      a[n1] = centred((w[0] >> 4) & 0x000f000fu);
+      a[n2] = centred((w[0] >> 8) & 0x000f000fu);
+      a[3] = centred((w[0] >> 12) & 0x000f000fu);
     } else {
       a[0] = w[0] & 0x00ff00ffu;
       a[1] = (w[0] >> 8) & 0x00ff00ffu;
       a[2] = w[1] & 0x00ff00ffu;
       a[3] = (w[1] >> 8) & 0x00ff00ffu;
+      if constexpr (SPLIT) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) a[k] = centred(a[k]);
+      }
     }
   }
 
-  static __device__ __forceinline__ void product(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                                 uint32_t b1) {
-    mma_16816<false>(d, a, b0, b1);
-  }
-
-  // One tile: tokens t0 .. t0 + 15, those in [first, L) attended.
-  __device__ __forceinline__ void tile(const QuantAttendParams &p, const char *buf, int t0,
-                                       int first, int L, int lane) {
-    const int g = lane >> 2, t = lane & 3;
-    float acc[NG][4];
-#pragma unroll
-    for (int a = 0; a < NG; ++a)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) acc[a][k] = 0.f;
-    constexpr int W = BITS / 4;  // words of a step
+  // The sums that a tile's scores are made of: x = (token g, columns 2t and 2t + 1),
+  // (token g + 8, ...).
+  __device__ __forceinline__ void sums(const char *buf, int lane, float (&x)[4]) const {
+    const int g = lane >> 2;
+    constexpr int W = BITS / 4;                                     // words of a step
+    constexpr int CH = !SPLIT ? KS / NG : KS / NG > 2 ? 2 : KS / NG;  // products of one sum
+    float acc[KS / CH][4];
 #pragma unroll
     for (int c = 0; c < Q::kWords / 4; ++c) {
       const uint4 v = reinterpret_cast<const uint4 *>(buf)[c * 32 + lane];
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int k = 0; k < 4 / W; ++k) {
-        const int s = c * (4 / W) + k;
+        const int s = c * (4 / W) + k, n = s / CH;
         uint32_t a[4];
         widen(w + k * W, false, a);
-        product(acc[s * NG / KS], a, qb[s][0], qb[s][1]);
+        if (s % CH == 0)
+          mma_f16(acc[n], a, qb[s][0], qb[s][1], 0.f, 0.f, 0.f, 0.f);
+        else
+          mma_f16(acc[n], a, qb[s][0], qb[s][1], acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
       }
     }
-    const bool edge = t0 < first || t0 + kQuantTile > L;
-    float x[4];  // (token g, columns 2t, 2t + 1), (token g + 8, ...)
-    {
-      float kl[2][NG], ks[2][NG];
-      params(buf, g, kl[0], ks[0]);
-      params(buf, g + 8, kl[1], ks[1]);
+    constexpr int PER = KS / CH / NG;  // sums of a group
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+    for (int a = 0; a < NG; ++a)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float s = 0.f;
+      for (int n = 1; n < PER; ++n)
 #pragma unroll
-          for (int a = 0; a < NG; ++a) {
-            s = fmaf(kl[r][a], qs[c][a], s);
-            s = fmaf(ks[r][a], acc[a][2 * r + c], s);
-          }
-          x[2 * r + c] = s * 0x1p24f * fac[c];
-        }
+        for (int k = 0; k < 4; ++k) acc[a * PER][k] += acc[a * PER + n][k];
+    float kl[2][NG], ks[2][NG];
+    params(buf, g, kl[0], ks[0]);
+    params(buf, g + 8, kl[1], ks[1]);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if constexpr (kMid != 0.f) {
+#pragma unroll
+        for (int a = 0; a < NG; ++a) kl[r][a] = fmaf(kMid, ks[r][a], kl[r][a]);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float s = kl[r][0] * qs[c][0];
+#pragma unroll
+        for (int a = 1; a < NG; ++a) s = fmaf(kl[r][a], qs[c][a], s);
+#pragma unroll
+        for (int a = 0; a < NG; ++a) s = fmaf(ks[r][a], acc[a * PER][2 * r + c], s);
+        x[2 * r + c] = s * fac[c];
+      }
     }
-    if (p.rule.cap_out == 0.f) {
+  }
+
+  // Scores in base-2 units from what sums() left, where more than a factor makes them; far: the
+  // tile's first token's distance.
+  __device__ __forceinline__ void rule(const QuantAttendParams &p, float far, float (&x)[4]) const {
+    if (vast) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] *= p.rule.scale_log2;
-    } else if (p.precise_cap) {
+      for (int k = 0; k < 4; ++k) x[k] *= pow2(kUnit);
+    }
+    if (p.rule.cap_out != 0.f) {
+      if (p.precise_cap) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = cap_any(p.rule, x[k]);
-    } else {
+        for (int k = 0; k < 4; ++k) x[k] = cap_any(p.rule, x[k]);
+      } else {
 #pragma unroll
-      for (int k = 0; k < 4; k += 2) {
-        const float2 y = cap_16bit(p.rule, make_float2(x[k], x[k + 1]));
-        x[k] = y.x, x[k + 1] = y.y;
+        for (int k = 0; k < 4; k += 2) {
+          const float2 y = cap_16bit(p.rule, make_float2(x[k], x[k + 1]));
+          x[k] = y.x, x[k + 1] = y.y;
+        }
       }
     }
     if (p.rule.slopes) {
-      const float far = (float)(L - 1 - t0 - g);
 #pragma unroll
       for (int k = 0; k < 4; ++k) x[k] = fmaf(-slope[k & 1], far - (k >> 1) * 8.f, x[k]);
     }
-    float vl[2][NG], vs[2][NG];
-    params(buf + Q::kHalf, g, vl[0], vs[0]);
-    params(buf + Q::kHalf, g + 8, vl[1], vs[1]);
-    if (edge) {
+  }
+
+  // A step: the tiles of tokens t0 .. t0 + 31, those in [first, end) attended (the second tile
+  // may hold none, and then anything).
+  __device__ __forceinline__ void step(const QuantAttendParams &p, const char *buf, int t0,
+                                       int first, int end, int L, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    float x[2][4], vl[2][2][NG], vs[2][2][NG];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int at = t0 + g + 8 * r;
-        if (at >= first && at < L) continue;
-        x[2 * r] = x[2 * r + 1] = -CUDART_INF_F;
+    for (int j = 0; j < 2; ++j) sums(buf + j * Q::kBytes, lane, x[j]);
+    if (!plain) {
 #pragma unroll
-        for (int a = 0; a < NG; ++a) vl[r][a] = vs[r][a] = 0.f;  // (what lies there may be anything)
-      }
+      for (int j = 0; j < 2; ++j) rule(p, (float)(L - 1 - t0 - g) - 16.f * j, x[j]);
     }
-    float z[4];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float top = vs[r][0];
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int a = 1; a < NG; ++a) top = fmaxf(top, vs[r][a]);
-      const int e = exponent(top);
-      const float down = pow2(-e);  // (e <= 125: a step is at most 2^128 / 15)
+      for (int r = 0; r < 2; ++r)
+        params(buf + j * Q::kBytes + Q::kHalf, g + 8 * r, vl[j][r], vs[j][r]);
+    if (t0 < first || t0 + 2 * kQuantTile > end) {
 #pragma unroll
-      for (int a = 0; a < NG; ++a) vs[r][a] *= down;
-      z[2 * r] = x[2 * r] + (float)e;
-      z[2 * r + 1] = x[2 * r + 1] + (float)e;
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int at = t0 + 16 * j + 8 * r + g;
+          if (at >= first && at < end) continue;
+          x[j][2 * r] = x[j][2 * r + 1] = -CUDART_INF_F;
+#pragma unroll
+          for (int a = 0; a < NG; ++a) vl[j][r][a] = vs[j][r][a] = 0.f;
+        }
     }
-    // A new reference only where a weight would leave its room: a vote in most tiles.
-    bool up = false;
+    // p, and the largest it, with the largest step, could make a weight
+    float pr[2][4], most = 0.f, pm[2] = {0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) up = up || z[k] > mz[k & 1] + kLag || x[k] > m[k & 1] + 60.f;
-    if (__any_sync(kFull, up)) {
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) pr[j][k] = ex2_approx(x[j][k] - m[k & 1]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) pm[c] = fmax3f(pm[c], pr[j][c], pr[j][2 + c]);
+#pragma unroll
+      for (int a = 0; a < NG; ++a) most = fmax3f(most, vs[j][0][a], vs[j][1][a]);
+    }
+    const float big = fmaxf(pm[0] * up[0], pm[1] * up[1]) * most;
+    // A new reference only where a weight could leave its room: a vote in most steps.
+    if (__any_sync(kFull, fmaxf(pm[0], pm[1]) > 0x1p60f || big > 32768.f)) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float a = fmaxf(m[c], fmaxf(x[c], x[2 + c])), b = fmaxf(mz[c], fmaxf(z[c], z[2 + c]));
+        float a = m[c], z = -CUDART_INF_F;
+        // z: the largest p step so far, as a power of 2
+        if (m[c] != -CUDART_INF_F) z = m[c] + (float)(kRoom - k2[c]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            a = fmaxf(a, x[j][2 * r + c]);
+            float top = vs[j][r][0];
+#pragma unroll
+            for (int n = 1; n < NG; ++n) top = fmaxf(top, vs[j][r][n]);
+            z = fmaxf(z, x[j][2 * r + c] + (float)exponent(top));
+          }
 #pragma unroll
         for (int k = 4; k < 32; k <<= 1) {
           a = fmaxf(a, __shfl_xor_sync(kFull, a, k));
-          b = fmaxf(b, __shfl_xor_sync(kFull, b, k));
+          z = fmaxf(z, __shfl_xor_sync(kFull, z, k));
         }
-        const float fa = a == m[c] ? 1.f : ex2_approx(m[c] - a);
-        const float fb = b == mz[c] ? 1.f : ex2_approx(mz[c] - b);
+        const int k = (int)fminf(fmaxf(floorf(a - z), -120.f), 115.f) + kRoom;
+        const bool same = a == m[c];
+        const float fa = same ? 1.f : ex2_approx(m[c] - a);
+        const float fb = ex2_approx((same ? 0.f : m[c] - a) + (float)(k - k2[c]));
         m[c] = a;
-        mz[c] = b;
+        k2[c] = k;
+        up[c] = pow2(k);
         l[c] *= fa;
 #pragma unroll
-        for (int k = 0; k < NG; ++k) lo[c][k] *= fa;
+        for (int n = 0; n < NG; ++n) lo[c][n] *= fa;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
           o[s][c] *= fb;
           o[s][2 + c] *= fb;
         }
       }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) pr[j][k] = ex2_approx(x[j][k] - m[k & 1]);
     }
-    float w[4];
+    uint32_t b[2][NG][2], b2[2][kTwo ? NG : 1][2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float pr = ex2_approx(x[k] - m[k & 1]);
-      w[k] = ex2_approx(z[k] - (mz[k & 1] - kShift));
-      l[k & 1] += pr;
+    for (int j = 0; j < 2; ++j) {
 #pragma unroll
-      for (int a = 0; a < NG; ++a) lo[k & 1][a] = fmaf(pr, vl[k >> 1][a], lo[k & 1][a]);
-    }
-    uint32_t b[NG][2], b2[NG][2];
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int a = 0; a < NG; ++a)
+        for (int a = 0; a < NG; ++a) {
+          if constexpr (kMid != 0.f) vl[j][r][a] = fmaf(kMid, vs[j][r][a], vl[j][r][a]);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float y0 = w[2 * r] * vs[r][a], y1 = w[2 * r + 1] * vs[r][a];
-        if constexpr (SPLIT) {
-          // high part: the first 11 bits; low part: the next 11
-          const float h0 = __uint_as_float(__float_as_uint(y0) & 0xffffe000u);
-          const float h1 = __uint_as_float(__float_as_uint(y1) & 0xffffe000u);
-          if constexpr (kTwo) {
-            b[a][r] = transpose8(pack_rz(h0, h1));
-            b2[a][r] = transpose8(pack_rz(y0 - h0, y1 - h1));
-          } else {
-            const float part = t >= 2 ? -1.f : 0.f;
-            b[a][r] = transpose8(pack_rz(fmaf(h0, part, y0), fmaf(h1, part, y1)));
-          }
-        } else {
-          b[a][r] = transpose8(pack2<__half>(y0, y1));
+          for (int c = 0; c < 2; ++c) lo[c][a] = fmaf(pr[j][2 * r + c], vl[j][r][a], lo[c][a]);
         }
+      float w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        l[k & 1] += pr[j][k];
+        w[k] = pr[j][k] * up[k & 1];
       }
 #pragma unroll
+      for (int a = 0; a < NG; ++a)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float y0 = w[2 * r] * vs[j][r][a], y1 = w[2 * r + 1] * vs[j][r][a];
+          if constexpr (SPLIT) {
+            // high part: the first 11 bits; low part: the next 11
+            const float h0 = __uint_as_float(__float_as_uint(y0) & 0xffffe000u);
+            const float h1 = __uint_as_float(__float_as_uint(y1) & 0xffffe000u);
+            if constexpr (kTwo) {
+              b[j][a][r] = transpose8(pack_rz(h0, h1));
+              b2[j][a][r] = transpose8(pack_rz(y0 - h0, y1 - h1));
+            } else {
+              const float part = t >= 2 ? -1.f : 0.f;
+              b[j][a][r] = transpose8(pack_rz(fmaf(h0, part, y0), fmaf(h1, part, y1)));
+            }
+          } else {
+            b[j][a][r] = transpose8(pack2<__half>(y0, y1));
+          }
+        }
+    }
+    // O += V weights
+    constexpr int W = BITS / 4;
+#pragma unroll
     for (int c = 0; c < Q::kWords / 4; ++c) {
-      const uint4 v = reinterpret_cast<const uint4 *>(buf + Q::kHalf)[c * 32 + lane];
-      const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+      uint32_t wd[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint4 v =
+            reinterpret_cast<const uint4 *>(buf + j * Q::kBytes + Q::kHalf)[c * 32 + lane];
+        wd[j][0] = v.x, wd[j][1] = v.y, wd[j][2] = v.z, wd[j][3] = v.w;
+      }
 #pragma unroll
       for (int k = 0; k < 4 / W; ++k) {
-        const int s = c * (4 / W) + k, a0 = s * NG / KS;
-        uint32_t a[4];
-        widen(wd + k * W, true, a);
-        product(o[s], a, b[a0][0], b[a0][1]);
-        if constexpr (kTwo) product(o[s], a, b2[a0][0], b2[a0][1]);
+        const int s = c * (4 / W) + k, n = s * NG / KS;
+        uint32_t a0[4], a1[4];
+        widen(wd[0] + k * W, true, a0);
+        widen(wd[1] + k * W, true, a1);
+        float *y = o[s], d[4];
+        if constexpr (SPLIT) {
+          mma_f16(d, a0, b[0][n][0], b[0][n][1], 0.f, 0.f, 0.f, 0.f);
+          if constexpr (kTwo) {
+            float e[4];
+            mma_f16(e, a0, b2[0][n][0], b2[0][n][1], 0.f, 0.f, 0.f, 0.f);
+            mma_f16(e, a1, b2[1][n][0], b2[1][n][1], e[0], e[1], e[2], e[3]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) y[r] += e[r];
+          }
+          mma_f16(d, a1, b[1][n][0], b[1][n][1], d[0], d[1], d[2], d[3]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) y[r] += d[r];
+        } else {
+          mma_f16(o[s], a0, b[0][n][0], b[0][n][1], y[0], y[1], y[2], y[3]);
+          mma_f16(o[s], a1, b[1][n][0], b[1][n][1], y[0], y[1], y[2], y[3]);
+        }
       }
     }
   }
 
   // The sums of what the warp saw, relative to m: l whole, o with the lowest values' part.
-  __device__ __forceinline__ void finish(int lane) {
-    (void)lane;
+  __device__ __forceinline__ void finish() {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -414,15 +529,14 @@ struct Warp {
 #pragma unroll
         for (int a = 0; a < NG; ++a) lo[c][a] += __shfl_xor_sync(kFull, lo[c][a], k);
       }
-      const float f = ex2_approx(mz[c] - m[c]);
+      const float f = pow2(-k2[c]);  // (|k| <= 126)
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           float &y = o[s][2 * r + c];
           if constexpr (kLanes) y += __shfl_xor_sync(kFull, y, 2);
-          // 2^24 of the codes (a nibble higher 2^20), 2^-11 of the weights' shift
-          y = fmaf(y * (BITS == 4 && r ? 0x1p9f : 0x1p13f), f, lo[c][s * NG / KS]);
+          y = fmaf(y * (kNibbles && r ? 0x1p20f : pow2(kUnit)), f, lo[c][s * NG / KS]);
         }
     }
   }
@@ -454,83 +568,98 @@ __device__ __forceinline__ void store_out(void *out, bool f32, size_t at, float4
 }
 
 template <typename T, int D, int BITS, int G, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kQuantPerSm)
     quant_attend_kernel(const __grid_constant__ QuantAttendParams p) {
   using S = Shape<D, BITS, G>;
   using Q = typename S::Q;
   using W = Warp<T, D, BITS, G, SPLIT>;
   extern __shared__ __align__(128) char smem[];
   char *const ring = smem;
-  char *const firsts = smem + S::kRingOrJoin;
-  uint64_t *const bars = reinterpret_cast<uint64_t *>(firsts + S::kFirst);
+  char *const firsts = p.firsts + (size_t)blockIdx.x * S::kLast;
+  uint64_t *const bars = reinterpret_cast<uint64_t *>(smem + S::kBars);
   __shared__ int unit_of[2 * kQuantWarps];  // of the warps' first and last partials, or -1
   __shared__ int last_flag;
+  __shared__ float share[2 * kQuantWarps][G];  // weights of the warps' partials
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  char *const mine = ring + warp * S::kStages * Q::kBytes;
+  char *const mine = ring + warp * S::kStages * S::kStage;
   uint64_t *const bar = bars + warp * S::kStages;
   if (lane == 0) {
     for (int k = 0; k < S::kStages; ++k) mbar_init(bar + k, 1);
     fence_mbar_init();
   }
   if (lane < 2) unit_of[2 * warp + lane] = -1;
+  const long long w0 = ((long long)blockIdx.x * kQuantWarps + warp) * p.per_warp;
+  const int from = (int)min(w0, (long long)p.total);
+  const int to = (int)min(w0 + p.per_warp, (long long)p.total);
+  Cursor at;
+  at.start(p, from, to);
+  Cursor in = at;
   __syncwarp();
   pdl_wait();
   pdl_launch_dependents();
 
-  const long long w0 = ((long long)blockIdx.x * kQuantWarps + warp) * p.per_warp;
-  const int from = (int)min(w0, (long long)p.total);
-  const int to = (int)min(w0 + p.per_warp, (long long)p.total);
-
-  // Copies: lane k holds the physical page of the unit's page `base` + k.
-  Cursor in;
-  in.start(p, from, to);
-  int page_unit = -1, base = 0, phys_lane = 0;
+  // Copies, a step's two tiles into a stage.  Lane k holds the physical page of the unit's page
+  // `base` + k.
   const int per_page = p.P / kQuantTile;
-  int page = 0, in_page = 0;
-  auto enter = [&]() {  // the unit's (or the next 32) pages, from `page` on
-    const QuantAttendSeq &s = p.seqs[in.i];
-    base = page;
-    const int blk = page + lane;
-    phys_lane = 0;
-    if (blk < p.max_pp && blk * (long long)p.P < s.L) {
-      phys_lane = p.page_table[(size_t)s.slot * p.max_pp + blk];
-      if (phys_lane < 0 || phys_lane >= p.num_phys) {
-        qd_set_err(p.err, kDevBadPhys, s.slot, blk, phys_lane);
-        phys_lane = 0;  // (read in its place: in the pool)
+  int base = 0, phys_lane = 0, run = 0, stage_in = 0, issued = 0;
+  int todo = 0, tile_in = 0, head_in = 0;  // of the unit being copied: tiles left, the next one
+  const QuantAttendSeq *seq_in = nullptr;
+  bool fresh = true;  // its pages are not known yet
+  const char *src = nullptr;
+  auto locate = [&]() {  // the next run of tiles on one page: src, run
+    const int page = tile_in / per_page, in_page = tile_in - page * per_page;
+    if (fresh || page - base >= 32) {
+      fresh = false;
+      base = page;
+      const int blk = page + lane;
+      phys_lane = 0;
+      if (blk < p.max_pp && blk * (long long)p.P < seq_in->L) {
+        phys_lane = p.page_table[(size_t)seq_in->slot * p.max_pp + blk];
+        if (phys_lane < 0 || phys_lane >= p.num_phys) {
+          qd_set_err(p.err, kDevBadPhys, seq_in->slot, blk, phys_lane);
+          phys_lane = 0;  // (read in its place: in the pool)
+        }
       }
     }
-  };
-  int issued = 0;
-  auto issue = [&]() {  // the copy of the tile at the cursor, into the next stage
-    if (in.left == 0) return;
-    const int unit = in.i * p.hkv + in.h;
-    if (unit != page_unit) {
-      const int first = p.seqs[in.i].first / kQuantTile + in.tile;
-      page_unit = unit;
-      page = first / per_page;
-      in_page = first - page * per_page;
-      enter();
-    } else if (page - base >= 32) {
-      enter();
-    }
     const int phys = __shfl_sync(kFull, phys_lane, page - base);
-    const int k = issued % S::kStages;
-    if (lane == 0) {
-      const char *src = static_cast<const char *>(p.pool) +
-                        (((size_t)phys * p.hkv + in.h) * per_page + in_page) * Q::kBytes;
-      mbar_arrive_expect_tx(bar + k, Q::kBytes);
-      bulk_load_1d(mine + k * Q::kBytes, src, Q::kBytes, bar + k);
+    src = static_cast<const char *>(p.pool) +
+          (((size_t)phys * p.hkv + head_in) * per_page + in_page) * Q::kBytes;
+    run = min(todo, per_page - in_page);
+  };
+  auto issue = [&]() {
+    if (todo == 0) {
+      if (in.left == 0) return;
+      todo = in.left;
+      seq_in = p.seqs + in.i;
+      head_in = in.h;
+      tile_in = seq_in->first / kQuantTile + in.tile;
+      fresh = true;
+      run = 0;
+      in.advance(p, todo);
     }
+    char *dst = mine + stage_in * S::kStage;
+    int want = min(2, todo);
+    if (lane == 0) mbar_arrive_expect_tx(bar + stage_in, want * Q::kBytes);
+#pragma unroll 1
+    while (want > 0) {
+      if (run == 0) locate();
+      const int n = min(want, run);
+      if (lane == 0) bulk_load_1d(dst, src, n * Q::kBytes, bar + stage_in);
+      dst += n * Q::kBytes;
+      src += n * Q::kBytes;
+      tile_in += n;
+      todo -= n;
+      run -= n;
+      want -= n;
+    }
+    stage_in = stage_in + 1 == S::kStages ? 0 : stage_in + 1;
     ++issued;
-    if (++in_page == per_page) in_page = 0, ++page;
-    in.step(p);
   };
 #pragma unroll 1
   for (int k = 0; k < S::kStages; ++k) issue();
 
-  Cursor at;
-  at.start(p, from, to);
-  int done = 0;
+  int done = 0, stage = 0;
+  uint32_t parity = 0;
   bool broken = false;
   W w;
   while (at.left > 0) {
@@ -538,26 +667,25 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool whole = at.tile == 0 && n == at.tiles;
     const int L = p.seqs[i].L, first = p.seqs[i].first;
     int t0 = (first / kQuantTile + at.tile) * kQuantTile;
+    const int end = min(L, t0 + n * kQuantTile);
     w.begin(p, i, h, lane);
 #pragma unroll 1
-    for (int k = 0; k < n; ++k, t0 += kQuantTile) {
-      const int st = done % S::kStages;
-      if (!broken && !mbar_wait(bar + st, (done / S::kStages) & 1, kWaitPolls)) {
+    for (; t0 < end; t0 += 2 * kQuantTile) {
+      if (!broken && !mbar_try_wait(bar + stage, parity) &&
+          !mbar_wait(bar + stage, parity, kWaitPolls)) {
         if (lane == 0) qd_set_err(p.err, kDevTimeout, p.seqs[i].slot, h, t0);
         broken = true;
       }
       broken = __any_sync(kFull, broken);
-      if (broken) continue;  // (nothing is read or copied any more, units still end)
-      w.tile(p, mine + st * Q::kBytes, t0, first, L, lane);
+      if (broken) break;  // (nothing is read or copied any more, units still end)
+      w.step(p, mine + stage * S::kStage, t0, first, end, L, lane);
+      if (++stage == S::kStages) stage = 0, parity ^= 1;
       ++done;
       __syncwarp();
       issue();
     }
-    at.at += n;
-    at.tile += n;
-    at.left = 0;
-    at.seek(p);
-    w.finish(lane);
+    at.advance(p, n);
+    w.finish();
     if (whole) {
       const float inv[2] = {1.f / w.l[0], 1.f / w.l[1]};
       w.rows(lane, [&](int head, int c, int ch, float4 v) {
@@ -599,17 +727,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto slot_of = [&](int k) {
     return reinterpret_cast<const float *>((k & 1 ? ring : firsts) + (k >> 1) * S::kSlot);
   };
-  float *const join = reinterpret_cast<float *>(ring + S::kLast);
+  constexpr int kSlots = 2 * kQuantWarps, kVectors = G * D / 4;
   const int per_cta = p.per_warp * kQuantWarps;
 #pragma unroll 1
-  for (int k0 = 0; k0 < 2 * kQuantWarps;) {
+  for (int k0 = 0; k0 < kSlots;) {
     const int unit = unit_of[k0];
-    int k1 = k0 + 1;
     if (unit < 0) {
-      k0 = k1;
+      ++k0;
       continue;
     }
-    while (k1 < 2 * kQuantWarps && (unit_of[k1] == unit || unit_of[k1] < 0)) ++k1;
     const int i = unit / p.hkv, h = unit - i * p.hkv;
     const QuantAttendSeq &s = p.seqs[i];
     const int u0 = s.off + h * s.stride;
@@ -617,77 +743,113 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool alone = c0 == c1;
     // this CTA's two partials: of a unit that it starts with, of one that it ends with
     auto part = [&](int c) { return 2 * c + (c > c0 || u0 == c * per_cta ? 0 : 1); };
-    const int to_slot = part(blockIdx.x);
-#pragma unroll 1
-    for (int e = threadIdx.x; e < G * D / 4; e += kThreads) {
-      const int head = e / (D / 4), ch = 4 * (e - head * (D / 4));
-      float m = -CUDART_INF_F, l = 0.f;
-      for (int k = k0; k < k1; ++k)
-        if (unit_of[k] >= 0) m = fmaxf(m, slot_of(k)[G * D + 2 * head]);
+    const size_t to_slot = part(blockIdx.x);
+    // a warp per head: the slots' weights, lane k for slot k
+    for (int head = warp; head < G; head += kQuantWarps) {
+      const bool mine = lane < kSlots && unit_of[lane < kSlots ? lane : 0] == unit;
+      const float *q = slot_of(mine ? lane : k0) + G * D + 2 * head;
+      const float m = mine ? q[0] : -CUDART_INF_F;
+      float top = m;
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, k));
+      const float f = mine ? ex2_approx(m - top) : 0.f;
+      float l = mine ? f * q[1] : 0.f;
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(kFull, l, k);
+      if (lane < kSlots) share[lane][head] = alone ? f / l : f;
+      if (!alone && lane == 0) p.part_ml[to_slot * G + head] = make_float2(top, l);
+    }
+    __syncthreads();
+    int k1 = k0 + 1;
+    while (k1 < kSlots && (unit_of[k1] == unit || unit_of[k1] < 0)) ++k1;
+    for (int e = threadIdx.x; e < kVectors; e += kThreads) {
+      const int head = e / (D / 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
       for (int k = k0; k < k1; ++k) {
         if (unit_of[k] < 0) continue;
-        const float *q = slot_of(k);
-        const float f = ex2_approx(q[G * D + 2 * head] - m);
-        const float4 y = *reinterpret_cast<const float4 *>(q + head * D + ch);
-        l = fmaf(f, q[G * D + 2 * head + 1], l);
+        const float4 y = reinterpret_cast<const float4 *>(slot_of(k))[e];
+        const float f = share[k][head];
         v.x = fmaf(f, y.x, v.x), v.y = fmaf(f, y.y, v.y);
         v.z = fmaf(f, y.z, v.z), v.w = fmaf(f, y.w, v.w);
       }
-      if (alone) {
-        const float f = 1.f / l;
-        store_out<T>(p.out, p.out_f32, ((size_t)unit * G + head) * D + ch,
-                     make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
-      } else {
-        *reinterpret_cast<float4 *>(p.part_o + ((size_t)to_slot * G + head) * D + ch) = v;
-        if (ch == 0) p.part_ml[(size_t)to_slot * G + head] = make_float2(m, l);
-      }
+      if (alone) store_out<T>(p.out, p.out_f32, (size_t)unit * G * D + 4 * e, v);
+      else reinterpret_cast<float4 *>(p.part_o + to_slot * G * D)[e] = v;
     }
     if (!alone) {
-      __threadfence();
+      // The last CTA of the unit to come joins its partials (in their order, whichever came
+      // last).  The barrier and the ticket's release publish them.
       __syncthreads();
       if (threadIdx.x == 0) {
-        const int ticket = atom_add_acq_rel_gpu(p.tickets + unit, 1);
-        last_flag = ticket == c1 - c0;
+        last_flag = atom_add_acq_rel_gpu(p.tickets + unit, 1) == c1 - c0;
         if (last_flag) p.tickets[unit] = 0;  // (for the next launch)
       }
       __syncthreads();
       if (last_flag) {
-        __threadfence();
-        const int parts = c1 - c0 + 1;
-        if (threadIdx.x < 32 * G) {  // a warp per head: the partials' weights
-          const int head = warp;
-          float m = -CUDART_INF_F, l = 0.f;
-          for (int c = lane; c < parts; c += 32)
-            m = fmaxf(m, __ldcg(&p.part_ml[(size_t)part(c0 + c) * G + head]).x);
+        // Threads in kSets sets, each with every kSets-th partial, eight loads under way.
+        constexpr int kSets = kThreads / kVectors < 1 ? 1 : kThreads / kVectors;
+        const int parts = c1 - c0 + 1, set = threadIdx.x / kVectors, e = threadIdx.x % kVectors;
+        const int head = e / (D / 4);
+        float m = -CUDART_INF_F, l = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 *const sums = reinterpret_cast<float4 *>(ring + S::kLast);
+        float2 *const stats = reinterpret_cast<float2 *>(sums + kSets * kVectors);
+        if (set < kSets) {
+#pragma unroll 1
+          for (int c = set; c < parts; c += 8 * kSets) {
+            float2 ml[8];
+            float4 y[8];
 #pragma unroll
-          for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, k));
-          for (int c = lane; c < parts; c += 32) {
-            const float2 ml = __ldcg(&p.part_ml[(size_t)part(c0 + c) * G + head]);
-            const float f = ex2_approx(ml.x - m);
-            join[c * G + head] = f;
-            l = fmaf(f, ml.y, l);
+            for (int k = 0; k < 8; ++k) {
+              const size_t from = part(c0 + min(c + k * kSets, parts - 1));
+              ml[k] = __ldcg(p.part_ml + from * G + head);
+              y[k] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + from * G * D) + e);
+            }
+            float top = m;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              if (c + k * kSets >= parts) ml[k] = make_float2(-CUDART_INF_F, 0.f);
+              top = fmaxf(top, ml[k].x);
+            }
+            const float f0 = m == top ? 1.f : ex2_approx(m - top);
+            m = top;
+            l *= f0;
+            v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              if (c + k * kSets >= parts) continue;
+              const float f = ex2_approx(ml[k].x - m);
+              l = fmaf(f, ml[k].y, l);
+              v.x = fmaf(f, y[k].x, v.x), v.y = fmaf(f, y[k].y, v.y);
+              v.z = fmaf(f, y[k].z, v.z), v.w = fmaf(f, y[k].w, v.w);
+            }
           }
-#pragma unroll
-          for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(kFull, l, k);
-          const float inv = 1.f / l;
-          for (int c = lane; c < parts; c += 32) join[c * G + head] *= inv;
+          if (kSets > 1) {
+            sums[set * kVectors + e] = v;
+            stats[set * kVectors + e] = make_float2(m, l);
+          }
         }
-        __syncthreads();
-        for (int e = threadIdx.x; e < G * D; e += kThreads) {
-          const int head = e / D, ch = e - head * D;
-          float v = 0.f;
-#pragma unroll 8
-          for (int c = 0; c < parts; ++c)
-            v = fmaf(join[c * G + head],
-                     __ldcg(p.part_o + ((size_t)part(c0 + c) * G + head) * D + ch), v);
-          const size_t to = ((size_t)unit * G + head) * D + ch;
-          if (p.out_f32) static_cast<float *>(p.out)[to] = v;
-          else static_cast<T *>(p.out)[to] = T(v);
+        if (kSets > 1) __syncthreads();
+        if (set == 0) {
+#pragma unroll
+          for (int k = 1; k < kSets; ++k) {
+            if (k >= parts) continue;
+            const float2 ml = stats[k * kVectors + e];
+            const float4 y = sums[k * kVectors + e];
+            const float top = fmaxf(m, ml.x);
+            const float f0 = m == top ? 1.f : ex2_approx(m - top), f = ex2_approx(ml.x - top);
+            m = top;
+            l = fmaf(f, ml.y, l * f0);
+            v.x = fmaf(f, y.x, v.x * f0), v.y = fmaf(f, y.y, v.y * f0);
+            v.z = fmaf(f, y.z, v.z * f0), v.w = fmaf(f, y.w, v.w * f0);
+          }
+          const float f = 1.f / l;
+          store_out<T>(p.out, p.out_f32, (size_t)unit * G * D + 4 * e,
+                       make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
         }
       }
-      __syncthreads();  // (last_flag and the weights are used again)
     }
+    __syncthreads();  // (shares, the flag and the sums are used again)
     k0 = k1;
   }
 }
@@ -695,8 +857,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 template <typename T, int D, int BITS, int G, bool SPLIT>
 cudaError_t launch_one(const QuantAttendParams &p, cudaStream_t st) {
   using S = Shape<D, BITS, G>;
-  static_assert(S::kSmem <= 113 * 1024, "two CTAs an SM");
-  static std::atomic<uint64_t> ready{0};
+    static std::atomic<uint64_t> ready{0};
   const auto kernel = quant_attend_kernel<T, D, BITS, G, SPLIT>;
   const cudaError_t e = allow_smem(kernel, S::kSmem, &ready);
   if (e != cudaSuccess) return e;
@@ -717,7 +878,7 @@ cudaError_t launch_heads(const QuantAttendParams &p, int G, cudaStream_t st) {
 // keep 22.
 template <typename T, int D, int BITS>
 cudaError_t launch_type(const QuantAttendParams &p, int G, cudaStream_t st) {
-  if constexpr (sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
     if (!p.out_f32) return launch_heads<T, D, BITS, false>(p, G, st);
   }
   return launch_heads<T, D, BITS, true>(p, G, st);

@@ -35,6 +35,7 @@ struct ScratchLayout {
   size_t part_ml;      // float2 [kMaxItems * G]   (row max in log2 units, sum)
   size_t part_o;       // float  [kMaxItems * G * d]
   size_t scores;       // float  [kSeqsPerLaunch * Hd * score_stride]
+  size_t firsts;       // quantised caches: single warps' partial sums
   size_t page_part;    // float2 [kSeqsPerLaunch * Hd * mass_tiles * G] per-tile (max, sum)
   size_t total;
 };
@@ -226,6 +227,7 @@ struct CtxView {
   int quant;          // bits of a quantised cache, or 0
   float *part_o;      // quantised: partial sums (kQuantCtas x 2)
   float2 *part_ml;
+  char *firsts;       // quantised: partial sums of single warps
 };
 // Host facts only (no device call); ctx_device fills device, num_sms and the
 // tensor maps in, setting the context up on its device the first time.

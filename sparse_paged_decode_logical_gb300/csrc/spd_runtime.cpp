@@ -156,6 +156,8 @@ const char *derive(const spd_config *c, Derived *d) {
     off = round_up(off + (size_t)kQuantCtas * 2 * d->G * 8, 256);
     sl.part_o = off;
     off = round_up(off + (size_t)kQuantCtas * 2 * d->G * c->head_dim * 4, 256);
+    sl.firsts = off;
+    off = round_up(off + (size_t)kQuantCtas * kQuantWarps * quant_slot_bytes(c->head_dim, d->G), 256);
     sl.total = off;
     z.scratch = off;
     return nullptr;
@@ -923,6 +925,7 @@ void ctx_view(spd_ctx *c, CtxView *v) {
   v->quant = c->dv.quant;
   v->part_o = c->dv.quant ? reinterpret_cast<float *>(c->scratch(c->dv.sl.part_o)) : nullptr;
   v->part_ml = c->dv.quant ? reinterpret_cast<float2 *>(c->scratch(c->dv.sl.part_ml)) : nullptr;
+  v->firsts = c->dv.quant ? c->scratch(c->dv.sl.firsts) : nullptr;
 }
 
 spd_status ctx_device(spd_ctx *c, cudaStream_t st, CtxView *v) {
