@@ -218,7 +218,8 @@ def prepare(case, seed):
     longest = max(lens) + 1
     if own:
         c = _cache(case, n, sum(-(-(x + 1) // case["page"]) for x in lens), longest)
-        s.update(cache=c, ids=[c.seq_create() for _ in lens], rule=_text_rule(d) if step else None,
+        s.update(cache=c, ids=[c.seq_create() for _ in lens], held=lens,
+                 rule=_text_rule(d) if step else None,
                  out_dtype=torch.float32 if case["out"] == "fp32" else dt)
     else:
         groups, at = (1 if case["bits"] == 8 else d // 32), []
@@ -297,7 +298,7 @@ def _step_own(s):
                            positions=s["positions"])
     out = _attend_own(s, q[:, 0])
     k, v = c.kv_read(s["ids"], begin=-1)
-    for i, x in zip(s["ids"], _lengths(s)):  # taken back, as a token that is rejected
+    for i, x in zip(s["ids"], s["held"]):  # taken back, as a token that is rejected
         c.seq_truncate(i, x)
     return out, q[:, 0], k[:, 0], v[:, 0]
 
