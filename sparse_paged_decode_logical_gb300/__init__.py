@@ -383,7 +383,12 @@ class SparsePagedKVCache:
         self._dev_index = self.device.index
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self._ids_cache = {}
-        self._step_fn = lib().spd_decode_step
+        L = lib()
+        self._step_fn = L.spd_decode_step
+        self._truncate_fn = L.spd_seq_truncate
+        self._append_rotary_fn = L.spd_kv_append_rotary
+        self._quant_attend_fn = L.spd_quant_decode_attention
+        self._length_fn, self._length = L.spd_seq_info, ctypes.c_longlong()
 
     def __del__(self):
         ctx = getattr(self, "ctx", None)
@@ -423,6 +428,12 @@ class SparsePagedKVCache:
 
     def free_pages(self):
         return spd_free_pages(self.ctx)
+
+    def _seq_length(self, seq_id):
+        st = self._length_fn(self.ctx, int(seq_id), self._length, None, None, None)
+        if st != SPD_OK:
+            _check(st, "spd_seq_info", self.ctx)
+        return self._length.value
 
     def kv_append(self, seq_ids, k, v, stream=None):
         """k, v: [n_seqs][n_tokens][Hkv][d] of the cache dtype."""
@@ -596,7 +607,11 @@ class SparsePagedKVCache:
 
     def seq_truncate(self, seq_id, n_tokens):
         """Back to the sequence's first n_tokens tokens (kv_quant)."""
-        spd_seq_truncate(self.ctx, seq_id, n_tokens)
+        if not 0 <= n_tokens <= _MAX_TOKENS:
+            spd_seq_truncate(self.ctx, seq_id, n_tokens)
+        st = self._truncate_fn(self.ctx, int(seq_id), int(n_tokens))
+        if st != SPD_OK:
+            _check(st, "spd_seq_truncate", self.ctx)
 
     def kv_append_rotary(self, seq_ids, table, q, k, v, positions=None, out=None, stream=None):
         """Append k, v [n][tokens][Hkv][d], the keys rotated on the way, and rotate
@@ -605,25 +620,28 @@ class SparsePagedKVCache:
         projection's output.  positions int32 [axes][n][tokens] ([n][tokens] with
         one axis); None: a token's place in its sequence.  `stream` as in
         :func:`prefill_attention`."""
-        t = self.torch
         ids, n = self._id_array(seq_ids)
         if k.dim() != 4:
             raise ValueError("k must be [n][tokens][Hkv][d]")
         tokens = k.shape[1]
-        qs, ks, vs = (self._rows(x, (n, tokens, h, self.d), name)
-                      for x, h, name in ((q, self.Hq, "q"), (k, self.Hkv, "k"), (v, self.Hkv, "v")))
+        qshape, kshape = (n, tokens, self.Hq, self.d), (n, tokens, self.Hkv, self.d)
+        qs = self._rows(q, qshape, "q")
+        ks = self._rows(k, kshape, "k")
+        vs = self._rows(v, kshape, "v")
         pos = None
         if positions is not None:
-            shape = (table.axes, n, tokens)
-            if positions.shape != shape and not (table.axes == 1 and positions.shape == shape[1:]):
-                raise ValueError("positions must be int32 %s" % (shape,))
-            pos = self._ptr(positions, positions.shape, t.int32)
+            if positions.shape != (table.axes, n, tokens) \
+                    and not (table.axes == 1 and positions.shape == (n, tokens)):
+                raise ValueError("positions must be int32 %s" % ((table.axes, n, tokens),))
+            pos = self._ptr(positions, positions.shape, self.torch.int32)
         if out is None:
-            out = _empty(t, (n, tokens, self.Hq, self.d), self.dtype, self.device, stream)
-        op = self._ptr(out, (n, tokens, self.Hq, self.d), self.dtype)
-        st = lib().spd_kv_append_rotary(self.ctx, table.table, ids, n, tokens, pos, q.data_ptr(), qs,
-                                        k.data_ptr(), ks, v.data_ptr(), vs, op,
-                                        self._stream(stream) or None)
+            out = _empty(self.torch, qshape, self.dtype, self.device, stream)
+            op = out.data_ptr()
+        else:
+            op = self._ptr(out, qshape, self.dtype)
+        st = self._append_rotary_fn(self.ctx, table.table, ids, n, tokens, pos, q.data_ptr(), qs,
+                                    k.data_ptr(), ks, v.data_ptr(), vs, op,
+                                    self._stream(stream) or None)
         if st != SPD_OK:
             _check(st, "spd_kv_append_rotary", self.ctx)
         return out
@@ -634,11 +652,11 @@ class SparsePagedKVCache:
             raise ValueError("%s: expected a %s tensor %s on %s, got %s %s on %s"
                              % (name, self.dtype, shape, self.device, x.dtype, tuple(x.shape), x.device))
         n, tokens, heads, d = shape
-        s = x.stride()
-        if s[3] != 1 or (heads > 1 and s[2] != d):
+        s0, s1, s2, s3 = x.stride()
+        if s3 != 1 or (heads > 1 and s2 != d):
             raise ValueError("%s: the heads of a token must be contiguous" % name)
-        stride = s[1] if tokens > 1 else s[0] if n > 1 else heads * d
-        if n > 1 and tokens > 1 and s[0] != tokens * stride:
+        stride = s1 if tokens > 1 else s0 if n > 1 else heads * d
+        if n > 1 and tokens > 1 and s0 != tokens * stride:
             raise ValueError("%s: all tokens must lie at one stride" % name)
         return stride
 
@@ -648,21 +666,20 @@ class SparsePagedKVCache:
         0, from -begin tokens before each sequence's end.  n_tokens None: all that
         the shortest sequence holds from there.  `stream` as in
         :func:`prefill_attention`."""
-        t = self.torch
         ids, n = self._id_array(seq_ids)
         begin = int(begin)
         if n_tokens is None:
-            if not n:
-                raise ValueError("no sequences")
-            n_tokens = -begin if begin < 0 else min(self.seq_info(s)["length"] for s in seq_ids) - begin
+            if begin < 0 or not n:
+                n_tokens = -begin
+            else:
+                n_tokens = min([self._seq_length(s) for s in seq_ids]) - begin
         n_tokens = int(n_tokens)
-        if n_tokens < 1 or n_tokens > _MAX_TOKENS or abs(begin) > _MAX_TOKENS:
+        # (refused before a buffer is made of that size)
+        if n_tokens < 1 or n_tokens > self.cfg.max_context or abs(begin) > _MAX_TOKENS:
             raise SpdError(4, "spd_kv_read", "begin and n_tokens must lie within the sequences")
         shape = (n, n_tokens, self.Hkv, self.d)
-        longest = max((self.seq_info(s)["length"] for s in seq_ids), default=0)
-        if n_tokens > longest:  # (refused before a buffer is made)
-            raise SpdError(4, "spd_kv_read", "a sequence does not hold all of these tokens")
-        k, v = (_empty(t, shape, self.dtype, self.device, stream) for _ in range(2))
+        k = _empty(self.torch, shape, self.dtype, self.device, stream)
+        v = _empty(self.torch, shape, self.dtype, self.device, stream)
         st = lib().spd_kv_read(self.ctx, ids, n, begin, n_tokens, k.data_ptr(), v.data_ptr(),
                                self._stream(stream) or None)
         if st != SPD_OK:
@@ -675,23 +692,27 @@ class SparsePagedKVCache:
         (kv_quant): the newest `window` tokens, or all (0).  Returns out [n][Hq][d],
         fp32 or (out_dtype) the cache's type; scale, softcap and slopes as in
         :func:`prefill_attention`, and `stream`."""
-        t = self.torch
+        f32 = self.torch.float32
         ids, n = self._id_array(seq_ids)
-        qp = self._ptr(q, (n, self.Hq, self.d), self.dtype)
+        shape = (n, self.Hq, self.d)
+        qp = self._ptr(q, shape, self.dtype)
         if out_dtype is None:
-            out_dtype = t.float32 if out is None else out.dtype
-        if out_dtype not in (t.float32, self.dtype):
+            out_dtype = f32 if out is None else out.dtype
+        if out_dtype is not self.dtype and out_dtype is not f32:
             raise ValueError("out_dtype must be torch.float32 or %s" % self.dtype)
         window = int(window)
         if window < 0:
             raise ValueError("window must be >= 0")
         if out is None:
-            out = _empty(t, (n, self.Hq, self.d), out_dtype, self.device, stream)
-        op = self._ptr(out, (n, self.Hq, self.d), out_dtype)
-        rule = _rule(scale, softcap, slopes, self.Hq, self._dev_index)
-        st = lib().spd_quant_decode_attention(self.ctx, qp, ids, n, min(window, _MAX_TOKENS), rule,
-                                              0 if out_dtype == t.float32 else 1, op,
-                                              self._stream(stream) or None)
+            out = _empty(self.torch, shape, out_dtype, self.device, stream)
+            op = out.data_ptr()
+        else:
+            op = self._ptr(out, shape, out_dtype)
+        rule = None
+        if scale or softcap or slopes is not None:
+            rule = _rule(scale, softcap, slopes, self.Hq, self._dev_index)
+        st = self._quant_attend_fn(self.ctx, qp, ids, n, min(window, _MAX_TOKENS), rule,
+                                   0 if out_dtype is f32 else 1, op, self._stream(stream) or None)
         if st != SPD_OK:
             _check(st, "spd_quant_decode_attention", self.ctx)
         return out
@@ -948,14 +969,11 @@ class Rotary:
         self.head_dim, self.rotary_dim, self.axes = int(head_dim), rotary_dim, len(sections)
 
 
-def rotary(table, positions, q, k=None, inverse=False, out=None, stream=None):
-    """Rotate q [n][Hq][d] and k [n][Hk][d] (or q alone) by the :class:`Rotary`
-    rule `table` (spd_rotary).  positions int32 [axes][n] ([n] with one axis).
-    q and k are fp16 or bf16 on one CUDA device; rows may be strided, as in a fused
-    projection's output.  inverse: back, which is also the rotation's gradient.
-    out: a tensor for the rotated q, or a pair of them; they may be q and k
-    themselves.  Returns (q, k) rotated, or q.  `stream` as in
-    :func:`prefill_attention`."""
+# What a rotary call's shapes, strides and types decide, by them: tokens, heads, strides.
+_rotary_plans = {}
+
+
+def _rotary_plan(table, positions, q, k):
     import torch
     dev = q.get_device()
     if q.dim() != 3 or q.shape[2] != table.head_dim or q.shape[0] < 1:
@@ -972,22 +990,54 @@ def rotary(table, positions, q, k=None, inverse=False, out=None, stream=None):
                 positions.shape == (table.axes, n) or (table.axes == 1 and positions.shape == (n,))):
         raise ValueError("positions must be contiguous int32 [%d][%d] on cuda:%d"
                          % (table.axes, n, dev))
-    xs = (q,) if k is None else (q, k)
+    return (torch, 1 if dt == torch.bfloat16 else 0, n, dt, q.device, tuple(q.shape),
+            _token_stride(q, "q"), None if k is None else tuple(k.shape),
+            0 if k is None else _token_stride(k, "k"))
+
+
+def rotary(table, positions, q, k=None, inverse=False, out=None, stream=None):
+    """Rotate q [n][Hq][d] and k [n][Hk][d] (or q alone) by the :class:`Rotary`
+    rule `table` (spd_rotary).  positions int32 [axes][n] ([n] with one axis).
+    q and k are fp16 or bf16 on one CUDA device; rows may be strided, as in a fused
+    projection's output.  inverse: back, which is also the rotation's gradient.
+    out: a tensor for the rotated q, or a pair of them; they may be q and k
+    themselves.  Returns (q, k) rotated, or q.  `stream` as in
+    :func:`prefill_attention`."""
+    dev = q.get_device()
+    key = (table.axes, table.head_dim, positions.shape, positions.dtype, positions.is_contiguous(),
+           positions.get_device(), dev, q.shape, q.stride(), q.dtype,
+           None if k is None else (k.shape, k.stride(), k.dtype, k.get_device()))
+    plan = _rotary_plans.get(key)
+    if plan is None:
+        plan = _rotary_plan(table, positions, q, k)
+        if len(_rotary_plans) >= 4096:
+            _rotary_plans.clear()
+        _rotary_plans[key] = plan
+    torch, code, n, dt, device, qshape, qs, kshape, ks = plan
+    d = table.head_dim
+    qo, ko, kp, kop, hk = None, None, None, None, 0
     if out is None:
-        ys = tuple(_empty(torch, tuple(x.shape), dt, x.device, stream) for x in xs)
+        qo = _empty(torch, qshape, dt, device, stream)
+        qos = qshape[1] * d
+        if kshape is not None:
+            ko = _empty(torch, kshape, dt, device, stream)
+            kos = kshape[1] * d
     else:
         ys = tuple(out) if isinstance(out, (tuple, list)) else (out,)
+        xs = (q,) if k is None else (q, k)
         if len(ys) != len(xs) or any(y.shape != x.shape or y.dtype != dt or y.get_device() != dev
                                      for x, y in zip(xs, ys)):
             raise ValueError("out must have the shapes and type of q and k")
-    args = []
-    for group in (xs, ys):
-        for i in range(2):
-            args.append((group[i].data_ptr(), _token_stride(group[i], "qk"[i]))
-                        if i < len(xs) else (None, 0))
-    raw = _raw_stream(torch, dev, stream)
-    (qp, qs), (kp, ks), (qo, qos), (ko, kos) = args
-    _check(lib().spd_rotary(table.table, 1 if dt == torch.bfloat16 else 0, n, positions.data_ptr(),
-                            qp, qs, q.shape[1], kp, ks, 0 if k is None else k.shape[1], qo, qos, ko,
-                            kos, 1 if inverse else 0, raw or None), "spd_rotary")
-    return ys[0] if k is None else ys
+        qo, qos = ys[0], _token_stride(ys[0], "out")
+        if k is not None:
+            ko, kos = ys[1], _token_stride(ys[1], "out")
+    if k is None:
+        kos = 0
+    else:
+        kp, kop, hk = k.data_ptr(), ko.data_ptr(), kshape[1]
+    st = lib().spd_rotary(table.table, code, n, positions.data_ptr(), q.data_ptr(), qs, qshape[1], kp,
+                          ks, hk, qo.data_ptr(), qos, kop, kos, 1 if inverse else 0,
+                          _raw_stream(torch, dev, stream) or None)
+    if st != SPD_OK:
+        _check(st, "spd_rotary")
+    return qo if k is None else (qo, ko)
