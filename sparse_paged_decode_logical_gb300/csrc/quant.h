@@ -48,6 +48,7 @@ inline size_t quant_tile_bytes(int d, int bits) {
 constexpr int kQuantSeqs = 256;  // sequences described per parameter block
 constexpr int kQuantCtas = 256;  // most CTAs of an attention launch
 constexpr int kQuantWarps = 12;  // per CTA
+constexpr int kQuantWriteWarps = 4;  // of a writing CTA
 constexpr int kQuantPerSm = 1;   // CTAs that an SM holds
 
 // A warp's share of a unit: [G][d] sums, [G] (reference, sum of weights).
@@ -59,11 +60,20 @@ struct RotaryParams {
   const void *q, *k;  // [n][heads][d] at strides, k may be null
   void *q_out, *k_out;
   long long q_stride, k_stride, q_out_stride, k_out_stride;  // elements between tokens
-  const int *positions;  // [axes][n]
+  const int *positions;  // [axes][axis_stride]
+  long long axis_stride;
   int n, hq, hkv, inverse;
-  int tokens_per_cta;
+  int tokens_per_cta;  // at most kRotaryTokens
 };
-cudaError_t launch_rotary(const RotaryParams &p, int dtype, cudaStream_t st);
+constexpr int kRotaryTokens = 4;
+// Tokens n_tokens by n_tokens of sequences that begin at first[i].
+struct RotaryPlaces {
+  int n_tokens;
+  int first[kQuantSeqs];
+};
+// places null: positions as p gives them
+cudaError_t launch_rotary(const RotaryParams &p, const RotaryPlaces *places, int dtype,
+                          cudaStream_t st);
 
 // ---- writing and reading back --------------------------------------------------------
 struct QuantSeq {
@@ -83,7 +93,7 @@ struct QuantAppendParams {
   int n_seqs, n_tokens, hq, hkv, P, max_pp, num_phys;
   int total_seqs;  // sequences of the whole call (positions' axes are this far apart)
   int seq0;        // sequences before this launch's
-  int rotate;
+  int rotate;      // keys, and hq heads of queries
   int tiles;       // of all sequences
   int parts;       // CTAs per tile, each with an equal share of the heads
   QuantSeq seqs[kQuantSeqs];

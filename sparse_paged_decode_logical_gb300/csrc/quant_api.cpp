@@ -38,6 +38,18 @@ spd_status need_quant(spd_ctx *c, const CtxView &v) {
   return fail_message(c, SPD_ERR_INVALID_ARG, "the context has no kv_quant");
 }
 
+// CTAs that share a tile's heads, kQuantWriteWarps at once each: as many as leave every SM a
+// few; each makes the tile's sines again.
+int parts_of(long long tiles, int works, int sms) {
+  const int most = (works + kQuantWriteWarps - 1) / kQuantWriteWarps;
+  return (int)std::max<long long>(1, std::min<long long>(most, 6LL * sms / std::max(tiles, 1LL)));
+}
+
+// A rotary launch takes up to kRotaryTokens tokens a CTA, fewer where that leaves SMs idle.
+int rotary_tokens(long long n, int sms) {
+  return (int)std::max(1LL, std::min<long long>(kRotaryTokens, n / (4 * sms)));
+}
+
 // Tiles that tokens [first, first + n) touch.
 long long tiles_of(long long first, long long n) {
   return (first + n + kQuantTile - 1) / kQuantTile - first / kQuantTile;
@@ -66,10 +78,12 @@ spd_status quant_append(spd_ctx *c, const QuantWrite &w, const int *ids, int n, 
       p.seqs[i] = QuantSeq{ids[b + i], (int)L, (int)tiles};
       tiles += tiles_of(L, n_tokens);
     }
-    const int works = 2 * cfg.num_kv_heads + (w.table ? cfg.num_q_heads : 0);
-    // few tiles: their heads go to several CTAs, each of which makes the sines again
-    const int most = (works + 7) / 8;
-    p.parts = (int)std::max<long long>(1, std::min<long long>(most, 2LL * v.num_sms / std::max(tiles, 1LL)));
+    // Queries of few tokens are rotated by the same launch, those of many by one of their own,
+    // whose threads need a third of the registers (16,385 tokens of 32 and 8 heads, 8 bits: 84 us;
+    // 125 in one launch).
+    const bool apart = w.table && tiles > 2LL * v.num_sms;
+    p.hq = w.table && !apart ? cfg.num_q_heads : 0;
+    p.parts = parts_of(tiles, cfg.num_kv_heads + p.hq, v.num_sms);
     if (tiles * p.parts > 0x7fffffffLL)
       return fail_message(c, SPD_ERR_CAPACITY, "append too large for one launch");
     if (w.table) p.table = *w.table;
@@ -86,7 +100,6 @@ spd_status quant_append(spd_ctx *c, const QuantWrite &w, const int *ids, int n, 
     p.page_table = static_cast<const int *>(v.buf->page_table);
     p.err = v.err;
     p.n_tokens = n_tokens;
-    p.hq = cfg.num_q_heads;
     p.hkv = cfg.num_kv_heads;
     p.P = cfg.physical_page;
     p.max_pp = v.max_pp;
@@ -94,8 +107,32 @@ spd_status quant_append(spd_ctx *c, const QuantWrite &w, const int *ids, int n, 
     p.total_seqs = n;
     p.seq0 = b;
     p.tiles = (int)tiles;
-    const cudaError_t e = launch_quant_append(p, cfg.dtype, cfg.head_dim, v.quant, st);
-    note_launches(c, st, 1);
+    cudaError_t e = cudaSuccess;
+    if (apart) {
+      static thread_local RotaryParams x;
+      static thread_local RotaryPlaces places;
+      const long long before = (long long)b * n_tokens, row = (long long)cfg.num_q_heads * cfg.head_dim;
+      if ((long long)p.n_seqs * n_tokens > 0x7fffffffLL)
+        return fail_message(c, SPD_ERR_CAPACITY, "append too large for one launch");
+      x.table = *w.table;
+      x.q = static_cast<const char *>(w.q) + 2 * before * w.q_stride;
+      x.q_out = static_cast<char *>(w.q_out) + 2 * before * row;
+      x.q_stride = w.q_stride;
+      x.q_out_stride = row;
+      x.positions = w.positions ? w.positions + before : nullptr;
+      x.axis_stride = (long long)n * n_tokens;
+      x.n = p.n_seqs * n_tokens;
+      x.hq = cfg.num_q_heads;
+      x.tokens_per_cta = rotary_tokens(x.n, v.num_sms);
+      places.n_tokens = n_tokens;
+      for (int i = 0; i < p.n_seqs; ++i) places.first[i] = p.seqs[i].first;
+      e = launch_rotary(x, w.positions ? nullptr : &places, cfg.dtype, st);
+      note_launches(c, st, 1);
+    }
+    if (e == cudaSuccess) {
+      e = launch_quant_append(p, cfg.dtype, cfg.head_dim, v.quant, st);
+      note_launches(c, st, 1);
+    }
     if (e != cudaSuccess) return fail_message(c, SPD_ERR_CUDA, cudaGetErrorString(e));
   }
   return SPD_OK;
@@ -186,10 +223,10 @@ spd_status spd_rotary(const spd_rotary_table *table, spd_dtype dtype, int n_toke
   p.hq = q_heads;
   p.hkv = hkv;
   p.inverse = inverse;
-  // few tokens: one per CTA; many: up to 8, which share the set-up
-  p.tokens_per_cta = std::max(1, std::min(8, n_tokens / (4 * sm_count(device))));
+  p.axis_stride = n_tokens;
+  p.tokens_per_cta = rotary_tokens(n_tokens, sm_count(device));
   const cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = launch_rotary(p, dtype, st);
+  const cudaError_t e = launch_rotary(p, nullptr, dtype, st);
   note_prompt_launch(st);
   return e == cudaSuccess ? SPD_OK : SPD_ERR_CUDA;
 }

@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "ptx.cuh"
@@ -64,147 +65,207 @@ __device__ __forceinline__ uint32_t join(uint32_t e, int lane_mask) {
   return min2_nan<T>(e, __shfl_xor_sync(kFull, e, lane_mask));
 }
 
+// The code of a distance d from lo, given one that may be one off: (code + 1/2) step is an exact
+// product.  Apart, and in a loop over four: 1 warp in 5 comes here in bf16, and copies in every
+// place would fill the instruction cache.
+__device__ __noinline__ uint32_t exact_codes(float2 a, float2 b, float step, uint32_t codes) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float d = i == 0 ? a.x : i == 1 ? a.y : i == 2 ? b.x : b.y;
+    const int c = (int)(codes >> (8 * i) & 255u);
+    const float over = ((float)c + 0.5f) * step, under = ((float)c - 0.5f) * step;
+    const bool odd = c & 1;
+    const int n = c + (d > over || (d == over && odd) ? 1 : 0) -
+                  (d < under || (d == under && odd) ? 1 : 0);
+    r |= (uint32_t)(n & 255) << (8 * i);
+  }
+  return r;
+}
+
 // What a group's codes are made with.
 template <typename T, int LEVELS>
 struct Scale {
   uint32_t bits;  // lo, step: as stored
   float lo, step, inv;
+  bool tiny;  // step below 2^-100: everything times 2^100
 
   __device__ __forceinline__ explicit Scale(uint32_t e) {  // (lowest, -highest)
     const float2 x = unpack2<T>(e);
     const float span = -x.y - x.x;
     lo = x.x;
+    tiny = false;
     if (!(span <= 3.402823466e38f)) {
       bits = 0x7fffu;  // NaN in either type, step 0
       lo = __uint_as_float(0x7fffffffu);
       step = inv = 0.f;
       return;
     }
-    uint32_t h = pack2<T>(__fdiv_rn(span, (float)LEVELS), 0.f) & 0xffffu;
+    // The least number of T that reaches: products with it are exact (11 + 8 bits).
+    uint32_t h = pack2<T>(span * (1.f / LEVELS), 0.f) & 0xffffu;
     step = unpack2<T>(h).x;
-    if (step * (float)LEVELS < span) {  // (the product is exact: 11 + 8 bits)
-      ++h;
-      step = unpack2<T>(h).x;
+    if (step * (float)LEVELS < span) {
+      step = unpack2<T>(++h).x;
+    } else if (h > 0) {
+      const float less = unpack2<T>(h - 1).x;
+      if (less * (float)LEVELS >= span) --h, step = less;
     }
     bits = (e & 0xffffu) | h << 16;
-    inv = step > 0.f ? __fdiv_rn(1.f, step) : 0.f;
+    tiny = step < 0x1p-100f;
+    if (tiny) {
+      lo *= 0x1p100f;
+      step *= 0x1p100f;
+    }
+    inv = step > 0.f ? rcp_near(step) : 0.f;
   }
-  // round((x - lo) / step).  The product with 1 / step is off by at most 3 2^-24 of a
-  // quotient of at most 255; what lies within 1e-3 of the middle between two codes is
-  // divided.  (bf16 steps below 2^-126 have no finite fp32 reciprocal: divided, too.)
-  __device__ __forceinline__ uint32_t code(float x) const {
-    const float d = x - lo, t = d * inv;
-    float n = rintf(t);
-    if (!(fabsf(t - n) < 0.499f) && step > 0.f) n = rintf(__fdiv_rn(d, step));
-    return (uint32_t)__float2int_rn(n) & (uint32_t)LEVELS;
+  static __device__ __forceinline__ float rcp_near(float x) {  // within 2^-23
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+  }
+  // round((x - lo) / step), ties to even, of the four channels of a pair of words: bytes.  The
+  // product with 1 / step is off by less than 2^-21 of a quotient of at most LEVELS; where one
+  // lies closer than that to the middle between two codes, exact_code decides.  (In bf16 that is
+  // common, values and steps have 8 bits.)  Rounded by adding 1.5 2^23, whose low bits then are
+  // the code: a conversion to an integer runs at a quarter of the rate.
+  __device__ __forceinline__ uint32_t codes(uint32_t v0, uint32_t v1) const {
+    constexpr float kMagic = 12582912.f, kNear = 0.5f - LEVELS * 0x1p-21f;
+    const float2 l = make_float2(lo, lo), r = make_float2(inv, inv), m = make_float2(kMagic, kMagic);
+    float2 a = unpack2<T>(v0), b = unpack2<T>(v1);
+    if (tiny) {
+      a = f2_mul(a, make_float2(0x1p100f, 0x1p100f));
+      b = f2_mul(b, make_float2(0x1p100f, 0x1p100f));
+    }
+    a = f2_sub(a, l);
+    b = f2_sub(b, l);
+    const float2 ta = f2_mul(a, r), tb = f2_mul(b, r), ya = f2_add(ta, m), yb = f2_add(tb, m);
+    const float2 ea = f2_sub(ta, f2_sub(ya, m)), eb = f2_sub(tb, f2_sub(yb, m));
+    const float near = fmaxf(fmax3f(fabsf(ea.x), fabsf(ea.y), fabsf(eb.x)), fabsf(eb.y));
+    const uint32_t c = bytes(ya.x, ya.y, yb.x, yb.y);
+    return near >= kNear ? exact_codes(a, b, step, c) : c;
+  }
+  static __device__ __forceinline__ uint32_t bytes(float a, float b, float c, float d) {
+    return __byte_perm(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040),
+                       __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040), 0x5410);
   }
 };
 
 // ---- whole tiles -------------------------------------------------------------------
-// x[token][grp][..]: the lane's channels (quant.h) of its tokens.
+// From the rows of 16 tokens in shared memory.  The loops over groups stay loops: unrolled, the
+// kernel waits for its instructions.
 template <typename T, int D, int BITS>
-__device__ __forceinline__ void put_k(char *half, int lane, const uint4 (&x)[2][D / 32]) {
+__device__ __forceinline__ void put_param(char *half, int token, int group, uint32_t bits) {
   using Q = QuantTile<D, BITS>;
+  uint16_t *par = reinterpret_cast<uint16_t *>(half + Q::kCodes + token * Q::kTokenParams) + group;
+  par[0] = (uint16_t)bits;
+  par[Q::kGroups] = (uint16_t)(bits >> 16);
+}
+
+template <typename T, int D, int BITS>
+__device__ __forceinline__ void put_k(char *half, int lane, const T *rows, int stride) {
+  using Q = QuantTile<D, BITS>;
+  using S = Scale<T, Q::kLevels>;
   const int g = lane >> 2, t = lane & 3;
-  uint32_t w[Q::kWords];
-  uint32_t e[2][D / 32];
+  rows += g * stride + 8 * t;
+  auto piece = [&](int r, int b) {  // token g + 8r, the lane's 8 channels of 32
+    return *reinterpret_cast<const uint4 *>(rows + 8 * r * stride + 32 * b);
+  };
+  auto span = [&](uint4 x) {
+    const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+    return extremes<T>(v);
+  };
+  auto scale = [&](uint32_t e, int r, int group) {
+    const S s(join<T>(join<T>(e, 1), 2));
+    if (t == 0) put_param<T, D, BITS>(half, g + 8 * r, group, s.bits);
+    return s;
+  };
+  if constexpr (BITS == 8) {
+    uint32_t e0 = span(piece(0, 0)), e1 = span(piece(1, 0));
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
-#pragma unroll
-    for (int a = 0; a < D / 32; ++a) {
-      const uint32_t v[4] = {x[r][a].x, x[r][a].y, x[r][a].z, x[r][a].w};
-      e[r][a] = extremes<T>(v);
+    for (int b = 1; b < D / 32; ++b) {
+      e0 = min2_nan<T>(e0, span(piece(0, b)));
+      e1 = min2_nan<T>(e1, span(piece(1, b)));
     }
-#pragma unroll
-  for (int i = 0; i < Q::kWords; ++i) w[i] = 0;
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    if constexpr (BITS == 8) {
-#pragma unroll
-      for (int a = 1; a < D / 32; ++a) e[r][0] = min2_nan<T>(e[r][0], e[r][a]);
+    const S s0 = scale(e0, 0, 0), s1 = scale(e1, 1, 0);
+#pragma unroll 1
+    for (int b = 0; b < D / 32; ++b) {
+      const uint4 x = piece(0, b), y = piece(1, b);
+      const uint32_t x0 = s0.codes(x.x, x.y), x1 = s0.codes(x.z, x.w);
+      const uint32_t y0 = s1.codes(y.x, y.y), y1 = s1.codes(y.z, y.w);
+      reinterpret_cast<uint4 *>(half)[b * 32 + lane] =
+          make_uint4(__byte_perm(x0, y0, 0x5140), __byte_perm(x0, y0, 0x7362),
+                     __byte_perm(x1, y1, 0x5140), __byte_perm(x1, y1, 0x7362));
     }
-    uint16_t *par = reinterpret_cast<uint16_t *>(half + Q::kCodes + (g + 8 * r) * Q::kTokenParams);
-#pragma unroll
-    for (int a = 0; a < Q::kGroups; ++a) {
-      const Scale<T, Q::kLevels> s(join<T>(join<T>(e[r][a], 1), 2));
-      if (t == 0) {
-        par[a] = (uint16_t)s.bits;
-        par[Q::kGroups + a] = (uint16_t)(s.bits >> 16);
-      }
-#pragma unroll
-      for (int b = a * Q::kGroup / 32; b < (a + 1) * Q::kGroup / 32; ++b) {
-        const uint32_t v[4] = {x[r][b].x, x[r][b].y, x[r][b].z, x[r][b].w};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {  // k-step 2b + i: four channels
-          const float2 p = unpack2<T>(v[2 * i]), q = unpack2<T>(v[2 * i + 1]);
-          const uint32_t c0 = s.code(p.x), c1 = s.code(p.y), c2 = s.code(q.x), c3 = s.code(q.y);
-          if constexpr (BITS == 4) {
-            w[2 * b + i] |= (c0 | c2 << 4 | c1 << 16 | c3 << 20) << (8 * r);
-          } else {
-            w[2 * (2 * b + i)] |= (c0 | c1 << 16) << (8 * r);
-            w[2 * (2 * b + i) + 1] |= (c2 | c3 << 16) << (8 * r);
-          }
-        }
-      }
+  } else {
+#pragma unroll 1
+    for (int b = 0; b < D / 32; ++b) {
+      const uint4 x = piece(0, b), y = piece(1, b);
+      const S s0 = scale(span(x), 0, b), s1 = scale(span(y), 1, b);
+      // (codes 0 and 2 in one byte, 1 and 3 in the next)
+      auto nibbles = [](uint32_t c) { return c | c >> 12; };
+      const uint32_t x0 = nibbles(s0.codes(x.x, x.y)), x1 = nibbles(s0.codes(x.z, x.w));
+      const uint32_t y0 = nibbles(s1.codes(y.x, y.y)), y1 = nibbles(s1.codes(y.z, y.w));
+      reinterpret_cast<uint2 *>(half)[((b >> 1) * 32 + lane) * 2 + (b & 1)] =
+          make_uint2(__byte_perm(x0, y0, 0x5140), __byte_perm(x1, y1, 0x5140));
     }
   }
-#pragma unroll
-  for (int i = 0; i < Q::kWords / 4; ++i)
-    reinterpret_cast<uint4 *>(half)[i * 32 + lane] =
-        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
 // Tokens 2t, 2t + 1, 2t + 8, 2t + 9.
 __device__ __forceinline__ int v_token(int t, int i) { return 2 * t + (i & 1) + 8 * (i >> 1); }
 
 template <typename T, int D, int BITS>
-__device__ __forceinline__ void put_v(char *half, int lane, const uint2 (&x)[4][D / 32]) {
+__device__ __forceinline__ void put_v(char *half, int lane, const T *rows, int stride) {
   using Q = QuantTile<D, BITS>;
+  using S = Scale<T, Q::kLevels>;
   const int g = lane >> 2, t = lane & 3;
-  uint32_t w[Q::kWords];
+  rows += 2 * t * stride + 4 * g;
+  auto piece = [&](int r, int b) {  // token v_token(t, r), the lane's 4 channels of 32
+    return *reinterpret_cast<const uint2 *>(rows + ((r & 1) + 8 * (r >> 1)) * stride + 32 * b);
+  };
+  auto span = [&](uint2 x) {
+    const uint32_t v[2] = {x.x, x.y};
+    return extremes<T>(v);
+  };
+  auto scale = [&](uint32_t e, int r, int group) {
+    const S s(join<T>(join<T>(join<T>(e, 4), 8), 16));
+    if (g == 0) put_param<T, D, BITS>(half, v_token(t, r), group, s.bits);
+    return s;
+  };
+  if constexpr (BITS == 8) {
+    uint32_t e[4];
 #pragma unroll
-  for (int i = 0; i < Q::kWords; ++i) w[i] = 0;
+    for (int r = 0; r < 4; ++r) {
+      e[r] = span(piece(r, 0));
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    uint32_t e[D / 32];
-#pragma unroll
-    for (int a = 0; a < D / 32; ++a) {
-      const uint32_t v[2] = {x[r][a].x, x[r][a].y};
-      e[a] = extremes<T>(v);
+      for (int b = 1; b < D / 32; ++b) e[r] = min2_nan<T>(e[r], span(piece(r, b)));
     }
-    if constexpr (BITS == 8) {
-#pragma unroll
-      for (int a = 1; a < D / 32; ++a) e[0] = min2_nan<T>(e[0], e[a]);
+    const S s0 = scale(e[0], 0, 0), s1 = scale(e[1], 1, 0), s2 = scale(e[2], 2, 0),
+            s3 = scale(e[3], 3, 0);
+#pragma unroll 1
+    for (int b = 0; b < D / 32; ++b) {
+      const uint2 x0 = piece(0, b), x1 = piece(1, b), x2 = piece(2, b), x3 = piece(3, b);
+      const uint32_t c0 = s0.codes(x0.x, x0.y), c1 = s1.codes(x1.x, x1.y);
+      const uint32_t c2 = s2.codes(x2.x, x2.y), c3 = s3.codes(x3.x, x3.y);
+      reinterpret_cast<uint4 *>(half)[b * 32 + lane] =
+          make_uint4(__byte_perm(c0, c1, 0x5410), __byte_perm(c2, c3, 0x5410),
+                     __byte_perm(c0, c1, 0x7632), __byte_perm(c2, c3, 0x7632));
     }
-    uint16_t *par =
-        reinterpret_cast<uint16_t *>(half + Q::kCodes + v_token(t, r) * Q::kTokenParams);
-    const int at = ((r & 1) << 4) | ((r >> 1) << 3);  // 4 bits: bit of the token's byte
+  } else {
+#pragma unroll 1
+    for (int b = 0; b < D / 32; ++b) {
+      uint32_t c[4];
 #pragma unroll
-    for (int a = 0; a < Q::kGroups; ++a) {
-      const Scale<T, Q::kLevels> s(join<T>(join<T>(join<T>(e[a], 4), 8), 16));
-      if (g == 0) {
-        par[a] = (uint16_t)s.bits;
-        par[Q::kGroups + a] = (uint16_t)(s.bits >> 16);
+      for (int r = 0; r < 4; ++r) {
+        const uint2 x = piece(r, b);
+        c[r] = scale(span(x), r, b).codes(x.x, x.y);
+        c[r] |= c[r] >> 4;  // (channels 0 and 1 in byte 0, 2 and 3 in byte 2)
       }
-#pragma unroll
-      for (int b = a * Q::kGroup / 32; b < (a + 1) * Q::kGroup / 32; ++b) {
-        const uint32_t v[2] = {x[r][b].x, x[r][b].y};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {  // m-tile 2b + i: two channels
-          const float2 p = unpack2<T>(v[i]);
-          const uint32_t c0 = s.code(p.x), c1 = s.code(p.y);
-          if constexpr (BITS == 4)
-            w[2 * b + i] |= (c0 | c1 << 4) << at;
-          else
-            w[2 * (2 * b + i) + (r >> 1)] |= (c0 | c1 << 8) << (16 * (r & 1));
-        }
-      }
+      const uint32_t a = __byte_perm(c[0], c[2], 0x6240), d = __byte_perm(c[1], c[3], 0x6240);
+      reinterpret_cast<uint2 *>(half)[((b >> 1) * 32 + lane) * 2 + (b & 1)] =
+          make_uint2(__byte_perm(a, d, 0x5410), __byte_perm(a, d, 0x7632));
     }
   }
-#pragma unroll
-  for (int i = 0; i < Q::kWords / 4; ++i)
-    reinterpret_cast<uint4 *>(half)[i * 32 + lane] =
-        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
 // ---- single tokens -----------------------------------------------------------------
@@ -221,42 +282,38 @@ __device__ __forceinline__ void put_row(char *half, int lane, int r, bool is_v, 
   for (int m = 1; m < Q::kGroup / 4; m <<= 1) e = join<T>(e, m);
   const Scale<T, Q::kLevels> s(e);
   if (lane >= D / 4) return;
-  uint16_t *par = reinterpret_cast<uint16_t *>(half + Q::kCodes + r * Q::kTokenParams);
-  if (i % (Q::kGroup / 4) == 0) {
-    const int a = i / (Q::kGroup / 4);
-    par[a] = (uint16_t)s.bits;
-    par[Q::kGroups + a] = (uint16_t)(s.bits >> 16);
-  }
-  const float2 p = unpack2<T>(x.x), q = unpack2<T>(x.y);
-  const uint32_t c0 = s.code(p.x), c1 = s.code(p.y), c2 = s.code(q.x), c3 = s.code(q.y);
+  if (i % (Q::kGroup / 4) == 0) put_param<T, D, BITS>(half, r, i / (Q::kGroup / 4), s.bits);
+  const uint32_t c = s.codes(x.x, x.y);
   auto word = [&](int w, int of) {  // byte address of word w of lane `of`
     return half + ((size_t)((w >> 2) * 32 + of) * 4 + (w & 3)) * 4;
   };
   if (!is_v) {
-    // channels 4i ..: k-step s, lane t of the row's eight
+    // channels 4i ..: k-step, lane t of the row's eight
     const int step = 2 * (i >> 3) + (i & 1), of = 4 * (r & 7) + ((i & 7) >> 1), b = r >> 3;
     if constexpr (BITS == 4) {
+      const uint32_t n = c | c >> 12;
       char *w = word(step, of);
-      w[b] = (char)(c0 | c2 << 4);
-      w[b + 2] = (char)(c1 | c3 << 4);
+      w[b] = (char)n;
+      w[b + 2] = (char)(n >> 8);
     } else {
       char *w = word(2 * step, of), *w1 = word(2 * step + 1, of);
-      w[b] = (char)c0;
-      w[b + 2] = (char)c1;
-      w1[b] = (char)c2;
-      w1[b + 2] = (char)c3;
+      w[b] = (char)c;
+      w[b + 2] = (char)(c >> 8);
+      w1[b] = (char)(c >> 16);
+      w1[b + 2] = (char)(c >> 24);
     }
   } else {
     const int j = 2 * (i >> 3), of = 4 * (i & 7) + ((r & 7) >> 1), odd = r & 1, up = r >> 3;
     if constexpr (BITS == 4) {
-      word(j, of)[2 * odd + up] = (char)(c0 | c1 << 4);
-      word(j + 1, of)[2 * odd + up] = (char)(c2 | c3 << 4);
+      const uint32_t n = c | c >> 4;
+      word(j, of)[2 * odd + up] = (char)n;
+      word(j + 1, of)[2 * odd + up] = (char)(n >> 16);
     } else {
       char *w = word(2 * j + up, of), *w1 = word(2 * (j + 1) + up, of);
-      w[2 * odd] = (char)c0;
-      w[2 * odd + 1] = (char)c1;
-      w1[2 * odd] = (char)c2;
-      w1[2 * odd + 1] = (char)c3;
+      w[2 * odd] = (char)c;
+      w[2 * odd + 1] = (char)(c >> 8);
+      w1[2 * odd] = (char)(c >> 16);
+      w1[2 * odd + 1] = (char)(c >> 24);
     }
   }
 }
@@ -282,19 +339,50 @@ __device__ __forceinline__ char *tile_at(const void *pool, const int *page_table
 }
 
 // ---- write ---------------------------------------------------------------------------
-// A CTA takes one tile's tokens and every parts-th of the heads: K and V of a head are a
-// warp's work each, and so are a query head's rows when positions are applied.
-constexpr int kWriteWarps = 8;
-constexpr int kPad = 8;  // 16-bit elements behind a rotated row in shared memory
+constexpr int kWriteWarps = kQuantWriteWarps;
+constexpr int kPad = 8;  // 16-bit elements behind a row in shared memory: rows start at other banks
 
+// A head's rows of n tokens, rotated, a warp's.
+template <typename T, typename Src, typename Dst>
+__device__ __forceinline__ void rotate_rows(const RotaryShape &shape, int n, const float2 *cs,
+                                            int lane, Src src, Dst dst) {
+  const int units = shape.units(), all = n * units;
+  const unsigned per = (65536u + units - 1) / units;  // u / units = u per / 2^16 for u <= 256
+#pragma unroll 2
+  for (int u = lane; u < all; u += 32) {
+    const int t = (int)((unsigned)u * per >> 16);
+    RotaryUnit<T> x;
+    x.load(shape, src(t), u - t * units);
+    x.turn(shape, cs + t * sine_stride(shape.rot));
+    x.store(dst(t));
+  }
+}
+
+// Rows of n tokens into a warp's buffer by asynchronous copies, which cost no registers while
+// they are under way.
+template <typename T, int D>
+__device__ __forceinline__ void stage_rows(T *buf, const T *src, long long stride, int n, int lane) {
+  constexpr int kChunks = D / 8;  // 16-byte pieces of a row
+#pragma unroll
+  for (int k = 0; k < kQuantTile * kChunks / 32; ++k) {
+    const int i = lane + 32 * k, t = i / kChunks, c = i % kChunks;
+    if (t < n)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(buf + t * (D + kPad) + 8 * c)),
+                   "l"(src + t * stride + 8 * c)
+                   : "memory");
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// A CTA takes one tile's tokens and every parts-th of the heads: K and V of a head are one
+// warp's work, and so are a query head's rows when positions are applied.  Keys are on their way
+// to shared memory, where they are rotated, while the sines are made and the values done.
 template <typename T, int D, int BITS, bool ROT>
-__global__ void __launch_bounds__(kWriteWarps * 32)
+__global__ void __launch_bounds__(kWriteWarps * 32, 5)
     quant_append_kernel(const __grid_constant__ QuantAppendParams p) {
   using Q = QuantTile<D, BITS>;
-  __shared__ __align__(16) float2 cs[ROT ? kQuantTile * D / 2 : 1];
-  __shared__ __align__(16) T rows[ROT ? kWriteWarps : 1][ROT ? kQuantTile * (D + kPad) : 1];
-  pdl_wait();
-  pdl_launch_dependents();
+  extern __shared__ __align__(16) char smem[];  // rows of K and V of every warp, the sines
+  float2 *const cs = reinterpret_cast<float2 *>(smem + kWriteWarps * 2 * kQuantTile * (D + kPad) * 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int item = blockIdx.x / p.parts, part = blockIdx.x - item * p.parts;
   int i = 0;
@@ -308,89 +396,75 @@ __global__ void __launch_bounds__(kWriteWarps * 32)
   const int a = max(t0, s.first), b = min(t0 + kQuantTile, s.first + p.n_tokens), n = b - a;
   const long long tok0 = (long long)(p.seq0 + i) * p.n_tokens + (a - s.first);  // of the call
   const RotaryShape shape{D, ROT ? p.table.rotary_dim : 0, ROT ? p.table.neighbours : 0};
-  const int pairs = shape.rot >> 1;
+  T *const mine = reinterpret_cast<T *>(smem) + warp * 2 * kQuantTile * (D + kPad);
+  pdl_wait();
+  pdl_launch_dependents();
+  T *const mine_v = mine + kQuantTile * (D + kPad);
+  auto load = [&](int h) {
+    stage_rows<T, D>(mine_v, static_cast<const T *>(p.v) + tok0 * p.v_stride + h * D, p.v_stride, n, lane);
+    stage_rows<T, D>(mine, static_cast<const T *>(p.k) + tok0 * p.k_stride + h * D, p.k_stride, n, lane);
+  };
+  int h = part * kWriteWarps + warp;
+  const int step = p.parts * kWriteWarps;
+  if (h < p.hkv) load(h);
   if constexpr (ROT) {
-    for (int e = threadIdx.x; e < n * pairs; e += kWriteWarps * 32) {
-      const int t = e / pairs, j = e - t * pairs;
-      const int pos = p.positions
-                          ? p.positions[(long long)p.table.axis[j] * p.total_seqs * p.n_tokens + tok0 + t]
-                          : a + t;
-      cs[e] = turn_of(pos, p.table.turns[j]);
-    }
+    const long long axis_stride = (long long)p.total_seqs * p.n_tokens;
+    make_sines<kWriteWarps * 32>(p.table, n, 0, cs, [&](int axis, int k) {
+      return p.positions ? p.positions[axis * axis_stride + tok0 + k] : a + k;
+    });
     __syncthreads();
   }
-  const int units = shape.units();
-  const int works = 2 * p.hkv + (ROT ? p.hq : 0);
-  for (int w = part * kWriteWarps + warp; w < works; w += p.parts * kWriteWarps) {
-    if (w >= 2 * p.hkv) {  // a query head's rows
-      const int h = w - 2 * p.hkv;
-      for (int u = lane; u < n * units; u += 32) {
-        const int t = u / units;
-        RotaryUnit<T> x;
-        x.load(shape, static_cast<const T *>(p.q) + (tok0 + t) * p.q_stride + h * D, u - t * units);
-        x.turn(shape, cs + t * pairs);
-        x.store(static_cast<T *>(p.q_out) + ((tok0 + t) * p.hq + h) * D);
-      }
-      continue;
-    }
-    const bool is_v = w >= p.hkv;
-    const int h = is_v ? w - p.hkv : w;
+#pragma unroll 1
+  for (; h < p.hkv; h += step) {
     char *tile = tile_at<Q::kBytes>(p.pool, p.page_table, s.slot, t0, h, p.hkv, p.P, p.max_pp,
                                     p.num_phys, p.err);
-    if (!tile) continue;
-    char *half = tile + (is_v ? Q::kHalf : 0);
-    const T *src = is_v ? static_cast<const T *>(p.v) + tok0 * p.v_stride + h * D
-                        : static_cast<const T *>(p.k) + tok0 * p.k_stride + h * D;
-    long long stride = is_v ? p.v_stride : p.k_stride;
-    if (ROT && !is_v) {
-      T *mine = rows[ROT ? warp : 0];
-      __syncwarp();  // (the tile before has been read)
-      for (int u = lane; u < n * units; u += 32) {
-        const int t = u / units;
-        RotaryUnit<T> x;
-        x.load(shape, src + t * stride, u - t * units);
-        x.turn(shape, cs + t * pairs);
-        x.store(mine + t * (D + kPad));
-      }
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncwarp();
+    if (tile) {
+      if (n == kQuantTile)
+        put_v<T, D, BITS>(tile + Q::kHalf, lane, mine_v, D + kPad);
+      else
+        for (int k = 0; k < n; ++k)
+          put_row<T, D, BITS>(tile + Q::kHalf, lane, a - t0 + k, true, mine_v + k * (D + kPad));
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+    if (ROT) {
+      rotate_rows<T>(
+          shape, n, cs, lane, [&](int k) { return mine + k * (D + kPad); },
+          [&](int k) { return mine + k * (D + kPad); });
       __syncwarp();
-      src = mine;
-      stride = D + kPad;
     }
-    if (n == kQuantTile) {
-      const int g = lane >> 2, t = lane & 3;
-      if (is_v) {
-        uint2 x[4][D / 32];
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c)
-            x[r][c] = *reinterpret_cast<const uint2 *>(src + v_token(t, r) * stride + 32 * c + 4 * g);
-        put_v<T, D, BITS>(half, lane, x);
-      } else {
-        uint4 x[2][D / 32];
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c)
-            x[r][c] = *reinterpret_cast<const uint4 *>(src + (g + 8 * r) * stride + 32 * c + 8 * t);
-        put_k<T, D, BITS>(half, lane, x);
-      }
-    } else {
-      for (int t = 0; t < n; ++t)
-        put_row<T, D, BITS>(half, lane, a - t0 + t, is_v, src + t * stride);
+    if (tile) {
+      if (n == kQuantTile)
+        put_k<T, D, BITS>(tile, lane, mine, D + kPad);
+      else
+        for (int k = 0; k < n; ++k)
+          put_row<T, D, BITS>(tile, lane, a - t0 + k, false, mine + k * (D + kPad));
     }
+    __syncwarp();
+    if (h + step < p.hkv) load(h + step);
+  }
+  if constexpr (ROT) {
+    for (h -= p.hkv; h < p.hq; h += step)  // query heads
+      rotate_rows<T>(
+          shape, n, cs, lane,
+          [&](int k) { return static_cast<const T *>(p.q) + (tok0 + k) * p.q_stride + h * D; },
+          [&](int k) { return static_cast<T *>(p.q_out) + ((tok0 + k) * p.hq + h) * D; });
   }
 }
 
 // ---- read ----------------------------------------------------------------------------
+constexpr int kReadWarps = 8;
+
 template <typename T, int D, int BITS>
-__global__ void __launch_bounds__(kWriteWarps * 32)
+__global__ void __launch_bounds__(kReadWarps * 32)
     quant_read_kernel(const __grid_constant__ QuantReadParams p) {
   using Q = QuantTile<D, BITS>;
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const long long job = (long long)blockIdx.x * kWriteWarps + (threadIdx.x >> 5);
+  const long long job = (long long)blockIdx.x * kReadWarps + (threadIdx.x >> 5);
   const int works = 2 * p.hkv;
   const int item = (int)(job / works), w = (int)(job - (long long)item * works);
   if (item >= p.tiles) return;
@@ -484,17 +558,24 @@ __global__ void __launch_bounds__(kWriteWarps * 32)
   }
 }
 
+template <typename T, int D, int BITS, bool ROT>
+cudaError_t append_one(const QuantAppendParams &p, cudaStream_t st) {
+  constexpr int smem = kWriteWarps * 2 * kQuantTile * (D + kPad) * 2 + (ROT ? kQuantTile * sine_stride(D) * 8 : 0);
+  static std::atomic<uint64_t> ready{0};
+  const auto kernel = quant_append_kernel<T, D, BITS, ROT>;
+  const cudaError_t e = allow_smem(kernel, smem, &ready);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, p.tiles * p.parts, kWriteWarps * 32, smem, st, p);
+}
 template <typename T, int D, int BITS>
 cudaError_t append_of(const QuantAppendParams &p, cudaStream_t st) {
-  const int grid = p.tiles * p.parts;
-  return p.rotate ? launch_pdl(quant_append_kernel<T, D, BITS, true>, grid, kWriteWarps * 32, 0, st, p)
-                  : launch_pdl(quant_append_kernel<T, D, BITS, false>, grid, kWriteWarps * 32, 0, st, p);
+  return p.rotate ? append_one<T, D, BITS, true>(p, st) : append_one<T, D, BITS, false>(p, st);
 }
 template <typename T, int D, int BITS>
 cudaError_t read_of(const QuantReadParams &p, cudaStream_t st) {
   const long long jobs = (long long)p.tiles * 2 * p.hkv;
-  const int grid = (int)((jobs + kWriteWarps - 1) / kWriteWarps);
-  return launch_pdl(quant_read_kernel<T, D, BITS>, grid, kWriteWarps * 32, 0, st, p);
+  const int grid = (int)((jobs + kReadWarps - 1) / kReadWarps);
+  return launch_pdl(quant_read_kernel<T, D, BITS>, grid, kReadWarps * 32, 0, st, p);
 }
 
 }  // namespace

@@ -55,6 +55,13 @@ struct RotaryShape {
   __device__ __forceinline__ int units() const { return turned() + ((d - rot) >> 3); }
 };
 
+// Where a pair's sines lie: what neighbouring units read together lies together.
+__device__ __forceinline__ int sine_place(const RotaryShape &s, int pair) {
+  const int n = s.turned();
+  return s.neighbours ? (pair & 3) * n + (pair >> 2)
+                      : 2 * (((pair & 7) >> 1) * n + (pair >> 3)) + (pair & 1);
+}
+
 template <typename T>
 struct RotaryUnit {
   uint4 a, b;
@@ -72,13 +79,14 @@ struct RotaryUnit {
     a = *reinterpret_cast<const uint4 *>(row + c0);
     if (c1 >= 0) b = *reinterpret_cast<const uint4 *>(row + c1);
   }
-  // cs: the token's (cos, sin) of every pair
+  // cs: the token's (cos, sin) of every pair, in the order of sine_place
   __device__ __forceinline__ void turn(const RotaryShape &s, const float2 *cs) {
+    const int n = s.turned();
     if (c1 >= 0) {
       uint32_t *x = &a.x, *y = &b.x;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float4 e = *reinterpret_cast<const float4 *>(cs + c0 + 2 * i);  // two pairs
+        const float4 e = reinterpret_cast<const float4 *>(cs)[i * n + (c0 >> 3)];  // two pairs
         const float2 p = unpack2<T>(x[i]), q = unpack2<T>(y[i]);
         x[i] = pack2<T>(p.x * e.x - q.x * e.y, p.y * e.z - q.y * e.w);
         y[i] = pack2<T>(q.x * e.x + p.x * e.y, q.y * e.z + p.y * e.w);
@@ -87,7 +95,7 @@ struct RotaryUnit {
       uint32_t *x = &a.x;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 e = cs[(c0 >> 1) + i], p = unpack2<T>(x[i]);
+        const float2 e = cs[i * n + (c0 >> 3)], p = unpack2<T>(x[i]);
         x[i] = pack2<T>(p.x * e.x - p.y * e.y, p.y * e.x + p.x * e.y);
       }
     }
@@ -97,5 +105,24 @@ struct RotaryUnit {
     if (c1 >= 0) *reinterpret_cast<uint4 *>(row + c1) = b;
   }
 };
+
+// Between the sines of two tokens (their 16-byte pieces begin at other banks).
+__device__ __host__ constexpr int sine_stride(int rot) { return (rot >> 1) + 2; }
+
+// The sines of n tokens' pairs, by a CTA's threads.  Neighbouring threads take the same pair of
+// different tokens: the table lies in constant memory, which serves one address at a time (by
+// pairs first, this took longer than the rows: 18 us of a 16,385-token append).
+template <int THREADS, typename Position>
+__device__ __forceinline__ void make_sines(const spd_rotary_table &table, int n, int inverse,
+                                           float2 *cs, Position position) {
+  const RotaryShape s{table.head_dim, table.rotary_dim, table.neighbours};
+  const int pairs = s.rot >> 1;
+  for (int e = threadIdx.x; e < n * pairs; e += THREADS) {
+    const int j = e / n, t = e - j * n;
+    float2 x = turn_of(position(table.axis[j], t), table.turns[j]);
+    if (inverse) x.y = -x.y;
+    cs[t * sine_stride(s.rot) + sine_place(s, j)] = x;
+  }
+}
 
 }  // namespace spd
