@@ -601,11 +601,12 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
   // Copies, a step's two tiles into a stage.  Lane k holds the physical page of the unit's page
   // `base` + k.
   const int per_page = p.P / kQuantTile;
-  int base = 0, phys_lane = 0, run = 0, stage_in = 0, issued = 0;
-  int todo = 0, tile_in = 0, head_in = 0;  // of the unit being copied: tiles left, the next one
-  const QuantAttendSeq *seq_in = nullptr;
-  bool fresh = true;  // its pages are not known yet
+  int base = 0, phys_lane = 0, issued = 0;
+  int todo = 0, tile_in = 0, head_in = 0;  // of the unit being copied: tiles behind the run, the next one
+  int run = 0;                             // tiles that follow one another at src
   const char *src = nullptr;
+  const QuantAttendSeq *seq_in = nullptr;
+  bool fresh = true;  // the unit's pages are not known yet
   auto locate = [&]() {  // the next run of tiles on one page: src, run
     const int page = tile_in / per_page, in_page = tile_in - page * per_page;
     if (fresh || page - base >= 32) {
@@ -625,38 +626,54 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
     src = static_cast<const char *>(p.pool) +
           (((size_t)phys * p.hkv + head_in) * per_page + in_page) * Q::kBytes;
     run = min(todo, per_page - in_page);
+    todo -= run;
+    tile_in += run;
   };
-  auto issue = [&]() {
-    if (todo == 0) {
+  // The stage's next copies: two tiles, but one at a unit's odd end.
+  auto issue_slow = [&](int stage) {
+    if (run == 0 && todo == 0) {
       if (in.left == 0) return;
       todo = in.left;
       seq_in = p.seqs + in.i;
       head_in = in.h;
       tile_in = seq_in->first / kQuantTile + in.tile;
       fresh = true;
-      run = 0;
+      // (the queries are asked for when the unit begins)
+      if (lane < G)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const T *>(p.q) +
+                                                      ((size_t)(in.i * p.hkv + in.h) * G + lane) * D));
       in.advance(p, todo);
     }
-    char *dst = mine + stage_in * S::kStage;
-    int want = min(2, todo);
-    if (lane == 0) mbar_arrive_expect_tx(bar + stage_in, want * Q::kBytes);
+    char *dst = mine + stage * S::kStage;
+    int want = min(2, run + todo);
+    if (lane == 0) mbar_arrive_expect_tx(bar + stage, want * Q::kBytes);
 #pragma unroll 1
     while (want > 0) {
       if (run == 0) locate();
       const int n = min(want, run);
-      if (lane == 0) bulk_load_1d(dst, src, n * Q::kBytes, bar + stage_in);
+      if (lane == 0) bulk_load_1d(dst, src, n * Q::kBytes, bar + stage);
       dst += n * Q::kBytes;
       src += n * Q::kBytes;
-      tile_in += n;
-      todo -= n;
       run -= n;
       want -= n;
     }
-    stage_in = stage_in + 1 == S::kStages ? 0 : stage_in + 1;
+    ++issued;
+  };
+  auto issue = [&](int stage) {
+    if (run < 2) {
+      issue_slow(stage);
+      return;
+    }
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar + stage, S::kStage);
+      bulk_load_1d(mine + stage * S::kStage, src, S::kStage, bar + stage);
+    }
+    src += S::kStage;
+    run -= 2;
     ++issued;
   };
 #pragma unroll 1
-  for (int k = 0; k < S::kStages; ++k) issue();
+  for (int k = 0; k < S::kStages; ++k) issue_slow(k);
 
   int done = 0, stage = 0;
   uint32_t parity = 0;
@@ -671,18 +688,21 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
     w.begin(p, i, h, lane);
 #pragma unroll 1
     for (; t0 < end; t0 += 2 * kQuantTile) {
-      if (!broken && !mbar_try_wait(bar + stage, parity) &&
-          !mbar_wait(bar + stage, parity, kWaitPolls)) {
-        if (lane == 0) qd_set_err(p.err, kDevTimeout, p.seqs[i].slot, h, t0);
-        broken = true;
+      if (!__all_sync(kFull, mbar_try_wait(bar + stage, parity))) {
+        bool there = false;
+        for (uint32_t k = 0; k < kWaitPolls && !there && !broken; ++k)
+          there = __all_sync(kFull, mbar_try_wait(bar + stage, parity));
+        if (!there) {
+          if (!broken && lane == 0) qd_set_err(p.err, kDevTimeout, p.seqs[i].slot, h, t0);
+          broken = true;
+          break;  // (nothing is read or copied any more, units still end)
+        }
       }
-      broken = __any_sync(kFull, broken);
-      if (broken) break;  // (nothing is read or copied any more, units still end)
       w.step(p, mine + stage * S::kStage, t0, first, end, L, lane);
-      if (++stage == S::kStages) stage = 0, parity ^= 1;
       ++done;
       __syncwarp();
-      issue();
+      issue(stage);
+      if (++stage == S::kStages) stage = 0, parity ^= 1;
     }
     at.advance(p, n);
     w.finish();
@@ -723,19 +743,33 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
   }
   __syncthreads();
 
-  // Slots in order belong to units in order: runs of the same unit are joined.
+  // Partials of the same unit are joined: by the whole CTA where all are of one, else every unit
+  // by a warp of its own.  (Unit after unit by the CTA, 1,024 units of 1,024 tokens took 52 us.)
   auto slot_of = [&](int k) {
     return reinterpret_cast<const float *>((k & 1 ? ring : firsts) + (k >> 1) * S::kSlot);
   };
   constexpr int kSlots = 2 * kQuantWarps, kVectors = G * D / 4;
+  static_assert(kSlots <= 32, "a lane per slot");
   const int per_cta = p.per_warp * kQuantWarps;
+  const int slot_unit = lane < kSlots ? unit_of[lane] : -1;
+  const unsigned taken = __ballot_sync(kFull, slot_unit >= 0);
+  const unsigned before = taken & ((1u << lane) - 1u);
+  const int last_unit = __shfl_sync(kFull, slot_unit, before ? 31 - __clz(before) : 0);
+  // (a unit's slots follow one another: its first one stands for it)
+  unsigned units = __ballot_sync(kFull, slot_unit >= 0 && (!before || last_unit != slot_unit));
+  const bool whole_cta = __popc(units) == 1;
+  const int tid = whole_cta ? threadIdx.x : lane, count = whole_cta ? kThreads : 32;
+  auto sync = [&]() {
+    if (whole_cta) __syncthreads();
+    else __syncwarp();
+  };
+  if (!whole_cta)
+    for (int k = 0; k < warp; ++k) units &= units - 1;  // from this warp's first unit on
 #pragma unroll 1
-  for (int k0 = 0; k0 < kSlots;) {
-    const int unit = unit_of[k0];
-    if (unit < 0) {
-      ++k0;
-      continue;
-    }
+  while (units) {
+    const int unit = __shfl_sync(kFull, slot_unit, __ffs(units) - 1);
+    const unsigned members = __ballot_sync(kFull, slot_unit == unit);
+    for (int k = 0; k < (whole_cta ? 1 : kQuantWarps); ++k) units &= units - 1;
     const int i = unit / p.hkv, h = unit - i * p.hkv;
     const QuantAttendSeq &s = p.seqs[i];
     const int u0 = s.off + h * s.stride;
@@ -744,10 +778,10 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
     // this CTA's two partials: of a unit that it starts with, of one that it ends with
     auto part = [&](int c) { return 2 * c + (c > c0 || u0 == c * per_cta ? 0 : 1); };
     const size_t to_slot = part(blockIdx.x);
-    // a warp per head: the slots' weights, lane k for slot k
-    for (int head = warp; head < G; head += kQuantWarps) {
-      const bool mine = lane < kSlots && unit_of[lane < kSlots ? lane : 0] == unit;
-      const float *q = slot_of(mine ? lane : k0) + G * D + 2 * head;
+    // the slots' weights, lane k for slot k
+    for (int head = whole_cta ? warp : 0; head < G; head += whole_cta ? kQuantWarps : 1) {
+      const bool mine = members >> lane & 1u;
+      const float *q = slot_of(mine ? lane : __ffs(members) - 1) + G * D + 2 * head;
       const float m = mine ? q[0] : -CUDART_INF_F;
       float top = m;
 #pragma unroll
@@ -756,18 +790,16 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
       float l = mine ? f * q[1] : 0.f;
 #pragma unroll
       for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(kFull, l, k);
-      if (lane < kSlots) share[lane][head] = alone ? f / l : f;
+      if (mine) share[lane][head] = alone ? f / l : f;
       if (!alone && lane == 0) p.part_ml[to_slot * G + head] = make_float2(top, l);
     }
-    __syncthreads();
-    int k1 = k0 + 1;
-    while (k1 < kSlots && (unit_of[k1] == unit || unit_of[k1] < 0)) ++k1;
-    for (int e = threadIdx.x; e < kVectors; e += kThreads) {
+    sync();
+    for (int e = tid; e < kVectors; e += count) {
       const int head = e / (D / 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-      for (int k = k0; k < k1; ++k) {
-        if (unit_of[k] < 0) continue;
+      for (unsigned left = members; left; left &= left - 1) {
+        const int k = __ffs(left) - 1;
         const float4 y = reinterpret_cast<const float4 *>(slot_of(k))[e];
         const float f = share[k][head];
         v.x = fmaf(f, y.x, v.x), v.y = fmaf(f, y.y, v.y);
@@ -776,81 +808,86 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
       if (alone) store_out<T>(p.out, p.out_f32, (size_t)unit * G * D + 4 * e, v);
       else reinterpret_cast<float4 *>(p.part_o + to_slot * G * D)[e] = v;
     }
-    if (!alone) {
-      // The last CTA of the unit to come joins its partials (in their order, whichever came
-      // last).  The barrier and the ticket's release publish them.
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        last_flag = atom_add_acq_rel_gpu(p.tickets + unit, 1) == c1 - c0;
-        if (last_flag) p.tickets[unit] = 0;  // (for the next launch)
-      }
-      __syncthreads();
-      if (last_flag) {
-        // Threads in kSets sets, each with every kSets-th partial, eight loads under way.
-        constexpr int kSets = kThreads / kVectors < 1 ? 1 : kThreads / kVectors;
-        const int parts = c1 - c0 + 1, set = threadIdx.x / kVectors, e = threadIdx.x % kVectors;
-        const int head = e / (D / 4);
-        float m = -CUDART_INF_F, l = 0.f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        float4 *const sums = reinterpret_cast<float4 *>(ring + S::kLast);
-        float2 *const stats = reinterpret_cast<float2 *>(sums + kSets * kVectors);
-        if (set < kSets) {
+    if (alone) continue;
+    // The last CTA of the unit to come joins its partials (in their order, whichever came
+    // last).  The barrier and the ticket's release publish them.
+    sync();
+    int last = 0;
+    if (tid == 0) {
+      last = atom_add_acq_rel_gpu(p.tickets + unit, 1) == c1 - c0;
+      if (last) p.tickets[unit] = 0;  // (for the next launch)
+      if (whole_cta) last_flag = last;
+    }
+    sync();
+    last = whole_cta ? last_flag : __shfl_sync(kFull, last, 0);
+    if (!last) continue;
+    // The CTA's threads in kSets sets, each with every kSets-th partial, eight loads under way.
+    constexpr int kSets = kThreads / kVectors < 1 ? 1 : kThreads / kVectors;
+    const int sets = whole_cta ? kSets : 1, parts = c1 - c0 + 1;
+    float4 *const sums = reinterpret_cast<float4 *>(ring + S::kLast);
+    float2 *const stats = reinterpret_cast<float2 *>(sums + kSets * kVectors);
 #pragma unroll 1
-          for (int c = set; c < parts; c += 8 * kSets) {
-            float2 ml[8];
-            float4 y[8];
+    for (int x = tid; x < sets * kVectors; x += count) {
+      const int set = x / kVectors, e = x % kVectors, head = e / (D / 4);
+      float m = -CUDART_INF_F, l = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int c = set; c < parts; c += 8 * sets) {
+        float2 ml[8];
+        float4 y[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const size_t from = part(c0 + min(c + k * kSets, parts - 1));
-              ml[k] = __ldcg(p.part_ml + from * G + head);
-              y[k] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + from * G * D) + e);
-            }
-            float top = m;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              if (c + k * kSets >= parts) ml[k] = make_float2(-CUDART_INF_F, 0.f);
-              top = fmaxf(top, ml[k].x);
-            }
-            const float f0 = m == top ? 1.f : ex2_approx(m - top);
-            m = top;
-            l *= f0;
-            v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              if (c + k * kSets >= parts) continue;
-              const float f = ex2_approx(ml[k].x - m);
-              l = fmaf(f, ml[k].y, l);
-              v.x = fmaf(f, y[k].x, v.x), v.y = fmaf(f, y[k].y, v.y);
-              v.z = fmaf(f, y[k].z, v.z), v.w = fmaf(f, y[k].w, v.w);
-            }
-          }
-          if (kSets > 1) {
-            sums[set * kVectors + e] = v;
-            stats[set * kVectors + e] = make_float2(m, l);
-          }
+        for (int k = 0; k < 8; ++k) {
+          const size_t from = part(c0 + min(c + k * sets, parts - 1));
+          ml[k] = __ldcg(p.part_ml + from * G + head);
+          y[k] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + from * G * D) + e);
         }
-        if (kSets > 1) __syncthreads();
-        if (set == 0) {
+        float top = m;
 #pragma unroll
-          for (int k = 1; k < kSets; ++k) {
-            if (k >= parts) continue;
-            const float2 ml = stats[k * kVectors + e];
-            const float4 y = sums[k * kVectors + e];
-            const float top = fmaxf(m, ml.x);
-            const float f0 = m == top ? 1.f : ex2_approx(m - top), f = ex2_approx(ml.x - top);
-            m = top;
-            l = fmaf(f, ml.y, l * f0);
-            v.x = fmaf(f, y.x, v.x * f0), v.y = fmaf(f, y.y, v.y * f0);
-            v.z = fmaf(f, y.z, v.z * f0), v.w = fmaf(f, y.w, v.w * f0);
-          }
-          const float f = 1.f / l;
-          store_out<T>(p.out, p.out_f32, (size_t)unit * G * D + 4 * e,
-                       make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+        for (int k = 0; k < 8; ++k) {
+          if (c + k * sets >= parts) ml[k] = make_float2(-CUDART_INF_F, 0.f);
+          top = fmaxf(top, ml[k].x);
         }
+        const float f0 = m == top ? 1.f : ex2_approx(m - top);
+        m = top;
+        l *= f0;
+        v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (c + k * sets >= parts) continue;
+          const float f = ex2_approx(ml[k].x - m);
+          l = fmaf(f, ml[k].y, l);
+          v.x = fmaf(f, y[k].x, v.x), v.y = fmaf(f, y[k].y, v.y);
+          v.z = fmaf(f, y[k].z, v.z), v.w = fmaf(f, y[k].w, v.w);
+        }
+      }
+      if (sets > 1) {
+        sums[x] = v;
+        stats[x] = make_float2(m, l);
+      } else {
+        const float f = 1.f / l;
+        store_out<T>(p.out, p.out_f32, (size_t)unit * G * D + 4 * e,
+                     make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
       }
     }
-    __syncthreads();  // (shares, the flag and the sums are used again)
-    k0 = k1;
+    if (sets == 1) continue;
+    __syncthreads();  // (of the whole CTA, which has this unit alone)
+    for (int e = tid; e < kVectors; e += kThreads) {
+      float m = stats[e].x, l = stats[e].y;
+      float4 v = sums[e];
+      for (int k = 1; k < kSets && k < parts; ++k) {
+        const float2 ml = stats[k * kVectors + e];
+        const float4 y = sums[k * kVectors + e];
+        const float top = fmaxf(m, ml.x);
+        const float f0 = m == top ? 1.f : ex2_approx(m - top), f = ex2_approx(ml.x - top);
+        m = top;
+        l = fmaf(f, ml.y, l * f0);
+        v.x = fmaf(f, y.x, v.x * f0), v.y = fmaf(f, y.y, v.y * f0);
+        v.z = fmaf(f, y.z, v.z * f0), v.w = fmaf(f, y.w, v.w * f0);
+      }
+      const float f = 1.f / l;
+      store_out<T>(p.out, p.out_f32, (size_t)unit * G * D + 4 * e,
+                   make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+    }
   }
 }
 
