@@ -383,6 +383,7 @@ class SparsePagedKVCache:
         self._dev_index = self.device.index
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self._ids_cache = {}
+        self._append_plans = {}
         L = lib()
         self._step_fn = L.spd_decode_step
         self._truncate_fn = L.spd_seq_truncate
@@ -437,10 +438,11 @@ class SparsePagedKVCache:
 
     def kv_append(self, seq_ids, k, v, stream=None):
         """k, v: [n_seqs][n_tokens][Hkv][d] of the cache dtype."""
-        n = len(seq_ids)
+        ids, n = self._id_array(seq_ids)
         shape = (n, k.shape[1], self.Hkv, self.d)
-        spd_kv_append(self.ctx, seq_ids, k.shape[1], self._ptr(k, shape, self.dtype),
-                      self._ptr(v, shape, self.dtype), self._stream(stream))
+        kp, vp = self._ptr(k, shape, self.dtype), self._ptr(v, shape, self.dtype)
+        _check(lib().spd_kv_append(self.ctx, ids, n, shape[1], kp, vp, self._stream(stream) or None),
+               "spd_kv_append", self.ctx)
 
     def select_pages(self, q, seq_ids, force=False, stream=None):
         qp = self._ptr(q, (len(seq_ids), self.Hq, self.d), self.dtype)
@@ -505,7 +507,7 @@ class SparsePagedKVCache:
         return out, rm, rs, pages, mass
 
     def _id_array(self, seq_ids):
-        key = tuple(seq_ids)
+        key = tuple(map(int, seq_ids))  # (by value: a tensor would be found by its identity)
         ids = self._ids_cache.get(key)
         if ids is None:
             ids = _ids(key)
@@ -621,19 +623,19 @@ class SparsePagedKVCache:
         one axis); None: a token's place in its sequence.  `stream` as in
         :func:`prefill_attention`."""
         ids, n = self._id_array(seq_ids)
-        if k.dim() != 4:
-            raise ValueError("k must be [n][tokens][Hkv][d]")
-        tokens = k.shape[1]
-        qshape, kshape = (n, tokens, self.Hq, self.d), (n, tokens, self.Hkv, self.d)
-        qs = self._rows(q, qshape, "q")
-        ks = self._rows(k, kshape, "k")
-        vs = self._rows(v, kshape, "v")
-        pos = None
-        if positions is not None:
-            if positions.shape != (table.axes, n, tokens) \
-                    and not (table.axes == 1 and positions.shape == (n, tokens)):
-                raise ValueError("positions must be int32 %s" % ((table.axes, n, tokens),))
-            pos = self._ptr(positions, positions.shape, self.torch.int32)
+        # (what shapes, strides and types decide is worked out once)
+        key = (n, table.axes, q.shape, q.stride(), q.dtype, q.get_device(), k.shape, k.stride(),
+               k.dtype, k.get_device(), v.shape, v.stride(), v.dtype, v.get_device(),
+               None if positions is None else (positions.shape, positions.dtype,
+                                               positions.get_device(), positions.is_contiguous()))
+        plan = self._append_plans.get(key)
+        if plan is None:
+            plan = self._append_plan(n, table.axes, q, k, v, positions)
+            if len(self._append_plans) >= 1024:
+                self._append_plans.clear()
+            self._append_plans[key] = plan
+        tokens, qshape, qs, ks, vs = plan
+        pos = None if positions is None else positions.data_ptr()
         if out is None:
             out = _empty(self.torch, qshape, self.dtype, self.device, stream)
             op = out.data_ptr()
@@ -645,6 +647,19 @@ class SparsePagedKVCache:
         if st != SPD_OK:
             _check(st, "spd_kv_append_rotary", self.ctx)
         return out
+
+    def _append_plan(self, n, axes, q, k, v, positions):
+        if k.dim() != 4:
+            raise ValueError("k must be [n][tokens][Hkv][d]")
+        tokens = k.shape[1]
+        qshape, kshape = (n, tokens, self.Hq, self.d), (n, tokens, self.Hkv, self.d)
+        strides = self._rows(q, qshape, "q"), self._rows(k, kshape, "k"), self._rows(v, kshape, "v")
+        if positions is not None:
+            if positions.shape != (axes, n, tokens) \
+                    and not (axes == 1 and positions.shape == (n, tokens)):
+                raise ValueError("positions must be int32 %s" % ((axes, n, tokens),))
+            self._ptr(positions, positions.shape, self.torch.int32)
+        return (tokens, qshape) + strides
 
     def _rows(self, x, shape, name):
         """Elements between the tokens of [n][tokens][heads][d]."""

@@ -1,5 +1,5 @@
 // Internal interface of the rotary kernels, the cache in 8 or 4 bits and the
-// decode attention over it (rotary.cu, quant_cache.cu, quant_decode.cu).
+// decode attention over it (rotary.cu, quant_cache.cu, quant_decode.cuh).
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -140,7 +140,9 @@ struct QuantAttendParams {
   int ctas;
   QuantAttendSeq seqs[kQuantSeqs];
 };
-cudaError_t launch_quant_attend(const QuantAttendParams &p, int dtype, int d, int bits, int G,
-                                cudaStream_t st);
+cudaError_t launch_quant_attend_f16(const QuantAttendParams &p, int d, int bits, int G,
+                                    cudaStream_t st);
+cudaError_t launch_quant_attend_bf16(const QuantAttendParams &p, int d, int bits, int G,
+                                     cudaStream_t st);
 
 }  // namespace spd

@@ -408,7 +408,8 @@ spd_status spd_quant_decode_attention(spd_ctx *c, const void *q, const int *seq_
     p.P = cfg.physical_page;
     p.max_pp = v.max_pp;
     p.num_phys = cfg.num_physical_pages;
-    const cudaError_t e = launch_quant_attend(p, cfg.dtype, cfg.head_dim, v.quant, v.G, st);
+    const auto launch = cfg.dtype == SPD_F16 ? launch_quant_attend_f16 : launch_quant_attend_bf16;
+    const cudaError_t e = launch(p, cfg.head_dim, v.quant, v.G, st);
     note_launches(c, st, 1);
     if (e != cudaSuccess) return fail_message(c, SPD_ERR_CUDA, cudaGetErrorString(e));
     b += n;

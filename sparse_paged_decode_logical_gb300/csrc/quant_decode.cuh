@@ -1,4 +1,5 @@
-// Decode attention over a quantised cache (sm_103a): spd_quant_decode_attention.
+// Decode attention over a quantised cache (sm_103a): the kernel of spd_quant_decode_attention
+// (instantiated in quant_decode_f16.cu and quant_decode_bf16.cu).
 //
 // With value = lo + step code for keys and values alike,
 //   q . k_t = sum over groups a of  lo_ta (sum of q in a) + step_ta (q . codes in a)
@@ -20,6 +21,7 @@
 // tiles evenly, a warp may end one unit (sequence, kv head) and start the next.  What a warp
 // holds of a unit that others hold parts of, too, is joined in the CTA, then over CTAs by the
 // last one to finish.
+#pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
@@ -143,21 +145,25 @@ struct Cursor {
   }
 };
 
-template <typename T, int D, int BITS, int G, bool SPLIT>
+template <typename T, int D, int BITS, int G, int MODE>
 struct Warp {
   using Q = QuantTile<D, BITS>;
   static constexpr int KS = D / 16;     // k-steps of S, m-tiles of O
   static constexpr int NG = Q::kGroups;
+  // MODE 0: outputs in bf16, weights of 11 bits.  1: in fp16, weights of 22 bits.  2: in fp32,
+  // and sums to fp32's own error.
+  static constexpr bool SPLIT = MODE >= 1, FINE = MODE == 2;
   static constexpr bool kTwo = SPLIT && G == 8;   // low halves need products of their own
   static constexpr bool kLanes = SPLIT && G < 8;  // low halves in the columns 4 .. 7
-  // Codes as fp16 numbers.  Outputs in bf16: as they lie, a subnormal number, code 2^-24 (2^-20
-  // in a high nibble).  The tensor cores cut sums off where their largest term, or what its
-  // exponent could hold, ends; the others therefore take ordinary numbers around 0, code - 2^(b-1)
-  // (11 instructions a word of 4 bits instead of 5, 5 for 4 codes of 8 bits instead of 3), and add
-  // products over more than two operands in fp32 outside.  (fp32 outputs 5.5e-6 off without.)
-  static constexpr bool kNibbles = BITS == 4 && !SPLIT;  // high nibbles 2^4 as large
-  static constexpr int kUnit = SPLIT ? 0 : 24;           // a code of 1 is 2^-kUnit
-  static constexpr float kMid = SPLIT ? (BITS == 4 ? 8.f : 128.f) : 0.f;
+  // Codes as fp16 numbers.  For 16-bit outputs: as they lie, a subnormal number, code 2^-24
+  // (2^-20 in a high nibble).  The tensor cores cut sums off where their largest term, or what
+  // its exponent could hold, ends: 2^-15 of it then, which 16 bits do not show.  For fp32: ordinary
+  // numbers around 0, code - 2^(b-1) (11 instructions a word of 4 bits instead of 5, 5 for 4 codes
+  // of 8 bits instead of 3), and products over more than two operands are added in fp32 outside.
+  // (fp32 outputs 5.5e-6 off without, 1.6e-7 with; 131,072 tokens in 4 bits 53 us, 38 without.)
+  static constexpr bool kNibbles = BITS == 4 && !FINE;  // high nibbles 2^4 as large
+  static constexpr int kUnit = FINE ? 0 : 24;           // a code of 1 is 2^-kUnit
+  static constexpr float kMid = FINE ? (BITS == 4 ? 8.f : 128.f) : 0.f;
 
   uint32_t qb[KS][2];  // q as the second operand of S
   float qs[2][NG];     // sums of q over the groups, of the lane's two columns
@@ -277,7 +283,7 @@ struct Warp {
       a[1] = (w[0] >> 8) & 0x00ff00ffu;
       a[2] = w[1] & 0x00ff00ffu;
       a[3] = (w[1] >> 8) & 0x00ff00ffu;
-      if constexpr (SPLIT) {
+      if constexpr (FINE) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) a[k] = centred(a[k]);
       }
@@ -289,7 +295,7 @@ struct Warp {
   __device__ __forceinline__ void sums(const char *buf, int lane, float (&x)[4]) const {
     const int g = lane >> 2;
     constexpr int W = BITS / 4;                                     // words of a step
-    constexpr int CH = !SPLIT ? KS / NG : KS / NG > 2 ? 2 : KS / NG;  // products of one sum
+    constexpr int CH = !FINE ? KS / NG : KS / NG > 2 ? 2 : KS / NG;  // products of one sum
     float acc[KS / CH][4];
 #pragma unroll
     for (int c = 0; c < Q::kWords / 4; ++c) {
@@ -499,7 +505,7 @@ struct Warp {
         widen(wd[0] + k * W, true, a0);
         widen(wd[1] + k * W, true, a1);
         float *y = o[s], d[4];
-        if constexpr (SPLIT) {
+        if constexpr (FINE) {
           mma_f16(d, a0, b[0][n][0], b[0][n][1], 0.f, 0.f, 0.f, 0.f);
           if constexpr (kTwo) {
             float e[4];
@@ -514,6 +520,10 @@ struct Warp {
         } else {
           mma_f16(o[s], a0, b[0][n][0], b[0][n][1], y[0], y[1], y[2], y[3]);
           mma_f16(o[s], a1, b[1][n][0], b[1][n][1], y[0], y[1], y[2], y[3]);
+          if constexpr (kTwo) {
+            mma_f16(o[s], a0, b2[0][n][0], b2[0][n][1], y[0], y[1], y[2], y[3]);
+            mma_f16(o[s], a1, b2[1][n][0], b2[1][n][1], y[0], y[1], y[2], y[3]);
+          }
         }
       }
     }
@@ -567,12 +577,12 @@ __device__ __forceinline__ void store_out(void *out, bool f32, size_t at, float4
   }
 }
 
-template <typename T, int D, int BITS, int G, bool SPLIT>
+template <typename T, int D, int BITS, int G, int MODE>
 __global__ void __launch_bounds__(kThreads, kQuantPerSm)
     quant_attend_kernel(const __grid_constant__ QuantAttendParams p) {
   using S = Shape<D, BITS, G>;
   using Q = typename S::Q;
-  using W = Warp<T, D, BITS, G, SPLIT>;
+  using W = Warp<T, D, BITS, G, MODE>;
   extern __shared__ __align__(128) char smem[];
   char *const ring = smem;
   char *const firsts = p.firsts + (size_t)blockIdx.x * S::kLast;
@@ -891,49 +901,32 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
   }
 }
 
-template <typename T, int D, int BITS, int G, bool SPLIT>
+template <typename T, int D, int BITS, int G, int MODE>
 cudaError_t launch_one(const QuantAttendParams &p, cudaStream_t st) {
   using S = Shape<D, BITS, G>;
     static std::atomic<uint64_t> ready{0};
-  const auto kernel = quant_attend_kernel<T, D, BITS, G, SPLIT>;
+  const auto kernel = quant_attend_kernel<T, D, BITS, G, MODE>;
   const cudaError_t e = allow_smem(kernel, S::kSmem, &ready);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, p.ctas, kThreads, S::kSmem, st, p);
 }
 
-template <typename T, int D, int BITS, bool SPLIT>
+template <typename T, int D, int BITS, int MODE>
 cudaError_t launch_heads(const QuantAttendParams &p, int G, cudaStream_t st) {
   switch (G) {
-    case 1: return launch_one<T, D, BITS, 1, SPLIT>(p, st);
-    case 2: return launch_one<T, D, BITS, 2, SPLIT>(p, st);
-    case 4: return launch_one<T, D, BITS, 4, SPLIT>(p, st);
-    default: return launch_one<T, D, BITS, 8, SPLIT>(p, st);
+    case 1: return launch_one<T, D, BITS, 1, MODE>(p, st);
+    case 2: return launch_one<T, D, BITS, 2, MODE>(p, st);
+    case 4: return launch_one<T, D, BITS, 4, MODE>(p, st);
+    default: return launch_one<T, D, BITS, 8, MODE>(p, st);
   }
 }
 
-// Outputs in bf16 (steps of 2^-8) do not show weights rounded to fp16's 11 bits; the others
-// keep 22.
-template <typename T, int D, int BITS>
-cudaError_t launch_type(const QuantAttendParams &p, int G, cudaStream_t st) {
-  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-    if (!p.out_f32) return launch_heads<T, D, BITS, false>(p, G, st);
-  }
-  return launch_heads<T, D, BITS, true>(p, G, st);
-}
-
-template <typename T>
+template <typename T, int MODE>
 cudaError_t launch_shape(const QuantAttendParams &p, int d, int bits, int G, cudaStream_t st) {
-  if (d == 64) return bits == 8 ? launch_type<T, 64, 8>(p, G, st) : launch_type<T, 64, 4>(p, G, st);
-  return bits == 8 ? launch_type<T, 128, 8>(p, G, st) : launch_type<T, 128, 4>(p, G, st);
+  if (d == 64)
+    return bits == 8 ? launch_heads<T, 64, 8, MODE>(p, G, st) : launch_heads<T, 64, 4, MODE>(p, G, st);
+  return bits == 8 ? launch_heads<T, 128, 8, MODE>(p, G, st) : launch_heads<T, 128, 4, MODE>(p, G, st);
 }
 
 }  // namespace
-
-cudaError_t launch_quant_attend(const QuantAttendParams &p, int dtype, int d, int bits, int G,
-                                cudaStream_t st) {
-  const cudaError_t e = dtype == 0 ? launch_shape<__half>(p, d, bits, G, st)
-                                   : launch_shape<__nv_bfloat16>(p, d, bits, G, st);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 }  // namespace spd

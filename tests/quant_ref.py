@@ -15,11 +15,16 @@ Attention.  With V = |lo| + step code and A = sum of softmax V:
   scores   d products and the groups' terms in fp32, sums that the tensor cores may
            cut off instead of rounding: d 2^-23 of sum |q| V; a cap 2^-21 of it
            (dense_ref); an error e of a score is one of 2 e of a weight's share
+           With 16-bit outputs the codes are subnormal fp16 numbers whose exponent is a
+           code's of 2^10, and the tensor cores cut each of a product's 17 terms off
+           2^-24 below the largest: 17 2^-14 |q| step at most, d / 16 times
   weights  11 bits (2^-11 of each) where the output is bf16, else 22, cut off
            (2^-21); 2^x 2^-22, twice
   floor    fp16 loses up to 2^-24 of a part where the largest weight is at least
            2^11 there: two parts, 2^-34 of the largest weight, times a step's codes
-  sums     n terms in fp32: n 2^-24 at most
+  sums     n terms in fp32: n 2^-24 at most; with 16-bit outputs a product over 16
+           tokens loses 17 2^-14 of its largest weight times step, all of them at
+           most 17 2^-14 of sum softmax step
   output   half a step of its type, as above
 """
 import math
@@ -97,6 +102,7 @@ def attend(q, k, v, bits, first=0, scale=None, softcap=0.0, slopes=None):
     scale = scale or d ** -0.5
     out = torch.zeros(hq, d, dtype=torch.float64, device=q.device)
     absum, mag, top = torch.zeros_like(out), 0.0, torch.zeros_like(out)
+    steps, cut = torch.zeros_like(out), 0.0
     back = torch.arange(L - 1 - first, -1, -1, device=q.device, dtype=torch.float64)
     for g in range(hkv):
         kv, ka = held(k[first:, g], bits)
@@ -104,6 +110,8 @@ def attend(q, k, v, bits, first=0, scale=None, softcap=0.0, slopes=None):
         hs = slice(g * hq // hkv, (g + 1) * hq // hkv)
         x = q[hs].double() @ kv.t() * scale
         mag = max(mag, float((q[hs].double().abs() @ ka.t()).max()) * scale)
+        ks, vs = (quantise(y[first:, g], bits)[1] for y in (k, v))
+        cut = max(cut, float(q[hs].double().abs().max() * ks.max()) * scale * 17 * 2.0 ** -14 * d / 16)
         if softcap:
             x = softcap * torch.tanh(x / softcap)
         if slopes is not None:
@@ -112,13 +120,15 @@ def attend(q, k, v, bits, first=0, scale=None, softcap=0.0, slopes=None):
         w = torch.softmax(x, 1)
         out[hs] = w @ vv
         absum[hs] = w @ va
+        steps[hs] = w @ vs
         top[hs] = va.sum(0)
     n = L - first
 
     def tolerance(out_dtype):
         w = 2.0 ** -11 if out_dtype == torch.bfloat16 else 2.0 ** -21
-        e = mag * d * 2.0 ** -23 + softcap * 2.0 ** -21
-        return absum * (w + 2 * e + n * 2.0 ** -24 + 2.0 ** -20) + 2.0 ** -34 * top + \
+        short = out_dtype != torch.float32
+        e = mag * d * 2.0 ** -23 + softcap * 2.0 ** -21 + (cut if short else 0.0)
+        return (17 * 2.0 ** -14 * steps if short else 0.0) + absum * (w + 2 * e + n * 2.0 ** -24 + 2.0 ** -20) + 2.0 ** -34 * top + \
             STEP[out_dtype] * out.abs() + FLOOR[out_dtype] + 1e-30
 
     return out, tolerance
