@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
   char *const firsts = p.firsts + (size_t)blockIdx.x * S::kLast;
   uint64_t *const bars = reinterpret_cast<uint64_t *>(smem + S::kBars);
   __shared__ int unit_of[2 * kQuantWarps];  // of the warps' first and last partials, or -1
-  __shared__ int last_flag;
+  __shared__ int last_flag[kQuantWarps];
   __shared__ float share[2 * kQuantWarps][G];  // weights of the warps' partials
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   char *const mine = ring + warp * S::kStages * S::kStage;
@@ -753,8 +753,9 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
   }
   __syncthreads();
 
-  // Partials of the same unit are joined: by the whole CTA where all are of one, else every unit
-  // by a warp of its own.  (Unit after unit by the CTA, 1,024 units of 1,024 tokens took 52 us.)
+  // Partials of the same unit are joined: by the whole CTA where all are of one, else side by
+  // side by four warps or one each.  (Unit after unit by the CTA, 1,024 units of 1,024 tokens
+  // took 52 us, 44 side by side.)
   auto slot_of = [&](int k) {
     return reinterpret_cast<const float *>((k & 1 ? ring : firsts) + (k >> 1) * S::kSlot);
   };
@@ -767,19 +768,21 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
   const int last_unit = __shfl_sync(kFull, slot_unit, before ? 31 - __clz(before) : 0);
   // (a unit's slots follow one another: its first one stands for it)
   unsigned units = __ballot_sync(kFull, slot_unit >= 0 && (!before || last_unit != slot_unit));
-  const bool whole_cta = __popc(units) == 1;
-  const int tid = whole_cta ? threadIdx.x : lane, count = whole_cta ? kThreads : 32;
+  // Teams of threads: the CTA, three of four warps, or warps.
+  const int found = __popc(units);
+  const int width = found == 1 ? kThreads : found <= kThreads / 128 ? 128 : 32;
+  const bool whole_cta = found == 1;
+  const int teams = kThreads / width, team = threadIdx.x / width, tid = threadIdx.x % width;
   auto sync = [&]() {
-    if (whole_cta) __syncthreads();
-    else __syncwarp();
+    if (width == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(whole_cta ? 0 : 1 + team), "r"(width) : "memory");
   };
-  if (!whole_cta)
-    for (int k = 0; k < warp; ++k) units &= units - 1;  // from this warp's first unit on
+  for (int k = 0; k < team; ++k) units &= units - 1;  // from this team's first unit on
 #pragma unroll 1
   while (units) {
     const int unit = __shfl_sync(kFull, slot_unit, __ffs(units) - 1);
     const unsigned members = __ballot_sync(kFull, slot_unit == unit);
-    for (int k = 0; k < (whole_cta ? 1 : kQuantWarps); ++k) units &= units - 1;
+    for (int k = 0; k < teams; ++k) units &= units - 1;
     const int i = unit / p.hkv, h = unit - i * p.hkv;
     const QuantAttendSeq &s = p.seqs[i];
     const int u0 = s.off + h * s.stride;
@@ -789,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
     auto part = [&](int c) { return 2 * c + (c > c0 || u0 == c * per_cta ? 0 : 1); };
     const size_t to_slot = part(blockIdx.x);
     // the slots' weights, lane k for slot k
-    for (int head = whole_cta ? warp : 0; head < G; head += whole_cta ? kQuantWarps : 1) {
+    for (int head = tid / 32; head < G; head += width / 32) {
       const bool mine = members >> lane & 1u;
       const float *q = slot_of(mine ? lane : __ffs(members) - 1) + G * D + 2 * head;
       const float m = mine ? q[0] : -CUDART_INF_F;
@@ -804,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
       if (!alone && lane == 0) p.part_ml[to_slot * G + head] = make_float2(top, l);
     }
     sync();
-    for (int e = tid; e < kVectors; e += count) {
+    for (int e = tid; e < kVectors; e += width) {
       const int head = e / (D / 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -826,10 +829,10 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
     if (tid == 0) {
       last = atom_add_acq_rel_gpu(p.tickets + unit, 1) == c1 - c0;
       if (last) p.tickets[unit] = 0;  // (for the next launch)
-      if (whole_cta) last_flag = last;
+      last_flag[team] = last;
     }
     sync();
-    last = whole_cta ? last_flag : __shfl_sync(kFull, last, 0);
+    last = last_flag[team];
     if (!last) continue;
     // The CTA's threads in kSets sets, each with every kSets-th partial, eight loads under way.
     constexpr int kSets = kThreads / kVectors < 1 ? 1 : kThreads / kVectors;
@@ -837,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
     float4 *const sums = reinterpret_cast<float4 *>(ring + S::kLast);
     float2 *const stats = reinterpret_cast<float2 *>(sums + kSets * kVectors);
 #pragma unroll 1
-    for (int x = tid; x < sets * kVectors; x += count) {
+    for (int x = tid; x < sets * kVectors; x += width) {
       const int set = x / kVectors, e = x % kVectors, head = e / (D / 4);
       float m = -CUDART_INF_F, l = 0.f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
