@@ -51,7 +51,7 @@ constexpr int kQuantWarps = 12;  // per CTA
 constexpr int kQuantWriteWarps = 4;  // of a writing CTA
 constexpr int kQuantPerSm = 1;   // CTAs that an SM holds
 
-// A warp's share of a unit: [G][d] sums, [G] (reference, sum of weights).
+// A share of a unit: [G][d] sums, [G] (reference, sum of weights).
 constexpr int quant_slot_bytes(int d, int G) { return (G * d * 4 + G * 8 + 15) / 16 * 16; }
 
 // ---- rotary ------------------------------------------------------------------------
@@ -128,9 +128,8 @@ struct QuantAttendParams {
   const void *q;  // [n][hq][d]
   void *out;      // [n][hq][d], fp32 or the cache's type
   const int *page_table;
-  float *part_o;    // [2 x CTAs][G][d]
-  float2 *part_ml;  // [2 x CTAs][G]
-  char *firsts;     // [CTAs][warps][quant_slot_bytes]: what a warp starts with
+  char *parts;   // [2 x CTAs][quant_slot_bytes]: of units that several CTAs hold parts of
+  char *firsts;  // [CTAs][warps][quant_slot_bytes]: of units that a warp ends before its last
   int *tickets;     // [n][hkv], zero before and after
   int *err;
   ScoreRule rule;

@@ -395,8 +395,7 @@ spd_status spd_quant_decode_attention(spd_ctx *c, const void *q, const int *seq_
     p.q = static_cast<const char *>(q) + (size_t)b * row * 2;
     p.out = static_cast<char *>(out) + (size_t)b * row * oe;
     p.page_table = static_cast<const int *>(v.buf->page_table);
-    p.part_o = v.part_o;
-    p.part_ml = v.part_ml;
+    p.parts = v.parts;
     p.firsts = v.firsts;
     p.tickets = v.tickets;
     p.err = v.err;

@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
   uint64_t *const bars = reinterpret_cast<uint64_t *>(smem + S::kBars);
   __shared__ int unit_of[2 * kQuantWarps];  // of the warps' first and last partials, or -1
   __shared__ int last_flag[kQuantWarps];
-  __shared__ float share[2 * kQuantWarps][G];  // weights of the warps' partials
+  __shared__ int4 span_of[2 * kQuantWarps];     // their units' first and last CTA, second slot
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   char *const mine = ring + warp * S::kStages * S::kStage;
   uint64_t *const bar = bars + warp * S::kStages;
@@ -695,6 +695,13 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
     const int L = p.seqs[i].L, first = p.seqs[i].first;
     int t0 = (first / kQuantTile + at.tile) * kQuantTile;
     const int end = min(L, t0 + n * kQuantTile);
+    if (lane == 0) {  // (while the first copies are under way)
+      const int u0 = p.seqs[i].off + h * p.seqs[i].stride, per_cta = p.per_warp * kQuantWarps;
+      const int c0 = u0 / per_cta;
+      const int4 span = make_int4(c0, (u0 + at.tiles - 1) / per_cta, u0 != c0 * per_cta, 0);
+      if (done == 0) span_of[2 * warp] = span;
+      span_of[2 * warp + 1] = span;
+    }
     w.begin(p, i, h, lane);
 #pragma unroll 1
     for (; t0 < end; t0 += 2 * kQuantTile) {
@@ -756,151 +763,126 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
   // Partials of the same unit are joined: by the whole CTA where all are of one, else side by
   // side by four warps or one each.  (Unit after unit by the CTA, 1,024 units of 1,024 tokens
   // took 52 us, 44 side by side.)
-  auto slot_of = [&](int k) {
-    return reinterpret_cast<const float *>((k & 1 ? ring : firsts) + (k >> 1) * S::kSlot);
-  };
   constexpr int kSlots = 2 * kQuantWarps, kVectors = G * D / 4;
   static_assert(kSlots <= 32, "a lane per slot");
-  const int per_cta = p.per_warp * kQuantWarps;
   const int slot_unit = lane < kSlots ? unit_of[lane] : -1;
   const unsigned taken = __ballot_sync(kFull, slot_unit >= 0);
   const unsigned before = taken & ((1u << lane) - 1u);
   const int last_unit = __shfl_sync(kFull, slot_unit, before ? 31 - __clz(before) : 0);
   // (a unit's slots follow one another: its first one stands for it)
   unsigned units = __ballot_sync(kFull, slot_unit >= 0 && (!before || last_unit != slot_unit));
-  // Teams of threads: the CTA, three of four warps, or warps.
   const int found = __popc(units);
   const int width = found == 1 ? kThreads : found <= kThreads / 128 ? 128 : 32;
-  const bool whole_cta = found == 1;
   const int teams = kThreads / width, team = threadIdx.x / width, tid = threadIdx.x % width;
   auto sync = [&]() {
     if (width == 32) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(whole_cta ? 0 : 1 + team), "r"(width) : "memory");
+    else asm volatile("bar.sync %0, %1;" ::"r"(width == 128 ? 1 + team : 0), "r"(width) : "memory");
   };
+  const int sets = width >= kVectors ? width / kVectors : 1;
+  float4 *const sums = reinterpret_cast<float4 *>(ring + S::kLast) + team * width;
+  float2 *const stats = reinterpret_cast<float2 *>(ring + S::kLast + kThreads * 16) + team * width;
   for (int k = 0; k < team; ++k) units &= units - 1;  // from this team's first unit on
 #pragma unroll 1
   while (units) {
-    const int unit = __shfl_sync(kFull, slot_unit, __ffs(units) - 1);
+    const int slot0 = __ffs(units) - 1, unit = __shfl_sync(kFull, slot_unit, slot0);
     const unsigned members = __ballot_sync(kFull, slot_unit == unit);
     for (int k = 0; k < teams; ++k) units &= units - 1;
-    const int i = unit / p.hkv, h = unit - i * p.hkv;
-    const QuantAttendSeq &s = p.seqs[i];
-    const int u0 = s.off + h * s.stride;
-    const int c0 = u0 / per_cta, c1 = (u0 + s.tiles - 1) / per_cta;  // the unit's CTAs
+    const int c0 = span_of[slot0].x, c1 = span_of[slot0].y;  // the unit's CTAs
     const bool alone = c0 == c1;
     // this CTA's two partials: of a unit that it starts with, of one that it ends with
-    auto part = [&](int c) { return 2 * c + (c > c0 || u0 == c * per_cta ? 0 : 1); };
-    const size_t to_slot = part(blockIdx.x);
-    // the slots' weights, lane k for slot k
-    for (int head = tid / 32; head < G; head += width / 32) {
-      const bool mine = members >> lane & 1u;
-      const float *q = slot_of(mine ? lane : __ffs(members) - 1) + G * D + 2 * head;
-      const float m = mine ? q[0] : -CUDART_INF_F;
-      float top = m;
-#pragma unroll
-      for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, k));
-      const float f = mine ? ex2_approx(m - top) : 0.f;
-      float l = mine ? f * q[1] : 0.f;
-#pragma unroll
-      for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(kFull, l, k);
-      if (mine) share[lane][head] = alone ? f / l : f;
-      if (!alone && lane == 0) p.part_ml[to_slot * G + head] = make_float2(top, l);
-    }
-    sync();
-    for (int e = tid; e < kVectors; e += width) {
-      const int head = e / (D / 4);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (unsigned left = members; left; left &= left - 1) {
-        const int k = __ffs(left) - 1;
-        const float4 y = reinterpret_cast<const float4 *>(slot_of(k))[e];
-        const float f = share[k][head];
-        v.x = fmaf(f, y.x, v.x), v.y = fmaf(f, y.y, v.y);
-        v.z = fmaf(f, y.z, v.z), v.w = fmaf(f, y.w, v.w);
-      }
-      if (alone) store_out<T>(p.out, p.out_f32, (size_t)unit * G * D + 4 * e, v);
-      else reinterpret_cast<float4 *>(p.part_o + to_slot * G * D)[e] = v;
-    }
-    if (alone) continue;
-    // The last CTA of the unit to come joins its partials (in their order, whichever came
-    // last).  The barrier and the ticket's release publish them.
-    sync();
-    int last = 0;
-    if (tid == 0) {
-      last = atom_add_acq_rel_gpu(p.tickets + unit, 1) == c1 - c0;
-      if (last) p.tickets[unit] = 0;  // (for the next launch)
-      last_flag[team] = last;
-    }
-    sync();
-    last = last_flag[team];
-    if (!last) continue;
-    // The CTA's threads in kSets sets, each with every kSets-th partial, eight loads under way.
-    constexpr int kSets = kThreads / kVectors < 1 ? 1 : kThreads / kVectors;
-    const int sets = whole_cta ? kSets : 1, parts = c1 - c0 + 1;
-    float4 *const sums = reinterpret_cast<float4 *>(ring + S::kLast);
-    float2 *const stats = reinterpret_cast<float2 *>(sums + kSets * kVectors);
+    const int second = span_of[slot0].z;  // (the unit begins inside its first CTA)
+    char *const own = p.parts + (size_t)(2 * blockIdx.x + (blockIdx.x == c0 ? second : 0)) * S::kSlot;
+    // The sources: last partials of neighbouring warps, then perhaps a first one; and once more
+    // for the last CTA of the unit to come, every CTA's partial (in their order, whichever came
+    // last).
+    const unsigned odd = members & 0xaaaaaaaau, even = members & 0x55555555u;
+    const char *base = ring + (odd ? (__ffs(odd) - 1) >> 1 : 0) * S::kSlot;
+    int stride = S::kSlot, total = __popc(members), special = even ? total - 1 : -1;
+    const char *there = firsts + (even ? (__ffs(even) - 1) >> 1 : 0) * S::kSlot;
+    bool ends = alone;
 #pragma unroll 1
-    for (int x = tid; x < sets * kVectors; x += width) {
-      const int set = x / kVectors, e = x % kVectors, head = e / (D / 4);
-      float m = -CUDART_INF_F, l = 0.f;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int pass = 0; pass < 2; ++pass) {
+      // Threads in sets, each with every sets-th source, eight loads under way.
 #pragma unroll 1
-      for (int c = set; c < parts; c += 8 * sets) {
-        float2 ml[8];
-        float4 y[8];
+      for (int x = tid; x < sets * kVectors; x += width) {
+        const int set = x / kVectors, e = x % kVectors, head = e / (D / 4);
+        float m = -CUDART_INF_F, l = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int c = set; c < total; c += 8 * sets) {
+          float2 ml[8];
+          float4 y[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const size_t from = part(c0 + min(c + k * sets, parts - 1));
-          ml[k] = __ldcg(p.part_ml + from * G + head);
-          y[k] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + from * G * D) + e);
+          for (int k = 0; k < 8; ++k) {
+            const int at = c + k * sets;
+            ml[k] = make_float2(-CUDART_INF_F, 0.f);
+            y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (at < total) {
+              const char *from = at == special ? there : base + (size_t)at * stride;
+              ml[k] = reinterpret_cast<const float2 *>(from + G * D * 4)[head];
+              y[k] = reinterpret_cast<const float4 *>(from)[e];
+            }
+          }
+          float top = m;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) top = fmaxf(top, ml[k].x);
+          const float f0 = m == top ? 1.f : ex2_approx(m - top);
+          m = top;
+          l *= f0;
+          v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if (c + k * sets >= total) continue;
+            const float f = ex2_approx(ml[k].x - m);
+            l = fmaf(f, ml[k].y, l);
+            v.x = fmaf(f, y[k].x, v.x), v.y = fmaf(f, y[k].y, v.y);
+            v.z = fmaf(f, y[k].z, v.z), v.w = fmaf(f, y[k].w, v.w);
+          }
         }
-        float top = m;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (c + k * sets >= parts) ml[k] = make_float2(-CUDART_INF_F, 0.f);
-          top = fmaxf(top, ml[k].x);
+        if (sets > 1) {
+          sums[x] = v;
+          stats[x] = make_float2(m, l);
+          sync();
+          if (set > 0) continue;
+          for (int k = 1; k < sets && k < total; ++k) {
+            const float2 ml = stats[k * kVectors + e];
+            const float4 y = sums[k * kVectors + e];
+            const float top = fmaxf(m, ml.x);
+            const float f0 = m == top ? 1.f : ex2_approx(m - top), f = ex2_approx(ml.x - top);
+            m = top;
+            l = fmaf(f, ml.y, l * f0);
+            v.x = fmaf(f, y.x, v.x * f0), v.y = fmaf(f, y.y, v.y * f0);
+            v.z = fmaf(f, y.z, v.z * f0), v.w = fmaf(f, y.w, v.w * f0);
+          }
         }
-        const float f0 = m == top ? 1.f : ex2_approx(m - top);
-        m = top;
-        l *= f0;
-        v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (c + k * sets >= parts) continue;
-          const float f = ex2_approx(ml[k].x - m);
-          l = fmaf(f, ml[k].y, l);
-          v.x = fmaf(f, y[k].x, v.x), v.y = fmaf(f, y[k].y, v.y);
-          v.z = fmaf(f, y[k].z, v.z), v.w = fmaf(f, y[k].w, v.w);
+        if (ends) {
+          const float f = 1.f / l;
+          store_out<T>(p.out, p.out_f32, (size_t)unit * G * D + 4 * e,
+                       make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+        } else {
+          reinterpret_cast<float4 *>(own)[e] = v;
+          if (e % (D / 4) == 0) reinterpret_cast<float2 *>(own + G * D * 4)[head] = make_float2(m, l);
         }
       }
-      if (sets > 1) {
-        sums[x] = v;
-        stats[x] = make_float2(m, l);
-      } else {
-        const float f = 1.f / l;
-        store_out<T>(p.out, p.out_f32, (size_t)unit * G * D + 4 * e,
-                     make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+      if (ends) break;
+      // (the barrier and the ticket's release publish this CTA's partial, its acquire and the
+      // barrier behind show the others')
+      sync();
+      if (tid == 0) {
+        const int last = atom_add_acq_rel_gpu(p.tickets + unit, 1) == c1 - c0;
+        if (last) p.tickets[unit] = 0;  // (for the next launch)
+        last_flag[team] = last;
       }
+      sync();
+      if (!last_flag[team]) break;
+      ends = true;
+      base = p.parts + (size_t)2 * c0 * S::kSlot;
+      stride = 2 * S::kSlot;
+      special = second ? 0 : -1;
+      there = base + S::kSlot;
+      total = c1 - c0 + 1;
     }
-    if (sets == 1) continue;
-    __syncthreads();  // (of the whole CTA, which has this unit alone)
-    for (int e = tid; e < kVectors; e += kThreads) {
-      float m = stats[e].x, l = stats[e].y;
-      float4 v = sums[e];
-      for (int k = 1; k < kSets && k < parts; ++k) {
-        const float2 ml = stats[k * kVectors + e];
-        const float4 y = sums[k * kVectors + e];
-        const float top = fmaxf(m, ml.x);
-        const float f0 = m == top ? 1.f : ex2_approx(m - top), f = ex2_approx(ml.x - top);
-        m = top;
-        l = fmaf(f, ml.y, l * f0);
-        v.x = fmaf(f, y.x, v.x * f0), v.y = fmaf(f, y.y, v.y * f0);
-        v.z = fmaf(f, y.z, v.z * f0), v.w = fmaf(f, y.w, v.w * f0);
-      }
-      const float f = 1.f / l;
-      store_out<T>(p.out, p.out_f32, (size_t)unit * G * D + 4 * e,
-                   make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
-    }
+    sync();  // (the flag and the sums are used again)
   }
 }
 

@@ -225,9 +225,8 @@ struct CtxView {
   int *tickets;       // [ticket_seqs][num_kv_heads], zero between launches
   int ticket_seqs;
   int quant;          // bits of a quantised cache, or 0
-  float *part_o;      // quantised: partial sums (kQuantCtas x 2)
-  float2 *part_ml;
-  char *firsts;       // quantised: partial sums of single warps
+  char *parts;        // quantised: partial sums of CTAs (kQuantCtas x 2)
+  char *firsts;       // and of single warps
 };
 // Host facts only (no device call); ctx_device fills device, num_sms and the
 // tensor maps in, setting the context up on its device the first time.

@@ -152,10 +152,9 @@ const char *derive(const spd_config *c, Derived *d) {
     size_t off = kScratchHeader;
     sl.tickets_dec = off;
     off = round_up(off + (size_t)d->seqs_per_launch * c->num_kv_heads * 4, 256);
-    sl.part_ml = off;
-    off = round_up(off + (size_t)kQuantCtas * 2 * d->G * 8, 256);
+    sl.part_ml = off;  // (what lies before is cleared at the first call)
     sl.part_o = off;
-    off = round_up(off + (size_t)kQuantCtas * 2 * d->G * c->head_dim * 4, 256);
+    off = round_up(off + (size_t)kQuantCtas * 2 * quant_slot_bytes(c->head_dim, d->G), 256);
     sl.firsts = off;
     off = round_up(off + (size_t)kQuantCtas * kQuantWarps * quant_slot_bytes(c->head_dim, d->G), 256);
     sl.total = off;
@@ -923,8 +922,7 @@ void ctx_view(spd_ctx *c, CtxView *v) {
   v->tickets = reinterpret_cast<int *>(c->scratch(c->dv.sl.tickets_dec));
   v->ticket_seqs = c->dv.seqs_per_launch;
   v->quant = c->dv.quant;
-  v->part_o = c->dv.quant ? reinterpret_cast<float *>(c->scratch(c->dv.sl.part_o)) : nullptr;
-  v->part_ml = c->dv.quant ? reinterpret_cast<float2 *>(c->scratch(c->dv.sl.part_ml)) : nullptr;
+  v->parts = c->dv.quant ? c->scratch(c->dv.sl.part_o) : nullptr;
   v->firsts = c->dv.quant ? c->scratch(c->dv.sl.firsts) : nullptr;
 }
 
