@@ -59,16 +59,14 @@ long long tiles_of(long long first, long long n) {
 
 namespace spd {
 
-// Writes n_tokens tokens of each listed sequence (their pages are there); lengths are the
-// caller's to set.
+// Writes n_tokens tokens of each listed sequence (their pages are there, the context's device is
+// current); lengths are the caller's to set.
 spd_status quant_append(spd_ctx *c, const QuantWrite &w, const int *ids, int n, int n_tokens,
                         cudaStream_t st) {
   CtxView v;
-  spd_status r = ctx_device(c, st, &v);
+  const spd_status r = ctx_device(c, st, &v);
   if (r != SPD_OK) return r;
   const spd_config &cfg = *v.cfg;
-  DeviceGuard guard;
-  if ((r = guard.bind(v.device)) != SPD_OK) return fail_message(c, r, "cudaSetDevice failed");
   for (int b = 0; b < n; b += kQuantSeqs) {
     static thread_local QuantAppendParams p;
     p.n_seqs = std::min(kQuantSeqs, n - b);

@@ -69,6 +69,11 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
         "f"(c3));
 }
+__device__ __forceinline__ void add4(float *y, const float (&x)[4]) {
+  const float2 a = f2_add(make_float2(y[0], y[1]), make_float2(x[0], x[1]));
+  const float2 b = f2_add(make_float2(y[2], y[3]), make_float2(x[2], x[3]));
+  y[0] = a.x, y[1] = a.y, y[2] = b.x, y[3] = b.y;
+}
 __device__ __forceinline__ uint32_t pack_rz(float a, float b) {
   uint32_t r;
   asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
@@ -192,7 +197,7 @@ struct Warp {
     top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
     top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
     // q in [2^14, 2^15) at its largest: fp16 keeps all of its bits down to 2^-28 of that
-    const int e = max(exponent(top) - 14, -100);
+    const int e = max(exponent(top) - 14, -126);
     const float down = pow2(-e);
     float sum[NG];
 #pragma unroll
@@ -317,8 +322,7 @@ struct Warp {
     for (int a = 0; a < NG; ++a)
 #pragma unroll
       for (int n = 1; n < PER; ++n)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[a * PER][k] += acc[a * PER + n][k];
+        add4(acc[a * PER], acc[a * PER + n]);
     float kl[2][NG], ks[2][NG];
     params(buf, g, kl[0], ks[0]);
     params(buf, g + 8, kl[1], ks[1]);
@@ -511,12 +515,10 @@ struct Warp {
             float e[4];
             mma_f16(e, a0, b2[0][n][0], b2[0][n][1], 0.f, 0.f, 0.f, 0.f);
             mma_f16(e, a1, b2[1][n][0], b2[1][n][1], e[0], e[1], e[2], e[3]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) y[r] += e[r];
+            add4(y, e);
           }
           mma_f16(d, a1, b[1][n][0], b[1][n][1], d[0], d[1], d[2], d[3]);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) y[r] += d[r];
+          add4(y, d);
         } else {
           mma_f16(o[s], a0, b[0][n][0], b[0][n][1], y[0], y[1], y[2], y[3]);
           mma_f16(o[s], a1, b[1][n][0], b[1][n][1], y[0], y[1], y[2], y[3]);

@@ -22,6 +22,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "api_util.h"
 #include "quant.h"
 #include "spd.h"
 #include "spd_internal.h"
@@ -995,6 +996,8 @@ spd_status append_quantised(spd_ctx *c, const QuantWrite &w, const int *ids, int
   spd_status r = check_append(c, ids, n, n_tokens, w.k, w.v);
   if (r != SPD_OK) return r;
   if ((r = ensure_device(c, st)) != SPD_OK) return r;
+  DeviceGuard guard;
+  if ((r = guard.bind(c->device)) != SPD_OK) return c->fail(r, "cudaSetDevice failed");
   for (int i = 0; i < n; ++i) take_pages(c, ids[i], n_tokens);
   if ((r = flush_page_table(c, st)) != SPD_OK) return r;
   if ((r = quant_append(c, w, ids, n, n_tokens, st)) != SPD_OK) return r;

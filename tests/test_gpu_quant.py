@@ -287,6 +287,34 @@ def test_rotated_on_the_way(n, tokens, bits, d, dtype, kind):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("n,tokens", [(2, 2600), (290, 19), (1, 5003)])
+@pytest.mark.parametrize("kind", ["places", "positions", "in place"])
+def test_rotated_on_the_way_in_long_and_wide_appends(n, tokens, kind):
+    """Queries in a launch of their own, and more sequences than a launch holds."""
+    hq, hkv, d, dt = 4, 2, 64, torch.bfloat16
+    c = cache(hq, hkv, d, "bf16", 4, tokens + 3, seqs=2 * n, page=64)
+    t = spd.Rotary(d, neighbours=True)
+    a, b = ([c.seq_create() for _ in range(n)] for _ in range(2))
+    for ids in (a, b):
+        for i, s in enumerate(ids):  # sequences that begin at different places
+            if i % 3:
+                c.kv_append([s], rows(i, 1, i % 3, hkv, d, "bf16"), rows(i, 1, i % 3, hkv, d, "bf16"))
+    q, k, v = (normal(i, n, tokens, h, d, dtype=dt) for i, h in ((1, hq), (2, hkv), (3, hkv)))
+    start = torch.tensor([i % 3 for i in range(n)], device="cuda", dtype=torch.int32)[:, None]
+    pos = start + torch.arange(tokens, device="cuda", dtype=torch.int32)
+    if kind != "places":
+        pos = places(4, n, tokens)
+    wq, wk = spd.rotary(t, pos.flatten(), q.flatten(0, 1), k.flatten(0, 1))
+    c.kv_append(a, wk.view(k.shape), v)
+    gq = c.kv_append_rotary(b, t, q, k, v, positions=None if kind == "places" else pos,
+                            out=q if kind == "in place" else None)
+    c.check_status()
+    assert torch.equal(gq, wq.view(gq.shape))
+    for x, y in zip(c.kv_read(a, -tokens), c.kv_read(b, -tokens)):
+        assert torch.equal(x, y)
+    check_held(c.kv_read(b, -tokens)[1], v, 4)
+
+
 def test_rotated_in_place():
     c = cache(4, 2, 128, "bf16", 8, 40)
     s, t = c.seq_create(), spd.Rotary(128)
@@ -398,6 +426,17 @@ def test_attend_more_sequences_than_a_launch_holds():
     check_attend(lens, 4, 1, 64, "bf16", 4, page=16)
 
 
+def test_reads_more_sequences_than_a_launch_holds():
+    c = cache(1, 1, 64, "fp16", 8, 40, seqs=260, page=16)
+    ids = [c.seq_create() for _ in range(260)]
+    k, v = rows(1, 260, 33, 1, 64, "fp16"), rows(2, 260, 33, 1, 64, "fp16")
+    c.kv_append(ids, k, v)
+    gk, gv = c.kv_read(ids)
+    check_held(gk, k, 8)
+    check_held(gv, v, 8)
+    c.check_status()
+
+
 @pytest.mark.parametrize("bits", [8, 4])
 def test_attend_scores_in_rising_and_falling_order(bits):
     """The reference of the weights moves with every tile, or never again."""
@@ -436,6 +475,17 @@ def test_attend_queries_of_every_size(gain, dtype):
     scale = 1e-5 if gain > 1 else 0.0
     check_attend([90], 4, 1, 64, dtype, 8, out="fp32", gain=gain, scale=scale)
     check_attend([90], 8, 1, 128, dtype, 4, gain=gain, scale=scale)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("rule", [dict(), dict(softcap=9.0), dict(slopes=True)])
+def test_attend_queries_and_keys_at_the_ends_of_the_range(bits, rule):
+    """Scores of ordinary size from queries near 2^110 (whose factor comes in two) and keys near
+    2^-110, and the other way round."""
+    for up in (2.0 ** 110, 2.0 ** -110):
+        def kv(i, L):
+            return (rows(11, 1, L, 1, 128, "bf16").double() / up).bfloat16(), rows(12, 1, L, 1, 128, "bf16")
+        check_attend([70], 4, 1, 128, "bf16", bits, out="fp32", kv=kv, gain=up, **rule)
 
 
 def test_attend_what_is_not_finite():
