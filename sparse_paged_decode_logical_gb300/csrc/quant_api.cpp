@@ -42,7 +42,7 @@ spd_status need_quant(spd_ctx *c, const CtxView &v) {
 // few; each makes the tile's sines again.
 int parts_of(long long tiles, int works, int sms) {
   const int most = (works + kQuantWriteWarps - 1) / kQuantWriteWarps;
-  return (int)std::max<long long>(1, std::min<long long>(most, 6LL * sms / std::max(tiles, 1LL)));
+  return (int)std::max<long long>(1, std::min<long long>(most, 14LL * sms / std::max(tiles, 1LL)));
 }
 
 // A rotary launch takes up to kRotaryTokens tokens a CTA, fewer where that leaves SMs idle.

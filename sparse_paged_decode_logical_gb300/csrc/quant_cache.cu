@@ -65,22 +65,25 @@ __device__ __forceinline__ uint32_t join(uint32_t e, int lane_mask) {
   return min2_nan<T>(e, __shfl_xor_sync(kFull, e, lane_mask));
 }
 
-// The code of a distance d from lo, given one that may be one off: (code + 1/2) step is an exact
-// product.  Apart, and in a loop over four: 1 warp in 5 comes here in bf16, and copies in every
-// place would fill the instruction cache.
-__device__ __noinline__ uint32_t exact_codes(float2 a, float2 b, float step, uint32_t codes) {
-  uint32_t r = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float d = i == 0 ? a.x : i == 1 ? a.y : i == 2 ? b.x : b.y;
-    const int c = (int)(codes >> (8 * i) & 255u);
-    const float over = ((float)c + 0.5f) * step, under = ((float)c - 0.5f) * step;
-    const bool odd = c & 1;
-    const int n = c + (d > over || (d == over && odd) ? 1 : 0) -
-                  (d < under || (d == under && odd) ? 1 : 0);
-    r |= (uint32_t)(n & 255) << (8 * i);
-  }
-  return r;
+constexpr float kMagic = 12582912.f;  // 1.5 2^23: added, it leaves a rounded number in the low bits
+
+// The low bytes of four numbers.
+__device__ __forceinline__ uint32_t low_bytes(float2 a, float2 b) {
+  return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                     __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
+}
+// A code n (kMagic + n in y) for a distance d, which may be one off: what n step leaves of d, an
+// exact difference, is compared with half a step, ties to even.
+__device__ __forceinline__ float exact_code(float y, float d, float step) {
+  const float r = fmaf(kMagic - y, step, d), twice = fabsf(r) + fabsf(r);
+  const bool odd = __float_as_uint(y) & 1u;
+  return twice > step || (twice == step && odd) ? y + copysignf(1.f, r) : y;
+}
+// Apart: 1 warp in 5 comes here in bf16, and copies in every place would fill the instruction
+// cache.
+__device__ __noinline__ uint32_t exact_codes(float2 ya, float2 yb, float2 a, float2 b, float step) {
+  return low_bytes(make_float2(exact_code(ya.x, a.x, step), exact_code(ya.y, a.y, step)),
+                   make_float2(exact_code(yb.x, b.x, step), exact_code(yb.y, b.y, step)));
 }
 
 // What a group's codes are made with.
@@ -126,10 +129,10 @@ struct Scale {
   // round((x - lo) / step), ties to even, of the four channels of a pair of words: bytes.  The
   // product with 1 / step is off by less than 2^-21 of a quotient of at most LEVELS; where one
   // lies closer than that to the middle between two codes, exact_code decides.  (In bf16 that is
-  // common, values and steps have 8 bits.)  Rounded by adding 1.5 2^23, whose low bits then are
-  // the code: a conversion to an integer runs at a quarter of the rate.
+  // common, values and steps have 8 bits.)  Rounded by adding kMagic, whose low
+  // bits then are the code: a conversion to an integer runs at a quarter of the rate.
   __device__ __forceinline__ uint32_t codes(uint32_t v0, uint32_t v1) const {
-    constexpr float kMagic = 12582912.f, kNear = 0.5f - LEVELS * 0x1p-21f;
+    constexpr float kNear = 0.5f - LEVELS * 0x1p-21f;
     const float2 l = make_float2(lo, lo), r = make_float2(inv, inv), m = make_float2(kMagic, kMagic);
     float2 a = unpack2<T>(v0), b = unpack2<T>(v1);
     if (tiny) {
@@ -141,12 +144,7 @@ struct Scale {
     const float2 ta = f2_mul(a, r), tb = f2_mul(b, r), ya = f2_add(ta, m), yb = f2_add(tb, m);
     const float2 ea = f2_sub(ta, f2_sub(ya, m)), eb = f2_sub(tb, f2_sub(yb, m));
     const float near = fmaxf(fmax3f(fabsf(ea.x), fabsf(ea.y), fabsf(eb.x)), fabsf(eb.y));
-    const uint32_t c = bytes(ya.x, ya.y, yb.x, yb.y);
-    return near >= kNear ? exact_codes(a, b, step, c) : c;
-  }
-  static __device__ __forceinline__ uint32_t bytes(float a, float b, float c, float d) {
-    return __byte_perm(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040),
-                       __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040), 0x5410);
+    return near >= kNear ? exact_codes(ya, yb, a, b, step) : low_bytes(ya, yb);
   }
 };
 
