@@ -390,6 +390,7 @@ class SparsePagedKVCache:
         self._append_rotary_fn = L.spd_kv_append_rotary
         self._quant_attend_fn = L.spd_quant_decode_attention
         self._length_fn, self._length = L.spd_seq_info, ctypes.c_longlong()
+        self._create_fn, self._free_fn, self._new_id = L.spd_seq_create, L.spd_seq_free, ctypes.c_int()
 
     def __del__(self):
         ctx = getattr(self, "ctx", None)
@@ -413,10 +414,15 @@ class SparsePagedKVCache:
         return t.data_ptr()
 
     def seq_create(self):
-        return spd_seq_create(self.ctx)
+        st = self._create_fn(self.ctx, self._new_id)
+        if st != SPD_OK:
+            _check(st, "spd_seq_create", self.ctx)
+        return self._new_id.value
 
     def seq_free(self, seq_id):
-        spd_seq_free(self.ctx, seq_id)
+        st = self._free_fn(self.ctx, int(seq_id))
+        if st != SPD_OK:
+            _check(st, "spd_seq_free", self.ctx)
 
     def seq_reserve(self, seq_id, n_tokens):
         spd_seq_reserve(self.ctx, seq_id, n_tokens)
@@ -683,11 +689,10 @@ class SparsePagedKVCache:
         :func:`prefill_attention`."""
         ids, n = self._id_array(seq_ids)
         begin = int(begin)
-        if n_tokens is None:
-            if begin < 0 or not n:
-                n_tokens = -begin
-            else:
-                n_tokens = min([self._seq_length(s) for s in seq_ids]) - begin
+        rest = n_tokens is None
+        if rest:
+            # (where the first sequence is not the shortest the library refuses, and all are asked)
+            n_tokens = -begin if begin < 0 or not n else self._seq_length(seq_ids[0]) - begin
         n_tokens = int(n_tokens)
         # (refused before a buffer is made of that size)
         if n_tokens < 1 or n_tokens > self.cfg.max_context or abs(begin) > _MAX_TOKENS:
@@ -698,6 +703,10 @@ class SparsePagedKVCache:
         st = lib().spd_kv_read(self.ctx, ids, n, begin, n_tokens, k.data_ptr(), v.data_ptr(),
                                self._stream(stream) or None)
         if st != SPD_OK:
+            if st == 4 and rest and begin >= 0:
+                least = min([self._seq_length(s) for s in seq_ids]) - begin
+                if least < n_tokens:
+                    return self.kv_read(seq_ids, begin, least, stream)
             _check(st, "spd_kv_read", self.ctx)
         return k, v
 

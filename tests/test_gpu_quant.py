@@ -251,7 +251,8 @@ def test_reading_ranges():
             a = L + begin if begin < 0 else begin
             assert torch.equal(k[r], whole[r][0][0, a:a + n])
             assert torch.equal(v[r], whole[r][1][0, a:a + n])
-    assert c.kv_read(ids, 7)[0].shape[1] == 54 and c.kv_read(ids, -9)[0].shape[1] == 9
+    assert c.kv_read(ids, 7)[0].shape[1] == 54 and c.kv_read(ids[::-1], 7)[0].shape[1] == 54
+    assert c.kv_read(ids, -9)[0].shape[1] == 9
     for begin, n in ((0, 62), (-62, 1), (61, 1), (-1, 2), (100, 1), (5, 0), (0, 1 << 40)):
         with pytest.raises(spd.SpdError):
             c.kv_read(ids, begin, n)
