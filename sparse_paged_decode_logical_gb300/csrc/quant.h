@@ -6,6 +6,7 @@
 
 #include "dense.h"
 #include "spd.h"
+#include "spd_internal.h"
 
 namespace spd {
 
@@ -81,6 +82,11 @@ struct QuantSeq {
   int first;  // first token of this call's
   int off;    // writing and reading: the tiles of the sequences before
 };
+struct QuantAppendSeq {
+  int slot, first, off;  // as QuantSeq
+  int page, pages, upd;  // its pages [page, page + pages) are upd[upd], ...: not in the table yet
+};
+constexpr int kQuantUpdates = 128;
 struct QuantAppendParams {
   spd_rotary_table table;  // (with rotate)
   const void *k, *v, *q;   // [n_seqs][n_tokens][heads][d], tokens at strides
@@ -88,15 +94,17 @@ struct QuantAppendParams {
   long long k_stride, v_stride, q_stride;
   const int *positions;  // [axes][n_seqs][n_tokens] or null: a token's place in its sequence
   void *pool;
-  const int *page_table;
+  int *page_table;
   int *err;
   int n_seqs, n_tokens, hq, hkv, P, max_pp, num_phys;
+  int n_updates;   // entries of the page table that this launch writes, any sequence's
+  PtUpdate updates[kQuantUpdates];
   int total_seqs;  // sequences of the whole call (positions' axes are this far apart)
   int seq0;        // sequences before this launch's
   int rotate;      // keys, and hq heads of queries
   int tiles;       // of all sequences
   int parts;       // CTAs per tile, each with an equal share of the heads
-  QuantSeq seqs[kQuantSeqs];
+  QuantAppendSeq seqs[kQuantSeqs];
 };
 cudaError_t launch_quant_append(const QuantAppendParams &p, int dtype, int d, int bits,
                                 cudaStream_t st);

@@ -59,10 +59,22 @@ long long tiles_of(long long first, long long n) {
 
 namespace spd {
 
+bool quant_takes(const int *ids, int n, const PtUpdate *updates, int n_updates) {
+  if (n > kQuantSeqs || n_updates > kQuantUpdates) return false;
+  // entries of one sequence follow one another, in order
+  for (int u = 1; u < n_updates; ++u) {
+    const bool same = updates[u].slot == updates[u - 1].slot;
+    if (same ? updates[u].index != updates[u - 1].index + 1 : false) return false;
+    for (int k = 0; !same && k + 1 < u; ++k)
+      if (updates[k].slot == updates[u].slot) return false;
+  }
+  return true;
+}
+
 // Writes n_tokens tokens of each listed sequence (their pages are there, the context's device is
 // current); lengths are the caller's to set.
 spd_status quant_append(spd_ctx *c, const QuantWrite &w, const int *ids, int n, int n_tokens,
-                        cudaStream_t st) {
+                        const PtUpdate *updates, int n_updates, cudaStream_t st) {
   CtxView v;
   const spd_status r = ctx_device(c, st, &v);
   if (r != SPD_OK) return r;
@@ -73,8 +85,22 @@ spd_status quant_append(spd_ctx *c, const QuantWrite &w, const int *ids, int n, 
     long long tiles = 0;
     for (int i = 0; i < p.n_seqs; ++i) {
       const long long L = seq_length(c, ids[b + i]);
-      p.seqs[i] = QuantSeq{ids[b + i], (int)L, (int)tiles};
+      p.seqs[i] = QuantAppendSeq{ids[b + i], (int)L, (int)tiles, 0, 0, 0};
       tiles += tiles_of(L, n_tokens);
+    }
+    p.n_updates = n_updates;  // (one launch where there are any: quant_takes)
+    for (int u = 0, at = 0; u < n_updates; ++u) {
+      p.updates[u] = updates[u];
+      if (u > 0 && updates[u].slot == updates[at].slot) continue;
+      at = u;
+      int many = 1;
+      while (u + many < n_updates && updates[u + many].slot == updates[u].slot) ++many;
+      for (int i = 0; i < p.n_seqs; ++i)
+        if (p.seqs[i].slot == updates[u].slot) {
+          p.seqs[i].page = updates[u].index;
+          p.seqs[i].pages = many;
+          p.seqs[i].upd = u;
+        }
     }
     // Queries of few tokens are rotated by the same launch, those of many by one of their own,
     // whose threads need a third of the registers (16,385 tokens of 32 and 8 heads, 8 bits: 84 us;
@@ -95,7 +121,7 @@ spd_status quant_append(spd_ctx *c, const QuantWrite &w, const int *ids, int n, 
     p.q_stride = w.q_stride;
     p.positions = w.positions;
     p.pool = v.buf->k_pool;
-    p.page_table = static_cast<const int *>(v.buf->page_table);
+    p.page_table = static_cast<int *>(v.buf->page_table);
     p.err = v.err;
     p.n_tokens = n_tokens;
     p.hkv = cfg.num_kv_heads;

@@ -316,24 +316,27 @@ __device__ __forceinline__ void put_row(char *half, int lane, int r, bool is_v, 
   }
 }
 
-// The tile of a sequence's token t0 (a multiple of 16) and kv head, or null (with the error
-// word set) where the page table points outside the pool.
-template <int BYTES>
-__device__ __forceinline__ char *tile_at(const void *pool, const int *page_table, int slot, int t0,
-                                         int h, int hkv, int P, int max_pp, int num_phys, int *err) {
-  const int blk = t0 / P;
+// The physical page of a sequence's block, or -1 (with the error word set) where the page table
+// has none in the pool.
+__device__ __forceinline__ int page_of(const int *page_table, int slot, int blk, int max_pp,
+                                       int num_phys, int *err) {
   if (blk >= max_pp) {
-    qc_set_err(err, kDevBadPage, slot, t0, blk);
-    return nullptr;
+    qc_set_err(err, kDevBadPage, slot, 0, blk);
+    return -1;
   }
   const int phys = page_table[(size_t)slot * max_pp + blk];
   if (phys < 0 || phys >= num_phys) {
     qc_set_err(err, kDevBadPhys, slot, blk, phys);
-    return nullptr;
+    return -1;
   }
+  return phys;
+}
+// The tile of token t0 (a multiple of 16) and kv head h on a page.
+template <int BYTES>
+__device__ __forceinline__ char *tile_at(const void *pool, int phys, int t0, int h, int hkv, int P) {
   const size_t tiles = P / kQuantTile;
   return static_cast<char *>(const_cast<void *>(pool)) +
-         (((size_t)phys * hkv + h) * tiles + (t0 - blk * P) / kQuantTile) * BYTES;
+         (((size_t)phys * hkv + h) * tiles + t0 % P / kQuantTile) * BYTES;
 }
 
 // ---- write ---------------------------------------------------------------------------
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 5)
     if (p.seqs[mid].off <= item) i = mid, lo = mid + 1;
     else hi = mid;
   }
-  const QuantSeq s = p.seqs[i];
+  const QuantAppendSeq s = p.seqs[i];
   const int t0 = s.first / kQuantTile * kQuantTile + (item - s.off) * kQuantTile;
   const int a = max(t0, s.first), b = min(t0 + kQuantTile, s.first + p.n_tokens), n = b - a;
   const long long tok0 = (long long)(p.seq0 + i) * p.n_tokens + (a - s.first);  // of the call
@@ -412,10 +415,18 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 5)
     });
     __syncthreads();
   }
+  // New pages come with the launch, which also writes them to the table: a decode step whose
+  // sequences take pages is one launch.
+  if (blockIdx.x == 0)
+    for (int u = threadIdx.x; u < p.n_updates; u += kWriteWarps * 32)
+      p.page_table[(size_t)p.updates[u].slot * p.max_pp + p.updates[u].index] = p.updates[u].phys;
+  const int blk = t0 / p.P, fresh = blk - s.page;
+  const int phys = fresh >= 0 && fresh < s.pages
+                       ? p.updates[s.upd + fresh].phys
+                       : page_of(p.page_table, s.slot, blk, p.max_pp, p.num_phys, p.err);
 #pragma unroll 1
   for (; h < p.hkv; h += step) {
-    char *tile = tile_at<Q::kBytes>(p.pool, p.page_table, s.slot, t0, h, p.hkv, p.P, p.max_pp,
-                                    p.num_phys, p.err);
+    char *tile = phys < 0 ? nullptr : tile_at<Q::kBytes>(p.pool, phys, t0, h, p.hkv, p.P);
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncwarp();
     if (tile) {
@@ -477,9 +488,9 @@ __global__ void __launch_bounds__(kReadWarps * 32)
   const int end = s.first + p.n_tokens;
   const bool is_v = w >= p.hkv;
   const int h = is_v ? w - p.hkv : w;
-  const char *tile = tile_at<Q::kBytes>(p.pool, p.page_table, s.slot, t0, h, p.hkv, p.P, p.max_pp,
-                                        p.num_phys, p.err);
-  if (!tile) return;
+  const int phys = page_of(p.page_table, s.slot, t0 / p.P, p.max_pp, p.num_phys, p.err);
+  if (phys < 0) return;
+  const char *tile = tile_at<Q::kBytes>(p.pool, phys, t0, h, p.hkv, p.P);
   const char *half = tile + (is_v ? Q::kHalf : 0);
   uint32_t x[Q::kWords];
 #pragma unroll

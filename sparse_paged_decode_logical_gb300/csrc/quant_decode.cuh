@@ -778,12 +778,18 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
   unsigned units = __ballot_sync(kFull, slot_unit >= 0 && (!before || last_unit != slot_unit));
   const int found = __popc(units);
   const int width = found == 1 ? kThreads : found <= kThreads / 128 ? 128 : 32;
-  const int teams = kThreads / width, team = threadIdx.x / width, tid = threadIdx.x % width;
+  // (selected, not divided: that would take longer than the ballots)
+  const bool fours = width == 128, single = width == 32;
+  const int teams = single ? kQuantWarps : fours ? kThreads / 128 : 1;
+  const int team = single ? warp : fours ? warp >> 2 : 0;
+  const int tid = threadIdx.x - team * width;
   auto sync = [&]() {
-    if (width == 32) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(width == 128 ? 1 + team : 0), "r"(width) : "memory");
+    if (single) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(fours ? 1 + team : 0), "r"(width) : "memory");
   };
-  const int sets = width >= kVectors ? width / kVectors : 1;
+  const int sets = single ? (32 > kVectors ? 32 / kVectors : 1)
+                   : fours ? (128 > kVectors ? 128 / kVectors : 1)
+                           : (kThreads > kVectors ? kThreads / kVectors : 1);
   float4 *const sums = reinterpret_cast<float4 *>(ring + S::kLast) + team * width;
   float2 *const stats = reinterpret_cast<float2 *>(ring + S::kLast + kThreads * 16) + team * width;
   for (int k = 0; k < team; ++k) units &= units - 1;  // from this team's first unit on

@@ -247,8 +247,11 @@ struct QuantWrite {
   long long k_stride, v_stride, q_stride;  // elements between tokens
   const int *positions;
 };
+// updates: entries of the page table that the launch writes.  Where it cannot take them (too
+// many, or a sequence's do not follow one another) quant_takes says so, and they go first.
+bool quant_takes(const int *ids, int n, const PtUpdate *updates, int n_updates);
 spd_status quant_append(spd_ctx *c, const QuantWrite &w, const int *ids, int n, int n_tokens,
-                        cudaStream_t st);
+                        const PtUpdate *updates, int n_updates, cudaStream_t st);
 // Checks, pages, quant_append and the new lengths.
 spd_status append_quantised(spd_ctx *c, const QuantWrite &w, const int *ids, int n, int n_tokens,
                             cudaStream_t st);

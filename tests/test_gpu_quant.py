@@ -325,6 +325,44 @@ def test_rotated_in_place():
     assert torch.equal(q[0], want)
 
 
+def test_new_pages_of_every_kind():
+    """Pages taken by the append itself, many at once, reserved before (also for others, and in
+    an order that does not follow), given back before they were written."""
+    c = cache(2, 1, 64, "fp16", 8, 3700, seqs=6, page=16, seed=9)
+    k, v = rows(1, 1, 3700, 1, 64, "fp16"), rows(2, 1, 3700, 1, 64, "fp16")
+    q = normal(3, 1, 2, 64, dtype=torch.float16)
+    ids = [c.seq_create() for _ in range(5)]
+    length = dict.fromkeys(ids, 0)
+
+    def put(which, n):
+        for i in which:
+            assert length[i] == length[which[0]]
+        a = length[which[0]]
+        c.kv_append(which, k[:, a:a + n].repeat(len(which), 1, 1, 1), v[:, a:a + n].repeat(len(which), 1, 1, 1))
+        for i in which:
+            length[i] += n
+
+    put(ids[:2], 3)                 # a page each
+    put([ids[0]], 1100)             # 69 pages
+    c.seq_reserve(ids[2], 100)      # another's, written by the next append of anyone
+    put([ids[0]], 2500)             # 156: more than a launch takes along
+    put([ids[1]], 40)
+    c.seq_reserve(ids[3], 20)
+    c.seq_reserve(ids[4], 20)
+    c.seq_reserve(ids[3], 60)       # not behind its own first ones
+    put(ids[2:5], 90)
+    c.seq_reserve(ids[2], 200)
+    c.seq_truncate(ids[2], 90)      # given back before anyone wrote them
+    put(ids[2:5], 31)
+    for i in ids:
+        gk, gv = c.kv_read([i])
+        check_held(gk, k[:, :length[i]], 8)
+        check_held(gv, v[:, :length[i]], 8)
+        ref, tol = attend(q[0], k[0, :length[i]], v[0, :length[i]], 8)
+        within(c.quant_decode_attention(q, [i])[0], ref, tol(F32))
+    c.check_status()
+
+
 def test_truncated_sequences_go_on():
     c = cache(2, 1, 64, "bf16", 4, 200, page=32)
     s = c.seq_create()
