@@ -52,6 +52,11 @@ constexpr int kQuantWarps = 12;  // per CTA
 constexpr int kQuantWriteWarps = 4;  // of a writing CTA
 constexpr int kQuantPerSm = 1;   // CTAs that an SM holds
 
+// Tiles that a warp takes in one step: what a step costs besides is shared by them, and their
+// chains of products fill one another's gaps (one tile a step: 42 instead of 37 us on 131,072
+// tokens of 128 channels in 4 bits; 16 warps of 128 registers with one: 49).
+constexpr int quant_step_tiles(int d) { return d == 64 ? 4 : 2; }
+
 // A share of a unit: [G][d] sums, [G] (reference, sum of weights).
 constexpr int quant_slot_bytes(int d, int G) { return (G * d * 4 + G * 8 + 15) / 16 * 16; }
 

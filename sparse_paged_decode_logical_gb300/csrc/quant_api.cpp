@@ -387,10 +387,10 @@ spd_status spd_quant_decode_attention(spd_ctx *c, const void *q, const int *seq_
     if (total > kMaxPlaces)
       return fail_message(c, SPD_ERR_CAPACITY, "a sequence is too long for one launch");
     // Every warp takes per_warp tiles.  Where all units can begin at a CTA of their own
-    // without another tile per warp they do, so that no unit has a stray part elsewhere.
+    // without another step per warp they do, so that no unit has a stray part elsewhere.
     const long long warps = (long long)most_ctas * kQuantWarps;
-    p.per_warp = (int)std::max<long long>(2, (total + warps - 1) / warps);
-    p.per_warp += p.per_warp & 1;  // (a step takes two)
+    const int step = quant_step_tiles(cfg.head_dim);
+    p.per_warp = (int)((total + warps - 1) / warps + step - 1) / step * step;  // (whole steps)
     auto ctas_of = [&](int per_warp) {  // with units that begin at CTAs
       long long k = 0;
       for (int i = 0; i < n; ++i)
@@ -399,8 +399,8 @@ spd_status spd_quant_decode_attention(spd_ctx *c, const void *q, const int *seq_
       return k;
     };
     int whole = p.per_warp;
-    const int give = std::max(whole + whole / 16, whole + 2);
-    while (whole < give && ctas_of(whole) > most_ctas) whole += 2;
+    const int give = std::max(whole + whole / 16, whole + step);
+    while (whole < give && ctas_of(whole) > most_ctas) whole += step;
     if (ctas_of(whole) <= most_ctas) {
       p.per_warp = whole;
       const int per_cta = whole * kQuantWarps;

@@ -61,7 +61,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// D = A B + C in fp16 with fp32 sums; not volatile, so that what belongs to a step's two tiles is
+// D = A B + C in fp16 with fp32 sums; not volatile, so that what belongs to a step's tiles is
 // scheduled into one another.
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1, float c0, float c1, float c2, float c3) {
@@ -91,7 +91,7 @@ template <int D, int BITS, int G>
 struct Shape {
   using Q = QuantTile<D, BITS>;
   static constexpr int kSlot = quant_slot_bytes(D, G);  // one warp's partial
-  static constexpr int kStage = 2 * Q::kBytes;          // a step's two tiles
+  static constexpr int kStage = quant_step_tiles(D) * Q::kBytes;
   // the CTAs of an SM share its 227 KB; the ring holds the partials at the end, too
   static constexpr int kMemory = (227 / kQuantPerSm - 2) * 1024;
   static constexpr int kFit = kMemory / (kQuantWarps * kStage);
@@ -156,6 +156,7 @@ template <typename T, int D, int BITS, int G, int MODE>
 struct Warp {
   using Q = QuantTile<D, BITS>;
   static constexpr int KS = D / 16;     // k-steps of S, m-tiles of O
+  static constexpr int NT = quant_step_tiles(D);
   static constexpr int NG = Q::kGroups;
   // MODE 0: outputs in bf16, weights of 11 bits.  1: in fp16, weights of 22 bits.  2: in fp32,
   // and sums to fp32's own error.
@@ -372,26 +373,26 @@ struct Warp {
     }
   }
 
-  // A step: the tiles of tokens t0 .. t0 + 31, those in [first, end) attended (the second tile
-  // may hold none, and then anything).
+  // A step: the NT tiles from token t0 on, tokens in [first, end) attended (tiles behind the
+  // first may hold none, and then anything).
   __device__ __forceinline__ void step(const QuantAttendParams &p, const char *buf, int t0,
                                        int first, int end, int L, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    float x[2][4], vl[2][2][NG], vs[2][2][NG];
+    float x[NT][4], vl[NT][2][NG], vs[NT][2][NG];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) sums(buf + j * Q::kBytes, lane, x[j]);
+    for (int j = 0; j < NT; ++j) sums(buf + j * Q::kBytes, lane, x[j]);
     if (!plain) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) rule(p, (float)(L - 1 - t0 - g) - 16.f * j, x[j]);
+      for (int j = 0; j < NT; ++j) rule(p, (float)(L - 1 - t0 - g) - 16.f * j, x[j]);
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int r = 0; r < 2; ++r)
         params(buf + j * Q::kBytes + Q::kHalf, g + 8 * r, vl[j][r], vs[j][r]);
-    if (t0 < first || t0 + 2 * kQuantTile > end) {
+    if (t0 < first || t0 + NT * kQuantTile > end) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int at = t0 + 16 * j + 8 * r + g;
@@ -402,9 +403,9 @@ struct Warp {
         }
     }
     // p, and the largest it, with the largest step, could make a weight
-    float pr[2][4], most = 0.f, pm[2] = {0.f, 0.f};
+    float pr[NT][4], most = 0.f, pm[2] = {0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < NT; ++j) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) pr[j][k] = ex2_approx(x[j][k] - m[k & 1]);
 #pragma unroll
@@ -421,7 +422,7 @@ struct Warp {
         // z: the largest p step so far, as a power of 2
         if (m[c] != -CUDART_INF_F) z = m[c] + (float)(kRoom - k2[c]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             a = fmaxf(a, x[j][2 * r + c]);
@@ -452,13 +453,13 @@ struct Warp {
         }
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) pr[j][k] = ex2_approx(x[j][k] - m[k & 1]);
     }
-    uint32_t b[2][NG][2], b2[2][kTwo ? NG : 1][2];
+    uint32_t b[NT][NG][2], b2[NT][kTwo ? NG : 1][2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < NT; ++j) {
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -498,9 +499,9 @@ struct Warp {
     constexpr int W = BITS / 4;
 #pragma unroll
     for (int c = 0; c < Q::kWords / 4; ++c) {
-      uint32_t wd[2][4];
+      uint32_t wd[NT][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < NT; ++j) {
         const uint4 v =
             reinterpret_cast<const uint4 *>(buf + j * Q::kBytes + Q::kHalf)[c * 32 + lane];
         wd[j][0] = v.x, wd[j][1] = v.y, wd[j][2] = v.z, wd[j][3] = v.w;
@@ -508,27 +509,22 @@ struct Warp {
 #pragma unroll
       for (int k = 0; k < 4 / W; ++k) {
         const int s = c * (4 / W) + k, n = s * NG / KS;
-        uint32_t a0[4], a1[4];
-        widen(wd[0] + k * W, true, a0);
-        widen(wd[1] + k * W, true, a1);
-        float *y = o[s], d[4];
+        float *y = o[s], d[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          uint32_t a[4];
+          widen(wd[j] + k * W, true, a);
+          if constexpr (FINE) {
+            mma_f16(d, a, b[j][n][0], b[j][n][1], d[0], d[1], d[2], d[3]);
+            if constexpr (kTwo) mma_f16(e, a, b2[j][n][0], b2[j][n][1], e[0], e[1], e[2], e[3]);
+          } else {
+            mma_f16(o[s], a, b[j][n][0], b[j][n][1], y[0], y[1], y[2], y[3]);
+            if constexpr (kTwo) mma_f16(o[s], a, b2[j][n][0], b2[j][n][1], y[0], y[1], y[2], y[3]);
+          }
+        }
         if constexpr (FINE) {
-          mma_f16(d, a0, b[0][n][0], b[0][n][1], 0.f, 0.f, 0.f, 0.f);
-          if constexpr (kTwo) {
-            float e[4];
-            mma_f16(e, a0, b2[0][n][0], b2[0][n][1], 0.f, 0.f, 0.f, 0.f);
-            mma_f16(e, a1, b2[1][n][0], b2[1][n][1], e[0], e[1], e[2], e[3]);
-            add4(y, e);
-          }
-          mma_f16(d, a1, b[1][n][0], b[1][n][1], d[0], d[1], d[2], d[3]);
           add4(y, d);
-        } else {
-          mma_f16(o[s], a0, b[0][n][0], b[0][n][1], y[0], y[1], y[2], y[3]);
-          mma_f16(o[s], a1, b[1][n][0], b[1][n][1], y[0], y[1], y[2], y[3]);
-          if constexpr (kTwo) {
-            mma_f16(o[s], a0, b2[0][n][0], b2[0][n][1], y[0], y[1], y[2], y[3]);
-            mma_f16(o[s], a1, b2[1][n][0], b2[1][n][1], y[0], y[1], y[2], y[3]);
-          }
+          if constexpr (kTwo) add4(y, e);
         }
       }
     }
@@ -613,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
   pdl_wait();
   pdl_launch_dependents();
 
-  // Copies, a step's two tiles into a stage.  Lane k holds the physical page of the unit's page
+  // Copies, a step's tiles into a stage.  Lane k holds the physical page of the unit's page
   // `base` + k.
   const int per_page = p.P / kQuantTile;
   int base = 0, phys_lane = 0, issued = 0;
@@ -644,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
     todo -= run;
     tile_in += run;
   };
-  // The stage's next copies: two tiles, but one at a unit's odd end.
+  // The stage's next copies: a step's tiles, or what is left of the unit.
   auto issue_slow = [&](int stage) {
     if (run == 0 && todo == 0) {
       if (in.left == 0) return;
@@ -660,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
       in.advance(p, todo);
     }
     char *dst = mine + stage * S::kStage;
-    int want = min(2, run + todo);
+    int want = min(W::NT, run + todo);
     if (lane == 0) mbar_arrive_expect_tx(bar + stage, want * Q::kBytes);
 #pragma unroll 1
     while (want > 0) {
@@ -675,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
     ++issued;
   };
   auto issue = [&](int stage) {
-    if (run < 2) {
+    if (run < W::NT) {
       issue_slow(stage);
       return;
     }
@@ -684,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
       bulk_load_1d(mine + stage * S::kStage, src, S::kStage, bar + stage);
     }
     src += S::kStage;
-    run -= 2;
+    run -= W::NT;
     ++issued;
   };
 #pragma unroll 1
@@ -709,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
     }
     w.begin(p, i, h, lane);
 #pragma unroll 1
-    for (; t0 < end; t0 += 2 * kQuantTile) {
+    for (; t0 < end; t0 += W::NT * kQuantTile) {
       if (!__all_sync(kFull, mbar_try_wait(bar + stage, parity))) {
         bool there = false;
         for (uint32_t k = 0; k < kWaitPolls && !there && !broken; ++k)
@@ -770,6 +766,7 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
   // took 52 us, 44 side by side.)
   constexpr int kSlots = 2 * kQuantWarps, kVectors = G * D / 4;
   static_assert(kSlots <= 32, "a lane per slot");
+  static_assert(kThreads % 128 == 0, "teams of four warps: a barrier that 128 threads come to");
   const int slot_unit = lane < kSlots ? unit_of[lane] : -1;
   const unsigned taken = __ballot_sync(kFull, slot_unit >= 0);
   const unsigned before = taken & ((1u << lane) - 1u);
