@@ -616,7 +616,7 @@ class SparsePagedKVCache:
     def seq_truncate(self, seq_id, n_tokens):
         """Back to the sequence's first n_tokens tokens (kv_quant)."""
         if not 0 <= n_tokens <= _MAX_TOKENS:
-            spd_seq_truncate(self.ctx, seq_id, n_tokens)
+            return spd_seq_truncate(self.ctx, seq_id, n_tokens)
         st = self._truncate_fn(self.ctx, int(seq_id), int(n_tokens))
         if st != SPD_OK:
             _check(st, "spd_seq_truncate", self.ctx)
