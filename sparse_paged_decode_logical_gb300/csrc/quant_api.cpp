@@ -59,8 +59,22 @@ long long tiles_of(long long first, long long n) {
 
 namespace spd {
 
-bool quant_takes(const int *ids, int n, const PtUpdate *updates, int n_updates) {
+// Queries of few tokens are rotated by the appending launch, those of many by one of their own,
+// whose threads need a third of the registers (16,385 tokens of 32 and 8 heads, 8 bits: 84 us;
+// 125 in one launch).  Before that the new pages go by themselves (102 us with reading back, 105
+// with the pages in the second launch).
+static bool queries_apart(const QuantWrite &w, long long tiles, int sms) {
+  return w.table && tiles > 2LL * sms;
+}
+
+bool quant_takes(spd_ctx *c, const QuantWrite &w, const int *ids, int n, int n_tokens,
+                 const PtUpdate *updates, int n_updates) {
   if (n > kQuantSeqs || n_updates > kQuantUpdates) return false;
+  CtxView v;
+  ctx_view(c, &v);
+  long long tiles = 0;
+  for (int i = 0; i < n; ++i) tiles += tiles_of(seq_length(c, ids[i]), n_tokens);
+  if (queries_apart(w, tiles, v.num_sms)) return false;
   // entries of one sequence follow one another, in order
   for (int u = 1; u < n_updates; ++u) {
     const bool same = updates[u].slot == updates[u - 1].slot;
@@ -102,10 +116,7 @@ spd_status quant_append(spd_ctx *c, const QuantWrite &w, const int *ids, int n, 
           p.seqs[i].upd = u;
         }
     }
-    // Queries of few tokens are rotated by the same launch, those of many by one of their own,
-    // whose threads need a third of the registers (16,385 tokens of 32 and 8 heads, 8 bits: 84 us;
-    // 125 in one launch).
-    const bool apart = w.table && tiles > 2LL * v.num_sms;
+    const bool apart = queries_apart(w, tiles, v.num_sms);
     p.hq = w.table && !apart ? cfg.num_q_heads : 0;
     p.parts = parts_of(tiles, cfg.num_kv_heads + p.hq, v.num_sms);
     if (tiles * p.parts > 0x7fffffffLL)

@@ -247,9 +247,10 @@ struct QuantWrite {
   long long k_stride, v_stride, q_stride;  // elements between tokens
   const int *positions;
 };
-// updates: entries of the page table that the launch writes.  Where it cannot take them (too
-// many, or a sequence's do not follow one another) quant_takes says so, and they go first.
-bool quant_takes(const int *ids, int n, const PtUpdate *updates, int n_updates);
+// updates: entries of the page table that the launch writes.  Where it cannot or should not take
+// them (too many, or a sequence's do not follow one another) quant_takes says so, and they go first.
+bool quant_takes(spd_ctx *c, const QuantWrite &w, const int *ids, int n, int n_tokens,
+                 const PtUpdate *updates, int n_updates);
 spd_status quant_append(spd_ctx *c, const QuantWrite &w, const int *ids, int n, int n_tokens,
                         const PtUpdate *updates, int n_updates, cudaStream_t st);
 // Checks, pages, quant_append and the new lengths.

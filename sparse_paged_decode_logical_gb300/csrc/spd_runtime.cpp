@@ -999,7 +999,7 @@ spd_status append_quantised(spd_ctx *c, const QuantWrite &w, const int *ids, int
   DeviceGuard guard;
   if ((r = guard.bind(c->device)) != SPD_OK) return c->fail(r, "cudaSetDevice failed");
   for (int i = 0; i < n; ++i) take_pages(c, ids[i], n_tokens);
-  if (!quant_takes(ids, n, c->pending_pt.data(), (int)c->pending_pt.size()) &&
+  if (!quant_takes(c, w, ids, n, n_tokens, c->pending_pt.data(), (int)c->pending_pt.size()) &&
       (r = flush_page_table(c, st)) != SPD_OK)
     return r;
   if ((r = quant_append(c, w, ids, n, n_tokens, c->pending_pt.data(), (int)c->pending_pt.size(),
