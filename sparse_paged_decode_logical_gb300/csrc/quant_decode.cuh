@@ -164,11 +164,16 @@ struct Warp {
   static constexpr bool kTwo = SPLIT && G == 8;   // low halves need products of their own
   static constexpr bool kLanes = SPLIT && G < 8;  // low halves in the columns 4 .. 7
   // Codes as fp16 numbers.  For 16-bit outputs: as they lie, a subnormal number, code 2^-24
-  // (2^-20 in a high nibble).  The tensor cores cut sums off where their largest term, or what
-  // its exponent could hold, ends: 2^-15 of it then, which 16 bits do not show.  For fp32: ordinary
+  // (2^-20 in a high nibble).  The tensor cores cut a product's terms and its sum off, always
+  // toward zero, so that sums of codes, never negative, lose in one direction.  V's tokens 8 to 15
+  // of a tile therefore enter from their highest value down, hi - step (levels - code): the
+  // complement of the codes, which the mask takes along, times a negative weight.  Both signs in
+  // every product, a step's sums added to the walk's in fp32 outside: 5e-7 (8 bits) and 2e-6 (4) of
+  // the output, from 3,000 tokens to walks of 1,024 tiles a warp.  (Codes of one sign: 1e-5 to 4e-4,
+  // and in the accumulator over the whole walk 1e-3 at 64 tiles, 0.2 at 1,024.)  For fp32: ordinary
   // numbers around 0, code - 2^(b-1) (11 instructions a word of 4 bits instead of 5, 5 for 4 codes
-  // of 8 bits instead of 3), and products over more than two operands are added in fp32 outside.
-  // (fp32 outputs 5.5e-6 off without, 1.6e-7 with; 131,072 tokens in 4 bits 53 us, 38 without.)
+  // of 8 bits instead of 3), and K's products over more than two operands are added in fp32 outside:
+  // 2e-7 and 4e-7.  (131,072 tokens in 4 bits 52 us, 38 for 16-bit outputs.)
   static constexpr bool kNibbles = BITS == 4 && !FINE;  // high nibbles 2^4 as large
   static constexpr int kUnit = FINE ? 0 : 24;           // a code of 1 is 2^-kUnit
   static constexpr float kMid = FINE ? (BITS == 4 ? 8.f : 128.f) : 0.f;
@@ -276,12 +281,13 @@ struct Warp {
   static __device__ __forceinline__ void widen(const uint32_t *w, bool is_v, uint32_t (&a)[4]) {
     // 4 bits.  K: low nibbles k, high ones k + 8; V: low ones row g, high ones row g + 8
     const int n1 = is_v ? 1 : 2, n2 = is_v ? 2 : 1;
+    const uint32_t flip = is_v && !FINE ? ~0u : 0u;  // of V's tokens 8 and up: levels - code
     if constexpr (kNibbles) {
       const uint32_t x = w[0], y = w[0] >> 8;
       a[0] = x & 0x000f000fu;
       a[n1] = x & 0x00f000f0u;
-      a[n2] = y & 0x000f000fu;
-      a[3] = y & 0x00f000f0u;
+      a[n2] = (y ^ flip) & 0x000f000fu;
+      a[3] = (y ^ flip) & 0x00f000f0u;
     } else if constexpr (BITS == 4) {
       a[0] = centred(w[0] & 0x000f000fu);
       a[n1] = centred((w[0] >> 4) & 0x000f000fu);
@@ -290,8 +296,8 @@ struct Warp {
     } else {
       a[0] = w[0] & 0x00ff00ffu;
       a[1] = (w[0] >> 8) & 0x00ff00ffu;
-      a[2] = w[1] & 0x00ff00ffu;
-      a[3] = (w[1] >> 8) & 0x00ff00ffu;
+      a[2] = (w[1] ^ flip) & 0x00ff00ffu;
+      a[3] = ((w[1] >> 8) ^ flip) & 0x00ff00ffu;
       if constexpr (FINE) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) a[k] = centred(a[k]);
@@ -464,7 +470,7 @@ struct Warp {
       for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int a = 0; a < NG; ++a) {
-          if constexpr (kMid != 0.f) vl[j][r][a] = fmaf(kMid, vs[j][r][a], vl[j][r][a]);
+          if (FINE || r) vl[j][r][a] = fmaf(FINE ? kMid : Q::kLevels, vs[j][r][a], vl[j][r][a]);
 #pragma unroll
           for (int c = 0; c < 2; ++c) lo[c][a] = fmaf(pr[j][2 * r + c], vl[j][r][a], lo[c][a]);
         }
@@ -472,7 +478,7 @@ struct Warp {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         l[k & 1] += pr[j][k];
-        w[k] = pr[j][k] * up[k & 1];
+        w[k] = pr[j][k] * (!FINE && k >= 2 ? -up[k & 1] : up[k & 1]);
       }
 #pragma unroll
       for (int a = 0; a < NG; ++a)
@@ -509,23 +515,23 @@ struct Warp {
 #pragma unroll
       for (int k = 0; k < 4 / W; ++k) {
         const int s = c * (4 / W) + k, n = s * NG / KS;
-        float *y = o[s], d[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
+        // (a step's sums are added to the walk's outside: in the accumulator every tile would be
+        // cut off below what the walk has gathered)
+        float d[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           uint32_t a[4];
           widen(wd[j] + k * W, true, a);
-          if constexpr (FINE) {
-            mma_f16(d, a, b[j][n][0], b[j][n][1], d[0], d[1], d[2], d[3]);
-            if constexpr (kTwo) mma_f16(e, a, b2[j][n][0], b2[j][n][1], e[0], e[1], e[2], e[3]);
-          } else {
-            mma_f16(o[s], a, b[j][n][0], b[j][n][1], y[0], y[1], y[2], y[3]);
-            if constexpr (kTwo) mma_f16(o[s], a, b2[j][n][0], b2[j][n][1], y[0], y[1], y[2], y[3]);
+          mma_f16(d, a, b[j][n][0], b[j][n][1], d[0], d[1], d[2], d[3]);
+          if constexpr (kTwo) {
+            if constexpr (FINE)
+              mma_f16(e, a, b2[j][n][0], b2[j][n][1], e[0], e[1], e[2], e[3]);
+            else
+              mma_f16(d, a, b2[j][n][0], b2[j][n][1], d[0], d[1], d[2], d[3]);
           }
         }
-        if constexpr (FINE) {
-          add4(y, d);
-          if constexpr (kTwo) add4(y, e);
-        }
+        add4(o[s], d);
+        if constexpr (kTwo && FINE) add4(o[s], e);
       }
     }
   }
