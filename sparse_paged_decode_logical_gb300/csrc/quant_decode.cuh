@@ -152,17 +152,17 @@ struct Cursor {
   }
 };
 
-template <typename T, int D, int BITS, int G, int MODE>
+template <typename T, int D, int BITS, int G, bool FINE>
 struct Warp {
   using Q = QuantTile<D, BITS>;
   static constexpr int KS = D / 16;     // k-steps of S, m-tiles of O
   static constexpr int NT = quant_step_tiles(D);
   static constexpr int NG = Q::kGroups;
-  // MODE 0: outputs in bf16, weights of 11 bits.  1: in fp16, weights of 22 bits.  2: in fp32,
-  // and sums to fp32's own error.
-  static constexpr bool SPLIT = MODE >= 1, FINE = MODE == 2;
-  static constexpr bool kTwo = SPLIT && G == 8;   // low halves need products of their own
-  static constexpr bool kLanes = SPLIT && G < 8;  // low halves in the columns 4 .. 7
+  // FINE: outputs in fp32, sums to fp32's own error.  Weights have 22 bits whatever the output (with
+  // 11, one bf16 output in five was not the rounding of the exact value; 131,072 tokens in 4 bits
+  // 38.0 us, 40.0 with 22).
+  static constexpr bool kTwo = G == 8;     // low halves need products of their own
+  static constexpr bool kLanes = !kTwo;    // low halves in the columns 4 .. 7
   // Codes as fp16 numbers.  For 16-bit outputs: as they lie, a subnormal number, code 2^-24
   // (2^-20 in a high nibble).  The tensor cores cut a product's terms and its sum off, always
   // toward zero, so that sums of codes, never negative, lose in one direction.  V's tokens 8 to 15
@@ -474,30 +474,30 @@ struct Warp {
 #pragma unroll
           for (int c = 0; c < 2; ++c) lo[c][a] = fmaf(pr[j][2 * r + c], vl[j][r][a], lo[c][a]);
         }
-      float w[4];
+      float2 w[2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        l[k & 1] += pr[j][k];
-        w[k] = pr[j][k] * (!FINE && k >= 2 ? -up[k & 1] : up[k & 1]);
+      for (int r = 0; r < 2; ++r) {
+        l[0] += pr[j][2 * r];
+        l[1] += pr[j][2 * r + 1];
+        const float sign = !FINE && r ? -1.f : 1.f;
+        w[r] = f2_mul(make_float2(pr[j][2 * r], pr[j][2 * r + 1]), make_float2(sign * up[0], sign * up[1]));
       }
 #pragma unroll
       for (int a = 0; a < NG; ++a)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float y0 = w[2 * r] * vs[j][r][a], y1 = w[2 * r + 1] * vs[j][r][a];
-          if constexpr (SPLIT) {
-            // high part: the first 11 bits; low part: the next 11
-            const float h0 = __uint_as_float(__float_as_uint(y0) & 0xffffe000u);
-            const float h1 = __uint_as_float(__float_as_uint(y1) & 0xffffe000u);
-            if constexpr (kTwo) {
-              b[j][a][r] = transpose8(pack_rz(h0, h1));
-              b2[j][a][r] = transpose8(pack_rz(y0 - h0, y1 - h1));
-            } else {
-              const float part = t >= 2 ? -1.f : 0.f;
-              b[j][a][r] = transpose8(pack_rz(fmaf(h0, part, y0), fmaf(h1, part, y1)));
-            }
+          const float2 y = f2_mul(w[r], make_float2(vs[j][r][a], vs[j][r][a]));
+          // high part: the first 11 bits; low part: the next 11
+          const float2 h = make_float2(__uint_as_float(__float_as_uint(y.x) & 0xffffe000u),
+                                       __uint_as_float(__float_as_uint(y.y) & 0xffffe000u));
+          if constexpr (kTwo) {
+            const float2 z = f2_sub(y, h);
+            b[j][a][r] = transpose8(pack_rz(h.x, h.y));
+            b2[j][a][r] = transpose8(pack_rz(z.x, z.y));
           } else {
-            b[j][a][r] = transpose8(pack2<__half>(y0, y1));
+            const float part = t >= 2 ? -1.f : 0.f;
+            const float2 z = f2_fma(h, make_float2(part, part), y);
+            b[j][a][r] = transpose8(pack_rz(z.x, z.y));
           }
         }
     }
@@ -584,12 +584,12 @@ __device__ __forceinline__ void store_out(void *out, bool f32, size_t at, float4
   }
 }
 
-template <typename T, int D, int BITS, int G, int MODE>
+template <typename T, int D, int BITS, int G, bool FINE>
 __global__ void __launch_bounds__(kThreads, kQuantPerSm)
     quant_attend_kernel(const __grid_constant__ QuantAttendParams p) {
   using S = Shape<D, BITS, G>;
   using Q = typename S::Q;
-  using W = Warp<T, D, BITS, G, MODE>;
+  using W = Warp<T, D, BITS, G, FINE>;
   extern __shared__ __align__(128) char smem[];
   char *const ring = smem;
   char *const firsts = p.firsts + (size_t)blockIdx.x * S::kLast;
@@ -900,31 +900,31 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
   }
 }
 
-template <typename T, int D, int BITS, int G, int MODE>
+template <typename T, int D, int BITS, int G, bool FINE>
 cudaError_t launch_one(const QuantAttendParams &p, cudaStream_t st) {
   using S = Shape<D, BITS, G>;
     static std::atomic<uint64_t> ready{0};
-  const auto kernel = quant_attend_kernel<T, D, BITS, G, MODE>;
+  const auto kernel = quant_attend_kernel<T, D, BITS, G, FINE>;
   const cudaError_t e = allow_smem(kernel, S::kSmem, &ready);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, p.ctas, kThreads, S::kSmem, st, p);
 }
 
-template <typename T, int D, int BITS, int MODE>
+template <typename T, int D, int BITS, bool FINE>
 cudaError_t launch_heads(const QuantAttendParams &p, int G, cudaStream_t st) {
   switch (G) {
-    case 1: return launch_one<T, D, BITS, 1, MODE>(p, st);
-    case 2: return launch_one<T, D, BITS, 2, MODE>(p, st);
-    case 4: return launch_one<T, D, BITS, 4, MODE>(p, st);
-    default: return launch_one<T, D, BITS, 8, MODE>(p, st);
+    case 1: return launch_one<T, D, BITS, 1, FINE>(p, st);
+    case 2: return launch_one<T, D, BITS, 2, FINE>(p, st);
+    case 4: return launch_one<T, D, BITS, 4, FINE>(p, st);
+    default: return launch_one<T, D, BITS, 8, FINE>(p, st);
   }
 }
 
-template <typename T, int MODE>
+template <typename T, bool FINE>
 cudaError_t launch_shape(const QuantAttendParams &p, int d, int bits, int G, cudaStream_t st) {
   if (d == 64)
-    return bits == 8 ? launch_heads<T, 64, 8, MODE>(p, G, st) : launch_heads<T, 64, 4, MODE>(p, G, st);
-  return bits == 8 ? launch_heads<T, 128, 8, MODE>(p, G, st) : launch_heads<T, 128, 4, MODE>(p, G, st);
+    return bits == 8 ? launch_heads<T, 64, 8, FINE>(p, G, st) : launch_heads<T, 64, 4, FINE>(p, G, st);
+  return bits == 8 ? launch_heads<T, 128, 8, FINE>(p, G, st) : launch_heads<T, 128, 4, FINE>(p, G, st);
 }
 
 }  // namespace

@@ -5,8 +5,8 @@ namespace spd {
 
 cudaError_t launch_quant_attend_f16(const QuantAttendParams &p, int d, int bits, int G,
                                    cudaStream_t st) {
-  const cudaError_t e = p.out_f32 ? launch_shape<__half, 2>(p, d, bits, G, st)
-                                  : launch_shape<__half, 1>(p, d, bits, G, st);
+  const cudaError_t e = p.out_f32 ? launch_shape<__half, true>(p, d, bits, G, st)
+                                  : launch_shape<__half, false>(p, d, bits, G, st);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

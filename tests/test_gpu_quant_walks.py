@@ -85,3 +85,27 @@ def test_walks_of_every_layout_do_not_drift(heads, d, bits):
     got = c.quant_decode_attention(q, ids, out_dtype=torch.float16)
     assert rms(got.double() - ref) <= (STEP[torch.float16] / math.sqrt(3) + MARGIN) * rms(ref)
     c.check_status()
+
+
+# ---- outputs ------------------------------------------------------------------------
+# An output that is not the rounding of the exact value lies within its error of the middle
+# between two numbers of its type: error / ulp of all, for errors spread evenly.  An error of MARGIN
+# of the outputs' root mean square and a bf16 ulp of at least 2^-8 of a value: 2^-8 where values are
+# of that size, three times that over a normal distribution, whose smaller values have smaller ulps.
+FLIPS = 3 * MARGIN / 2.0 ** -8
+
+
+@pytest.mark.parametrize("heads,d", [((32, 8), 128), ((64, 8), 128), ((8, 4), 64), ((16, 16), 64)])
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("rule", [dict(), dict(softcap=50.0, gain=4.0), dict(window=700)])
+def test_bf16_outputs_are_the_exact_values_rounded(heads, d, bits, rule):
+    n, L = 16, 3000
+    c, ids, k, v = filled(L, *heads, d, "bf16", bits, seed=3, n=n)
+    q = normal(5, n, heads[0], d, dtype=torch.bfloat16, gain=rule.get("gain", 1.0))
+    cap, window = rule.get("softcap", 0.0), rule.get("window", 0)
+    ref = torch.stack([exact(q[i], k[i], v[i], bits, softcap=cap, first=L - window if window else 0)
+                       for i in range(n)])
+    got = c.quant_decode_attention(q, ids, softcap=cap, window=window, out_dtype=torch.bfloat16)
+    off = (got != ref.bfloat16()).double().mean()
+    assert float(off) <= FLIPS
+    c.check_status()
