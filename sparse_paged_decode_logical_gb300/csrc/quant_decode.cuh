@@ -45,8 +45,11 @@ constexpr int kThreads = kQuantWarps * 32;
 
 // A weight enters the product as p 2^k step, p = 2^(score - m): 2^k moves the largest p step of
 // a column to between 2^10 and 2^12, and a new k is taken where one would pass 2^15.  What fp16
-// loses below its normal range is then 2^-35 of the largest.
+// loses below its normal range is then 2^-35 of the largest.  p itself may grow to 2^kHead before
+// a new reference is taken, and k ends at 126 - kHead, which a column of nothing but constant
+// groups (step 0) is given: p 2^k stays finite, and 0 times it 0.
 constexpr int kRoom = 11;
+constexpr int kHead = 10;
 
 __device__ __forceinline__ void qd_set_err(int *err, int code, int a, int b, int c) {
   if (atomicCAS(err, 0, code) == 0) {
@@ -420,8 +423,9 @@ struct Warp {
       for (int a = 0; a < NG; ++a) most = fmax3f(most, vs[j][0][a], vs[j][1][a]);
     }
     const float big = fmaxf(pm[0] * up[0], pm[1] * up[1]) * most;
-    // A new reference only where a weight could leave its room: a vote in most steps.
-    if (__any_sync(kFull, fmaxf(pm[0], pm[1]) > 0x1p60f || big > 32768.f)) {
+    // A new reference only where a weight could leave its room (or the bound is not a number): a
+    // vote in most steps.
+    if (__any_sync(kFull, fmaxf(pm[0], pm[1]) > (float)(1 << kHead) || !(big <= 32768.f))) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         float a = m[c], z = -CUDART_INF_F;
@@ -442,7 +446,7 @@ struct Warp {
           a = fmaxf(a, __shfl_xor_sync(kFull, a, k));
           z = fmaxf(z, __shfl_xor_sync(kFull, z, k));
         }
-        const int k = (int)fminf(fmaxf(floorf(a - z), -120.f), 115.f) + kRoom;
+        const int k = (int)fminf(fmaxf(floorf(a - z), -120.f), 126.f - kHead - kRoom) + kRoom;
         const bool same = a == m[c];
         const float fa = same ? 1.f : ex2_approx(m[c] - a);
         const float fb = ex2_approx((same ? 0.f : m[c] - a) + (float)(k - k2[c]));

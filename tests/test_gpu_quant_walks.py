@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from quant_ref import STEP, held
+from quant_ref import FLOOR, STEP, held, quantise
 from test_gpu_quant import DT, F32, cache, normal
 
 pytestmark = pytest.mark.gpu
@@ -109,3 +109,125 @@ def test_bf16_outputs_are_the_exact_values_rounded(heads, d, bits, rule):
     off = (got != ref.bfloat16()).double().mean()
     assert float(off) <= FLIPS
     c.check_status()
+
+
+# ---- references that move ------------------------------------------------------------
+
+def step_tiles(d):
+    return 4 if d == 64 else 2
+
+
+def tolerance(q, k, v, bits, scale, steps, d, out_dtype):
+    """Of every output of one kv head: q [heads][d], k and v [L][d] as written.  A score's products
+    and sums are d + 8 roundings of 2^-23 of sum |q| (|lo| + step code), and with 16-bit outputs 17 terms
+    of every product over 16 channels are cut at 2^-14 of the largest |q| step; an error e of the
+    scores is one of 2 e of a weight's share.  Weights: 2^-21 cut off, 2^x 2^-21 in all.  Sums:
+    2 tiles, one more a step, and at most 24 + 152 + 24 partials, 2^-24 each; with 16-bit outputs 17
+    2^-14 of a step, as the weights have them.  What fp16 loses below its range: 2^-34 of the largest
+    weight times step codes, all tokens' at most.  Then half a step of the output."""
+    short = out_dtype != F32
+    q = q.double().abs()
+    kv, ka = held(k, bits)
+    lo, step, code = quantise(v, bits)
+    e = float((q @ ka.t()).max()) * scale * (d + 8) * 2.0 ** -23
+    if short:
+        e += float(q.max() * quantise(k, bits)[1].max()) * scale * 17 * 2.0 ** -14 * d / 16
+    return lambda w, out: (
+        w @ (lo.abs() + step * (2 ** bits - 1)) *
+        (2.0 ** -20 + 2 * e + 2.0 ** -24 * (2 * step_tiles(d) * steps + steps + 200))
+        + (17 * 2.0 ** -14 * (w @ step) if short else 0.0)
+        + 2.0 ** -34 * (step * code).sum(0) + STEP[out_dtype] * out.abs() + FLOOR[out_dtype] + 1e-30)
+
+
+def saw(L, height, period):
+    t = torch.arange(L, device="cuda")
+    return (t % period).float() / period * height
+
+
+def scores_of(kind, L):
+    """What every key's channels are moved by."""
+    return {"noise": lambda: torch.zeros(L, device="cuda"),
+            "gently": lambda: saw(L, 8.0, 700),     # 11 bits in 700 tokens
+            "rising": lambda: saw(L, 40.0, 700),    # 58 bits
+            "falling": lambda: 40.0 - saw(L, 40.0, 700)}[kind]()
+
+
+def values_of(kind, seed, L, d):
+    v = normal(seed, L, d)
+    block = torch.arange(L, device="cuda") // 96 % 4
+    if kind == "zero":
+        return torch.zeros_like(v)
+    if kind == "ones":
+        return torch.ones_like(v)
+    if kind == "blocks":  # nothing, ordinary ones, the same everywhere, tiny ones
+        v[block == 0] = 0.0
+        v[block == 2] = 1.5
+        v[block == 3] *= 2.0 ** -20
+    if kind == "sizes":
+        v *= torch.exp2((block * 6 - 9).float())[:, None]
+    return v
+
+
+HEADS = [("noise", "normal"), ("rising", "normal"), ("falling", "normal"), ("gently", "zero"),
+         ("gently", "ones"), ("rising", "blocks"), ("gently", "blocks"), ("falling", "sizes")]
+
+
+@pytest.mark.parametrize("g", [1, 2, 4, 8])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("dtype,out", [("bf16", "same"), ("bf16", "fp32"), ("fp16", "same"),
+                                       ("fp16", "fp32")])
+def test_references_move_in_the_middle_of_a_walk(g, d, bits, dtype, out):
+    """Eight steps and more of every warp, whose scores rise or fall and whose values are ordinary,
+    constant, nothing, or change from one to the other."""
+    n, dt = len(HEADS), DT[dtype]
+    L = tokens_for(9 * step_tiles(d), n)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    steps = -(-L // 16) * n // (WARPS * sms) // step_tiles(d)
+    assert steps >= 8
+    k = torch.stack([normal(10 + h, L, d) + scores_of(s, L)[:, None] for h, (s, _) in enumerate(HEADS)],
+                    1).to(dt)
+    v = torch.stack([values_of(x, 30 + h, L, d) for h, (_, x) in enumerate(HEADS)], 1).to(dt)
+    c = cache(n * g, n, d, dtype, bits, L, page=256, seed=2)
+    s = c.seq_create()
+    c.kv_append([s], k[None], v[None])
+    q = (1.0 + normal(50, n * g, d, gain=0.1)).to(dt)
+    od = F32 if out == "fp32" else dt
+    got = c.quant_decode_attention(q[None], [s], scale=1.0 / d, out_dtype=od)[0]
+    c.check_status()
+    for h, (_, kind) in enumerate(HEADS):
+        mine = slice(h * g, (h + 1) * g)
+        x = q[mine].double() @ held(k[:, h], bits)[0].t() / d
+        w = torch.softmax(x, 1)
+        ref = w @ held(v[:, h], bits)[0]
+        tol = tolerance(q[mine], k[:, h], v[:, h], bits, 1.0 / d, steps, d, od)(w, ref)
+        err = (got[mine].double() - ref).abs()
+        assert bool((err <= tol).all()), (HEADS[h], float((err / tol).max()))
+        if kind == "zero":
+            assert bool((got[mine] == 0).all())
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("out", ["same", "fp32"])
+@pytest.mark.parametrize("size", [2.0 ** 80, 2.0 ** -80])
+def test_constant_and_vast_values_under_rising_scores(bits, out, size):
+    d, hkv = 128, 4
+    L = tokens_for(16, hkv)
+    k = (normal(1, L, hkv, d) + saw(L, 30.0, 500)[:, None, None]).bfloat16()
+    v = normal(2, L, hkv, d) * size
+    v[:, ::2] = size
+    v = v.bfloat16()
+    c = cache(hkv * 2, hkv, d, "bf16", bits, L, page=256)
+    s = c.seq_create()
+    c.kv_append([s], k[None], v[None])
+    q = torch.ones(hkv * 2, d, device="cuda").bfloat16()
+    od = F32 if out == "fp32" else torch.bfloat16
+    got = c.quant_decode_attention(q[None], [s], scale=1.0 / d, out_dtype=od)[0]
+    c.check_status()
+    for h in range(hkv):
+        mine = slice(2 * h, 2 * h + 2)
+        w = torch.softmax(q[mine].double() @ held(k[:, h], bits)[0].t() / d, 1)
+        ref = w @ held(v[:, h], bits)[0]
+        tol = tolerance(q[mine], k[:, h], v[:, h], bits, 1.0 / d, 9, d, od)(w, ref)
+        err = (got[mine].double() - ref).abs()
+        assert bool((err <= tol).all()), (h, float((err / tol).max()))
