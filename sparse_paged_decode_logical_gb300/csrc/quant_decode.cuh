@@ -428,25 +428,27 @@ struct Warp {
     if (__any_sync(kFull, fmaxf(pm[0], pm[1]) > (float)(1 << kHead) || !(big <= 32768.f))) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float a = m[c], z = -CUDART_INF_F;
-        // z: the largest p step so far, as a power of 2
-        if (m[c] != -CUDART_INF_F) z = m[c] + (float)(kRoom - k2[c]);
+        float a = m[c];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) a = fmax3f(a, x[j][c], x[j][2 + c]);
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) a = fmaxf(a, __shfl_xor_sync(kFull, a, k));
+        // z: the largest p step so far, as a power of 2 (of differences of scores: a vast score
+        // itself would round the exponent away)
+        float z = (m[c] - a) + (float)(kRoom - k2[c]);
+        if (m[c] == -CUDART_INF_F) z = -CUDART_INF_F;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            a = fmaxf(a, x[j][2 * r + c]);
             float top = vs[j][r][0];
 #pragma unroll
             for (int n = 1; n < NG; ++n) top = fmaxf(top, vs[j][r][n]);
-            z = fmaxf(z, x[j][2 * r + c] + (float)exponent(top));
+            z = fmaxf(z, (x[j][2 * r + c] - a) + (float)exponent(top));
           }
 #pragma unroll
-        for (int k = 4; k < 32; k <<= 1) {
-          a = fmaxf(a, __shfl_xor_sync(kFull, a, k));
-          z = fmaxf(z, __shfl_xor_sync(kFull, z, k));
-        }
-        const int k = (int)fminf(fmaxf(floorf(a - z), -120.f), 126.f - kHead - kRoom) + kRoom;
+        for (int k = 4; k < 32; k <<= 1) z = fmaxf(z, __shfl_xor_sync(kFull, z, k));
+        const int k = (int)fminf(fmaxf(floorf(-z), -120.f), 126.f - kHead - kRoom) + kRoom;
         const bool same = a == m[c];
         const float fa = same ? 1.f : ex2_approx(m[c] - a);
         const float fb = ex2_approx((same ? 0.f : m[c] - a) + (float)(k - k2[c]));

@@ -231,3 +231,36 @@ def test_constant_and_vast_values_under_rising_scores(bits, out, size):
         tol = tolerance(q[mine], k[:, h], v[:, h], bits, 1.0 / d, 9, d, od)(w, ref)
         err = (got[mine].double() - ref).abs()
         assert bool((err <= tol).all()), (h, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("dtype,out", [("bf16", "same"), ("bf16", "fp32"), ("fp16", "same"),
+                                       ("fp16", "fp32")])
+@pytest.mark.parametrize("at", [0, 40, 1499, 2999])
+def test_vast_scores_and_steps(bits, dtype, out, at):
+    """Scores near 10^9 (fp32 numbers 64 and more apart) over steps of 2^5 and more: one key's score
+    is 2 10^7 above the others', further than what fp32 leaves open (64 2^-23 of 3 10^9), so that
+    the output is what is held of its value, rounded."""
+    L, d, dt = 3000, 64, DT[dtype]
+    k = normal(1, 1, L, 1, d, gain=10.0) + 3e4
+    k[:, at] += 6e3
+    v = normal(2, 1, L, 1, d, gain=1e4)
+    k, v = k.to(dt), v.to(dt)
+    c = cache(4, 1, d, dtype, bits, L)
+    s = c.seq_create()
+    c.kv_append([s], k, v)
+    q = torch.full((1, 4, d), 512.0, device="cuda").to(dt)
+    x = q[0].double() @ held(k[0, :, 0], bits)[0].t()
+    top = x[0].topk(2).values
+    assert int(x[0].argmax()) == at and float(top[0] - top[1]) > 2e7 and float(top[0]) > 1e9
+    assert float(quantise(v, bits)[1].max()) >= 32
+    od = F32 if out == "fp32" else dt
+    got = c.quant_decode_attention(q, [s], scale=1.0, out_dtype=od)[0]
+    ref, mag = held(v[0, at, 0], bits)
+    lo, step, _ = quantise(v[0, at, 0], bits)
+    # (its weight is 1, cut off to 22 bits; sums of what is subtracted again: hi and lo)
+    tol = 2.0 ** -20 * (lo.abs() + step * (2 ** bits - 1)) + STEP[od] * ref.abs() + FLOOR[od]
+    if od != F32:
+        tol = tol + 17 * 2.0 ** -14 * step
+    assert bool(((got.double() - ref).abs() <= tol).all())
+    c.check_status()
