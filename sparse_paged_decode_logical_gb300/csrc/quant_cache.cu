@@ -2,7 +2,7 @@
 //
 // A group of channels of a token is held as value = lo + step * code: lo its lowest value,
 // step the least number of the cache's type with levels * step >= highest - lowest, codes
-// rounded to nearest, 0 .. levels.  A group that holds a value that is not finite (or whose
+// rounded to nearest, 0 .. levels; differences count exactly, also where fp32 rounds them.  A group that holds a value that is not finite (or whose
 // span exceeds fp32) gets lo = NaN and step 0: it reads back as NaN throughout.
 //
 // Both directions are bound by memory: 2 bytes a value on one side, 1.03 or 0.63 on the other.
@@ -72,18 +72,26 @@ __device__ __forceinline__ uint32_t low_bytes(float2 a, float2 b) {
   return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
                      __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
 }
-// A code n (kMagic + n in y) for a distance d, which may be one off: what n step leaves of d, an
-// exact difference, is compared with half a step, ties to even.
-__device__ __forceinline__ float exact_code(float y, float d, float step) {
-  const float r = fmaf(kMagic - y, step, d), twice = fabsf(r) + fabsf(r);
+// What rounding left of a - b, the difference d: a - b = d + rest exactly.
+__device__ __forceinline__ float rest_of(float a, float b, float d) {
+  const float a1 = d + b, b1 = a1 - d;  // (Knuth's two-sum, of a and -b)
+  return (a - a1) + (b1 - b);
+}
+// A code n (kMagic + n in y) for a distance x - lo, which may be one off: what n step leaves of it
+// is compared with half a step, ties to even.  d, the rounded distance, and n step are numbers of
+// a spacing that 2 |r| - step keeps, so that only the last sum is rounded, which keeps its sign.
+__device__ __forceinline__ float exact_code(float y, float x, float lo, float step) {
+  const float d = x - lo, r = fmaf(kMagic - y, step, d), rest = rest_of(x, lo, d);
+  const float over = (fabsf(r) + fabsf(r) - step) + copysignf(2.f, r) * rest;
   const bool odd = __float_as_uint(y) & 1u;
-  return twice > step || (twice == step && odd) ? y + copysignf(1.f, r) : y;
+  return over > 0.f || (over == 0.f && odd) ? y + copysignf(1.f, r) : y;
 }
 // Apart: 1 warp in 5 comes here in bf16, and copies in every place would fill the instruction
-// cache.
-__device__ __noinline__ uint32_t exact_codes(float2 ya, float2 yb, float2 a, float2 b, float step) {
-  return low_bytes(make_float2(exact_code(ya.x, a.x, step), exact_code(ya.y, a.y, step)),
-                   make_float2(exact_code(yb.x, b.x, step), exact_code(yb.y, b.y, step)));
+// cache.  (What rounding takes from a distance costs 16,385 tokens in 8 bits 2 of 103 us.)
+__device__ __noinline__ uint32_t exact_codes(float2 ya, float2 yb, float2 a, float2 b, float lo,
+                                             float step) {
+  return low_bytes(make_float2(exact_code(ya.x, a.x, lo, step), exact_code(ya.y, a.y, lo, step)),
+                   make_float2(exact_code(yb.x, b.x, lo, step), exact_code(yb.y, b.y, lo, step)));
 }
 
 // What a group's codes are made with.
@@ -95,7 +103,7 @@ struct Scale {
 
   __device__ __forceinline__ explicit Scale(uint32_t e) {  // (lowest, -highest)
     const float2 x = unpack2<T>(e);
-    const float span = -x.y - x.x;
+    const float span = -x.y - x.x;  // highest - lowest, rounded
     lo = x.x;
     tiny = false;
     if (!(span <= 3.402823466e38f)) {
@@ -107,12 +115,16 @@ struct Scale {
     // The least number of T that reaches: products with it are exact (11 + 8 bits).
     uint32_t h = pack2<T>(span * (1.f / LEVELS), 0.f) & 0xffffu;
     step = unpack2<T>(h).x;
-    if (step * (float)LEVELS < span) {
-      step = unpack2<T>(++h).x;
-    } else if (h > 0) {
-      const float less = unpack2<T>(h - 1).x;
-      if (less * (float)LEVELS >= span) --h, step = less;
+    const float most = step * (float)LEVELS, less = h > 0 ? unpack2<T>(h - 1).x : -1.f;
+    bool more = most < span, fewer = less * (float)LEVELS >= span;
+    // (what rounding took from the span counts only here)
+    if (most == span || less * (float)LEVELS == span) {
+      const bool beyond = rest_of(-x.y, x.x, span) > 0.f;
+      more |= beyond && most == span;
+      fewer &= !beyond || less * (float)LEVELS > span;
     }
+    if (more) step = unpack2<T>(++h).x;
+    if (fewer) --h, step = less;
     bits = (e & 0xffffu) | h << 16;
     tiny = step < 0x1p-100f;
     if (tiny) {
@@ -139,12 +151,11 @@ struct Scale {
       a = f2_mul(a, make_float2(0x1p100f, 0x1p100f));
       b = f2_mul(b, make_float2(0x1p100f, 0x1p100f));
     }
-    a = f2_sub(a, l);
-    b = f2_sub(b, l);
-    const float2 ta = f2_mul(a, r), tb = f2_mul(b, r), ya = f2_add(ta, m), yb = f2_add(tb, m);
+    const float2 ta = f2_mul(f2_sub(a, l), r), tb = f2_mul(f2_sub(b, l), r);
+    const float2 ya = f2_add(ta, m), yb = f2_add(tb, m);
     const float2 ea = f2_sub(ta, f2_sub(ya, m)), eb = f2_sub(tb, f2_sub(yb, m));
     const float near = fmaxf(fmax3f(fabsf(ea.x), fabsf(ea.y), fabsf(eb.x)), fabsf(eb.y));
-    return near >= kNear ? exact_codes(ya, yb, a, b, step) : low_bytes(ya, yb);
+    return near >= kNear ? exact_codes(ya, yb, a, b, lo, step) : low_bytes(ya, yb);
   }
 };
 
@@ -378,8 +389,10 @@ __device__ __forceinline__ void stage_rows(T *buf, const T *src, long long strid
 // A CTA takes one tile's tokens and every parts-th of the heads: K and V of a head are one
 // warp's work, and so are a query head's rows when positions are applied.  Keys are on their way
 // to shared memory, where they are rotated, while the sines are made and the values done.
+// (80 registers where they suffice, for a sixth CTA on the SM: 6 x 1,111 tokens into 4 bits with
+// reading back 9.4 us, 11.1 with 92.)
 template <typename T, int D, int BITS, bool ROT>
-__global__ void __launch_bounds__(kWriteWarps * 32, 5)
+__global__ void __launch_bounds__(kWriteWarps * 32, !ROT && (D == 64 || BITS == 4) ? 6 : 5)
     quant_append_kernel(const __grid_constant__ QuantAppendParams p) {
   using Q = QuantTile<D, BITS>;
   extern __shared__ __align__(16) char smem[];  // rows of K and V of every warp, the sines
