@@ -40,7 +40,7 @@ def sources():
 
 def _deps():
     return sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC)
-                        if f.endswith(".h")] + [os.path.join(INCLUDE, "spd.h")]
+                        if f.endswith((".h", ".cuh"))] + [os.path.join(INCLUDE, "spd.h")]
 
 
 def up_to_date():
