@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
 
   int done = 0, stage = 0;
   uint32_t parity = 0;
-  bool broken = false;
+  bool broken = false, begun = false;
   W w;
   while (at.left > 0) {
     const int i = at.i, h = at.h, unit = i * p.hkv + h, n = at.left;
@@ -712,9 +712,10 @@ __global__ void __launch_bounds__(kThreads, kQuantPerSm)
       const int u0 = p.seqs[i].off + h * p.seqs[i].stride, per_cta = p.per_warp * kQuantWarps;
       const int c0 = u0 / per_cta;
       const int4 span = make_int4(c0, (u0 + at.tiles - 1) / per_cta, u0 != c0 * per_cta, 0);
-      if (done == 0) span_of[2 * warp] = span;
+      if (!begun) span_of[2 * warp] = span;  // (not by steps done: a wait that gave up leaves none)
       span_of[2 * warp + 1] = span;
     }
+    begun = true;
     w.begin(p, i, h, lane);
 #pragma unroll 1
     for (; t0 < end; t0 += W::NT * kQuantTile) {
