@@ -1019,6 +1019,46 @@ def _rotary_plan(table, positions, q, k):
             0 if k is None else _token_stride(k, "k"))
 
 
+_rotated_class = None
+
+
+def _rotated():
+    """The rotation as autograd knows it: linear, so that its gradient is the rotation
+    back (and the gradient's gradient the rotation)."""
+    global _rotated_class
+    if _rotated_class is None:
+        import torch
+
+        def rows(g):
+            """What a call reads: tokens at one stride, 16-byte aligned (a gradient may be
+            broadcast, or begin anywhere)."""
+            g = g.contiguous()
+            return g if g.data_ptr() % 16 == 0 else g.clone()
+
+        class Rotated(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, table, positions, q, k, inverse, stream):
+                ctx.set_materialize_grads(False)
+                ctx.save_for_backward(positions)
+                ctx.table, ctx.inverse = table, inverse
+                return rotary(table, positions, q, k, inverse, stream=stream)
+
+            @staticmethod
+            def backward(ctx, *grads):
+                positions, = ctx.saved_tensors
+                asked = [g is not None and need for g, need in zip(grads, ctx.needs_input_grad[2:4])]
+                found = [rows(g) for g, need in zip(grads, asked) if need]
+                if found:
+                    y = rotary(ctx.table, positions, *found, inverse=not ctx.inverse)
+                    found = [y] if len(found) == 1 else list(y)
+                found = iter(found)
+                back = [next(found) if need else None for need in asked]
+                return (None, None, *(back + [None])[:2], None, None)
+
+        _rotated_class = Rotated
+    return _rotated_class
+
+
 def rotary(table, positions, q, k=None, inverse=False, out=None, stream=None):
     """Rotate q [n][Hq][d] and k [n][Hk][d] (or q alone) by the :class:`Rotary`
     rule `table` (spd_rotary).  positions int32 [axes][n] ([n] with one axis).
@@ -1026,7 +1066,15 @@ def rotary(table, positions, q, k=None, inverse=False, out=None, stream=None):
     projection's output.  inverse: back, which is also the rotation's gradient.
     out: a tensor for the rotated q, or a pair of them; they may be q and k
     themselves.  Returns (q, k) rotated, or q.  `stream` as in
-    :func:`prefill_attention`."""
+    :func:`prefill_attention`.  Gradients of q and k go back through the rotation
+    (on the stream that is current at the call); with `out` there are none, and
+    inputs that ask for them are refused."""
+    if q.requires_grad or (k is not None and k.requires_grad):
+        import torch
+        if torch.is_grad_enabled():
+            if out is not None:
+                raise ValueError("no gradient passes through out: q and k must not require one")
+            return _rotated().apply(table, positions, q, k, bool(inverse), stream)
     dev = q.get_device()
     key = (table.axes, table.head_dim, positions.shape, positions.dtype, positions.is_contiguous(),
            positions.get_device(), dev, q.shape, q.stride(), q.dtype,
