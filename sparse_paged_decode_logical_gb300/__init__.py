@@ -167,6 +167,11 @@ def lib():
 
 # ---- low level: the C entry points with Python arguments --------------------
 
+def _int32(x):
+    """x as the library's int; what 32 bits would wrap becomes a number that it refuses."""
+    return min(max(int(x), -(1 << 31)), (1 << 31) - 1)
+
+
 def make_config(num_q_heads, num_kv_heads, head_dim, dtype, logical_page,
                 physical_page, num_physical_pages, max_seqs, max_context,
                 streaming=None, sink=0, window=0, token_budget=0,
@@ -188,7 +193,7 @@ def make_config(num_q_heads, num_kv_heads, head_dim, dtype, logical_page,
     c.sink, c.window, c.token_budget = sink, window, token_budget
     c.reuse_interval, c.free_list_seed = reuse_interval, free_list_seed
     c.kv_fp8 = 1 if kv_fp8 else 0
-    c.kv_quant = int(kv_quant)
+    c.kv_quant = _int32(kv_quant)
     for name, vals in (("k_scale", k_scale), ("v_scale", v_scale)):
         if vals is not None:
             arr = (ctypes.c_float * num_kv_heads)(*[float(x) for x in vals])
@@ -983,8 +988,8 @@ class Rotary:
             if len(inv_freq) != rotary_dim // 2:
                 raise ValueError("inv_freq must have rotary_dim / 2 entries")
             freq = (ctypes.c_double * max(len(inv_freq), 1))(*[float(f) for f in inv_freq])
-        rule = spd_rotary_rule(int(head_dim), rotary_dim, len(sections),
-                               (ctypes.c_int * 4)(*sections), 1 if axes_in_turn else 0,
+        rule = spd_rotary_rule(_int32(head_dim), _int32(rotary_dim), len(sections),
+                               (ctypes.c_int * 4)(*map(_int32, sections)), 1 if axes_in_turn else 0,
                                1 if neighbours else 0, float(base),
                                ctypes.cast(freq, ctypes.POINTER(ctypes.c_double)) if freq else None)
         self.table = spd_rotary_table()
