@@ -50,6 +50,9 @@ constexpr int kThreads = kQuantWarps * 32;
 // groups (step 0) is given: p 2^k stays finite, and 0 times it 0.
 constexpr int kRoom = 11;
 constexpr int kHead = 10;
+// The reference before any score: finite, so that scores of -inf (a bias beyond fp32's range) are
+// weights of 0 where a warp meets nothing else, too.
+constexpr float kNoScore = -3.402823466e38f;
 
 __device__ __forceinline__ void qd_set_err(int *err, int code, int a, int b, int c) {
   if (atomicCAS(err, 0, code) == 0) {
@@ -243,7 +246,7 @@ struct Warp {
       slope[c] = __shfl_sync(kFull, sl, from);
 #pragma unroll
       for (int a = 0; a < NG; ++a) qs[c][a] = __shfl_sync(kFull, sum[a], from);
-      m[c] = -CUDART_INF_F;
+      m[c] = kNoScore;
       up[c] = 1.f;
       k2[c] = 0;
       l[c] = 0.f;
@@ -436,7 +439,6 @@ struct Warp {
         // z: the largest p step so far, as a power of 2 (of differences of scores: a vast score
         // itself would round the exponent away)
         float z = (m[c] - a) + (float)(kRoom - k2[c]);
-        if (m[c] == -CUDART_INF_F) z = -CUDART_INF_F;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll

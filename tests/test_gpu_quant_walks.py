@@ -264,3 +264,48 @@ def test_vast_scores_and_steps(bits, dtype, out, at):
         tol = tol + 17 * 2.0 ** -14 * step
     assert bool(((got.double() - ref).abs() <= tol).all())
     c.check_status()
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("out", ["same", "fp32"])
+@pytest.mark.parametrize("L,g", [(700, 1), (3000, 4), (3000, 8)])
+def test_biases_beyond_the_range_leave_the_newest_token(bits, out, L, g):
+    """Slopes of 10^36: scores of all but some hundred tokens are -inf in fp32, and whole walks see
+    nothing else."""
+    d, dt = 128, torch.bfloat16
+    c, ids, k, v = filled(L, 2 * g, 2, d, "bf16", bits, seed=9)
+    q = normal(1, 1, 2 * g, d, dtype=dt)
+    slopes = torch.full((2 * g,), 1e36, device="cuda")
+    od = F32 if out == "fp32" else dt
+    got = c.quant_decode_attention(q, ids, slopes=slopes, out_dtype=od)[0].unflatten(0, (2, g))
+    ref, _ = held(v[0, -1], bits)
+    lo, step, _ = quantise(v[0, -1], bits)
+    # (a weight of 1, cut off to 22 bits)
+    tol = 2.0 ** -20 * (lo.abs() + step * (2 ** bits - 1)) + STEP[od] * ref.abs() + FLOOR[od]
+    if od != F32:
+        tol = tol + 17 * 2.0 ** -14 * step
+    assert bool(((got.double() - ref[:, None]).abs() <= tol[:, None]).all())
+    c.check_status()
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("out", ["same", "fp32"])
+def test_queries_that_are_not_finite_stay_with_their_heads(bits, out):
+    """Infinite and NaN queries give NaN in their own heads; the others', in the same columns of the
+    products, are as exact as ever."""
+    L, hkv, g, d, dt = 3000, 2, 4, 128, torch.float16
+    c, ids, k, v = filled(L, hkv * g, hkv, d, "fp16", bits, seed=4)
+    q = normal(2, 1, hkv * g, d, dtype=dt)
+    q[0, 1, 7], q[0, 2, 9], q[0, 7, 0] = math.inf, math.nan, -math.inf
+    od = F32 if out == "fp32" else dt
+    got = c.quant_decode_attention(q, ids, out_dtype=od)[0]
+    c.check_status()
+    for h in range(hkv * g):
+        if h in (1, 2, 7):
+            assert bool(got[h].isnan().all())
+            continue
+        kh, vh, row = k[0, :, h // g], v[0, :, h // g], q[0, h:h + 1]
+        w = torch.softmax(row.double() @ held(kh, bits)[0].t() * d ** -0.5, 1)
+        ref = w @ held(vh, bits)[0]
+        tol = tolerance(row, kh, vh, bits, d ** -0.5, 1, d, od)(w, ref)
+        assert bool(((got[h:h + 1].double() - ref).abs() <= tol).all()), h
