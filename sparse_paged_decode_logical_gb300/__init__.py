@@ -632,7 +632,8 @@ class SparsePagedKVCache:
         contiguous tensor for it, or q itself).  Rows may be strided, as in a fused
         projection's output.  positions int32 [axes][n][tokens] ([n][tokens] with
         one axis); None: a token's place in its sequence.  `stream` as in
-        :func:`prefill_attention`."""
+        :func:`prefill_attention`.  No gradient passes through a cache, nor through the
+        q that comes back here (:func:`rotary` has one)."""
         ids, n = self._id_array(seq_ids)
         # (what shapes, strides and types decide is worked out once)
         key = (n, table.axes, q.shape, q.stride(), q.dtype, q.get_device(), k.shape, k.stride(),

@@ -38,8 +38,10 @@ spd_status need_quant(spd_ctx *c, const CtxView &v) {
   return fail_message(c, SPD_ERR_INVALID_ARG, "the context has no kv_quant");
 }
 
-// CTAs that share a tile's heads, kQuantWriteWarps at once each: as many as leave every SM a
-// few; each makes the tile's sines again.
+// CTAs that share a tile's heads, kQuantWriteWarps at once each: as many as make 14 CTAs an SM;
+// each makes the tile's sines again.  (2,048 tokens of 32 and 8 heads of 128 channels into 8 bits
+// 16.9 us, 17.6 with 6; 4,096, where the queries are in the launch, 30.8 and 26.2; 8,192 into 4 bits
+// 54.1 and 56.9, 16,385 92.0 and 95.0; 30 is as 14.)
 int parts_of(long long tiles, int works, int sms) {
   const int most = (works + kQuantWriteWarps - 1) / kQuantWriteWarps;
   return (int)std::max<long long>(1, std::min<long long>(most, 14LL * sms / std::max(tiles, 1LL)));
@@ -60,9 +62,12 @@ long long tiles_of(long long first, long long n) {
 namespace spd {
 
 // Queries of few tokens are rotated by the appending launch, those of many by one of their own,
-// whose threads need a third of the registers (16,385 tokens of 32 and 8 heads, 8 bits: 84 us;
-// 125 in one launch).  Before that the new pages go by themselves (102 us with reading back, 105
-// with the pages in the second launch).
+// whose threads need a third of the registers.  Tokens of 32 query heads, apart and together: with 8
+// kv heads of 128 channels in 8 bits 2,048 tokens 22.0 and 16.7 us, 4,096 27.2 and 31.2, 4,880 29.9
+// and 33.9, 16,385 79.6 and 88.7; in 4 bits 27.0 and 21.5, 31.1 and 36.2, 34.1 and 40.0, 92.6 and
+// 100.7; with 4 kv heads of 64 channels in 4 bits 14.7 and 11.0, 16.7 and 16.4, 17.3 and 16.8, 38.0
+// and 43.7.  Before a launch of their own the new pages go by themselves (16,385 tokens with reading
+// back 102 us, 105 with the pages in the second launch).
 static bool queries_apart(const QuantWrite &w, long long tiles, int sms) {
   return w.table && tiles > 2LL * sms;
 }
@@ -383,7 +388,7 @@ spd_status spd_quant_decode_attention(spd_ctx *c, const void *q, const int *seq_
   for (int b = 0; b < n_seqs;) {
     static thread_local QuantAttendParams p;
     // as many sequences as fit one launch
-    int n = 0, most = 0;
+    int n = 0;
     long long total = 0;
     while (n < kQuantSeqs && b + n < n_seqs) {
       const int L = (int)seq_length(c, seq_ids[b + n]);
@@ -392,16 +397,18 @@ spd_status spd_quant_decode_attention(spd_ctx *c, const void *q, const int *seq_
       if (n > 0 && total + (long long)tiles * Hkv > kMaxPlaces) break;
       p.seqs[n] = QuantAttendSeq{seq_ids[b + n], L, first, tiles, tiles, 0};
       total += (long long)tiles * Hkv;
-      most = std::max(most, tiles);
       ++n;
     }
     if (total > kMaxPlaces)
       return fail_message(c, SPD_ERR_CAPACITY, "a sequence is too long for one launch");
-    // Every warp takes per_warp tiles.  Where all units can begin at a CTA of their own
-    // without another step per warp they do, so that no unit has a stray part elsewhere.
+    // Every warp takes per_warp tiles, whole steps of them.  Where one step (or a sixteenth) more
+    // lets all units begin at a CTA of their own they do, so that no unit has a stray part
+    // elsewhere, and fewer are joined over CTAs: 16 windows of 4,096 tokens that begin inside a tile
+    // (257 tiles a unit) take 29.9 us with 22 tiles a warp on 128 CTAs, 33.0 with 20 on all SMs (fp32
+    // out; 27.0 and 29.5 for 16 bits).
     const long long warps = (long long)most_ctas * kQuantWarps;
     const int step = quant_step_tiles(cfg.head_dim);
-    p.per_warp = (int)((total + warps - 1) / warps + step - 1) / step * step;  // (whole steps)
+    p.per_warp = (int)((total + warps - 1) / warps + step - 1) / step * step;
     auto ctas_of = [&](int per_warp) {  // with units that begin at CTAs
       long long k = 0;
       for (int i = 0; i < n; ++i)

@@ -5,11 +5,14 @@
 // rounded to nearest, 0 .. levels; differences count exactly, also where fp32 rounds them.  A group that holds a value that is not finite (or whose
 // span exceeds fp32) gets lo = NaN and step 0: it reads back as NaN throughout.
 //
-// Both directions are bound by memory: 2 bytes a value on one side, 1.03 or 0.63 on the other.
-// One warp takes a whole tile of 16 tokens of K or of V of a head; its lanes read the
-// channels whose codes fill the words that they store (layout in quant.h), so that a group's
-// extremes are a few shuffles away and nothing passes through shared memory, except keys that
-// are rotated first.  Tiles that are not filled at once go token by token, byte stores.
+// A warp takes a head's tile of 16 tokens, K and V.  Their rows come to shared memory by
+// asynchronous copies, keys are rotated there, and every lane reads the channels whose codes fill
+// the words that it stores (layout in quant.h), so that a group's extremes are a few shuffles away.
+// Tiles that are not filled at once go token by token, byte stores.
+//
+// 2 bytes a value on one side, 1.03 or 0.63 on the other.  Reading back is bound by memory (16,385
+// tokens of 8 kv heads of 128 channels in 8 bits 15 us, its floor; 4 bits 14.7).  Writing keys and
+// values is not: 43 us for a floor of 15, DRAM at 21% of its peak, ALU at 50%, 27% of the warps.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

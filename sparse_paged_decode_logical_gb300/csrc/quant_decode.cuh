@@ -7,8 +7,9 @@
 // so that the matrix products run over the codes themselves, which an fp16 operand holds
 // exactly: an integer of 8 or 4 bits in the low bits of an fp16 number is that integer times
 // 2^-24, a subnormal, 2^-20 four bits higher.  A word of codes becomes operands by masks and
-// shifts alone: 5 instructions for 8 codes of 4 bits, 3 for 4 of 8.  (tcgen05 has no use here: it reads operands from shared or tensor
-// memory, where the widened codes would first have to be written.)
+// shifts alone: 5 instructions for 8 codes of 4 bits, 3 for 4 of 8.  (tcgen05 has no use here: it
+// reads operands from shared or tensor memory, where the widened codes would first have to be
+// written.)
 //
 // The products are transposed, S = K q and O = V p, so that a kv head's 1 to 8 query heads are
 // the short side (n = 8) of m16n8k16; scores reach the second product by movmatrix.  Where at
@@ -16,13 +17,13 @@
 // halves of the weights, so that weights in two fp16 parts cost no product more.
 //
 // Bound by memory, in 4 bits as nearly by instructions: the cache is read once.  131,072 tokens of
-// 8 kv heads of 128 channels (32 query heads, bf16) take 48.8 us in 8 bits (84% of the measured
-// copy rate) and 37.5 in 4 (66%): of these about 31 us in the loop, at 81% of that rate and with
-// 335 instructions a tile, and 6 us behind it, in five dependent rounds of joining.  Every warp walks a stretch of tiles through its own
-// ring of bulk copies, without a barrier between warps; the launch's warps share all sequences'
-// tiles evenly, a warp may end one unit (sequence, kv head) and start the next.  What a warp
-// holds of a unit that others hold parts of, too, is joined in the CTA, then over CTAs by the
-// last one to finish.
+// 8 kv heads of 128 channels (32 query heads, bf16) take 49.3 us in 8 bits (83% of the measured
+// copy rate) and 40.3 in 4 (62%), with 367 instructions a tile in all; about 6 us of that lie
+// behind the loop, in five dependent rounds of joining.  Every warp walks a stretch of tiles
+// through its own ring of bulk copies, without a barrier between warps; the launch's warps share
+// all sequences' tiles evenly, a warp may end one unit (sequence, kv head) and start the next.
+// What a warp holds of a unit that others hold parts of, too, is joined in the CTA, then over CTAs
+// by the last one to finish.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -179,7 +180,7 @@ struct Warp {
   // and in the accumulator over the whole walk 1e-3 at 64 tiles, 0.2 at 1,024.)  For fp32: ordinary
   // numbers around 0, code - 2^(b-1) (11 instructions a word of 4 bits instead of 5, 5 for 4 codes
   // of 8 bits instead of 3), and K's products over more than two operands are added in fp32 outside:
-  // 2e-7 and 4e-7.  (131,072 tokens in 4 bits 52 us, 38 for 16-bit outputs.)
+  // 2e-7 and 4e-7.  (131,072 tokens in 4 bits 51.5 us, 40.3 for 16-bit outputs.)
   static constexpr bool kNibbles = BITS == 4 && !FINE;  // high nibbles 2^4 as large
   static constexpr int kUnit = FINE ? 0 : 24;           // a code of 1 is 2^-kUnit
   static constexpr float kMid = FINE ? (BITS == 4 ? 8.f : 128.f) : 0.f;
