@@ -681,8 +681,9 @@ spd_status spd_seq_truncate(spd_ctx *ctx, int seq_id, int n_tokens);
  *   q    device [n_seqs][Hq][d];  out device [n_seqs][Hq][d], fp32 or dtype
  *   rule NULL: plain
  * Softmax weights enter the products with 22 bits and the codes exactly; sums are
- * fp32, and no error grows with the length of a sequence (where out has 16 bits, the
- * tensor cores cut a product over 16 tokens or channels off at 2^-10 of a step).
+ * fp32, and no error grows with the length of a sequence, relative to what is summed
+ * (where out has 16 bits, the tensor cores cut a product over 16 tokens or channels
+ * off at 2^-10 of a step).
  * Keys beyond 2^104 (bf16) may make scores infinite that the product with a small
  * query would not, values beyond 2^88 (bf16) their sums.  Keys or values outside the
  * window never reach the output, finite or not.

@@ -1047,7 +1047,10 @@ def _rotated():
                 ctx.set_materialize_grads(False)
                 ctx.save_for_backward(positions)
                 ctx.table, ctx.inverse = table, inverse
-                return rotary(table, positions, q, k, inverse, stream=stream)
+                y = rotary(table, positions, q, k, inverse, stream=stream)
+                if k is not None and not all(ctx.needs_input_grad[2:4]):
+                    ctx.mark_non_differentiable(y[0 if ctx.needs_input_grad[3] else 1])
+                return y
 
             @staticmethod
             def backward(ctx, *grads):

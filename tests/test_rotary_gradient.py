@@ -59,6 +59,14 @@ def test_only_what_asks_for_a_gradient_is_rotated_back(rec):
     assert calls(rec)[-1] == (4, False, 1) and q.grad.shape == q.shape
 
 
+def test_what_asks_for_no_gradient_comes_back_without_one(rec):
+    for grad in ((True, False), (False, True)):
+        pos, q, k = operands(grad)
+        assert tuple(y.requires_grad for y in spd.rotary(TABLE, pos, q, k)) == grad
+    pos, q, k = operands((False, False))
+    assert not any(y.requires_grad for y in spd.rotary(TABLE, pos, q, k))
+
+
 def test_nothing_is_kept_where_no_gradient_is_asked_for(rec):
     pos, q, k = operands()
     with torch.no_grad():
