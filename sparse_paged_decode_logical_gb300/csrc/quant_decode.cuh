@@ -46,9 +46,9 @@ constexpr int kThreads = kQuantWarps * 32;
 
 // A weight enters the product as p 2^k step, p = 2^(score - m): 2^k moves the largest p step of
 // a column to between 2^10 and 2^12, and a new k is taken where one would pass 2^15.  What fp16
-// loses below its normal range is then 2^-35 of the largest.  p itself may grow to 2^kHead before
-// a new reference is taken, and k ends at 126 - kHead, which a column of nothing but constant
-// groups (step 0) is given: p 2^k stays finite, and 0 times it 0.
+// loses below its normal range is then 2^-35 of the largest.  k ends at 126, which a column of
+// nothing but constant groups (step 0) is given, too: p 2^k beyond fp32's range, and 0 times that,
+// take a new reference.  So does a p of 2^kHead (sums of p lo stay in range).
 constexpr int kRoom = 11;
 constexpr int kHead = 10;
 // The reference before any score: finite, so that scores of -inf (a bias beyond fp32's range) are
@@ -451,7 +451,7 @@ struct Warp {
           }
 #pragma unroll
         for (int k = 4; k < 32; k <<= 1) z = fmaxf(z, __shfl_xor_sync(kFull, z, k));
-        const int k = (int)fminf(fmaxf(floorf(-z), -120.f), 126.f - kHead - kRoom) + kRoom;
+        const int k = (int)fminf(fmaxf(floorf(-z), -120.f), 126.f - kRoom) + kRoom;
         const bool same = a == m[c];
         const float fa = same ? 1.f : ex2_approx(m[c] - a);
         const float fb = ex2_approx((same ? 0.f : m[c] - a) + (float)(k - k2[c]));

@@ -211,9 +211,21 @@ def test_references_move_in_the_middle_of_a_walk(g, d, bits, dtype, out):
 @pytest.mark.parametrize("out", ["same", "fp32"])
 @pytest.mark.parametrize("size", [2.0 ** 80, 2.0 ** -80])
 def test_constant_and_vast_values_under_rising_scores(bits, out, size):
+    vast_values(bits, out, size, 30.0)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("out", ["same", "fp32"])
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -124])
+def test_tiny_values_keep_the_bits_of_their_weights(bits, out, size):
+    vast_values(bits, out, size, 0.0)
+
+
+def vast_values(bits, out, size, height):
     d, hkv = 128, 4
     L = tokens_for(16, hkv)
-    k = (normal(1, L, hkv, d) + saw(L, 30.0, 500)[:, None, None]).bfloat16()
+    k = normal(1, L, hkv, d)
+    k = (k + saw(L, height, 500)[:, None, None]).bfloat16()
     v = normal(2, L, hkv, d) * size
     v[:, ::2] = size
     v = v.bfloat16()
